@@ -342,6 +342,97 @@ fljsd_status fljsd_ce_forward(const fljsd_ce_problem* problem, const fljsd_plan_
                               void* grad_input, void* grad_weight, void* workspace,
                               size_t workspace_bytes, fljsd_stream_t stream);
 
+/*
+ * Token log probabilities: for every row of logits z (z = x . w^T of hidden
+ * states and an lm_head weight, or given logits), with s = z / temperature and
+ * p = softmax(s):
+ *   lse = log sum_j e^{s_j},  logp = s_y - lse,  entropy = -sum_j p_j log p_j,
+ *   the top_k largest logits as (column, log probability), in descending order,
+ *   equal logits by the lower column.
+ * Upstream gradients a (grad_logp) and b (grad_entropy), [bt] fp32 each, give
+ *   dz_j = (a (1[j = y] - p_j) - b p_j (log p_j + entropy)) / temperature,
+ *   grad_input = dz . w,  grad_weight = dz^T . x.
+ * All of it is computed in fp32 from unrounded logits (the fused form never
+ * writes them); the top alternatives carry no gradient.
+ *
+ * Rows and values outside the ordinary:
+ *  - a row whose label is ignore_index, or outside [0, v), has logp 0, entropy 0
+ *    and gradient 0; its lse and alternatives are written all the same. A label
+ *    outside [0, v) other than ignore_index also sets the status word to
+ *    FLJSD_ERR_INVALID_ARG (fljsd_workspace_status; fljsd_logits_lp: the first
+ *    int32 of the workspace).
+ *  - a logit of -inf (a masked token) has probability 0 and is no alternative:
+ *    where fewer than top_k remain, the rest is column -1 with -inf. A row of
+ *    nothing else has lse -inf, logp -inf, entropy 0 and gradient 0.
+ *  - a logit of NaN or +inf makes the row's lse, logp and entropy NaN; NaN is no
+ *    alternative.
+ *
+ * fljsd_lp_plan / fljsd_lp_forward / fljsd_lp_backward follow fljsd_plan and
+ * fljsd_forward: caller-owned device memory, asynchronous on `stream`, errors
+ * found on the host before anything is launched. x [bt x h] and w [v x h] in
+ * dtype, 16-byte aligned; labels [bt] int64 or NULL (then no logp); logp,
+ * entropy, lse [bt] fp32; norm [bt x 2] fp32, for the backward pass (the row's
+ * largest logit and log2 of the sum of e^{s_j} relative to it); top_logp [bt x top_k] fp32 and top_id [bt x top_k]
+ * int64 (NULL with top_k 0). bf16 with h a multiple of 8 runs on the tensor
+ * cores, everything else on the CUDA cores.
+ *
+ * FLJSD_LP_BACKWARD sizes the workspace for fljsd_lp_backward, and lets the
+ * forward of a one-chunk plan leave there what the backward would otherwise
+ * compute again: pass kept = 1 when the workspace is as the forward of the same
+ * problem and inputs left it (a backward pass uses it up), kept = 0 to compute
+ * it again. logp, entropy and norm are the forward's results; grad_logp
+ * (needs labels) and grad_entropy may be NULL (zero). grad_input and grad_weight are
+ * written in full, as by fljsd_forward; one of them may be NULL and is left out.
+ *
+ * fljsd_logits_lp / fljsd_logits_lp_backward are the same of given logits
+ * [rows x v] in dtype with row stride ld (elements, any alignment) and of their
+ * gradient, written in dtype with row stride ld_grad; it may overwrite the
+ * logits (same address and stride).
+ *
+ * Errors: FLJSD_ERR_INVALID_ARG for a dimension <= 0, a stride below v, an
+ * unknown dtype or flag, top_k outside [0, v], a temperature that is not
+ * positive and finite, grad_logp without labels, a null or unaligned pointer, or
+ * kept = 1 with more than one chunk; FLJSD_ERR_UNSUPPORTED for top_k above 32,
+ * bt, rows or v above 2^30 or h above 2^20; FLJSD_ERR_WORKSPACE for a workspace
+ * below the plan's (or, in fljsd_lp_plan, when not even one row fits the
+ * budget); FLJSD_ERR_CUDA when a launch fails.
+ */
+typedef struct {
+  int64_t bt, h, v;
+  int32_t dtype;         /* fljsd_dtype */
+  int32_t top_k;         /* alternatives of each row, 0..32 */
+  int64_t ignore_index;
+  int64_t chunk_rows;    /* 0 lets fljsd_lp_plan choose */
+  float temperature;     /* > 0 and finite */
+  int32_t flags;         /* FLJSD_LP_BACKWARD, FLJSD_FLAG_ACCUM_FP32 */
+} fljsd_lp_problem;
+#define FLJSD_LP_BACKWARD 4
+
+fljsd_status fljsd_lp_plan(const fljsd_lp_problem* problem, size_t free_hbm_bytes,
+                           fljsd_plan_t* out);
+fljsd_status fljsd_lp_forward(const fljsd_lp_problem* problem, const fljsd_plan_t* plan,
+                              const void* x, const void* w, const int64_t* labels, float* logp,
+                              float* entropy, float* lse, float* norm, float* top_logp, int64_t* top_id,
+                              void* workspace, size_t workspace_bytes, fljsd_stream_t stream);
+fljsd_status fljsd_lp_backward(const fljsd_lp_problem* problem, const fljsd_plan_t* plan,
+                               const void* x, const void* w, const int64_t* labels,
+                               const float* logp, const float* entropy, const float* norm,
+                               const float* grad_logp, const float* grad_entropy, int32_t kept,
+                               void* grad_input, void* grad_weight, void* workspace,
+                               size_t workspace_bytes, fljsd_stream_t stream);
+size_t fljsd_logits_lp_workspace_bytes(int64_t rows, int64_t v, int32_t top_k);
+fljsd_status fljsd_logits_lp(int64_t rows, int64_t v, int64_t ld, int32_t dtype, int32_t top_k,
+                             float temperature, int64_t ignore_index, const void* logits,
+                             const int64_t* labels, float* logp, float* entropy, float* lse, float* norm,
+                             float* top_logp, int64_t* top_id, void* workspace,
+                             size_t workspace_bytes, fljsd_stream_t stream);
+fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64_t ld_grad,
+                                      int32_t dtype, float temperature, int64_t ignore_index,
+                                      const void* logits, const int64_t* labels,
+                                      const float* logp, const float* entropy, const float* norm,
+                                      const float* grad_logp, const float* grad_entropy,
+                                      void* grad_logits, fljsd_stream_t stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fljsd_status_string(fljsd_status status);
 

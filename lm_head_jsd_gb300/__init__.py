@@ -18,6 +18,13 @@ from ._lib import (  # noqa: F401
     fljsd_scale,
     fljsd_tvd,
     fljsd_launch_count,
+    fljsd_logits_lp,
+    fljsd_logits_lp_backward,
+    fljsd_logits_lp_workspace_bytes,
+    fljsd_lp_backward,
+    fljsd_lp_forward,
+    fljsd_lp_plan,
+    make_lp_problem,
     fljsd_launch_count_reset,
     fljsd_plan,
     fljsd_status_string,
@@ -34,6 +41,14 @@ from .api import (  # noqa: F401
     fused_linear_jsd,
     jsd_logspace,
     tvd,
+)
+from .logprobs import (  # noqa: F401
+    FusedLinearLogprobs,
+    Logprobs,
+    fused_linear_logprobs,
+    logits_logprobs,
+    logits_logprobs_backward,
+    token_logprobs,
 )
 
 LIB_PATH = _lib.LIB_PATH

@@ -45,8 +45,16 @@ class fljsd_ce_problem(ctypes.Structure):
                 ("softcap", ctypes.c_float), ("flags", ctypes.c_int32)]
 
 
+class fljsd_lp_problem(ctypes.Structure):
+    _fields_ = [("bt", ctypes.c_int64), ("h", ctypes.c_int64), ("v", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64), ("chunk_rows", ctypes.c_int64),
+                ("temperature", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
 FLJSD_FLAG_T2 = 1
 FLJSD_FLAG_ACCUM_FP32 = 2
+FLJSD_LP_BACKWARD = 4
 
 
 class fljsd_plan_t(ctypes.Structure):
@@ -99,6 +107,22 @@ def _load():
                                      ctypes.POINTER(fljsd_plan_t), P, P, P, P, P, P, P,
                                      ctypes.c_size_t, P]
     lib.fljsd_ce_forward.restype = ctypes.c_int
+    i32, i64, f32, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    lib.fljsd_lp_plan.argtypes = [ctypes.POINTER(fljsd_lp_problem), size,
+                                  ctypes.POINTER(fljsd_plan_t)]
+    lib.fljsd_lp_plan.restype = ctypes.c_int
+    lib.fljsd_lp_forward.argtypes = [ctypes.POINTER(fljsd_lp_problem),
+                                     ctypes.POINTER(fljsd_plan_t), *[P] * 10, size, P]
+    lib.fljsd_lp_forward.restype = ctypes.c_int
+    lib.fljsd_lp_backward.argtypes = [ctypes.POINTER(fljsd_lp_problem),
+                                      ctypes.POINTER(fljsd_plan_t), *[P] * 8, i32, P, P, P, size, P]
+    lib.fljsd_lp_backward.restype = ctypes.c_int
+    lib.fljsd_logits_lp_workspace_bytes.argtypes = [i64, i64, i32]
+    lib.fljsd_logits_lp_workspace_bytes.restype = size
+    lib.fljsd_logits_lp.argtypes = [i64, i64, i64, i32, i32, f32, i64, *[P] * 9, size, P]
+    lib.fljsd_logits_lp.restype = ctypes.c_int
+    lib.fljsd_logits_lp_backward.argtypes = [i64, i64, i64, i64, i32, f32, i64, *[P] * 9]
+    lib.fljsd_logits_lp_backward.restype = ctypes.c_int
     lib.fljsd_status_string.argtypes = [ctypes.c_int]
     lib.fljsd_status_string.restype = ctypes.c_char_p
     lib.fljsd_launch_count.argtypes = []
@@ -284,6 +308,78 @@ def fljsd_ce_forward(problem, plan, x, w, labels, loss, grad_input, grad_weight,
                               _ptr(workspace), workspace_bytes, _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_ce_forward")
+    return st
+
+
+def make_lp_problem(bt, h, v, dtype="bf16", top_k=0, temperature=1.0, ignore_index=-100,
+                    chunk_rows=0, backward=False, accum_fp32=False) -> fljsd_lp_problem:
+    flags = (FLJSD_LP_BACKWARD if backward else 0) | (FLJSD_FLAG_ACCUM_FP32 if accum_fp32 else 0)
+    return fljsd_lp_problem(bt, h, v, _dt(dtype), top_k, ignore_index, chunk_rows, temperature,
+                            flags)
+
+
+def fljsd_lp_plan(problem, free_hbm_bytes: int = 0) -> fljsd_plan_t:
+    plan = fljsd_plan_t()
+    st = lib.fljsd_lp_plan(ctypes.byref(problem), free_hbm_bytes, ctypes.byref(plan))
+    if st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_lp_plan")
+    return plan
+
+
+def fljsd_lp_forward(problem, plan, x, w, labels, logp, entropy, lse, norm, top_logp, top_id, workspace,
+                     workspace_bytes=None, stream=None, check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_lp_forward(ctypes.byref(problem), ctypes.byref(plan), _ptr(x), _ptr(w),
+                              _ptr(labels), _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(norm),
+                              _ptr(top_logp), _ptr(top_id), _ptr(workspace), workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_lp_forward")
+    return st
+
+
+def fljsd_lp_backward(problem, plan, x, w, labels, logp, entropy, norm, grad_logp, grad_entropy,
+                      kept, grad_input, grad_weight, workspace, workspace_bytes=None, stream=None,
+                      check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_lp_backward(ctypes.byref(problem), ctypes.byref(plan), _ptr(x), _ptr(w),
+                               _ptr(labels), _ptr(logp), _ptr(entropy), _ptr(norm),
+                               _ptr(grad_logp), _ptr(grad_entropy), kept, _ptr(grad_input),
+                               _ptr(grad_weight), _ptr(workspace), workspace_bytes,
+                               _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_lp_backward")
+    return st
+
+
+def fljsd_logits_lp_workspace_bytes(rows: int, v: int, top_k: int) -> int:
+    return lib.fljsd_logits_lp_workspace_bytes(rows, v, top_k)
+
+
+def fljsd_logits_lp(rows, v, ld, dtype, top_k, temperature, ignore_index, logits, labels, logp,
+                    entropy, lse, norm, top_logp, top_id, workspace, workspace_bytes=None, stream=None,
+                    check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_logits_lp(rows, v, ld, _dt(dtype), top_k, temperature, ignore_index,
+                             _ptr(logits), _ptr(labels), _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(norm),
+                             _ptr(top_logp), _ptr(top_id), _ptr(workspace), workspace_bytes,
+                             _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_logits_lp")
+    return st
+
+
+def fljsd_logits_lp_backward(rows, v, ld, ld_grad, dtype, temperature, ignore_index, logits,
+                             labels, logp, entropy, norm, grad_logp, grad_entropy, grad_logits,
+                             stream=None, check=True) -> int:
+    st = lib.fljsd_logits_lp_backward(rows, v, ld, ld_grad, _dt(dtype), temperature, ignore_index,
+                                      _ptr(logits), _ptr(labels), _ptr(logp), _ptr(entropy),
+                                      _ptr(norm), _ptr(grad_logp), _ptr(grad_entropy),
+                                      _ptr(grad_logits), _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_logits_lp_backward")
     return st
 
 

@@ -1,0 +1,504 @@
+// Token log probabilities fused with the lm_head product (sm_103a): z = X . W^T
+// on the tensor cores, reduced in the epilogue; the logits never reach memory.
+//
+// The product is that of gemm_tc_kernel.cuh (TMA ring, tcgen05.mma, two
+// accumulators in tensor memory, CTA pairs on 256 x 256 tiles); what differs is
+// the epilogue: eight warps, each thread one row of 128 columns (a part), which
+// reads its accumulator twice:
+//   1. the part's maximum, the label's logit, the candidates for the k largest;
+//   2. d = sum 2^t and s = sum 2^t t relative to that maximum, and for a
+//      backward pass 2^t itself in bf16.
+// Two readings of tensor memory cost less than rescaling running sums and give
+// every stored 2^t the same reference. 2^t is rounded to bf16 (at most 2^-9 of
+// its value) because the gradient that is made of it is rounded to bf16 too;
+// keeping the logits instead would need fp32 for the same error.
+//
+// The k largest: every thread keeps a sorted list of its part in registers. What
+// keeps this rare is a threshold for each row: the parts are dealt into k groups
+// (part index mod k), gmax[row][g] is the largest logit seen in group g, and at
+// least k logits of the row reach the least of the k group maxima, so anything
+// below it can be skipped. A chunk of 32 columns whose maximum is below every
+// lane's threshold costs one vote. The order in which parts arrive changes how
+// much is skipped, never the result: candidates equal to the threshold are
+// kept, and k_lp_join orders them by value and column.
+#include "gemm_tc_kernel.cuh"
+#include "lp.cuh"
+
+#include <mutex>
+
+namespace fljsd {
+namespace {
+
+using namespace tcgemm;
+
+constexpr int kThreads = 320;  // producer, MMA, eight epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kKeepBufs = 2;   // staging buffers of an epilogue warp
+
+struct HeadParams {
+  int64_t m, n;
+  int num_n_blocks, num_k_blocks, m_units, num_units, group_m, nst;
+  float c;
+  const int64_t* labels;
+  float4* part;
+  int64_t parts;
+  float* zy;
+  int top;
+  unsigned* gmax;
+  int* count;
+  int2* cand;
+  unsigned long long timeout_ns;
+  int* status;
+};
+
+__host__ __device__ constexpr int head_smem(int nst, bool pair, bool keep) {
+  return nst * stage_bytes(pair) + (keep ? kEpiWarps * kKeepBufs * OUT_BUF_BYTES : 0) + 1024 +
+         CTRL_BYTES;
+}
+__host__ __device__ constexpr int head_stages(bool pair, bool keep) {
+  return pair ? (keep ? 5 : 6) : (keep ? 3 : 4);
+}
+static_assert(head_smem(head_stages(true, true), true, true) <= SMEM_MAX &&
+                  head_smem(head_stages(true, false), true, false) <= SMEM_MAX &&
+                  head_smem(head_stages(false, true), false, true) <= SMEM_MAX &&
+                  head_smem(head_stages(false, false), false, false) <= SMEM_MAX,
+              "shared memory");
+
+// A thread's list of its part's largest logits, in descending order; ties keep
+// the earlier column in front.
+template <int KT>
+struct TopList {
+  float v[KT];
+  int id[KT];
+  __device__ __forceinline__ void clear(float below) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+      v[j] = below;
+      id[j] = -1;
+    }
+  }
+  __device__ __forceinline__ void insert(float x, int col) {
+#pragma unroll
+    for (int j = KT - 1; j > 0; --j) {
+      const bool above = x > v[j - 1], here = x > v[j];
+      v[j] = above ? v[j - 1] : (here ? x : v[j]);
+      id[j] = above ? id[j - 1] : (here ? col : id[j]);
+    }
+    if (x > v[0]) {
+      v[0] = x;
+      id[0] = col;
+    }
+  }
+};
+
+// The largest value below x (-inf stays): candidates must exceed it.
+__device__ __forceinline__ float below(unsigned key) {
+  if (key <= 0x00800000u) return -INFINITY;  // no value yet, or -inf
+  const unsigned k = key - 1;
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+template <bool PAIR, int KT, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_lp_head(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmE, const HeadParams p) {
+  constexpr int SB = stage_bytes(PAIR);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* stg = smem_raw + (base - raw) + p.nst * SB;
+  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + (KEEP ? kEpiWarps * kKeepBufs * OUT_BUF_BYTES : 0));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&cb->full[s]), 1);
+      mbar_init(smem_u32(&cb->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&cb->tmem_full[a]), 1);
+      mbar_init(smem_u32(&cb->tmem_empty[a]), PAIR ? 2 * kEpiWarps : kEpiWarps);
+    }
+    mbar_init(smem_u32(&cb->drain), 1);
+    cb->abort = 0;
+    cb->timeout_ns = p.timeout_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    if (KEEP) prefetch_tensormap(&tmE);
+  }
+  if (PAIR) cluster_sync_all();
+  if (warp == 1) tmem_alloc<PAIR>(smem_u32(&cb->tmem_base), TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = cb->tmem_base;
+  const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int unit_step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+  // bands of group_m m-units sweeping all n-blocks (the band of X stays in L2
+  // while W streams once per band)
+  auto tile_coords = [&](int t, int& mb, int& nb) {
+    const int band = t / (p.group_m * p.num_n_blocks);
+    const int m0 = band * p.group_m;
+    const int gm = min(p.group_m, p.m_units - m0);
+    const int r = t - band * p.group_m * p.num_n_blocks;
+    const int mu = m0 + r % gm;
+    nb = r / gm;
+    mb = PAIR ? 2 * mu + (int)rank : mu;
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer (hand-over of a pair's stages: gemm_tc_kernel.cuh) ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued_parity[STAGES];
+      bool issued[STAGES];
+      for (int s = 0; s < STAGES; ++s) issued[s] = false;
+      bool ok = true;
+      const uint32_t flip = (PAIR && !leader) ? 0u : 1u;
+      for (int t = unit0; ok && t < p.num_units; t += unit_step) {
+        int mb, nb;
+        tile_coords(t, mb, nb);
+        const int nrow = nb * BN + (PAIR ? (int)rank * (BN / 2) : 0);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+          if (!wait_bar(cb, smem_u32(&cb->empty[stage]), phase ^ flip, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + stage * SB;
+          uint32_t fb;
+          if (PAIR) {
+            fb = map_to_cta(smem_u32(&cb->full[stage]), 0);
+            if (leader) {
+              mbar_arrive_expect_tx(smem_u32(&cb->full[stage]), 2 * SB);
+              mbar_arrive_remote_relaxed(map_to_cta(smem_u32(&cb->empty[stage]), 1));
+            }
+          } else {
+            fb = smem_u32(&cb->full[stage]);
+            mbar_arrive_expect_tx(fb, SB);
+          }
+          tma_operand<PAIR>(sa, &tmA, fb, kb * BK, mb * BM);
+          tma_operand<PAIR>(sa + A_BYTES, &tmB, fb, kb * BK, nrow);
+          issued[stage] = true;
+          issued_parity[stage] = phase;
+          if (++stage == p.nst) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!PAIR || leader)
+        for (int s = 0; s < STAGES; ++s)
+          if (issued[s]) wait_bar(cb, smem_u32(&cb->full[s]), issued_parity[s], p.status);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = instr_desc(false, false, PAIR);
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      bool any = false;
+      for (int t = unit0; ok && t < p.num_units; t += unit_step, ++local) {
+        const int acc = local & 1;
+        if (!wait_bar<PAIR>(cb, smem_u32(&cb->tmem_empty[acc]), ((local >> 1) & 1) ^ 1u, p.status))
+          break;
+        tc_fence_after();
+        const uint32_t tmem_d = tmem_base + acc * ACC_COLS;
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+          if (!wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + stage * SB;
+#pragma unroll
+          for (int kk = 0; kk < BK / UMMA_K; ++kk)
+            mma_bf16<PAIR>(tmem_d, smem_desc(sa + kk * (UMMA_K * 2), 16, 1024),
+                           smem_desc(sa + A_BYTES + kk * (UMMA_K * 2), 16, 1024), idesc,
+                           (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit<PAIR>(smem_u32(&cb->empty[stage]));
+          any = true;
+          if (++stage == p.nst) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit<PAIR>(smem_u32(&cb->tmem_full[acc]));
+      }
+      if (any) {
+        mma_commit<PAIR>(smem_u32(&cb->drain));
+        wait_bar(cb, smem_u32(&cb->drain), 0, p.status);
+      }
+    }
+  } else {
+    // ---------------- epilogue: one row of 128 columns to a thread ----------------
+    const int sub = warp & 3;         // tensor-memory lane quarter of this warp
+    const int grp = (warp - 2) >> 2;  // columns 0..127 or 128..255 of the tile
+    const int ew = warp - 2;
+    int local = 0;
+    int sbuf = 0;
+    TopList<KT ? KT : 1> list;
+    for (int t = unit0; t < p.num_units; t += unit_step, ++local) {
+      int mb, nb;
+      tile_coords(t, mb, nb);
+      const int acc = local & 1;
+      const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
+      const bool row_ok = row < p.m;
+      const int col0 = nb * BN + grp * LP_PART_COLS;
+      const int ncols = (int)min((int64_t)LP_PART_COLS, p.n - col0);
+      const bool live = row0 < p.m && ncols > 0;  // of this warp
+      int lab = -1;
+      float thr = -INFINITY;
+      if (live && row_ok) {
+        if (p.labels) {
+          const int64_t y = p.labels[row];
+          if (y >= col0 && y < col0 + ncols) lab = (int)(y - col0);
+        }
+        if (KT) {  // the least of the row's group maxima, read from L2
+          unsigned least = 0xffffffffu;
+          const unsigned* g = p.gmax + row * p.top;
+          for (int j = 0; j < p.top; ++j) least = min(least, __ldcg(g + j));
+          thr = below(least);
+        }
+      }
+      bool ok = true;
+      if (lane == 0) {
+        ok = wait_bar<PAIR>(cb, smem_u32(&cb->tmem_full[acc]), (local >> 1) & 1, p.status);
+        if (PAIR && ok && leader && ew == 0)
+          mbar_arrive_remote_relaxed(map_to_cta(smem_u32(&cb->tmem_full[acc]), 1));
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      tc_fence_after();
+      if (live) {
+        const uint32_t tacc = tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS +
+                              grp * LP_PART_COLS;
+        // ---- the maximum, the label's logit, the candidates ----
+        float mx = -INFINITY;
+        if (KT) list.clear(thr);
+#pragma unroll 1
+        for (int c = 0; c < ncols; c += 32) {
+          float v[32];
+          tmem_ld32(tacc + c, v);
+          if (ncols - c < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e >= ncols) v[e] = -INFINITY;
+          }
+          float cm = v[0];
+#pragma unroll
+          for (int e = 1; e < 32; ++e) cm = fmaxf(cm, v[e]);
+          mx = fmaxf(mx, cm);
+          const bool has = lab >= c && lab < c + 32;
+          if (__any_sync(0xffffffffu, has)) {
+            float z = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z = c + e == lab ? v[e] : z;
+            if (has) p.zy[row] = z;
+          }
+          if (KT) {
+            // rows past the last hold zeros and list nothing
+            const bool want = row_ok && cm > list.v[KT ? KT - 1 : 0];
+            if (__any_sync(0xffffffffu, want)) {
+              float mem[32];  // indexed by the loop: in local memory
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mem[e] = v[e];
+              unsigned left = 0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) left |= (want && v[e] > list.v[KT ? KT - 1 : 0]) ? 1u << e : 0u;
+#pragma unroll 1
+              while (__any_sync(0xffffffffu, left != 0)) {
+                if (left) {
+                  const int e = __ffs(left) - 1;
+                  left &= left - 1;
+                  list.insert(mem[e], col0 + c + e);
+                }
+              }
+            }
+          }
+        }
+        // ---- sums relative to the maximum ----
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float2 c2 = make_float2(p.c, p.c), nref = make_float2(-ref, -ref);
+        float2 d = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < ncols; c += 32) {
+          float v[32];
+          tmem_ld32(tacc + c, v);
+          if (ncols - c < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e >= ncols) v[e] = -INFINITY;
+          }
+          if (KEEP && (c & 32) == 0) {
+            // the store that last used this buffer has read it
+            if (lane == 0) bulk_wait_read_1();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = __fmul2_rn(__fadd2_rn(make_float2(v[e], v[e + 1]), nref), c2);
+            const float2 y = make_float2(ex2f_approx(x.x), ex2f_approx(x.y));
+            d = __fadd2_rn(d, y);
+            // 2^t t is 0 for a logit of -inf, and NaN stays NaN
+            s = __ffma2_rn(y, make_float2(fmaxf(x.x, -1024.f), fmaxf(x.y, -1024.f)), s);
+            v[e] = y.x;
+            v[e + 1] = y.y;
+          }
+          if (KEEP) {
+            uint8_t* srow = stg + ((ew * kKeepBufs + sbuf) * 32 + lane) * 128;
+            const int h = (c & 32) ? 4 : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(srow + (((h + q) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16(v[q * 8], v[q * 8 + 1]), pack_bf16(v[q * 8 + 2], v[q * 8 + 3]),
+                             pack_bf16(v[q * 8 + 4], v[q * 8 + 5]),
+                             pack_bf16(v[q * 8 + 6], v[q * 8 + 7]));
+            if ((c & 32) || c + 32 >= ncols) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmE, smem_u32(stg + (ew * kKeepBufs + sbuf) * OUT_BUF_BYTES),
+                             col0 + (c & ~63), (int32_t)row0);
+                bulk_commit();
+              }
+              sbuf ^= 1;
+            }
+          }
+        }
+        if (row_ok) {
+          const int part = nb * 2 + grp;
+          p.part[row * p.parts + part] =
+              make_float4(mx, d.x + d.y, s.x + s.y, 0.f);
+          if (KT) {
+            if (mx > -INFINITY) atomicMax(p.gmax + row * p.top + part % p.top, lp_key(mx));
+            int cnt = 0;
+#pragma unroll
+            for (int j = 0; j < KT; ++j) cnt += (j < p.top && list.id[j] >= 0) ? 1 : 0;
+            if (cnt) {
+              const int64_t cap = p.parts * p.top;
+              int2* dst = p.cand + row * cap + atomicAdd(p.count + row, cnt);
+#pragma unroll
+              for (int j = 0; j < KT; ++j)
+                if (j < cnt) dst[j] = make_int2(__float_as_int(list.v[j]), list.id[j]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR && !leader)
+          mbar_arrive_remote_relaxed(map_to_cta(smem_u32(&cb->tmem_empty[acc]), 0));
+        else
+          mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+      }
+    }
+    if (KEEP && lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<PAIR>(tmem_base, TMEM_COLS);
+  }
+}
+
+template <bool PAIR, int KT, bool KEEP>
+cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
+                     const HeadParams& p, cudaStream_t st) {
+  auto kern = k_lp_head<PAIR, KT, KEEP>;
+  const int smem = head_smem(p.nst, PAIR, KEEP);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+  if (e != cudaSuccess) return e;
+  if (!PAIR) {
+    kern<<<p.num_units < num_sms() ? p.num_units : num_sms(), kThreads, smem, st>>>(ma, mb, me, p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static int resident[64] = {0};  // clusters that run at once, by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int most = dev >= 0 && dev < 64 ? resident[dev] : 0;
+  if (most == 0) {
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most <= 0) most = 1;
+    if (dev >= 0 && dev < 64) resident[dev] = most;
+  }
+  cfg.gridDim = dim3(2 * (p.num_units < most ? p.num_units : most));
+  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, me, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool PAIR, bool KEEP>
+cudaError_t launch_k(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
+                     const HeadParams& p, cudaStream_t st) {
+  if (p.top == 0) return launch_v<PAIR, 0, KEEP>(ma, mb, me, p, st);
+  if (p.top <= 8) return launch_v<PAIR, 8, KEEP>(ma, mb, me, p, st);
+  return launch_v<PAIR, LP_MAX_TOP, KEEP>(ma, mb, me, p, st);
+}
+
+}  // namespace
+
+bool lp_head_supported(const LpHeadArgs& a) {
+  auto al = [](const void* q) { return ((uintptr_t)q & 15u) == 0; };
+  return a.m > 0 && a.n > 0 && a.k > 0 && al(a.x) && al(a.w) && a.ldx % 8 == 0 && a.ldw % 8 == 0 &&
+         (a.e == nullptr || (al(a.e) && a.lde % 8 == 0)) && a.m < (1ll << 31) - 512 &&
+         a.n < (1ll << 31) - 512 && a.k < (1ll << 31);
+}
+
+cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
+  if (!lp_head_supported(a)) return cudaErrorInvalidValue;
+  const int64_t mblocks = (a.m + BM - 1) / BM, nblocks = (a.n + BN - 1) / BN;
+  // the schedule rule of launch_gemm_tc (gemm_tc.cu)
+  const int64_t sms = num_sms(), clusters = sms >= 2 ? sms / 2 : 1;
+  const int64_t waves_one = (mblocks * nblocks + sms - 1) / sms;
+  const int64_t waves_pair = ((mblocks + 1) / 2 * nblocks + clusters - 1) / clusters;
+  const bool pair = mblocks >= 2 && (a.k + BK - 1) / BK >= 4 && waves_pair * 100 <= waves_one * 112;
+  const bool keep = a.e != nullptr;
+  CUtensorMap ma, mb, me;
+  if (!tc_make_map(&ma, a.x, a.k, a.m, a.ldx, BK, BM) ||
+      !tc_make_map(&mb, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
+    return cudaErrorInvalidValue;
+  me = ma;
+  if (keep && !tc_make_map(&me, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
+  HeadParams p{};
+  p.m = a.m; p.n = a.n;
+  p.num_n_blocks = (int)nblocks;
+  p.num_k_blocks = (int)((a.k + BK - 1) / BK);
+  p.m_units = (int)(pair ? (mblocks + 1) / 2 : mblocks);
+  if (p.m_units * nblocks > 0x7fffffff) return cudaErrorInvalidValue;
+  p.num_units = (int)(p.m_units * nblocks);
+  // bands of about 32 MB of X, as for the logits product
+  int64_t gm = (32ll << 20) / ((int64_t)BM * (pair ? 2 : 1) * a.k * 2);
+  p.group_m = (int)(gm < 1 ? 1 : gm > p.m_units ? p.m_units : gm);
+  p.nst = head_stages(pair, keep);
+  p.c = a.c; p.labels = a.labels; p.part = a.part; p.parts = a.parts; p.zy = a.zy;
+  p.top = a.top; p.gmax = a.gmax; p.count = a.count; p.cand = a.cand;
+  p.timeout_ns = kTimeoutNs;
+  p.status = a.status;
+  if (pair) return keep ? launch_k<true, true>(ma, mb, me, p, st) : launch_k<true, false>(ma, mb, me, p, st);
+  return keep ? launch_k<false, true>(ma, mb, me, p, st) : launch_k<false, false>(ma, mb, me, p, st);
+}
+
+}  // namespace fljsd

@@ -1,0 +1,234 @@
+"""Token log probabilities, entropies and most likely alternatives of an lm_head's
+rows (the C entry points fljsd_lp_* and fljsd_logits_lp*), with allocation and
+autograd. The formulas and the treatment of ignored, masked and empty rows are in
+include/fljsd.h."""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from .api import _DT, _check
+
+
+class Logprobs(NamedTuple):
+    """Per row: log probability of the label (None without labels), entropy, log of
+    the softmax denominator, the same in two parts for the backward pass (the largest
+    logit, and log2 of the sum relative to it), and the top_k alternatives (None with
+    top_k 0)."""
+
+    logp: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    norm: torch.Tensor
+    top_logp: Optional[torch.Tensor]
+    top_id: Optional[torch.Tensor]
+
+
+def _results(rows, top_k, with_logp, device) -> Logprobs:
+    f = torch.empty((5, rows), dtype=torch.float32, device=device)
+    return Logprobs(f[3] if with_logp else None, f[4], f[2], f[:2].view(rows, 2),
+                    torch.empty((rows, top_k), dtype=torch.float32, device=device) if top_k else None,
+                    torch.empty((rows, top_k), dtype=torch.int64, device=device) if top_k else None)
+
+
+def _check_grad(name, t, rows, device):
+    if t is not None:
+        _check(name, t, torch.float32, device, (rows,))
+
+
+class FusedLinearLogprobs:
+    """Plans one problem shape and keeps its workspace for repeated calls.
+
+    ``forward`` returns :class:`Logprobs`; with ``keep_for_backward`` the plan also
+    serves ``backward``, which takes the upstream gradients of logp and entropy.
+    A forward whose plan is one chunk leaves the probabilities (bt x v bf16) in the
+    workspace for the first backward of its result; any other backward computes
+    them again.
+    """
+
+    def __init__(self, bt, h, v, dtype=torch.bfloat16, *, top_k=0, temperature=1.0,
+                 ignore_index=-100, chunk_rows=0, keep_for_backward=False, accum_fp32=False,
+                 device="cuda", free_hbm_bytes=None):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        if dtype not in _DT:
+            raise ValueError(f"dtype {dtype} is not one of {list(_DT)}")
+        self.dtype = dtype
+        self.problem = _lib.make_lp_problem(bt, h, v, _DT[dtype], top_k, temperature, ignore_index,
+                                            chunk_rows, keep_for_backward, accum_fp32)
+        if free_hbm_bytes is None:
+            free_hbm_bytes = torch.cuda.mem_get_info(self.device)[0]
+        self.plan = _lib.fljsd_lp_plan(self.problem, int(free_hbm_bytes))
+        self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8,
+                                     device=self.device)
+        self._kept = None  # the result whose probabilities the workspace holds
+
+    def forward(self, x, w, labels=None, out=None, stream=None) -> Logprobs:
+        p = self.problem
+        _check("x", x, self.dtype, self.device, (p.bt, p.h))
+        _check("w", w, self.dtype, self.device, (p.v, p.h))
+        if labels is not None:
+            _check("labels", labels, torch.int64, self.device, (p.bt,))
+        r = _results(p.bt, p.top_k, labels is not None, self.device) if out is None else out
+        self._kept = None
+        _lib.fljsd_lp_forward(p, self.plan, x, w, labels, r.logp, r.entropy, r.lse, r.norm,
+                              r.top_logp, r.top_id, self.workspace, stream=stream)
+        if p.flags & _lib.FLJSD_LP_BACKWARD and self.plan.num_chunks == 1:
+            self._kept = r
+        return r
+
+    def backward(self, x, w, labels, result, grad_logp=None, grad_entropy=None, out=None,
+                 need=(True, True), stream=None):
+        """(grad_input, grad_weight) for the upstream gradients of ``result``'s logp
+        and entropy ([bt] fp32, None for zero); ``need`` skips one of them."""
+        p = self.problem
+        _check("x", x, self.dtype, self.device, (p.bt, p.h))
+        _check("w", w, self.dtype, self.device, (p.v, p.h))
+        if labels is not None:
+            _check("labels", labels, torch.int64, self.device, (p.bt,))
+        _check_grad("grad_logp", grad_logp, p.bt, self.device)
+        _check_grad("grad_entropy", grad_entropy, p.bt, self.device)
+        if out is None:
+            out = (torch.empty_like(x) if need[0] else None, torch.empty_like(w) if need[1] else None)
+        kept = self._kept is result
+        self._kept = None
+        _lib.fljsd_lp_backward(p, self.plan, x, w, labels, result.logp, result.entropy, result.norm,
+                               grad_logp, grad_entropy, int(kept), out[0], out[1], self.workspace,
+                               stream=stream)
+        return out
+
+
+def _outputs(ctx, r):
+    """Views of a result as a Function's outputs: what backward keeps of the result
+    must not refer to the graph. Only logp and entropy carry gradients."""
+    out = tuple(None if t is None else t.view_as(t) for t in r)
+    ctx.mark_non_differentiable(*(t for t in out[2:] if t is not None))
+    return out
+
+
+def _upstream(g):
+    return None if g is None else g.detach().to(torch.float32).contiguous()
+
+
+class _FusedLinearLogprobsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, labels, top_k, temperature, ignore_index, chunk_rows, need):
+        run = FusedLinearLogprobs(x.shape[0], x.shape[1], w.shape[0], x.dtype, top_k=top_k,
+                                  temperature=temperature, ignore_index=ignore_index,
+                                  chunk_rows=chunk_rows, keep_for_backward=need, device=x.device)
+        xc, wc = x.detach().contiguous(), w.detach().contiguous()
+        lab = None if labels is None else labels.contiguous()
+        r = run.forward(xc, wc, lab)
+        ctx.set_materialize_grads(False)
+        if need:
+            ctx.run, ctx.result = run, r
+            ctx.save_for_backward(xc, wc, lab)
+        return _outputs(ctx, r)
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy, *_):
+        if g_logp is None and g_entropy is None:
+            return (None,) * 8
+        x, w, labels = ctx.saved_tensors
+        need = ctx.needs_input_grad[:2]
+        gx, gw = ctx.run.backward(x, w, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
+                                  need=need)
+        return gx, gw, None, None, None, None, None, None
+
+
+def fused_linear_logprobs(x, w, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
+                          chunk_rows=0) -> Logprobs:
+    """:class:`Logprobs` of the logits x.w^T without forming them, differentiable in x
+    and w through logp and entropy. 2-D tensors on one CUDA device, fp32 or bf16."""
+    need = torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)
+    return Logprobs(*_FusedLinearLogprobsFunction.apply(x, w, labels, int(top_k), float(temperature),
+                                                        int(ignore_index), int(chunk_rows), need))
+
+
+def _logits_check(logits, labels):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("expected [rows x V] logits")
+    if logits.dtype not in _DT:
+        raise ValueError(f"logits have dtype {logits.dtype}, expected one of {list(_DT)}")
+    if logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("the rows of logits must be contiguous")
+    if labels is not None:
+        _check("labels", labels, torch.int64, logits.device, (logits.shape[0],))
+
+
+def _row_stride(t):
+    # a single row's stride may be anything, and an expanded tensor's rows are 0 apart
+    return max(t.stride(0), t.shape[1]) if t.shape[0] == 1 else t.stride(0)
+
+
+def logits_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
+                    stream=None) -> Logprobs:
+    """:class:`Logprobs` of given logits [rows x V], fp32 or bf16 (rows may be any
+    stride apart). For a differentiable form see :func:`token_logprobs`."""
+    _logits_check(logits, labels)
+    rows, v = logits.shape
+    r = _results(rows, top_k, labels is not None, logits.device)
+    ws = torch.empty(_lib.fljsd_logits_lp_workspace_bytes(rows, v, top_k), dtype=torch.uint8,
+                     device=logits.device)
+    _lib.fljsd_logits_lp(rows, v, _row_stride(logits), _DT[logits.dtype], top_k, temperature,
+                         ignore_index, logits, labels, r.logp, r.entropy, r.lse, r.norm,
+                         r.top_logp, r.top_id, ws, stream=stream)
+    if stream is not None and not isinstance(stream, int):
+        ws.record_stream(stream)
+    return r
+
+
+def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entropy=None, *,
+                             temperature=1.0, ignore_index=-100, out=None, stream=None):
+    """The gradient in the logits for upstream gradients of ``result``'s logp and
+    entropy ([rows] fp32, None for zero); ``out`` may be the logits themselves."""
+    _logits_check(logits, labels)
+    rows, v = logits.shape
+    _check_grad("grad_logp", grad_logp, rows, logits.device)
+    _check_grad("grad_entropy", grad_entropy, rows, logits.device)
+    if out is None:
+        out = torch.empty((rows, v), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device or (
+            out.stride(1) != 1 and v > 1):
+        raise ValueError("out must be like the logits, with contiguous rows")
+    _lib.fljsd_logits_lp_backward(rows, v, _row_stride(logits), _row_stride(out),
+                                  _DT[logits.dtype], temperature, ignore_index, logits, labels,
+                                  result.logp, result.entropy, result.norm, grad_logp, grad_entropy,
+                                  out, stream=stream)
+    return out
+
+
+class _TokenLogprobsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, labels, top_k, temperature, ignore_index):
+        z = logits.detach()
+        if z.dim() == 2 and z.stride(1) != 1:
+            z = z.contiguous()
+        lab = None if labels is None else labels.contiguous()
+        r = logits_logprobs(z, lab, top_k=top_k, temperature=temperature, ignore_index=ignore_index)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(z, lab)
+        ctx.result, ctx.opts = r, (temperature, ignore_index)
+        return _outputs(ctx, r)
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy, *_):
+        if g_logp is None and g_entropy is None:
+            return (None,) * 5
+        z, labels = ctx.saved_tensors
+        g = logits_logprobs_backward(z, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
+                                     temperature=ctx.opts[0], ignore_index=ctx.opts[1])
+        return g, None, None, None, None
+
+
+def token_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100) -> Logprobs:
+    """:func:`logits_logprobs`, differentiable in the logits through logp and entropy."""
+    return Logprobs(*_TokenLogprobsFunction.apply(logits, labels, int(top_k), float(temperature),
+                                                  int(ignore_index)))
+
+
+__all__ = ["FusedLinearLogprobs", "Logprobs", "fused_linear_logprobs", "logits_logprobs",
+           "logits_logprobs_backward", "token_logprobs"]

@@ -21,3 +21,4 @@ from .fljsd_oracle import (  # noqa: F401
     tvd_ref,
     zero_masks,
 )
+from .lp_oracle import lp_grad_ref, lp_rows_ref  # noqa: F401
