@@ -433,6 +433,57 @@ fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64
                                       const float* grad_logp, const float* grad_entropy,
                                       void* grad_logits, fljsd_stream_t stream);
 
+/*
+ * fljsd_adamw_step -- one AdamW step over `count` tensors, in place. Per element,
+ * in fp32, each operation rounded once, t = options->step (the number of this
+ * step, from 1):
+ *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,
+ *   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * param [n] in param_dtype, grad [n] in grad_dtype. With master = 1 (bf16 params)
+ * the fp32 `master` [n] is what is stepped, and param receives it rounded.
+ * state_bits 32: exp_avg and exp_avg_sq hold m and v, fp32 [n]. state_bits 8:
+ * exp_avg and exp_avg_sq are e4m3 codes [n] of m and of sqrt(v), with one fp32
+ * scale for every 128 consecutive elements ([ceil(n / 128)] each): value = code
+ * * scale, scale = amax * (1 / 448) (amax of the block, not below 2^-100), code =
+ * the nearest to value * (448 * (1 / amax)). States may start as zeros.
+ * grad_scale: device fp32 scalar or NULL (1), e.g. 1 / loss scale, or the factor
+ * of a clipped gradient norm.
+ * `tensors` is host memory, read before the call returns; the tensors' memory is
+ * device memory, element-aligned (16 bytes, 8 for 8-bit states, is fastest), and
+ * must not overlap. Tensors with n == 0 are left out (their pointers may be NULL).
+ * Hyperparameters are taken at the call: a captured call repeats its step number.
+ * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for an unknown
+ * dtype, state_bits other than 8 and 32, beta outside [0, 1), a negative or
+ * non-finite eps, a non-finite lr or weight_decay, step < 1, n < 0, a null or
+ * misaligned pointer, master with fp32 params, a master pointer without master;
+ * FLJSD_ERR_UNSUPPORTED for n above 2^40; FLJSD_ERR_CUDA when a launch fails.
+ */
+typedef struct {
+  const void* grad;
+  void* param;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+} fljsd_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;        /* 1 for the first */
+  int32_t param_dtype; /* fljsd_dtype */
+  int32_t grad_dtype;
+  int32_t state_bits;  /* 32 or 8 */
+  int32_t master;      /* 0 or 1 */
+} fljsd_adamw_options;
+
+fljsd_status fljsd_adamw_step(const fljsd_adamw_options* options,
+                              const fljsd_adamw_tensor* tensors, int32_t count,
+                              const float* grad_scale, fljsd_stream_t stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fljsd_status_string(fljsd_status status);
 

@@ -17,6 +17,7 @@ from ._lib import (  # noqa: F401
     fljsd_rows_workspace_bytes,
     fljsd_scale,
     fljsd_tvd,
+    fljsd_adamw_step,
     fljsd_launch_count,
     fljsd_logits_lp,
     fljsd_logits_lp_backward,
@@ -24,6 +25,7 @@ from ._lib import (  # noqa: F401
     fljsd_lp_backward,
     fljsd_lp_forward,
     fljsd_lp_plan,
+    make_adamw_options,
     make_lp_problem,
     fljsd_launch_count_reset,
     fljsd_plan,
@@ -50,5 +52,6 @@ from .logprobs import (  # noqa: F401
     logits_logprobs_backward,
     token_logprobs,
 )
+from .optim import AdamW  # noqa: F401
 
 LIB_PATH = _lib.LIB_PATH

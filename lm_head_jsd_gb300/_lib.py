@@ -52,6 +52,18 @@ class fljsd_lp_problem(ctypes.Structure):
                 ("temperature", ctypes.c_float), ("flags", ctypes.c_int32)]
 
 
+class fljsd_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("grad", "param", "master", "exp_avg", "exp_avg_sq",
+                                               "exp_avg_scale", "exp_avg_sq_scale")] + [
+        ("n", ctypes.c_int64)]
+
+
+class fljsd_adamw_options(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("master", ctypes.c_int32)]
+
+
 FLJSD_FLAG_T2 = 1
 FLJSD_FLAG_ACCUM_FP32 = 2
 FLJSD_LP_BACKWARD = 4
@@ -123,6 +135,8 @@ def _load():
     lib.fljsd_logits_lp.restype = ctypes.c_int
     lib.fljsd_logits_lp_backward.argtypes = [i64, i64, i64, i64, i32, f32, i64, *[P] * 9]
     lib.fljsd_logits_lp_backward.restype = ctypes.c_int
+    lib.fljsd_adamw_step.argtypes = [ctypes.POINTER(fljsd_adamw_options), P, i32, P, P]
+    lib.fljsd_adamw_step.restype = ctypes.c_int
     lib.fljsd_status_string.argtypes = [ctypes.c_int]
     lib.fljsd_status_string.restype = ctypes.c_char_p
     lib.fljsd_launch_count.argtypes = []
@@ -380,6 +394,21 @@ def fljsd_logits_lp_backward(rows, v, ld, ld_grad, dtype, temperature, ignore_in
                                       _ptr(grad_logits), _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_logits_lp_backward")
+    return st
+
+
+def make_adamw_options(lr, beta1, beta2, eps, weight_decay, step, param_dtype="bf16",
+                       grad_dtype="bf16", state_bits=32, master=0) -> fljsd_adamw_options:
+    return fljsd_adamw_options(lr, beta1, beta2, eps, weight_decay, step, _dt(param_dtype),
+                               _dt(grad_dtype), state_bits, master)
+
+
+def fljsd_adamw_step(options, tensors, count, grad_scale=None, stream=None, check=True) -> int:
+    """``tensors``: address of ``count`` fljsd_adamw_tensor in host memory."""
+    st = lib.fljsd_adamw_step(ctypes.byref(options), tensors, count, _ptr(grad_scale),
+                              _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_adamw_step")
     return st
 
 

@@ -22,3 +22,4 @@ from .fljsd_oracle import (  # noqa: F401
     zero_masks,
 )
 from .lp_oracle import lp_grad_ref, lp_rows_ref  # noqa: F401
+from .adamw_oracle import adamw_ref, e4m3_values, quantise_ref  # noqa: F401
