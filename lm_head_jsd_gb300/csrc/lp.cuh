@@ -60,7 +60,7 @@ struct LpRowsArgs {
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st);
 
 // dz = (a (1[j = y] - p_j) - b p_j (log p_j + entropy)) / T from logits
-// (z_dtype) into out (out_dtype); from_e: z holds 2^t_j in bf16, relative to
+// (z_dtype) into out (out_dtype); from_e: z holds 2^t_j in fp16, relative to
 // the maximum of each part, and out may be the same memory.
 struct LpGradArgs {
   const void* z;
@@ -92,7 +92,7 @@ struct LpHeadArgs {
   unsigned* gmax;      // [m x top], zeroed
   int* count;          // [m], zeroed
   int2* cand;          // [m x parts * top]
-  void* e;             // [m x lde] bf16: 2^t_j relative to each part's maximum, or null
+  void* e;             // [m x lde] fp16: 2^t_j relative to each part's maximum, or null
   int64_t lde;
   int* status;
 };

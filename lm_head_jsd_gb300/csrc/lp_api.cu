@@ -49,7 +49,7 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.zy = take(rows * sizeof(float));
   L.cand = take(rows * L.cap * sizeof(int2));
   L.stats_bytes = at;
-  // 2^t in bf16 that the backward pass turns into dz, or fp32 logits (and their
+  // 2^t in fp16 that the backward pass turns into dz in place, or fp32 logits (and their
   // bf16 gradient beside them)
   const size_t zb = L.tc ? (bwd ? rows * L.ld * 2 : 0) : rows * L.ld * 4;
   L.z = take(zb);

@@ -9,6 +9,8 @@
 #include "lp.cuh"
 #include "jsd_math.cuh"
 
+#include <cuda_fp16.h>
+
 namespace fljsd {
 namespace {
 
@@ -23,6 +25,34 @@ constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
 __device__ __forceinline__ float val(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float val(const __half* p) { return __half2float(*p); }
+
+// Eight values, 16-byte aligned.
+__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+  o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&o)[8]) {
+  Vec<__nv_bfloat16>::load(p, o);
+}
+__device__ __forceinline__ void load8(const __half* p, float (&o)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    o[2 * i] = f.x;
+    o[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&o)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&o)[8]) {
+  Vec<__nv_bfloat16>::store(p, o);
+}
 
 // Value first, then the lower column: one key for each candidate.
 __device__ __forceinline__ unsigned long long cand_key(int2 c) {
@@ -358,23 +388,10 @@ __global__ void __launch_bounds__(kThreads) k_lp_grad(LpGradArgs a, int64_t segs
         const float ref = FROM_E ? __fmul_rn(a.part[r * a.parts + j / LP_PART_COLS].x - g.m, a.c) - g.l2 : 0.f;
         float z[N];
         if (j + N <= a.v) {
-          constexpr int NI = Vec<TI>::N, NO = Vec<TO>::N;
-#pragma unroll
-          for (int q = 0; q < N; q += NI) {
-            float t[NI];
-            Vec<TI>::load(zr + j + q, t);
-#pragma unroll
-            for (int e = 0; e < NI; ++e) z[q + e] = t[e];
-          }
+          load8(zr + j, z);
 #pragma unroll
           for (int e = 0; e < N; ++e) z[e] = one(z[e], j + e, ref);
-#pragma unroll
-          for (int q = 0; q < N; q += NO) {
-            float t[NO];
-#pragma unroll
-            for (int e = 0; e < NO; ++e) t[e] = z[q + e];
-            Vec<TO>::store(orow + j + q, t);
-          }
+          store8(orow + j, z);
         } else {
           for (int e = 0; j + e < a.v; ++e) Vec<TO>::put(orow + j + e, one(val(zr + j + e), j + e, ref));
         }
@@ -424,7 +441,7 @@ cudaError_t launch_lp_grad(int z_dtype, int out_dtype, bool from_e, const LpGrad
   using bf = __nv_bfloat16;
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
   if (from_e)
-    k_lp_grad<bf, bf, true><<<grid, kThreads, 0, st>>>(a, segs);
+    k_lp_grad<__half, bf, true><<<grid, kThreads, 0, st>>>(a, segs);
   else if (z_dtype == FLJSD_F32 && out_dtype == FLJSD_F32)
     k_lp_grad<float, float, false><<<grid, kThreads, 0, st>>>(a, segs);
   else if (z_dtype == FLJSD_F32)
