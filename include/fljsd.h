@@ -484,6 +484,43 @@ fljsd_status fljsd_adamw_step(const fljsd_adamw_options* options,
                               const fljsd_adamw_tensor* tensors, int32_t count,
                               const float* grad_scale, fljsd_stream_t stream);
 
+/*
+ * Product in 8-bit floating point with a scale for each block of 128, for a frozen
+ * lm_head (a teacher's, or one that only scores): out = x . w^T with w [n x k]
+ * held as e4m3 codes and one fp32 scale for each 128 x 128 block, and x [m x k]
+ * quantised on the way with one scale for each 1 x 128. Sums inside a block are
+ * exact products added in fp32, blocks are scaled and added in fp32, and the
+ * result is rounded once to out_dtype.
+ *
+ * fljsd_fp8_quantize -- codes and scales of x [rows x cols] (dtype, row stride
+ * ldx): per block of block_rows (1 or 128) x 128, amax = max |x|, not below
+ * 2^-100; scale = amax * (1 / 448), code = the e4m3 nearest to x * (448 * (1 /
+ * amax)). codes [rows x ldq], ldq a multiple of 16, 16-byte aligned (columns past
+ * cols are written as zeros). scales: for 128 rows [ceil(rows / 128) x
+ * ceil(cols / 128)], for one row [ceil(cols / 128) x rows]. A NaN keeps its place
+ * (code NaN); an infinite amax makes its block NaN.
+ *
+ * fljsd_fp8_linear -- the product. x in x_dtype with row stride ldx; w_codes with
+ * row stride ldw (a multiple of 16; 16-byte aligned), w_scales [ceil(n / 128) x
+ * ceil(k / 128)]; out [m x n] in out_dtype with row stride ldo. workspace:
+ * fljsd_fp8_linear_workspace_bytes(m, k) bytes, 16-byte aligned; its first int32
+ * is a status word (FLJSD_ERR_TIMEOUT if a bounded device wait expired).
+ *
+ * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for a dimension
+ * <= 0, a stride below its row or not a multiple of 16 where one is asked for, an
+ * unknown dtype, block_rows other than 1 and 128, a null or misaligned pointer;
+ * FLJSD_ERR_UNSUPPORTED for m, n or rows above 2^30 or k or cols above 2^20;
+ * FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
+ */
+fljsd_status fljsd_fp8_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows,
+                                const void* x, int64_t ldx, void* codes, int64_t ldq, float* scales,
+                                fljsd_stream_t stream);
+size_t fljsd_fp8_linear_workspace_bytes(int64_t m, int64_t k);
+fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, const void* x,
+                              int64_t ldx, const void* w_codes, int64_t ldw, const float* w_scales,
+                              int32_t out_dtype, void* out, int64_t ldo, void* workspace,
+                              size_t workspace_bytes, fljsd_stream_t stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fljsd_status_string(fljsd_status status);
 

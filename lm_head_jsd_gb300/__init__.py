@@ -18,6 +18,9 @@ from ._lib import (  # noqa: F401
     fljsd_scale,
     fljsd_tvd,
     fljsd_adamw_step,
+    fljsd_fp8_linear,
+    fljsd_fp8_linear_workspace_bytes,
+    fljsd_fp8_quantize,
     fljsd_launch_count,
     fljsd_logits_lp,
     fljsd_logits_lp_backward,
@@ -44,6 +47,7 @@ from .api import (  # noqa: F401
     jsd_logspace,
     tvd,
 )
+from .fp8 import fp8_linear, fp8_quantize  # noqa: F401
 from .logprobs import (  # noqa: F401
     FusedLinearLogprobs,
     Logprobs,

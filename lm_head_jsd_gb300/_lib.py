@@ -137,6 +137,12 @@ def _load():
     lib.fljsd_logits_lp_backward.restype = ctypes.c_int
     lib.fljsd_adamw_step.argtypes = [ctypes.POINTER(fljsd_adamw_options), P, i32, P, P]
     lib.fljsd_adamw_step.restype = ctypes.c_int
+    lib.fljsd_fp8_quantize.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P]
+    lib.fljsd_fp8_quantize.restype = ctypes.c_int
+    lib.fljsd_fp8_linear_workspace_bytes.argtypes = [i64, i64]
+    lib.fljsd_fp8_linear_workspace_bytes.restype = size
+    lib.fljsd_fp8_linear.argtypes = [i64, i64, i64, i32, P, i64, P, i64, P, i32, P, i64, P, size, P]
+    lib.fljsd_fp8_linear.restype = ctypes.c_int
     lib.fljsd_status_string.argtypes = [ctypes.c_int]
     lib.fljsd_status_string.restype = ctypes.c_char_p
     lib.fljsd_launch_count.argtypes = []
@@ -409,6 +415,31 @@ def fljsd_adamw_step(options, tensors, count, grad_scale=None, stream=None, chec
                               _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_adamw_step")
+    return st
+
+
+def fljsd_fp8_quantize(rows, cols, dtype, block_rows, x, ldx, codes, ldq, scales, stream=None,
+                       check=True) -> int:
+    st = lib.fljsd_fp8_quantize(rows, cols, _dt(dtype), block_rows, _ptr(x), ldx, _ptr(codes), ldq,
+                                _ptr(scales), _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_fp8_quantize")
+    return st
+
+
+def fljsd_fp8_linear_workspace_bytes(m: int, k: int) -> int:
+    return lib.fljsd_fp8_linear_workspace_bytes(m, k)
+
+
+def fljsd_fp8_linear(m, n, k, x_dtype, x, ldx, w_codes, ldw, w_scales, out_dtype, out, ldo,
+                     workspace, workspace_bytes=None, stream=None, check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_fp8_linear(m, n, k, _dt(x_dtype), _ptr(x), ldx, _ptr(w_codes), ldw,
+                              _ptr(w_scales), _dt(out_dtype), _ptr(out), ldo, _ptr(workspace),
+                              workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_fp8_linear")
     return st
 
 

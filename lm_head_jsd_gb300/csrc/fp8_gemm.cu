@@ -1,0 +1,488 @@
+// Product in 8-bit floating point with a scale for each block of 128 (sm_103a):
+//   out[i, j] = sum_b sx[b, i] sw[j / 128, b] sum_{k in block b} qx[i, k] qw[j, k]
+// with e4m3 codes qx [m x k], qw [n x k]; the inner sums on the tensor cores
+// (tcgen05.mma kind::f8f6f4, products exact, fp32 sums), the outer sum in fp32
+// registers.
+//
+// One CTA computes a 128 x 256 tile. Each 128-deep block of the contraction is one
+// stage of the TMA ring (128-byte rows, 128B swizzle) and starts a new accumulator
+// in tensor memory; the two accumulators alternate, so that while the tensor cores
+// form one block's sums, eight warps add the other's, scaled, to 128 fp32 registers
+// a thread (one row, half of the columns: one sw for each thread and block). A scale
+// that is no power of two cannot be applied by the tensor cores, and folding it into
+// the codes would round them again; reading the accumulator back once per block
+// costs 256 of the 512 cycles that its products take.
+//
+// Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
+// codes are the nearest to x (448 (1 / amax)).
+#include "gemm_tc_kernel.cuh"
+
+#include <cuda_fp8.h>
+
+namespace fljsd {
+namespace {
+
+using namespace tcgemm;
+
+constexpr int FB = 128;         // elements of a scale's block, and of a stage's rows
+constexpr int F_UMMA_K = 32;
+constexpr int F_STAGES = 4;
+constexpr int F_STAGE_BYTES = (BM + BN) * FB;
+constexpr int F_EPI = 8;        // epilogue warps
+constexpr int F_THREADS = 64 + 32 * F_EPI;
+constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * OUT_BUF_BYTES + 1024 + CTRL_BYTES;
+static_assert(F_SMEM <= SMEM_MAX, "shared memory");
+
+// fp32 accumulator, e4m3 operands (format 0), both K-major
+constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+
+__device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate));
+}
+
+struct F8Params {
+  int64_t m, n;
+  int num_n_blocks, num_k_blocks, m_units, num_units, group_m;
+  const float* sx;  // [num_k_blocks x m]
+  const float* sw;  // [ceil(n / 128) x num_k_blocks]
+  void* out;
+  int64_t ldo;
+  int use_tma;      // rows of out are whole 16-byte units
+  unsigned long long timeout_ns;
+  int* status;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(F_THREADS, 1)
+    k_fp8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmO, const F8Params p) {
+  constexpr int COLS = 128 / sizeof(T);  // columns of a staged row
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* stg = smem_raw + (base - raw) + F_STAGES * F_STAGE_BYTES;
+  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + F_EPI * OUT_BUF_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F_STAGES; ++s) {
+      mbar_init(smem_u32(&cb->full[s]), 1);
+      mbar_init(smem_u32(&cb->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&cb->tmem_full[a]), 1);
+      mbar_init(smem_u32(&cb->tmem_empty[a]), F_EPI);
+    }
+    mbar_init(smem_u32(&cb->drain), 1);
+    cb->abort = 0;
+    cb->timeout_ns = p.timeout_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    if (p.use_tma) prefetch_tensormap(&tmO);
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(&cb->tmem_base), TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = cb->tmem_base;
+
+  auto tile_coords = [&](int t, int& mb, int& nb) {
+    const int band = t / (p.group_m * p.num_n_blocks);
+    const int m0 = band * p.group_m;
+    const int gm = min(p.group_m, p.m_units - m0);
+    const int r = t - band * p.group_m * p.num_n_blocks;
+    mb = m0 + r % gm;
+    nb = r / gm;
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued_parity[F_STAGES];
+      bool issued[F_STAGES];
+      for (int s = 0; s < F_STAGES; ++s) issued[s] = false;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
+        int mb, nb;
+        tile_coords(t, mb, nb);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+          if (!wait_bar(cb, smem_u32(&cb->empty[stage]), phase ^ 1u, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + stage * F_STAGE_BYTES;
+          const uint32_t fb = smem_u32(&cb->full[stage]);
+          mbar_arrive_expect_tx(fb, F_STAGE_BYTES);
+          tma_load_2d(sa, &tmA, fb, kb * FB, mb * BM);
+          tma_load_2d(sa + BM * FB, &tmB, fb, kb * FB, nb * BN);
+          issued[stage] = true;
+          issued_parity[stage] = phase;
+          if (++stage == F_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      for (int s = 0; s < F_STAGES; ++s)
+        if (issued[s]) wait_bar(cb, smem_u32(&cb->full[s]), issued_parity[s], p.status);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: one accumulator for each 128-deep block ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t use = 0;  // accumulators handed out
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
+        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
+          const int acc = use & 1;
+          if (!wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use >> 1) & 1) ^ 1u, p.status) ||
+              !wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + stage * F_STAGE_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < FB / F_UMMA_K; ++kk)
+            mma_e4m3(tmem_base + acc * ACC_COLS, smem_desc(sa + kk * F_UMMA_K, 16, 1024),
+                     smem_desc(sa + BM * FB + kk * F_UMMA_K, 16, 1024), kk > 0 ? 1u : 0u);
+          mma_commit<false>(smem_u32(&cb->empty[stage]));
+          mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
+          if (++stage == F_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (use > 0) {
+        mma_commit<false>(smem_u32(&cb->drain));
+        wait_bar(cb, smem_u32(&cb->drain), 0, p.status);
+      }
+    }
+  } else {
+    // ---------------- epilogue: one row of 128 columns to a thread ----------------
+    const int sub = warp & 3, ew = warp - 2;
+    const int grp = (warp - 2) >> 2;
+    uint32_t use = 0;
+    bool ok = true;
+    uint8_t* srow0 = stg + ew * OUT_BUF_BYTES;
+    for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
+      int mb, nb;
+      tile_coords(t, mb, nb);
+      const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
+      const int64_t col0 = (int64_t)nb * BN + grp * 128;
+      const bool live = row0 < p.m && col0 < p.n;  // of this warp
+      float2 sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+      const float* sx = p.sx + (row < p.m ? row : 0);
+      const float* sw = p.sw + (live ? col0 / FB : 0) * p.num_k_blocks;
+      float s_next = live ? __ldg(sx) * __ldg(sw) : 0.f;
+      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
+        const int acc = use & 1;
+        const float s = s_next;
+        if (live && kb + 1 < p.num_k_blocks)
+          s_next = __ldg(sx + (int64_t)(kb + 1) * p.m) * __ldg(sw + kb + 1);
+        ok = wait_bar(cb, smem_u32(&cb->tmem_full[acc]), (use >> 1) & 1, p.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (live) {
+          const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS + grp * 128;
+          const float2 s2 = make_float2(s, s);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(ta + c * 32, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              sum[c * 16 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, sum[c * 16 + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+      }
+      if (!ok || !live) continue;
+      // ---- out: 128 bytes of a row at a time through shared memory (swizzled:
+      // 16-byte unit u of row r sits at u ^ (r & 7)) ----
+#pragma unroll
+      for (int c = 0; c < 128 / COLS; ++c) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        uint8_t* srow = srow0 + lane * 128;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint4 w;
+          if (sizeof(T) == 2) {
+            const float2* q = sum + c * 32 + u * 4;
+            w = make_uint4(pack_bf16(q[0].x, q[0].y), pack_bf16(q[1].x, q[1].y),
+                           pack_bf16(q[2].x, q[2].y), pack_bf16(q[3].x, q[3].y));
+          } else {
+            const float2* q = sum + c * 16 + u * 2;
+            w = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y),
+                           __float_as_uint(q[1].x), __float_as_uint(q[1].y));
+          }
+          *reinterpret_cast<uint4*>(srow + ((u ^ (lane & 7)) << 4)) = w;
+        }
+        const int64_t cc = col0 + c * COLS;
+        if (p.use_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (cc < p.n) tma_store_2d(&tmO, smem_u32(srow0), (int32_t)cc, (int32_t)row0);
+            bulk_commit();
+          }
+        } else {
+          // rows of any alignment: one element a lane, whole rows in turn
+          __syncwarp();
+          const int rows = (int)min((int64_t)32, p.m - row0);
+          for (int r = 0; r < rows; ++r) {
+            T* o = reinterpret_cast<T*>(p.out) + (row0 + r) * p.ldo + cc;
+#pragma unroll
+            for (int e = lane; e < COLS; e += 32) {
+              const int b = e * (int)sizeof(T);
+              const T x = *reinterpret_cast<const T*>(srow0 + r * 128 +
+                                                      ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
+              if (cc + e < p.n) o[e] = x;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<false>(tmem_base, TMEM_COLS);
+  }
+}
+
+__device__ __forceinline__ float val(const float* p) { return *p; }
+__device__ __forceinline__ float val(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+constexpr float kAmaxFloor = 0x1p-100f;
+
+__device__ __forceinline__ uint32_t code4(const float (&x)[4], float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv)),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[2], inv), __fmul_rn(x[3], inv)),
+                                               __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// One warp to a 1 x 128 block, four consecutive elements a lane. `scales` is
+// [blocks x rows], so that the product's threads (one row each) read it whole.
+template <typename T>
+__global__ void __launch_bounds__(256) k_quantise_rows(const T* x, int64_t ldx, int64_t rows,
+                                                       int64_t cols, int64_t blocks, uint8_t* q,
+                                                       int64_t ldq, float* scales, int* status) {
+  const int lane = threadIdx.x & 31;
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+  const int64_t units = rows * blocks;
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * 8) {
+    const int64_t r = u / blocks, b = u - r * blocks;
+    const int64_t j = b * FB + lane * 4;
+    const T* px = x + r * ldx + j;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = j + e < cols ? val(px + e) : 0.f;
+    float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    a = fmaxf(a, kAmaxFloor);
+    const uint32_t c = code4(v, __fmul_rn(__frcp_rn(a), 448.f));
+    if (j < ldq) *reinterpret_cast<uint32_t*>(q + r * ldq + j) = c;  // (ldq: whole 16-byte units)
+    if (lane == 0) scales[b * rows + r] = __fmul_rn(a, 1.f / 448.f);
+  }
+}
+
+// One CTA to a 128 x 128 block, 64 elements a thread. scales: [row blocks x blocks].
+template <typename T>
+__global__ void __launch_bounds__(256) k_quantise_blocks(const T* x, int64_t ldx, int64_t rows,
+                                                         int64_t cols, int64_t blocks, uint8_t* q,
+                                                         int64_t ldq, float* scales) {
+  __shared__ float sh[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rb = blockIdx.x / blocks, b = blockIdx.x - rb * blocks;
+  const int64_t j = b * FB + lane * 4;
+  float v[16][4];
+  float a = kAmaxFloor;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t r = rb * FB + i * 8 + warp;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[i][e] = r < rows && j + e < cols ? val(x + r * ldx + j + e) : 0.f;
+      a = fmaxf(a, fabsf(v[i][e]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if (lane == 0) sh[warp] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) a = fmaxf(a, sh[w]);
+  const float inv = __fmul_rn(__frcp_rn(a), 448.f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t r = rb * FB + i * 8 + warp;
+    if (r < rows && j < ldq) *reinterpret_cast<uint32_t*>(q + r * ldq + j) = code4(v[i], inv);
+  }
+  if (threadIdx.x == 0) scales[blockIdx.x] = __fmul_rn(a, 1.f / 448.f);
+}
+
+inline bool aligned(const void* q, uintptr_t a) { return ((uintptr_t)q & (a - 1)) == 0; }
+inline size_t dsize(int dt) { return dt == FLJSD_BF16 ? 2 : 4; }
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+inline int64_t up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
+
+bool known(int dt) { return dt == FLJSD_F32 || dt == FLJSD_BF16; }
+
+cudaError_t quantise(int64_t rows, int64_t cols, int dtype, int block_rows, const void* x,
+                     int64_t ldx, void* codes, int64_t ldq, float* scales, int* status,
+                     cudaStream_t st) {
+  const int64_t blocks = (cols + FB - 1) / FB;
+  auto* q = static_cast<uint8_t*>(codes);
+  trace_begin(FLJSD_KERNEL_SMALL, st);
+  if (block_rows == 1) {
+    const int64_t need = (rows * blocks + 7) / 8, most = (int64_t)num_sms() * 32;
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (dtype == FLJSD_BF16)
+      k_quantise_rows<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, cols,
+                                            blocks, q, ldq, scales, status);
+    else
+      k_quantise_rows<<<grid, 256, 0, st>>>(static_cast<const float*>(x), ldx, rows, cols, blocks,
+                                            q, ldq, scales, status);
+  } else {
+    const unsigned grid = (unsigned)((rows + FB - 1) / FB * blocks);
+    if (dtype == FLJSD_BF16)
+      k_quantise_blocks<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows,
+                                              cols, blocks, q, ldq, scales);
+    else
+      k_quantise_blocks<<<grid, 256, 0, st>>>(static_cast<const float*>(x), ldx, rows, cols,
+                                              blocks, q, ldq, scales);
+  }
+  trace_end(FLJSD_KERNEL_SMALL, st);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
+                           const F8Params& p, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       F_SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = p.num_units < num_sms() ? p.num_units : num_sms();
+  k_fp8_gemm<T><<<grid, F_THREADS, F_SMEM, st>>>(ma, mb, mo, p);
+  return cudaGetLastError();
+}
+
+struct F8Layout {
+  int64_t ldq, blocks;
+  size_t codes, scales, total;  // the status word comes first
+};
+F8Layout f8_layout(int64_t m, int64_t k) {
+  F8Layout L;
+  L.ldq = up(k, 16);
+  L.blocks = (k + FB - 1) / FB;
+  L.codes = 256;
+  L.scales = L.codes + align_up((size_t)m * L.ldq);
+  L.total = L.scales + align_up((size_t)m * L.blocks * sizeof(float));
+  return L;
+}
+
+}  // namespace
+}  // namespace fljsd
+
+using namespace fljsd;
+
+extern "C" {
+
+fljsd_status fljsd_fp8_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows,
+                                const void* x, int64_t ldx, void* codes, int64_t ldq, float* scales,
+                                fljsd_stream_t stream) {
+  if (rows <= 0 || cols <= 0 || ldx < cols || ldq < cols || ldq % 16 != 0 || !known(dtype) ||
+      (block_rows != 1 && block_rows != FB))
+    return FLJSD_ERR_INVALID_ARG;
+  if (!x || !codes || !scales || !aligned(x, dsize(dtype)) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return FLJSD_ERR_INVALID_ARG;
+  if (rows > (int64_t)1 << 30 || cols > (int64_t)1 << 20) return FLJSD_ERR_UNSUPPORTED;
+  if (block_rows == FB && (rows + FB - 1) / FB * ((cols + FB - 1) / FB) > 0x7fffffff)
+    return FLJSD_ERR_UNSUPPORTED;
+  return quantise(rows, cols, dtype, block_rows, x, ldx, codes, ldq, scales, nullptr,
+                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FLJSD_OK
+             : FLJSD_ERR_CUDA;
+}
+
+size_t fljsd_fp8_linear_workspace_bytes(int64_t m, int64_t k) {
+  return m <= 0 || k <= 0 ? 0 : f8_layout(m, k).total;
+}
+
+fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, const void* x,
+                              int64_t ldx, const void* w_codes, int64_t ldw, const float* w_scales,
+                              int32_t out_dtype, void* out, int64_t ldo, void* workspace,
+                              size_t workspace_bytes, fljsd_stream_t stream) {
+  if (m <= 0 || n <= 0 || k <= 0 || ldx < k || ldw < k || ldw % 16 != 0 || ldo < n ||
+      !known(x_dtype) || !known(out_dtype))
+    return FLJSD_ERR_INVALID_ARG;
+  if (!x || !w_codes || !w_scales || !out || !workspace || !aligned(x, dsize(x_dtype)) ||
+      !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(out, dsize(out_dtype)) ||
+      !aligned(workspace, 16))
+    return FLJSD_ERR_INVALID_ARG;
+  if (m > (int64_t)1 << 30 || n > (int64_t)1 << 30 || k > (int64_t)1 << 20)
+    return FLJSD_ERR_UNSUPPORTED;
+  const F8Layout L = f8_layout(m, k);
+  if (workspace_bytes < L.total) return FLJSD_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  int* status = reinterpret_cast<int*>(ws);
+  float* sx = reinterpret_cast<float*>(ws + L.scales);
+  F8Params p{};
+  const int64_t mblocks = (m + BM - 1) / BM, nblocks = (n + BN - 1) / BN;
+  if (mblocks * nblocks > 0x7fffffff) return FLJSD_ERR_UNSUPPORTED;
+  p.m = m; p.n = n;
+  p.num_n_blocks = (int)nblocks;
+  p.num_k_blocks = (int)L.blocks;
+  p.m_units = (int)mblocks;
+  p.num_units = (int)(mblocks * nblocks);
+  int64_t gm = (32ll << 20) / ((int64_t)BM * k);  // bands of about 32 MB of x, as for bf16
+  p.group_m = (int)(gm < 1 ? 1 : gm > mblocks ? mblocks : gm);
+  p.sx = sx; p.sw = w_scales; p.out = out; p.ldo = ldo;
+  p.use_tma = aligned(out, 16) && (ldo * dsize(out_dtype)) % 16 == 0 && (n * dsize(out_dtype)) % 16 == 0;
+  p.timeout_ns = kTimeoutNs;
+  p.status = status;
+  CUtensorMap ma, mb, mo;
+  if (!tc_make_map_u8(&ma, ws + L.codes, k, m, L.ldq, FB, BM) ||
+      !tc_make_map_u8(&mb, w_codes, k, n, ldw, FB, BN))
+    return FLJSD_ERR_CUDA;
+  mo = ma;
+  if (p.use_tma && !tc_make_map(&mo, out, n, m, ldo, out_dtype == FLJSD_BF16 ? 64 : 32, 32,
+                                out_dtype == FLJSD_F32))
+    return FLJSD_ERR_CUDA;
+  if (quantise(m, k, x_dtype, 1, x, ldx, ws + L.codes, L.ldq, sx, status, st) != cudaSuccess)
+    return FLJSD_ERR_CUDA;
+  trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
+  const cudaError_t e = out_dtype == FLJSD_BF16 ? launch_product<__nv_bfloat16>(ma, mb, mo, p, st)
+                                                : launch_product<float>(ma, mb, mo, p, st);
+  trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
+  return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
+}
+
+}  // extern "C"
