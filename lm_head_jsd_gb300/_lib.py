@@ -175,7 +175,8 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        # (is_available() would ask the driver at every call)
+        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_initialized() else None
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -16,6 +16,7 @@
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).
 #include "gemm_tc_kernel.cuh"
+#include "skinny_tc.cuh"
 
 #include <cuda_fp8.h>
 
@@ -28,9 +29,11 @@ constexpr int FB = 128;         // elements of a scale's block, and of a stage's
 constexpr int F_UMMA_K = 32;
 constexpr int F_STAGES = 4;
 constexpr int F_STAGE_BYTES = (BM + BN) * FB;
-constexpr int F_EPI = 8;        // epilogue warps
+constexpr int F_EPI = 16;       // epilogue warps
+constexpr int F_COLS = BN / (F_EPI / 4);  // columns of an epilogue thread
+constexpr int F_OUT_BYTES = 32 * 64;      // an epilogue warp's staging: 32 rows of 64 bytes
 constexpr int F_THREADS = 64 + 32 * F_EPI;
-constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * OUT_BUF_BYTES + 1024 + CTRL_BYTES;
+constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * F_OUT_BYTES + 1024 + CTRL_BYTES;
 static_assert(F_SMEM <= SMEM_MAX, "shared memory");
 
 // fp32 accumulator, e4m3 operands (format 0), both K-major
@@ -61,12 +64,12 @@ template <typename T>
 __global__ void __launch_bounds__(F_THREADS, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmO, const F8Params p) {
-  constexpr int COLS = 128 / sizeof(T);  // columns of a staged row
+  constexpr int COLS = 64 / sizeof(T);  // columns of a staged row
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* stg = smem_raw + (base - raw) + F_STAGES * F_STAGE_BYTES;
-  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + F_EPI * OUT_BUF_BYTES);
+  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + F_EPI * F_OUT_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < F_STAGES; ++s) {
@@ -168,21 +171,21 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       }
     }
   } else {
-    // ---------------- epilogue: one row of 128 columns to a thread ----------------
+    // ---------------- epilogue: one row of F_COLS columns to a thread ----------------
     const int sub = warp & 3, ew = warp - 2;
-    const int grp = (warp - 2) >> 2;
+    const int grp = ew >> 2;
     uint32_t use = 0;
     bool ok = true;
-    uint8_t* srow0 = stg + ew * OUT_BUF_BYTES;
+    uint8_t* srow0 = stg + ew * F_OUT_BYTES;
     for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
       int mb, nb;
       tile_coords(t, mb, nb);
       const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
-      const int64_t col0 = (int64_t)nb * BN + grp * 128;
+      const int64_t col0 = (int64_t)nb * BN + grp * F_COLS;
       const bool live = row0 < p.m && col0 < p.n;  // of this warp
-      float2 sum[64];
+      float2 sum[F_COLS / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < F_COLS / 2; ++i) sum[i] = make_float2(0.f, 0.f);
       const float* sx = p.sx + (row < p.m ? row : 0);
       const float* sw = p.sw + (live ? col0 / FB : 0) * p.num_k_blocks;
       float s_next = live ? __ldg(sx) * __ldg(sw) : 0.f;
@@ -198,10 +201,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         }
         tc_fence_after();
         if (live) {
-          const uint32_t ta = tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS + grp * 128;
+          const uint32_t ta =
+              tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS + grp * F_COLS;
           const float2 s2 = make_float2(s, s);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < F_COLS / 32; ++c) {
             float v[32];
             tmem_ld32(ta + c * 32, v);
 #pragma unroll
@@ -214,26 +218,21 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
       }
       if (!ok || !live) continue;
-      // ---- out: 128 bytes of a row at a time through shared memory (swizzled:
-      // 16-byte unit u of row r sits at u ^ (r & 7)) ----
+      // ---- out: 64 bytes of a row at a time through shared memory ----
 #pragma unroll
-      for (int c = 0; c < 128 / COLS; ++c) {
+      for (int c = 0; c < F_COLS / COLS; ++c) {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
-        uint8_t* srow = srow0 + lane * 128;
+        uint4* srow = reinterpret_cast<uint4*>(srow0 + lane * 64);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint4 w;
-          if (sizeof(T) == 2) {
-            const float2* q = sum + c * 32 + u * 4;
-            w = make_uint4(pack_bf16(q[0].x, q[0].y), pack_bf16(q[1].x, q[1].y),
-                           pack_bf16(q[2].x, q[2].y), pack_bf16(q[3].x, q[3].y));
-          } else {
-            const float2* q = sum + c * 16 + u * 2;
-            w = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y),
-                           __float_as_uint(q[1].x), __float_as_uint(q[1].y));
-          }
-          *reinterpret_cast<uint4*>(srow + ((u ^ (lane & 7)) << 4)) = w;
+        for (int u = 0; u < 4; ++u) {
+          const float2* q = sum + (c * COLS + u * (COLS / 4)) / 2;
+          if (sizeof(T) == 2)
+            srow[u] = make_uint4(pack_bf16(q[0].x, q[0].y), pack_bf16(q[1].x, q[1].y),
+                                 pack_bf16(q[2].x, q[2].y), pack_bf16(q[3].x, q[3].y));
+          else
+            srow[u] = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y),
+                                 __float_as_uint(q[1].x), __float_as_uint(q[1].y));
         }
         const int64_t cc = col0 + c * COLS;
         if (p.use_tma) {
@@ -244,19 +243,14 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             bulk_commit();
           }
         } else {
-          // rows of any alignment: one element a lane, whole rows in turn
+          // rows of any alignment: one element a lane, 32 / COLS rows at a time
           __syncwarp();
           const int rows = (int)min((int64_t)32, p.m - row0);
-          for (int r = 0; r < rows; ++r) {
-            T* o = reinterpret_cast<T*>(p.out) + (row0 + r) * p.ldo + cc;
-#pragma unroll
-            for (int e = lane; e < COLS; e += 32) {
-              const int b = e * (int)sizeof(T);
-              const T x = *reinterpret_cast<const T*>(srow0 + r * 128 +
-                                                      ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
-              if (cc + e < p.n) o[e] = x;
-            }
-          }
+          const int e = lane % COLS;
+          if (cc + e < p.n)
+            for (int r = lane / COLS; r < rows; r += 32 / COLS)
+              reinterpret_cast<T*>(p.out)[(row0 + r) * p.ldo + cc + e] =
+                  reinterpret_cast<const T*>(srow0 + r * 64)[e];
           __syncwarp();
         }
       }
@@ -473,13 +467,20 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
       !tc_make_map_u8(&mb, w_codes, k, n, ldw, FB, BN))
     return FLJSD_ERR_CUDA;
   mo = ma;
-  if (p.use_tma && !tc_make_map(&mo, out, n, m, ldo, out_dtype == FLJSD_BF16 ? 64 : 32, 32,
-                                out_dtype == FLJSD_F32))
+  if (p.use_tma && !tc_make_map(&mo, out, n, m, ldo, out_dtype == FLJSD_BF16 ? 32 : 16, 32,
+                                out_dtype == FLJSD_F32, false))
     return FLJSD_ERR_CUDA;
   if (quantise(m, k, x_dtype, 1, x, ldx, ws + L.codes, L.ldq, sx, status, st) != cudaSuccess)
     return FLJSD_ERR_CUDA;
+  // a few rows are bound by reading w: the product arranged around that
+  SkinnyArgs few{1, ws + L.codes, L.ldq, w_codes, ldw, m, n, k, sx, w_scales, out, ldo,
+                 out_dtype == FLJSD_BF16, status};
+  cudaError_t e;
   trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
-  const cudaError_t e = out_dtype == FLJSD_BF16 ? launch_product<__nv_bfloat16>(ma, mb, mo, p, st)
+  if (skinny_supported(few))
+    e = launch_skinny(few, st);
+  else
+    e = out_dtype == FLJSD_BF16 ? launch_product<__nv_bfloat16>(ma, mb, mo, p, st)
                                                 : launch_product<float>(ma, mb, mo, p, st);
   trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
   return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;

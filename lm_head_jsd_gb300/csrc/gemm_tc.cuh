@@ -59,9 +59,10 @@ constexpr int TC_PLAN_CTAS = 152;
 size_t tc_splitk_bytes(int64_t m, int64_t n, int64_t k, int ctas);
 
 // 2-D tensor map over a row-major [outer x inner] bf16 (or fp32) matrix with row
-// stride ld elements: box_inner x box_outer boxes, 128-byte swizzle, zero fill.
+// stride ld elements: box_inner x box_outer boxes, 128-byte swizzle (or none), zero
+// fill.
 bool tc_make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-                 int box_inner, int box_outer, bool f32 = false);
+                 int box_inner, int box_outer, bool f32 = false, bool swizzle = true);
 // The same over 8-bit elements.
 bool tc_make_map_u8(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
                     int box_inner, int box_outer);

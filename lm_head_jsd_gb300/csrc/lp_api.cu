@@ -3,6 +3,7 @@
 // formulas in lp.cuh.
 #include "gemm_tc.cuh"
 #include "lp.cuh"
+#include "skinny_tc.cuh"
 
 #include <cmath>
 
@@ -19,7 +20,20 @@ inline bool aligned(const void* q, uintptr_t a) { return ((uintptr_t)q & (a - 1)
 // fp32 logits and the row kernels.
 bool on_tensor_cores(const fljsd_lp_problem& p) { return p.dtype == FLJSD_BF16 && p.h % 8 == 0; }
 
+// How the logits of a plan's chunks are reduced.
+//  kFused: in the product's epilogue.
+//  kFew:   a forward of up to 16 rows, bound by reading w: the product for few rows
+//          (skinny_tc.cu) and the row kernels over its fp32 logits, 4 bytes for
+//          every 2 h of w.
+//  kRows:  the CUDA-core product and the row kernels.
+enum Path { kFused, kFew, kRows };
+Path path_of(const fljsd_lp_problem& p) {
+  if (!on_tensor_cores(p)) return kRows;
+  return !(p.flags & FLJSD_LP_BACKWARD) && p.bt <= SK_ROWS ? kFew : kFused;
+}
+
 struct LpLayout {
+  Path path;
   bool tc, use_acc32;
   int64_t ld, parts, cap;
   // zeroed: status, count, gmax (in one piece, [zero, zero + zero_bytes))
@@ -31,8 +45,10 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   LpLayout L{};
   const bool bwd = (p.flags & FLJSD_LP_BACKWARD) != 0;
   L.tc = on_tensor_cores(p);
+  L.path = path_of(p);
+  const bool fused = L.path == kFused;
   L.ld = (p.v + 7) / 8 * 8;
-  L.parts = L.tc ? (p.v + LP_PART_COLS - 1) / LP_PART_COLS : lp_row_parts(p.v);
+  L.parts = fused ? (p.v + LP_PART_COLS - 1) / LP_PART_COLS : lp_row_parts(p.v);
   L.cap = L.parts * p.top_k;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -42,8 +58,8 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   };
   const size_t rows = (size_t)c;
   L.zero = L.status = take(sizeof(int));
-  L.count = take(L.tc && p.top_k ? rows * sizeof(int) : 0);
-  L.gmax = take(L.tc ? rows * p.top_k * sizeof(unsigned) : 0);
+  L.count = take(fused && p.top_k ? rows * sizeof(int) : 0);
+  L.gmax = take(fused ? rows * p.top_k * sizeof(unsigned) : 0);
   L.zero_bytes = at - L.zero;
   L.part = take(rows * L.parts * sizeof(float4));
   L.zy = take(rows * sizeof(float));
@@ -51,7 +67,7 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.stats_bytes = at;
   // 2^t in fp16 that the backward pass turns into dz in place, or fp32 logits (and their
   // bf16 gradient beside them)
-  const size_t zb = L.tc ? (bwd ? rows * L.ld * 2 : 0) : rows * L.ld * 4;
+  const size_t zb = fused ? (bwd ? rows * L.ld * 2 : 0) : rows * L.ld * 4;
   L.z = take(zb);
   L.dz = L.z;
   if (bwd && !L.tc && p.dtype == FLJSD_BF16) L.dz = take(rows * L.ld * 2);
@@ -112,7 +128,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
                      const int64_t* labels, int64_t rows, int top, bool keep, char* ws,
                      cudaStream_t st) {
   const float c = log2_scale(p.temperature);
-  if (L.tc) {
+  if (L.path == kFused) {
     LpHeadArgs h{};
     h.x = x; h.ldx = p.h; h.w = w; h.ldw = p.h; h.m = rows; h.n = p.v; h.k = p.h; h.c = c;
     h.labels = labels;
@@ -132,8 +148,19 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     return e;
   }
   float* z = reinterpret_cast<float*>(ws + L.z);
-  cudaError_t e = lp_gemm(FLJSD_KERNEL_GEMM_LOGITS, p.dtype, false, x, p.h, 0, w, p.h, 0, z, L.ld,
-                          rows, p.v, p.h, 0, z, 0, nullptr, nullptr, 0, st);
+  cudaError_t e;
+  if (L.path == kFew) {
+    SkinnyArgs k{};
+    k.x = x; k.ldx = p.h; k.w = w; k.ldw = p.h; k.m = rows; k.n = p.v; k.k = p.h;
+    k.out = z; k.ldo = L.ld;
+    k.status = reinterpret_cast<int*>(ws + L.status);
+    trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
+    e = launch_skinny(k, st);
+    trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
+  } else {
+    e = lp_gemm(FLJSD_KERNEL_GEMM_LOGITS, p.dtype, false, x, p.h, 0, w, p.h, 0, z, L.ld, rows, p.v,
+                p.h, 0, z, 0, nullptr, nullptr, 0, st);
+  }
   if (e != cudaSuccess) return e;
   LpRowsArgs r{};
   r.z = z; r.ld = L.ld; r.v = p.v; r.rows = rows; r.c = c; r.labels = labels;
@@ -261,8 +288,8 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
     j.k = p->top_k;
     j.cand = reinterpret_cast<const int2*>(ws + L.cand);
     j.cap = L.cap;
-    j.count = L.tc ? reinterpret_cast<const int*>(ws + L.count) : nullptr;
-    j.gmax = L.tc ? reinterpret_cast<const unsigned*>(ws + L.gmax) : nullptr;
+    j.count = L.path == kFused ? reinterpret_cast<const int*>(ws + L.count) : nullptr;
+    j.gmax = L.path == kFused ? reinterpret_cast<const unsigned*>(ws + L.gmax) : nullptr;
     j.top_logp = top_logp; j.top_id = top_id;
     if (launch_lp_join(j, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   }

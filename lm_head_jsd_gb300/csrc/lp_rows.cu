@@ -20,7 +20,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = LP_SEG / kThreads;  // logits a thread holds
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kJoinThreads = 128;
+constexpr int kGroups = kThreads / 4;  // groups of threads whose maxima are ranked
+constexpr int kList = 512;             // candidates of a segment ranked in shared memory
+static_assert(LP_MAX_TOP <= kGroups, "the k-th of the groups' maxima");
+constexpr int kJoinThreads = 256;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
@@ -68,37 +71,6 @@ __device__ __forceinline__ int key_col(unsigned long long key) {
 }
 
 template <int W>
-__device__ __forceinline__ float block_max(float x, float* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-#pragma unroll
-  for (int w = 1; w < W; ++w) x = fmaxf(x, sh[w]);
-  __syncthreads();
-  return x;
-}
-// Sums in a fixed order, so that results do not vary from run to run.
-template <int W>
-__device__ __forceinline__ float2 block_sum2(float2 x, float2* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-    x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-  }
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-#pragma unroll
-  for (int w = 1; w < W; ++w) {
-    x.x += sh[w].x;
-    x.y += sh[w].y;
-  }
-  __syncthreads();
-  return x;
-}
-template <int W>
 __device__ __forceinline__ unsigned long long block_max64(unsigned long long x,
                                                           unsigned long long* sh) {
 #pragma unroll
@@ -115,114 +87,156 @@ __device__ __forceinline__ unsigned long long block_max64(unsigned long long x,
   return x;
 }
 
-// Element offsets of one thread's values inside its segment: vectors of N
-// elements, kThreads vectors apart. `lead` elements before the segment's first
-// 16-byte boundary belong to a vector that starts before it and is read one
-// element at a time, as is the vector that crosses the end.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_lp_rows(LpRowsArgs a, int64_t parts) {
+// (m, d, s) of two sets, each relative to its own maximum (lp.cuh); a set without a
+// finite value has m = -inf and d = s = 0, or NaN where it holds one.
+struct Mds {
+  float m, d, s;
+};
+__device__ __forceinline__ Mds merge(const Mds& a, const Mds& b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  const float ta = a.m == -INFINITY ? 0.f : __fmul_rn(a.m - m, c);
+  const float tb = b.m == -INFINITY ? 0.f : __fmul_rn(b.m - m, c);
+  const float fa = ex2(ta), fb = ex2(tb);
+  // 2^t (s + d t): both vanish where 2^t does
+  return Mds{m, __fmaf_rn(a.d, fa, b.d * fb),
+             __fmaf_rn(fa, __fmaf_rn(a.d, fmaxf(ta, -1024.f), a.s),
+                       fb * __fmaf_rn(b.d, fmaxf(tb, -1024.f), b.s))};
+}
+// The block's, in a fixed order (in every thread of the first warp).
+template <int W>
+__device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = merge(x, Mds{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.d, o),
+                     __shfl_xor_sync(0xffffffffu, x.s, o)}, c);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    x = threadIdx.x < W ? sh[threadIdx.x] : Mds{-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1)
+      x = merge(x, Mds{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.d, o),
+                       __shfl_xor_sync(0xffffffffu, x.s, o)}, c);
+  }
+  return x;
+}
+
+// A segment's logits, 32 to a thread: vectors of N elements, kThreads vectors
+// apart, from a 16-byte boundary. The vector that starts before the row (whose
+// first element may lie anywhere) and the one that crosses its end are read one
+// element at a time. Sums are taken relative to each thread's own maximum, so
+// that one reduction serves maximum and sums.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) k_lp_rows(LpRowsArgs a, int64_t parts) {
   constexpr int N = Vec<T>::N;
   constexpr int V = kPer / N;
-  __shared__ float shf[kWarps];
-  __shared__ float2 sh2[kWarps];
+  __shared__ Mds shm[kWarps];
   __shared__ unsigned long long sh64[kWarps];
-  __shared__ float tmax[kThreads];
-  __shared__ unsigned long long list[2 * kThreads];
+  __shared__ float gmax[kGroups];
+  __shared__ unsigned long long list[kList];
   __shared__ int n_list;
   __shared__ float s_thr;
   const int tid = threadIdx.x;
-  for (int64_t unit = blockIdx.x; unit < a.rows * parts; unit += gridDim.x) {
-    const int64_t r = unit / parts, part = unit - r * parts;
+  const int64_t part = blockIdx.x;
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const T* zr = reinterpret_cast<const T*>(a.z) + r * a.ld;
-    // segments start on a 16-byte boundary (counted from the row's first one)
-    const int64_t lead = (((uintptr_t)zr) & 15u) / sizeof(T);
+    const int lead = (int)((((uintptr_t)zr) & 15u) / sizeof(T));
     const int64_t e0 = part * LP_SEG - lead;  // first element, may be before the row
-    const int64_t e1 = e0 + LP_SEG < a.v ? e0 + LP_SEG : a.v;
+    const int n = (int)(a.v - e0 < LP_SEG ? (a.v > e0 ? a.v - e0 : 0) : LP_SEG);
+    const int first = e0 < 0 ? lead : 0;      // elements [first, n) of the segment count
+    const T* zs = zr + e0;
     float z[kPer];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const int64_t j = e0 + (int64_t)(u * kThreads + tid) * N;
-      if (j >= 0 && j + N <= e1) {
+      const int j = (u * kThreads + tid) * N;
+      if (j >= first && j + N <= n) {
         float o[N];
-        Vec<T>::load(zr + j, o);
+        Vec<T>::load(zs + j, o);
 #pragma unroll
         for (int e = 0; e < N; ++e) z[u * N + e] = o[e];
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e)
-          z[u * N + e] = (j + e >= 0 && j + e < e1) ? val(zr + j + e) : -INFINITY;
+          z[u * N + e] = (j + e >= first && j + e < n) ? val(zs + j + e) : -INFINITY;
       }
     }
-    float mx = -INFINITY;  // (skips NaN)
+    Mds x{-INFINITY, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, z[i]);
-    const float tm = mx;
-    mx = block_max<kWarps>(mx, shf);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float2 ds = make_float2(0.f, 0.f);
+    for (int i = 0; i < kPer; ++i) x.m = fmaxf(x.m, z[i]);  // (skips NaN)
+    {
+      const float ref = x.m == -INFINITY ? 0.f : x.m;
+      const float2 c2 = make_float2(a.c, a.c), nref = make_float2(-ref, -ref);
+      float2 d = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float x = __fmul_rn(z[i] - ref, a.c);
-      const float y = ex2(x);
-      ds.x += y;
-      ds.y = __fmaf_rn(y, fmaxf(x, -1024.f), ds.y);  // a logit of -inf adds 0, NaN stays
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 q = __fmul2_rn(__fadd2_rn(make_float2(z[i], z[i + 1]), nref), c2);
+        const float2 y = make_float2(ex2(q.x), ex2(q.y));
+        d = __fadd2_rn(d, y);
+        // a logit of -inf adds 0, NaN stays
+        t = __ffma2_rn(y, make_float2(fmaxf(q.x, -1024.f), fmaxf(q.y, -1024.f)), t);
+      }
+      x.d = d.x + d.y;
+      x.s = t.x + t.y;
     }
-    ds = block_sum2<kWarps>(ds, sh2);
+    const float tm = x.m;
+    x = block_mds<kWarps>(x, a.c, shm);
     if (tid == 0) {
-      a.part[r * parts + part] = make_float4(mx, ds.x, ds.y, 0.f);
+      a.part[r * parts + part] = make_float4(x.m, x.d, x.s, 0.f);
       if (a.labels && part == 0) {
         const int64_t y = a.labels[a.row0 + r];
         if (y >= 0 && y < a.v) a.zy[r] = val(zr + y);
       }
     }
-    if (a.k > 0) {
-      // The k-th largest of the threads' maxima bounds the k-th largest logit
-      // from below: what reaches it is listed and ranked. A list that
-      // overflows (many equal logits) is replaced by k rounds of the largest
+    if (TOP) {
+      // The k-th largest of 64 groups' maxima (four threads each) bounds the k-th
+      // largest logit from below: what reaches it is listed and ranked. A list
+      // that overflows (many equal logits) is replaced by k rounds of the largest
       // remaining key.
-      tmax[tid] = tm;
-      if (tid == 0) {
-        n_list = 0;
-        s_thr = -INFINITY;
-      }
+      float g = tm;
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+      if ((tid & 3) == 0) gmax[tid >> 2] = g;
+      if (tid == 0) n_list = 0;
       __syncthreads();
-      int rank = 0;
-      for (int j = 0; j < kThreads; ++j) {
-        const float o = tmax[j];
-        rank += (o > tm || (o == tm && j < tid)) ? 1 : 0;
+      if (tid < kGroups) {
+        const float o = gmax[tid];
+        int rank = 0;
+#pragma unroll 16
+        for (int j = 0; j < kGroups; ++j) rank += (gmax[j] > o || (gmax[j] == o && j < tid)) ? 1 : 0;
+        if (rank == a.k - 1) s_thr = o;
       }
-      if (rank == a.k - 1) s_thr = tm;
       __syncthreads();
       const float thr = s_thr;
+      if (tm >= thr) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (z[i] >= thr && z[i] > -INFINITY) {
-          const int at = atomicAdd(&n_list, 1);
-          const int64_t col = e0 + (int64_t)((i / N) * kThreads + tid) * N + i % N;
-          if (at < 2 * kThreads)
-            list[at] = cand_key(make_int2(__float_as_int(z[i]), (int)col));
+        for (int i = 0; i < kPer; ++i) {
+          if (z[i] >= thr && z[i] > -INFINITY) {
+            const int at = atomicAdd(&n_list, 1);
+            const int col = (int)e0 + ((i / N) * kThreads + tid) * N + i % N;
+            if (at < kList) list[at] = cand_key(make_int2(__float_as_int(z[i]), col));
+          }
         }
       }
       __syncthreads();
-      const int n = n_list;
+      const int n_all = n_list;
       int2* out = a.cand + (r * parts + part) * a.k;
-      if (n <= 2 * kThreads) {
-        for (int i = tid; i < n; i += kThreads) {
+      if (n_all <= kList) {
+        for (int i = tid; i < n_all; i += kThreads) {
           const unsigned long long key = list[i];
           int above = 0;
-          for (int j = 0; j < n; ++j) above += list[j] > key ? 1 : 0;
+          for (int j = 0; j < n_all; ++j) above += list[j] > key ? 1 : 0;
           if (above < a.k) out[above] = make_int2(__float_as_int(key_value(key)), key_col(key));
         }
-        for (int i = n + tid; i < a.k; i += kThreads) out[i] = make_int2(0, -1);
+        for (int i = n_all + tid; i < a.k; i += kThreads) out[i] = make_int2(0, -1);
       } else {
         unsigned long long last = ~0ull;
         for (int q = 0; q < a.k; ++q) {
           unsigned long long best = 0;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
-            const int64_t col = e0 + (int64_t)((i / N) * kThreads + tid) * N + i % N;
+            const int col = (int)e0 + ((i / N) * kThreads + tid) * N + i % N;
             const unsigned long long key =
-                z[i] > -INFINITY ? cand_key(make_int2(__float_as_int(z[i]), (int)col)) : 0ull;
+                z[i] > -INFINITY ? cand_key(make_int2(__float_as_int(z[i]), col)) : 0ull;
             best = key < last && key > best ? key : best;
           }
           best = block_max64<kWarps>(best, sh64);
@@ -231,8 +245,8 @@ __global__ void __launch_bounds__(kThreads) k_lp_rows(LpRowsArgs a, int64_t part
           last = best;
         }
       }
-      __syncthreads();
     }
+    __syncthreads();  // the shared results are written again by the next row
   }
 }
 
@@ -240,36 +254,40 @@ __global__ void __launch_bounds__(kThreads) k_lp_rows(LpRowsArgs a, int64_t part
 // k largest.
 __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   constexpr int W = kJoinThreads / 32;
-  __shared__ float shf[W];
-  __shared__ float2 sh2[W];
+  __shared__ Mds shm[W];
+  __shared__ float2 sh_norm;
   __shared__ unsigned long long sh64[W];
   __shared__ unsigned long long list[kJoinCap];
   __shared__ int n_list;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x, out = a.row0 + r;
   const float4* ps = a.part + r * a.parts;
-  float m = -INFINITY;
-  for (int64_t i = tid; i < a.parts; i += kJoinThreads) m = fmaxf(m, ps[i].x);
-  m = block_max<W>(m, shf);
-  float2 ds = make_float2(0.f, 0.f);
-  for (int64_t i = tid; i < a.parts; i += kJoinThreads) {
-    const float4 q = ps[i];
-    // a part without a finite logit has d = s = 0 (NaN where it holds one)
-    const float dm = q.x == -INFINITY ? 0.f : __fmul_rn(q.x - m, a.c);
-    const float f = ex2(dm);
-    ds.x = __fmaf_rn(q.y, f, ds.x);
-    // 2^dm (s + d dm): both vanish where 2^dm does
-    ds.y = __fmaf_rn(f, __fmaf_rn(q.y, fmaxf(dm, -1024.f), q.z), ds.y);
+  // four parts in flight a thread
+  Mds x{-INFINITY, 0.f, 0.f};
+  for (int64_t i0 = tid; i0 < a.parts; i0 += 4 * kJoinThreads) {
+    float4 q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + u * kJoinThreads;
+      q[u] = i < a.parts ? ps[i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x = merge(x, Mds{q[u].x, q[u].y, q[u].z}, a.c);
   }
-  ds = block_sum2<W>(ds, sh2);
+  if (tid == 0) n_list = 0;
+  x = block_mds<W>(x, a.c, shm);
+  const float m = x.m;  // (in the first warp)
+  const float2 ds = make_float2(x.d, x.s);
   // a row without a finite logit has d = 0: lse = -inf, entropy 0
   const bool empty = ds.x == 0.f;
   const float l2d = empty ? 0.f : log2f(ds.x);
   // not through log2 units, in which the type's lowest value overflows
-  auto log_p = [&](float z) { return __fmaf_rn(z - m, a.inv_t, -kLn2 * l2d); };
+  auto log_p = [&](float z, float2 norm) {
+    return __fmaf_rn(z - norm.x, a.inv_t, -kLn2 * norm.y);
+  };
   if (tid == 0) {
     a.lse[out] = empty ? -INFINITY : __fmaf_rn(m, a.inv_t, kLn2 * l2d);
-    a.norm[out] = make_float2(empty ? -INFINITY : m, l2d);
+    a.norm[out] = sh_norm = make_float2(empty ? -INFINITY : m, l2d);
     const int64_t y = a.labels ? a.labels[out] : 0;
     bool live = true;
     if (a.labels) {
@@ -279,7 +297,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
         atomicExch(a.status, (int)FLJSD_ERR_INVALID_ARG);
       }
       float lp = 0.f;
-      if (live) lp = empty ? -INFINITY : log_p(a.zy[r]);
+      if (live) lp = empty ? -INFINITY : log_p(a.zy[r], make_float2(m, l2d));
       a.logp[out] = lp;
     }
     a.entropy[out] = live && !empty ? kLn2 * (l2d - ds.y / ds.x) : 0.f;
@@ -293,8 +311,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
     least = 0xffffffffu;
     for (int j = 0; j < a.k; ++j) least = min(least, a.gmax[r * a.k + j]);
   }
-  if (tid == 0) n_list = 0;
-  __syncthreads();
   for (int64_t i = tid; i < n_cand; i += kJoinThreads) {
     const unsigned long long key = cand_key(cand[i]);
     if (key != 0 && (unsigned)(key >> 32) >= least) {
@@ -304,10 +320,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   }
   __syncthreads();
   const int n = n_list;
+  const float2 norm = sh_norm;
   float* tl = a.top_logp + out * a.k;
   int64_t* ti = a.top_id + out * a.k;
   auto put = [&](int q, unsigned long long key) {
-    tl[q] = key ? log_p(key_value(key)) : -INFINITY;
+    tl[q] = key ? log_p(key_value(key), norm) : -INFINITY;
     ti[q] = key ? (int64_t)key_col(key) : -1;
   };
   if (n <= kJoinCap) {
@@ -333,81 +350,95 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   }
 }
 
-struct GradRow {
-  float a, b, ent, m, l2;  // log2 p = c (z - m) - l2
-  int64_t y;
-  float py;
-  bool live;
-};
-
 // dz of one logit; lp2 = log2 p. -inf: p = 0 and p log p = 0.
-__device__ __forceinline__ float grad_of(const GradRow& g, float lp2) {
-  const float p = ex2(lp2);
-  const float t = __fmaf_rn(g.b, __fmaf_rn(kLn2, fmaxf(lp2, -1024.f), g.ent), g.a);
-  return -p * t;
+//   -p (a + b (log p + entropy)) = -p (b ln2 log2 p + (a + b entropy))
+__device__ __forceinline__ float grad_of(float lp2, float bl, float ab) {
+  return -ex2(lp2) * __fmaf_rn(bl, fmaxf(lp2, -1024.f), ab);
 }
 
+// One CTA to a segment of a row, in vectors of eight where the logits and their
+// gradient lie alike relative to a 16-byte boundary (rows of odd length start
+// anywhere, but both at the same place), else one element at a time. All loads of
+// a thread are issued before the first is used.
 template <typename TI, typename TO, bool FROM_E>
-__global__ void __launch_bounds__(kThreads) k_lp_grad(LpGradArgs a, int64_t segs) {
-  constexpr int N = 8;
-  for (int64_t unit = blockIdx.x; unit < a.rows * segs; unit += gridDim.x) {
-    const int64_t r = unit / segs, seg = unit - r * segs;
+__global__ void __launch_bounds__(kThreads) k_lp_grad(LpGradArgs a) {
+  constexpr int N = 8, U = LP_SEG / (kThreads * N);
+  const int tid = threadIdx.x;
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const TI* zr = reinterpret_cast<const TI*>(a.z) + r * a.ldz;
     TO* orow = reinterpret_cast<TO*>(a.out) + r * a.ldo;
     const int64_t row = a.row0 + r;
-    GradRow g;
-    g.y = a.labels ? a.labels[row] : -1;
-    g.live = !a.labels || (g.y != a.ignore_index && g.y >= 0 && g.y < a.v);
+    const int64_t y = a.labels ? a.labels[row] : -1;
     const float2 norm = a.norm[row];
-    g.m = norm.x;
-    g.l2 = norm.y;
-    g.live = g.live && !(g.m == -INFINITY && g.l2 == 0.f);  // (a row of NaN stays NaN)
-    g.a = a.grad_logp && a.labels ? a.grad_logp[row] * a.inv_t : 0.f;
-    g.b = a.grad_entropy ? a.grad_entropy[row] * a.inv_t : 0.f;
-    g.ent = a.entropy[row];
-    const bool has_y = g.live && a.labels;
-    const float lpy = has_y ? a.logp[row] : 0.f;
-    // the label's own element from its fp32 log probability: 1 - p_y would
-    // lose its digits to a rounded p_y
-    const float dzy =
-        has_y ? __fmaf_rn(-ex2(lpy * (1.f / kLn2)),
-                          __fmaf_rn(g.b, fmaxf(lpy, -1024.f) + g.ent, g.a), g.a)
-              : 0.f;
-    // vectors where both sides' addresses allow them (rows of odd length start
-    // anywhere), else elements
-    const bool vec = ((((uintptr_t)zr) | ((uintptr_t)orow)) & 15u) == 0;
-    const int64_t j0 = seg * LP_SEG, j1 = j0 + LP_SEG < a.v ? j0 + LP_SEG : a.v;
-    auto one = [&](float z, int64_t j, float ref) {
-      const float lp2 = FROM_E ? lg2(z) + ref : __fmul_rn(z - g.m, a.c) - g.l2;
-      float o = g.live ? grad_of(g, lp2) : 0.f;
-      if (has_y && j == g.y) o = dzy;
-      return o;
+    // (a row of NaN is no empty row: its gradient is NaN)
+    const bool live = (!a.labels || (y != a.ignore_index && y >= 0 && y < a.v)) &&
+                      !(norm.x == -INFINITY && norm.y == 0.f);
+    const float ga = a.grad_logp && a.labels ? a.grad_logp[row] * a.inv_t : 0.f;
+    const float gb = a.grad_entropy ? a.grad_entropy[row] * a.inv_t : 0.f;
+    const float ent = a.entropy[row];
+    const float bl = gb * kLn2, ab = __fmaf_rn(gb, ent, ga);
+    const bool same = ((uintptr_t)zr & 15u) / sizeof(TI) == ((uintptr_t)orow & 15u) / sizeof(TO);
+    const int lead = same ? (int)(((uintptr_t)zr & 15u) / sizeof(TI)) : 0;
+    const int64_t e0 = (int64_t)blockIdx.x * LP_SEG - lead;
+    const int n = (int)(a.v - e0 < LP_SEG ? (a.v > e0 ? a.v - e0 : 0) : LP_SEG);
+    const int first = e0 < 0 ? lead : 0;  // elements [first, n) of the segment count
+    const TI* zs = zr + e0;
+    TO* os = orow + e0;
+    // log2 p = c (z - m) - log2 d; from 2^t, log2 p = t + c (m of its part - m) - log2 d
+    auto one = [&](float z, float ref) {
+      const float lp2 = FROM_E ? lg2(z) + ref : __fmul_rn(z - norm.x, a.c) - norm.y;
+      return grad_of(lp2, bl, ab);
     };
-    if (vec) {
-      for (int64_t j = j0 + (int64_t)threadIdx.x * N; j < j1; j += (int64_t)kThreads * N) {
-        const float ref = FROM_E ? __fmul_rn(a.part[r * a.parts + j / LP_PART_COLS].x - g.m, a.c) - g.l2 : 0.f;
-        float z[N];
-        if (j + N <= a.v) {
-          load8(zr + j, z);
+    auto ref_of = [&](int j) {  // (FROM_E: lead is 0)
+      return FROM_E ? __fmul_rn(a.part[r * a.parts + (e0 + j) / LP_PART_COLS].x - norm.x, a.c) - norm.y
+                    : 0.f;
+    };
+    if (same) {
+      float z[U][N], ref[U];
 #pragma unroll
-          for (int e = 0; e < N; ++e) z[e] = one(z[e], j + e, ref);
-          store8(orow + j, z);
+      for (int u = 0; u < U; ++u) {
+        const int j = (u * kThreads + tid) * N;
+        ref[u] = 0.f;
+        if (live && j >= first && j + N <= n) {
+          load8(zs + j, z[u]);
+          ref[u] = ref_of(j);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = (u * kThreads + tid) * N;
+        if (j >= first && j + N <= n) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) z[u][e] = live ? one(z[u][e], ref[u]) : 0.f;
+          store8(os + j, z[u]);
         } else {
-          for (int e = 0; j + e < a.v; ++e) Vec<TO>::put(orow + j + e, one(val(zr + j + e), j + e, ref));
+          for (int e = 0; e < N; ++e)
+            if (j + e >= first && j + e < n)
+              Vec<TO>::put(os + j + e, live ? one(val(zs + j + e), ref_of(j + e)) : 0.f);
         }
       }
     } else {
-      for (int64_t j = j0 + threadIdx.x; j < j1; j += kThreads) {
-        const float ref = FROM_E ? __fmul_rn(a.part[r * a.parts + j / LP_PART_COLS].x - g.m, a.c) - g.l2 : 0.f;
-        Vec<TO>::put(orow + j, one(val(zr + j), j, ref));
+      for (int j = tid; j < n; j += kThreads)
+        Vec<TO>::put(os + j, live ? one(val(zs + j), ref_of(j)) : 0.f);
+    }
+    // The label's own element from its fp32 log probability (1 - p_y would lose its
+    // digits to a rounded p_y), written over what the loop left there.
+    if (live && a.labels && y >= e0 + first && y < e0 + n) {
+      __syncthreads();
+      if (tid == 0) {
+        const float lp = a.logp[row];
+        Vec<TO>::put(orow + y, __fmaf_rn(-ex2(lp * (1.f / kLn2)),
+                                         __fmaf_rn(gb, fmaxf(lp, -1024.f) + ent, ga), ga));
       }
     }
   }
 }
 
-int64_t units_grid(int64_t units, int per_sm) {
-  const int64_t most = (int64_t)num_sms() * per_sm;
-  return units < most ? units : most;
+// x: segments of a row; y: rows, up to what keeps the GPU full (a CTA then walks on)
+dim3 row_grid(int64_t segs, int64_t rows) {
+  const int64_t most = ((int64_t)num_sms() * 32 + segs - 1) / segs;
+  const int64_t y = rows < most ? rows : most;
+  return dim3((unsigned)segs, (unsigned)(y < 65535 ? y : 65535));
 }
 
 }  // namespace
@@ -423,12 +454,19 @@ cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   const int64_t parts = lp_row_parts(a.v);
-  const unsigned grid = (unsigned)units_grid(a.rows * parts, 32);
+  const dim3 grid = row_grid(parts, a.rows);
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
-  if (dtype == FLJSD_BF16)
-    k_lp_rows<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, parts);
-  else
-    k_lp_rows<float><<<grid, kThreads, 0, st>>>(a, parts);
+  if (dtype == FLJSD_BF16) {
+    if (a.k > 0)
+      k_lp_rows<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a, parts);
+    else
+      k_lp_rows<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a, parts);
+  } else {
+    if (a.k > 0)
+      k_lp_rows<float, true><<<grid, kThreads, 0, st>>>(a, parts);
+    else
+      k_lp_rows<float, false><<<grid, kThreads, 0, st>>>(a, parts);
+  }
   trace_end(FLJSD_KERNEL_JSD_ROWS, st);
   return cudaGetLastError();
 }
@@ -436,18 +474,17 @@ cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_grad(int z_dtype, int out_dtype, bool from_e, const LpGradArgs& a,
                            cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  const int64_t segs = (a.v + LP_SEG - 1) / LP_SEG;
-  const unsigned grid = (unsigned)units_grid(a.rows * segs, 32);
+  const dim3 grid = row_grid(from_e ? (a.v + LP_SEG - 1) / LP_SEG : lp_row_parts(a.v), a.rows);
   using bf = __nv_bfloat16;
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
   if (from_e)
-    k_lp_grad<__half, bf, true><<<grid, kThreads, 0, st>>>(a, segs);
+    k_lp_grad<__half, bf, true><<<grid, kThreads, 0, st>>>(a);
   else if (z_dtype == FLJSD_F32 && out_dtype == FLJSD_F32)
-    k_lp_grad<float, float, false><<<grid, kThreads, 0, st>>>(a, segs);
+    k_lp_grad<float, float, false><<<grid, kThreads, 0, st>>>(a);
   else if (z_dtype == FLJSD_F32)
-    k_lp_grad<float, bf, false><<<grid, kThreads, 0, st>>>(a, segs);
+    k_lp_grad<float, bf, false><<<grid, kThreads, 0, st>>>(a);
   else
-    k_lp_grad<bf, bf, false><<<grid, kThreads, 0, st>>>(a, segs);
+    k_lp_grad<bf, bf, false><<<grid, kThreads, 0, st>>>(a);
   trace_end(FLJSD_KERNEL_JSD_ROWS, st);
   return cudaGetLastError();
 }

@@ -1,0 +1,328 @@
+// Products of a few rows (up to 16) with a large weight on the tensor cores: the
+// lm_head at a decoding step. Bound by reading w once from HBM, so everything else
+// is arranged around that stream:
+//  - w's rows are the instruction's 128 rows and x's rows its 16 columns: a tile is
+//    128 rows of w, half of what the other way round would take, and spreads over
+//    the SMs with less left over (128256 rows: 6.6 rounds of 152 instead of 3.3 of
+//    twice the length);
+//  - x stays in shared memory for the CTA's whole life (2 KB for each 128 bytes of
+//    k) where it fits beside five stages of w. One row of x lies in one or two
+//    slices of L2; read again for every tile by every SM, it held the stream up
+//    (one row took 220 us where sixteen took 175 us; H = 4096, V = 128256);
+//  - the rest of shared memory is the ring of w's tiles, 16 KB each.
+// e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
+// ring of eight, and is scaled and added in fp32 registers.
+#include "gemm_tc_kernel.cuh"
+#include "skinny_tc.cuh"
+
+namespace fljsd {
+namespace {
+
+using namespace tcgemm;
+
+constexpr int kThreads = 192;  // producer, MMA, four epilogue warps
+constexpr int kStage = BM * 128;        // a tile of w: 128 rows of 128 bytes
+constexpr int kXBlock = SK_ROWS * 128;  // x beside it
+constexpr int kMaxStages = 13;
+constexpr int kMinStages = 5;
+constexpr int kAccs = 8, kAccCols = 16;
+constexpr int kTmemCols = kAccs * kAccCols;
+constexpr int kCtrl = 1024;
+constexpr int kScaleBlocks = 256;  // blocks of k whose x scales are held in shared memory
+
+struct SkCtrl {
+  unsigned long long full[kMaxStages], empty[kMaxStages];
+  unsigned long long tmem_full[kAccs], tmem_empty[kAccs];
+  unsigned long long x_full, drain;
+  unsigned long long timeout_ns;
+  uint32_t tmem_base;
+  volatile int abort;
+};
+static_assert(sizeof(SkCtrl) <= kCtrl, "control block");
+
+struct SkParams {
+  int64_t m, n;
+  int num_tiles, num_k_blocks, nst, resident;
+  const float *sx, *sw;
+  void* out;
+  int64_t ldo;
+  unsigned long long timeout_ns;
+  int* status;
+};
+
+__device__ __forceinline__ bool sk_wait(SkCtrl* cb, uint32_t bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (cb->abort) return false;
+      if (globaltimer() - t0 > cb->timeout_ns) {
+        cb->abort = 1;
+        if (status) atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// 32 lanes x 16 columns of accumulators.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// M = 128, N = 16, fp32 accumulator, both operands K-major; bf16 (format 1) or
+// e4m3 (format 0 of kind::f8f6f4).
+template <bool E4M3>
+__device__ __forceinline__ void mma16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                      uint32_t accumulate) {
+  constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) |
+                             ((uint32_t)(SK_ROWS >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+  if (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <bool E4M3, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_skinny(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+             const SkParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float s_sx[E4M3 ? kScaleBlocks * SK_ROWS : 1];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const int nkb = p.num_k_blocks;
+  const uint32_t xbase = base;  // resident x; otherwise behind each stage
+  const int sb = kStage + (p.resident ? 0 : kXBlock);
+  const uint32_t wbase = base + (p.resident ? nkb * kXBlock : 0);
+  SkCtrl* cb = reinterpret_cast<SkCtrl*>(smem_raw + (wbase - raw) + p.nst * sb);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int KE = E4M3 ? 128 : 64;  // elements in 128 bytes
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.nst; ++s) {
+      mbar_init(smem_u32(&cb->full[s]), 1);
+      mbar_init(smem_u32(&cb->empty[s]), 1);
+    }
+    for (int a = 0; a < kAccs; ++a) {
+      mbar_init(smem_u32(&cb->tmem_full[a]), 1);
+      mbar_init(smem_u32(&cb->tmem_empty[a]), 4);
+    }
+    mbar_init(smem_u32(&cb->x_full), 1);
+    mbar_init(smem_u32(&cb->drain), 1);
+    cb->abort = 0;
+    cb->timeout_ns = p.timeout_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmW);
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(&cb->tmem_base), kTmemCols);
+  if (E4M3)
+    for (int i = threadIdx.x; i < nkb * SK_ROWS; i += kThreads) {
+      const int j = i % SK_ROWS;
+      s_sx[i] = j < p.m ? p.sx[(int64_t)(i / SK_ROWS) * p.m + j] : 0.f;
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = cb->tmem_base;
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t filled = 0;  // stages filled since the start
+      bool ok = true;
+      if (p.resident && (int)blockIdx.x < p.num_tiles) {
+        const uint32_t xb = smem_u32(&cb->x_full);
+        mbar_arrive_expect_tx(xb, nkb * kXBlock);
+        for (int kb = 0; kb < nkb; ++kb) tma_load_2d(xbase + kb * kXBlock, &tmX, xb, kb * KE, 0);
+      }
+      for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!sk_wait(cb, smem_u32(&cb->empty[stage]), phase ^ 1u, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = wbase + stage * sb, fb = smem_u32(&cb->full[stage]);
+          mbar_arrive_expect_tx(fb, sb);
+          tma_load_2d(dst, &tmW, fb, kb * KE, t * BM);
+          if (!p.resident) tma_load_2d(dst + kStage, &tmX, fb, kb * KE, 0);
+          ++filled;
+          if (++stage == p.nst) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every copy has landed before the CTA may exit: the last fill of each stage
+      if (p.resident && (int)blockIdx.x < p.num_tiles)
+        sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
+      for (int s = 0; s < p.nst; ++s) {
+        const uint32_t fills = filled / p.nst + ((uint32_t)s < filled % p.nst ? 1u : 0u);
+        if (fills > 0) sk_wait(cb, smem_u32(&cb->full[s]), (fills - 1) & 1u, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t use = 0;  // accumulators handed out
+      bool any = false;
+      bool ok = true;
+      if (p.resident && (int)blockIdx.x < p.num_tiles)
+        ok = sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
+      for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb) {
+          const int acc = use % kAccs;
+          if ((E4M3 || kb == 0) && !sk_wait(cb, smem_u32(&cb->tmem_empty[acc]),
+                                            ((use / kAccs) & 1u) ^ 1u, p.status)) {
+            ok = false;
+            break;
+          }
+          if (!sk_wait(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = wbase + stage * sb;
+          const uint32_t sx = p.resident ? xbase + kb * kXBlock : sa + kStage;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 bytes of k each
+            mma16<E4M3>(tmem_base + acc * kAccCols, smem_desc(sa + kk * 32, 16, 1024),
+                        smem_desc(sx + kk * 32, 16, 1024), (kk > 0 || (!E4M3 && kb > 0)) ? 1u : 0u);
+          mma_commit<false>(smem_u32(&cb->empty[stage]));
+          any = true;
+          if (E4M3 || kb == nkb - 1) {
+            mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
+            ++use;
+          }
+          if (++stage == p.nst) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (any) {
+        mma_commit<false>(smem_u32(&cb->drain));
+        sk_wait(cb, smem_u32(&cb->drain), 0, p.status);
+      }
+    }
+  } else {
+    // ---------------- epilogue: one row of w (a column of out) to a thread ----------------
+    const int sub = warp & 3;
+    uint32_t use = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
+      const int64_t col = (int64_t)t * BM + sub * 32 + lane;
+      float sum[SK_ROWS];
+#pragma unroll
+      for (int j = 0; j < SK_ROWS; ++j) sum[j] = 0.f;
+      const int steps = E4M3 ? nkb : 1;
+      for (int kb = 0; kb < steps; ++kb, ++use) {
+        const int acc = use % kAccs;
+        const float sw = E4M3 ? __ldg(p.sw + (int64_t)t * nkb + kb) : 1.f;
+        ok = sk_wait(cb, smem_u32(&cb->tmem_full[acc]), (use / kAccs) & 1u, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float v[SK_ROWS];
+        tmem_ld16(tmem_base + ((uint32_t)(sub * 32) << 16) + acc * kAccCols, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+#pragma unroll
+        for (int j = 0; j < SK_ROWS; ++j)
+          sum[j] = E4M3 ? __fmaf_rn(v[j], s_sx[kb * SK_ROWS + j] * sw, sum[j]) : v[j];
+      }
+      if (ok && col < p.n) {
+        T* o = reinterpret_cast<T*>(p.out) + col;
+#pragma unroll
+        for (int j = 0; j < SK_ROWS; ++j)
+          if (j < p.m) put(o + j * p.ldo, sum[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<false>(tmem_base, kTmemCols);
+  }
+}
+
+template <bool E4M3, typename T>
+cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const SkParams& p, int smem,
+                   cudaStream_t st) {
+  auto kern = k_skinny<E4M3, T>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<p.num_tiles < num_sms() ? p.num_tiles : num_sms(), kThreads, smem, st>>>(mx, mw, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool skinny_supported(const SkinnyArgs& a) {
+  auto al = [](const void* q) { return ((uintptr_t)q & 15u) == 0; };
+  const int64_t unit = a.e4m3 ? 16 : 8;  // elements of 16 bytes
+  return a.m > 0 && a.m <= SK_ROWS && a.n > 0 && a.n < (1ll << 31) - BM && a.k > 0 &&
+         a.k < (1ll << 24) && al(a.x) && al(a.w) && a.ldx % unit == 0 && a.ldw % unit == 0 &&
+         (!a.e4m3 || a.k <= (int64_t)kScaleBlocks * 128);
+}
+
+cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
+  if (!skinny_supported(a)) return cudaErrorInvalidValue;
+  SkParams p{};
+  const int ke = a.e4m3 ? 128 : 64;
+  p.m = a.m; p.n = a.n;
+  p.num_tiles = (int)((a.n + BM - 1) / BM);
+  p.num_k_blocks = (int)((a.k + ke - 1) / ke);
+  const int fixed = kCtrl + 1024 + (a.e4m3 ? kScaleBlocks * SK_ROWS * (int)sizeof(float) : 0) + 1024;
+  const int64_t xb = (int64_t)p.num_k_blocks * kXBlock;
+  p.resident = xb + kMinStages * kStage + fixed <= SMEM_MAX;
+  const int sb = kStage + (p.resident ? 0 : kXBlock);
+  const int left = SMEM_MAX - fixed - (p.resident ? (int)xb : 0);
+  p.nst = left / sb < kMaxStages ? left / sb : kMaxStages;
+  p.sx = a.sx; p.sw = a.sw; p.out = a.out; p.ldo = a.ldo;
+  p.timeout_ns = kTimeoutNs;
+  p.status = a.status;
+  CUtensorMap mx, mw;
+  const bool ok = a.e4m3 ? tc_make_map_u8(&mx, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&
+                               tc_make_map_u8(&mw, a.w, a.k, a.n, a.ldw, ke, BM)
+                         : tc_make_map(&mx, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&
+                               tc_make_map(&mw, a.w, a.k, a.n, a.ldw, ke, BM);
+  if (!ok) return cudaErrorInvalidValue;
+  const int smem = (p.resident ? (int)xb : 0) + p.nst * sb + kCtrl + 1024;
+  if (a.e4m3)
+    return a.out_bf16 ? launch<true, __nv_bfloat16>(mx, mw, p, smem, st)
+                      : launch<true, float>(mx, mw, p, smem, st);
+  return launch<false, float>(mx, mw, p, smem, st);
+}
+
+}  // namespace fljsd

@@ -1,0 +1,28 @@
+// Products of a few rows with a large weight (internal). See skinny_tc.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fljsd {
+
+constexpr int SK_ROWS = 16;  // rows of x at most
+
+// out[i, j] = x[i] . w[j] for m <= SK_ROWS rows of x, w [n x k].
+// bf16: x, w bf16, out fp32. e4m3: codes with scales sx [ceil(k / 128) x m] and
+// sw [ceil(n / 128) x ceil(k / 128)] (fp8_gemm.cu), out fp32 or bf16.
+struct SkinnyArgs {
+  int e4m3;
+  const void* x; int64_t ldx;
+  const void* w; int64_t ldw;
+  int64_t m, n, k;
+  const float *sx, *sw;
+  void* out; int64_t ldo;
+  int out_bf16;
+  int* status;
+};
+// Whether the kernel takes the shape (alignment as for the tensor maps).
+bool skinny_supported(const SkinnyArgs& a);
+cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st);
+
+}  // namespace fljsd
