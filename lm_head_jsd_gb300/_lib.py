@@ -175,8 +175,13 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
-        # (is_available() would ask the driver at every call)
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_initialized() else None
+        if not torch.cuda.is_initialized():  # (is_available() would ask the driver at every call)
+            return None
+        # the handle alone: a Stream object takes longer to make than a launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

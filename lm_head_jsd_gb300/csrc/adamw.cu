@@ -294,7 +294,7 @@ cudaError_t run(const fljsd_adamw_tensor* ts, int count, const fljsd_adamw_optio
   return cudaSuccess;
 }
 
-constexpr int kFew = 48, kMany = 400;
+constexpr int kFew = 64, kMany = 400;
 static_assert(sizeof(Table<kMany>) + sizeof(Hyper) <= 32764, "kernel parameters");
 
 }  // namespace

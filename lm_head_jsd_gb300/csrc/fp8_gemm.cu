@@ -29,10 +29,13 @@ constexpr int FB = 128;         // elements of a scale's block, and of a stage's
 constexpr int F_UMMA_K = 32;
 constexpr int F_STAGES = 4;
 constexpr int F_STAGE_BYTES = (BM + BN) * FB;
-constexpr int F_EPI = 16;       // epilogue warps
+constexpr int F_EPI = 8;        // epilogue warps
 constexpr int F_COLS = BN / (F_EPI / 4);  // columns of an epilogue thread
 constexpr int F_OUT_BYTES = 32 * 64;      // an epilogue warp's staging: 32 rows of 64 bytes
-constexpr int F_THREADS = 64 + 32 * F_EPI;
+// Registers: launched with 168 for each of 12 warps; the four that copy and issue
+// keep 40, the eight epilogue warps take 232 (128 x 40 + 256 x 232 = 384 x 168).
+constexpr int F_REGS_LOW = 40, F_REGS_HIGH = 232;
+constexpr int F_THREADS = 128 + 32 * F_EPI;
 constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * F_OUT_BYTES + 1024 + CTRL_BYTES;
 static_assert(F_SMEM <= SMEM_MAX, "shared memory");
 
@@ -103,9 +106,10 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     nb = r / gm;
   };
 
-  if (warp == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F_REGS_LOW));
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued_parity[F_STAGES];
@@ -136,9 +140,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       for (int s = 0; s < F_STAGES; ++s)
         if (issued[s]) wait_bar(cb, smem_u32(&cb->full[s]), issued_parity[s], p.status);
     }
-  } else if (warp == 1) {
     // ---------------- MMA issuer: one accumulator for each 128-deep block ----------------
-    if (lane == 0) {
+    if (warp == 1 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t use = 0;  // accumulators handed out
@@ -171,8 +174,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F_REGS_HIGH));
     // ---------------- epilogue: one row of F_COLS columns to a thread ----------------
-    const int sub = warp & 3, ew = warp - 2;
+    const int sub = warp & 3, ew = warp - 4;
     const int grp = ew >> 2;
     uint32_t use = 0;
     bool ok = true;
@@ -188,12 +192,18 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       for (int i = 0; i < F_COLS / 2; ++i) sum[i] = make_float2(0.f, 0.f);
       const float* sx = p.sx + (row < p.m ? row : 0);
       const float* sw = p.sw + (live ? col0 / FB : 0) * p.num_k_blocks;
-      float s_next = live ? __ldg(sx) * __ldg(sw) : 0.f;
+      float x0 = __ldg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+      if (p.num_k_blocks > 1) {
+        x1 = __ldg(sx + p.m);
+        w1 = __ldg(sw + 1);
+      }
       for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
         const int acc = use & 1;
-        const float s = s_next;
-        if (live && kb + 1 < p.num_k_blocks)
-          s_next = __ldg(sx + (int64_t)(kb + 1) * p.m) * __ldg(sw + kb + 1);
+        float x2 = 0.f, w2 = 0.f;
+        if (kb + 2 < p.num_k_blocks) {
+          x2 = __ldg(sx + (int64_t)(kb + 2) * p.m);
+          w2 = __ldg(sw + kb + 2);
+        }
         ok = wait_bar(cb, smem_u32(&cb->tmem_full[acc]), (use >> 1) & 1, p.status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -203,19 +213,27 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         if (live) {
           const uint32_t ta =
               tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS + grp * F_COLS;
+          const float s = x0 * w0;
           const float2 s2 = make_float2(s, s);
 #pragma unroll
           for (int c = 0; c < F_COLS / 32; ++c) {
             float v[32];
             tmem_ld32(ta + c * 32, v);
+            if (c == F_COLS / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               sum[c * 16 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, sum[c * 16 + i]);
           }
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+        x0 = x1; w0 = w1;
+        x1 = x2; w1 = w2;
       }
       if (!ok || !live) continue;
       // ---- out: 64 bytes of a row at a time through shared memory ----

@@ -42,6 +42,8 @@ struct LpJoinArgs {
   int64_t cap;
   const int* count;    // [rows] candidates of each row, or null: all cap of them
   const unsigned* gmax;  // [rows x k] group maxima (see lp_head_tc.cu), or null
+  const float* dump;   // [rows x dump_cols] logits of the first columns, or null
+  int64_t dump_cols;
   float* top_logp;     // [bt x k]
   int64_t* top_id;     // [bt x k]
 };
@@ -56,6 +58,7 @@ struct LpRowsArgs {
   float* zy;
   int k;
   int2* cand;          // [rows x parts * k]
+  int* status;         // set to 0, or null
 };
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st);
 
@@ -92,11 +95,15 @@ struct LpHeadArgs {
   unsigned* gmax;      // [m x top], zeroed
   int* count;          // [m], zeroed
   int2* cand;          // [m x parts * top]
+  float* dump;         // [m x 256 dump_blocks] logits of the first 256-column blocks
+  int dump_blocks;
   void* e;             // [m x lde] fp16: 2^t_j relative to each part's maximum, or null
   int64_t lde;
   int* status;
 };
 bool lp_head_supported(const LpHeadArgs& a);
+// Blocks of 256 columns whose logits are best written out instead of listed.
+int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top);
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st);
 
 // Floats as integers in their order (0 is below every value).

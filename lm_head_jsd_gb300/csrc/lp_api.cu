@@ -38,7 +38,8 @@ struct LpLayout {
   int64_t ld, parts, cap;
   // zeroed: status, count, gmax (in one piece, [zero, zero + zero_bytes))
   size_t zero, zero_bytes, status, count, gmax;
-  size_t part, zy, cand, z, dz, acc32, splitk, splitk_bytes, total, logits_bytes, stats_bytes;
+  int dump_blocks;
+  size_t part, zy, cand, dump, z, dz, acc32, splitk, splitk_bytes, total, logits_bytes, stats_bytes;
 };
 
 LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
@@ -64,6 +65,8 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.part = take(rows * L.parts * sizeof(float4));
   L.zy = take(rows * sizeof(float));
   L.cand = take(rows * L.cap * sizeof(int2));
+  L.dump_blocks = fused ? lp_head_dump_blocks(c, p.v, p.h, p.top_k) : 0;
+  L.dump = take(rows * L.dump_blocks * 256 * sizeof(float));
   L.stats_bytes = at;
   // 2^t in fp16 that the backward pass turns into dz in place, or fp32 logits (and their
   // bf16 gradient beside them)
@@ -139,6 +142,8 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     h.gmax = reinterpret_cast<unsigned*>(ws + L.gmax);
     h.count = reinterpret_cast<int*>(ws + L.count);
     h.cand = reinterpret_cast<int2*>(ws + L.cand);
+    h.dump = reinterpret_cast<float*>(ws + L.dump);
+    h.dump_blocks = top ? L.dump_blocks : 0;
     h.e = keep ? ws + L.z : nullptr;
     h.lde = L.ld;
     h.status = reinterpret_cast<int*>(ws + L.status);
@@ -290,6 +295,8 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
     j.cap = L.cap;
     j.count = L.path == kFused ? reinterpret_cast<const int*>(ws + L.count) : nullptr;
     j.gmax = L.path == kFused ? reinterpret_cast<const unsigned*>(ws + L.gmax) : nullptr;
+    j.dump = L.dump_blocks ? reinterpret_cast<const float*>(ws + L.dump) : nullptr;
+    j.dump_cols = (int64_t)L.dump_blocks * 256;
     j.top_logp = top_logp; j.top_id = top_id;
     if (launch_lp_join(j, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   }
@@ -380,8 +387,8 @@ fljsd_status fljsd_logits_lp(int64_t rows, int64_t v, int64_t ld, int32_t dtype,
   if (workspace_bytes < L.total) return FLJSD_ERR_WORKSPACE;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   char* ws = static_cast<char*>(workspace);
-  if (cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   LpRowsArgs r{};
+  r.status = reinterpret_cast<int*>(ws);
   r.z = logits; r.ld = ld; r.v = v; r.rows = rows; r.c = log2_scale(temperature);
   r.labels = labels;
   r.part = reinterpret_cast<float4*>(ws + L.part);

@@ -23,6 +23,10 @@
 // lane's threshold costs one vote. The order in which parts arrive changes how
 // much is skipped, never the result: candidates equal to the threshold are
 // kept, and k_lp_join orders them by value and column.
+// The first columns, whose tiles run before there is a threshold, are not listed:
+// their logits are written out (about one tile for each SM) and k_lp_join reads
+// them against the final threshold. Listing them took longer than their products:
+// 333 rows of H = 2048, V = 40960 with 20 alternatives 150 us, DUMP_US so.
 #include "gemm_tc_kernel.cuh"
 #include "lp.cuh"
 
@@ -49,6 +53,8 @@ struct HeadParams {
   unsigned* gmax;
   int* count;
   int2* cand;
+  float* dump;
+  int dump_blocks;
   unsigned long long timeout_ns;
   int* status;
 };
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t y = p.labels[row];
           if (y >= col0 && y < col0 + ncols) lab = (int)(y - col0);
         }
-        if (KT) {  // the least of the row's group maxima, read from L2
+        if (KT && nb >= p.dump_blocks) {  // the least of the row's group maxima, read from L2
           unsigned least = 0xffffffffu;
           const unsigned* g = p.gmax + row * p.top;
           for (int j = 0; j < p.top; ++j) least = min(least, __ldcg(g + j));
@@ -310,7 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) z = c + e == lab ? v[e] : z;
             if (has) p.zy[row] = z;
           }
-          if (KT) {
+          if (KT && nb < p.dump_blocks) {
+            if (row_ok) {
+              float4* o = reinterpret_cast<float4*>(p.dump + row * p.dump_blocks * BN + col0 + c);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+          } else if (KT) {
             // rows past the last hold zeros and list nothing
             const bool want = row_ok && cm > list.v[KT ? KT - 1 : 0];
             if (__any_sync(0xffffffffu, want)) {
@@ -474,15 +487,41 @@ bool lp_head_supported(const LpHeadArgs& a) {
          a.n < (1ll << 31) - 512 && a.k < (1ll << 31);
 }
 
+namespace {
+struct HeadSchedule {
+  bool pair;
+  int64_t nblocks, m_units, group_m;
+};
+// the schedule rule of launch_gemm_tc (gemm_tc.cu)
+HeadSchedule head_schedule(int64_t m, int64_t n, int64_t k, int64_t sms) {
+  HeadSchedule h;
+  const int64_t mblocks = (m + BM - 1) / BM, clusters = sms >= 2 ? sms / 2 : 1;
+  h.nblocks = (n + BN - 1) / BN;
+  const int64_t waves_one = (mblocks * h.nblocks + sms - 1) / sms;
+  const int64_t waves_pair = ((mblocks + 1) / 2 * h.nblocks + clusters - 1) / clusters;
+  h.pair = mblocks >= 2 && (k + BK - 1) / BK >= 4 && waves_pair * 100 <= waves_one * 112;
+  h.m_units = h.pair ? (mblocks + 1) / 2 : mblocks;
+  // bands of about 32 MB of X, as for the logits product
+  const int64_t gm = (32ll << 20) / ((int64_t)BM * (h.pair ? 2 : 1) * k * 2);
+  h.group_m = gm < 1 ? 1 : gm > h.m_units ? h.m_units : gm;
+  return h;
+}
+}  // namespace
+
+int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top) {
+  if (top == 0 || m <= 0) return 0;
+  const HeadSchedule h = head_schedule(m, n, k, TC_PLAN_CTAS);
+  const int64_t at_once = h.pair ? TC_PLAN_CTAS / 2 : TC_PLAN_CTAS;
+  int64_t blocks = (at_once + h.group_m - 1) / h.group_m;
+  // the threshold needs a part in each of the k groups
+  if (blocks < (top + 1) / 2) blocks = (top + 1) / 2;
+  return (int)(blocks < h.nblocks ? blocks : h.nblocks);
+}
+
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   if (!lp_head_supported(a)) return cudaErrorInvalidValue;
-  const int64_t mblocks = (a.m + BM - 1) / BM, nblocks = (a.n + BN - 1) / BN;
-  // the schedule rule of launch_gemm_tc (gemm_tc.cu)
-  const int64_t sms = num_sms(), clusters = sms >= 2 ? sms / 2 : 1;
-  const int64_t waves_one = (mblocks * nblocks + sms - 1) / sms;
-  const int64_t waves_pair = ((mblocks + 1) / 2 * nblocks + clusters - 1) / clusters;
-  const bool pair = mblocks >= 2 && (a.k + BK - 1) / BK >= 4 && waves_pair * 100 <= waves_one * 112;
-  const bool keep = a.e != nullptr;
+  const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms());
+  const bool pair = h.pair, keep = a.e != nullptr;
   CUtensorMap ma, mb, me;
   if (!tc_make_map(&ma, a.x, a.k, a.m, a.ldx, BK, BM) ||
       !tc_make_map(&mb, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
@@ -491,16 +530,15 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   if (keep && !tc_make_map(&me, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
   HeadParams p{};
   p.m = a.m; p.n = a.n;
-  p.num_n_blocks = (int)nblocks;
+  p.num_n_blocks = (int)h.nblocks;
   p.num_k_blocks = (int)((a.k + BK - 1) / BK);
-  p.m_units = (int)(pair ? (mblocks + 1) / 2 : mblocks);
-  if (p.m_units * nblocks > 0x7fffffff) return cudaErrorInvalidValue;
-  p.num_units = (int)(p.m_units * nblocks);
-  // bands of about 32 MB of X, as for the logits product
-  int64_t gm = (32ll << 20) / ((int64_t)BM * (pair ? 2 : 1) * a.k * 2);
-  p.group_m = (int)(gm < 1 ? 1 : gm > p.m_units ? p.m_units : gm);
+  p.m_units = (int)h.m_units;
+  if (h.m_units * h.nblocks > 0x7fffffff) return cudaErrorInvalidValue;
+  p.num_units = (int)(h.m_units * h.nblocks);
+  p.group_m = (int)h.group_m;
   p.nst = head_stages(pair, keep);
   p.c = a.c; p.labels = a.labels; p.part = a.part; p.parts = a.parts; p.zy = a.zy;
+  p.dump = a.dump; p.dump_blocks = a.dump_blocks;
   p.top = a.top; p.gmax = a.gmax; p.count = a.count; p.cand = a.cand;
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;

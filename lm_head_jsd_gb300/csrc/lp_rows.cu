@@ -25,6 +25,7 @@ constexpr int kList = 512;             // candidates of a segment ranked in shar
 static_assert(LP_MAX_TOP <= kGroups, "the k-th of the groups' maxima");
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
+static_assert(kJoinThreads <= kJoinCap && kJoinThreads >= LP_MAX_TOP, "the threads' largest");
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
 __device__ __forceinline__ float val(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) k_lp_rows(LpRowsArgs a,
   __shared__ float s_thr;
   const int tid = threadIdx.x;
   const int64_t part = blockIdx.x;
+  if (a.status && part == 0 && blockIdx.y == 0 && tid == 0) *a.status = 0;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const T* zr = reinterpret_cast<const T*>(a.z) + r * a.ld;
     const int lead = (int)((((uintptr_t)zr) & 15u) / sizeof(T));
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   __shared__ unsigned long long sh64[W];
   __shared__ unsigned long long list[kJoinCap];
   __shared__ int n_list;
+  __shared__ unsigned sh_least;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x, out = a.row0 + r;
   const float4* ps = a.part + r * a.parts;
@@ -311,14 +314,46 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
     least = 0xffffffffu;
     for (int j = 0; j < a.k; ++j) least = min(least, a.gmax[r * a.k + j]);
   }
-  for (int64_t i = tid; i < n_cand; i += kJoinThreads) {
-    const unsigned long long key = cand_key(cand[i]);
-    if (key != 0 && (unsigned)(key >> 32) >= least) {
-      const int at = atomicAdd(&n_list, 1);
-      if (at < kJoinCap) list[at] = key;
-    }
-  }
+  const float* dump = a.dump + r * a.dump_cols;
+  const int64_t n_dump = a.dump ? (a.dump_cols < a.v ? a.dump_cols : a.v) : 0;
+  auto dump_key = [&](int64_t i) {
+    const float z = dump[i];
+    return z > -INFINITY ? cand_key(make_int2(__float_as_int(z), (int)i)) : 0ull;
+  };
+  // every candidate's key, four loads in flight a thread
+  auto each = [&](auto&& f) {
+#pragma unroll 4
+    for (int64_t i = tid; i < n_cand; i += kJoinThreads) f(cand_key(cand[i]));
+#pragma unroll 4
+    for (int64_t i = tid; i < n_dump; i += kJoinThreads) f(dump_key(i));
+  };
+  auto gather = [&]() {
+    each([&](unsigned long long key) {
+      if (key != 0 && (unsigned)(key >> 32) >= least) {
+        const int at = atomicAdd(&n_list, 1);
+        if (at < kJoinCap) list[at] = key;
+      }
+    });
+  };
+  gather();
   __syncthreads();
+  if (n_list > kJoinCap) {
+    // no threshold, or many equal logits: the k-th largest of the threads' own
+    // largest keys bounds the k-th largest from below, ties apart
+    unsigned long long mine = 0;
+    each([&](unsigned long long key) { mine = key > mine ? key : mine; });
+    __syncthreads();
+    list[tid] = mine;
+    __syncthreads();
+    int rank = 0;
+    for (int j = 0; j < kJoinThreads; ++j) rank += (list[j] > mine || (list[j] == mine && j < tid)) ? 1 : 0;
+    if (rank == a.k - 1) sh_least = (unsigned)(mine >> 32);
+    if (tid == 0) n_list = 0;
+    __syncthreads();
+    least = sh_least;
+    gather();
+    __syncthreads();
+  }
   const int n = n_list;
   const float2 norm = sh_norm;
   float* tl = a.top_logp + out * a.k;
@@ -340,10 +375,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   unsigned long long last = ~0ull;
   for (int q = 0; q < a.k; ++q) {
     unsigned long long best = 0;
-    for (int64_t i = tid; i < n_cand; i += kJoinThreads) {
-      const unsigned long long key = cand_key(cand[i]);
-      best = key < last && key > best ? key : best;
-    }
+    each([&](unsigned long long key) { best = key < last && key > best ? key : best; });
     best = block_max64<W>(best, sh64);
     if (tid == 0) put(q, best);
     last = best;

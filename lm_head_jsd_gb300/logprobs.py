@@ -27,8 +27,9 @@ class Logprobs(NamedTuple):
 
 
 def _results(rows, top_k, with_logp, device) -> Logprobs:
-    f = torch.empty((5, rows), dtype=torch.float32, device=device)
-    return Logprobs(f[3] if with_logp else None, f[4], f[2], f[:2].view(rows, 2),
+    logp, entropy, lse = torch.empty((3, rows), dtype=torch.float32, device=device).unbind()
+    return Logprobs(logp if with_logp else None, entropy, lse,
+                    torch.empty((rows, 2), dtype=torch.float32, device=device),
                     torch.empty((rows, top_k), dtype=torch.float32, device=device) if top_k else None,
                     torch.empty((rows, top_k), dtype=torch.int64, device=device) if top_k else None)
 

@@ -1,6 +1,8 @@
 """AdamW over many tensors in one launch (the C entry point fljsd_adamw_step)."""
 from __future__ import annotations
 
+from operator import attrgetter
+
 import numpy as np
 import torch
 
@@ -15,8 +17,11 @@ _ENTRY = np.dtype([(n, np.uint64) for n in ("grad", "param", "master", "exp_avg"
                   [("n", np.int64)])
 
 
+_DTYPE, _DEVICE = attrgetter("dtype"), attrgetter("device")
+
+
 def _ptrs(ts):
-    return [t.data_ptr() for t in ts]
+    return list(map(torch.Tensor.data_ptr, ts))
 
 
 class AdamW:
@@ -114,24 +119,28 @@ class AdamW:
             self._check("params", self.params, self.dtype, self._sizes)
             self._at = at
             t["param"] = at
-        if None in [g if g is None else 0 for g in grads]:
+        live, sizes = grads, self._sizes
+        if any(g is None for g in grads):
             t = t.copy()
-            t["n"] = [0 if g is None else n for g, n in zip(grads, self._sizes)]
-        live = [g for g in grads if g is not None]
-        if not live:
-            return
+            t["n"] = [0 if g is None else n for g, n in zip(grads, sizes)]
+            live = [g for g in grads if g is not None]
+            sizes = [n for g, n in zip(grads, sizes) if g is not None]
+            if not live:
+                return
         dt, dev = live[0].dtype, self.device
-        if dt not in _DT:
-            raise ValueError(f"gradients have dtype {dt}, expected one of {list(_DT)}")
-        for g, n in zip(grads, self._sizes):
-            if g is not None and (g.numel() != n or g.dtype != dt or g.device != dev
-                                  or not g.is_contiguous()):
-                raise ValueError(f"gradients must be contiguous, of one dtype, on {dev}, and as large "
-                                 "as their parameters")
+        # (whole-list checks: a step of many small tensors is bound by this function)
+        if (dt not in _DT or set(map(_DTYPE, live)) != {dt} or set(map(_DEVICE, live)) != {dev}
+                or not all(map(torch.Tensor.is_contiguous, live))
+                or list(map(torch.Tensor.numel, live)) != sizes):
+            raise ValueError(f"gradients must be contiguous, of one dtype of {list(_DT)}, on {dev}, "
+                             "and as large as their parameters")
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one fp32 value on {dev}")
-        t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
+        if live is grads:
+            t["grad"] = _ptrs(grads)
+        else:
+            t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
         o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay,
                                     self.steps + 1, _DT[self.dtype], _DT[dt], self.state_bits,
                                     int(self.master is not None))
