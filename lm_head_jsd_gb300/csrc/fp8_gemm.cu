@@ -8,10 +8,19 @@
 // stage of the TMA ring (128-byte rows, 128B swizzle) and starts a new accumulator
 // in tensor memory; the two accumulators alternate, so that while the tensor cores
 // form one block's sums, eight warps add the other's, scaled, to 128 fp32 registers
-// a thread (one row, half of the columns: one sw for each thread and block). A scale
-// that is no power of two cannot be applied by the tensor cores, and folding it into
-// the codes would round them again; reading the accumulator back once per block
-// costs 256 of the 512 cycles that its products take.
+// a thread (one row, half of the columns). A scale that is no power of two cannot be
+// applied by the tensor cores, and folding it into the codes would round them again.
+// Scales are read two blocks ahead: their way from L2 is longer than a block's
+// products (read one block ahead: 650 ns a block instead of 572).
+//
+// What bounds it, in ns for each 128 x 256 x 128 block of a tile (4096 x 32768 x
+// 4096): 547 as it is; 457 with the products left out, of which the additions alone
+// are 151; 439 with the accumulators handed back unread; 347 for the products with
+// nothing but the copies' barriers. So the additions' pass over the accumulator,
+// 2.6 cycles for each FFMA2 and about 2 for each column read, sets the pace, and the
+// hand-overs between two accumulators add a fifth. Tried and slower: CTA pairs on
+// 256 x 256 tiles (570), sixteen epilogue warps of 64 columns (598), four
+// accumulators of 128 columns (857), loads of 64 columns at once (667).
 //
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).
@@ -27,17 +36,17 @@ using namespace tcgemm;
 
 constexpr int FB = 128;         // elements of a scale's block, and of a stage's rows
 constexpr int F_UMMA_K = 32;
-constexpr int F_STAGES = 4;
-constexpr int F_STAGE_BYTES = (BM + BN) * FB;
+constexpr int F_ACCS = TMEM_COLS / ACC_COLS;  // accumulators in tensor memory
 constexpr int F_EPI = 8;        // epilogue warps
-constexpr int F_COLS = BN / (F_EPI / 4);  // columns of an epilogue thread
-constexpr int F_OUT_BYTES = 32 * 64;      // an epilogue warp's staging: 32 rows of 64 bytes
+constexpr int F_OUT_BYTES = 32 * 64;  // an epilogue warp's staging: 32 rows of 64 bytes
 // Registers: launched with 168 for each of 12 warps; the four that copy and issue
 // keep 40, the eight epilogue warps take 232 (128 x 40 + 256 x 232 = 384 x 168).
 constexpr int F_REGS_LOW = 40, F_REGS_HIGH = 232;
 constexpr int F_THREADS = 128 + 32 * F_EPI;
+constexpr int F_STAGES = 4;
+constexpr int F_STAGE_BYTES = (BM + BN) * FB;
 constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * F_OUT_BYTES + 1024 + CTRL_BYTES;
-static_assert(F_SMEM <= SMEM_MAX, "shared memory");
+static_assert(F_SMEM <= SMEM_MAX && F_STAGES <= STAGES && F_ACCS == 2, "control block and memory");
 
 // fp32 accumulator, e4m3 operands (format 0), both K-major
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -49,6 +58,40 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate));
+}
+
+// 32 lanes x 32 columns of accumulators, in flight until ld_wait names their registers.
+__device__ __forceinline__ void ld_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+// Every load started by this thread is done (nothing that uses r moves before it).
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void add32(float2* sum, const uint32_t (&r)[32], float s) {
+  const float2 s2 = make_float2(s, s);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    sum[i] = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2,
+                        sum[i]);
 }
 
 struct F8Params {
@@ -79,7 +122,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       mbar_init(smem_u32(&cb->full[s]), 1);
       mbar_init(smem_u32(&cb->empty[s]), 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < F_ACCS; ++a) {
       mbar_init(smem_u32(&cb->tmem_full[a]), 1);
       mbar_init(smem_u32(&cb->tmem_empty[a]), F_EPI);
     }
@@ -112,9 +155,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued_parity[F_STAGES];
-      bool issued[F_STAGES];
-      for (int s = 0; s < F_STAGES; ++s) issued[s] = false;
+      uint32_t filled = 0;  // stages filled since the start
       bool ok = true;
       for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
         int mb, nb;
@@ -129,16 +170,18 @@ __global__ void __launch_bounds__(F_THREADS, 1)
           mbar_arrive_expect_tx(fb, F_STAGE_BYTES);
           tma_load_2d(sa, &tmA, fb, kb * FB, mb * BM);
           tma_load_2d(sa + BM * FB, &tmB, fb, kb * FB, nb * BN);
-          issued[stage] = true;
-          issued_parity[stage] = phase;
+          ++filled;
           if (++stage == F_STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      for (int s = 0; s < F_STAGES; ++s)
-        if (issued[s]) wait_bar(cb, smem_u32(&cb->full[s]), issued_parity[s], p.status);
+      // every copy has landed before the CTA may exit: the last fill of each stage
+      for (int s = 0; s < F_STAGES; ++s) {
+        const uint32_t fills = filled / F_STAGES + ((uint32_t)s < filled % F_STAGES ? 1u : 0u);
+        if (fills > 0) wait_bar(cb, smem_u32(&cb->full[s]), (fills - 1) & 1u, p.status);
+      }
     }
     // ---------------- MMA issuer: one accumulator for each 128-deep block ----------------
     if (warp == 1 && lane == 0) {
@@ -147,21 +190,26 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       uint32_t use = 0;  // accumulators handed out
       bool ok = true;
       for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
-        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
-          const int acc = use & 1;
-          if (!wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use >> 1) & 1) ^ 1u, p.status) ||
-              !wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
+        for (int kb = 0; ok && kb < p.num_k_blocks; ++kb) {
+          if (!wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
             ok = false;
             break;
           }
+          const uint32_t acc = use % F_ACCS;
+          if (!wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use / F_ACCS) & 1u) ^ 1u,
+                             p.status)) {
+            ok = false;
+            break;
+          }
+          ++use;
           tc_fence_after();
-          const uint32_t sa = base + stage * F_STAGE_BYTES;
+          const uint32_t sa = base + stage * F_STAGE_BYTES, sb = sa + BM * FB;
 #pragma unroll
           for (int kk = 0; kk < FB / F_UMMA_K; ++kk)
             mma_e4m3(tmem_base + acc * ACC_COLS, smem_desc(sa + kk * F_UMMA_K, 16, 1024),
-                     smem_desc(sa + BM * FB + kk * F_UMMA_K, 16, 1024), kk > 0 ? 1u : 0u);
-          mma_commit<false>(smem_u32(&cb->empty[stage]));
+                           smem_desc(sb + kk * F_UMMA_K, 16, 1024), kk > 0 ? 1u : 0u);
           mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
+          mma_commit<false>(smem_u32(&cb->empty[stage]));
           if (++stage == F_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -175,70 +223,81 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F_REGS_HIGH));
-    // ---------------- epilogue: one row of F_COLS columns to a thread ----------------
+    // ---------------- epilogue: one row of 128 columns to a thread ----------------
     const int sub = warp & 3, ew = warp - 4;
     const int grp = ew >> 2;
     uint32_t use = 0;
     bool ok = true;
     uint8_t* srow0 = stg + ew * F_OUT_BYTES;
+    const uint32_t tsub = tmem_base + ((uint32_t)(sub * 32) << 16) + grp * 128;
+    uint32_t ra[32], rb[32];  // two loads take turns: one in flight while the other is added
+    auto full = [&]() {
+      ok = wait_bar(cb, smem_u32(&cb->tmem_full[use % F_ACCS]), (use / F_ACCS) & 1u, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    };
+    auto hand_back = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[use % F_ACCS]));
+      ++use;
+    };
     for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
       int mb, nb;
       tile_coords(t, mb, nb);
       const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
-      const int64_t col0 = (int64_t)nb * BN + grp * F_COLS;
+      const int64_t col0 = (int64_t)nb * BN + grp * 128;
       const bool live = row0 < p.m && col0 < p.n;  // of this warp
-      float2 sum[F_COLS / 2];
-#pragma unroll
-      for (int i = 0; i < F_COLS / 2; ++i) sum[i] = make_float2(0.f, 0.f);
-      const float* sx = p.sx + (row < p.m ? row : 0);
-      const float* sw = p.sw + (live ? col0 / FB : 0) * p.num_k_blocks;
-      float x0 = __ldg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
-      if (p.num_k_blocks > 1) {
-        x1 = __ldg(sx + p.m);
-        w1 = __ldg(sw + 1);
+      if (!live) {
+        for (int kb = 0; ok && kb < p.num_k_blocks; ++kb) {
+          full();
+          if (ok) hand_back();
+        }
+        continue;
       }
-      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
-        const int acc = use & 1;
-        float x2 = 0.f, w2 = 0.f;
-        if (kb + 2 < p.num_k_blocks) {
-          x2 = __ldg(sx + (int64_t)(kb + 2) * p.m);
-          w2 = __ldg(sw + kb + 2);
-        }
-        ok = wait_bar(cb, smem_u32(&cb->tmem_full[acc]), (use >> 1) & 1, p.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (live) {
-          const uint32_t ta =
-              tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS + grp * F_COLS;
-          const float s = x0 * w0;
-          const float2 s2 = make_float2(s, s);
+      float2 sum[64];
 #pragma unroll
-          for (int c = 0; c < F_COLS / 32; ++c) {
-            float v[32];
-            tmem_ld32(ta + c * 32, v);
-            if (c == F_COLS / 32 - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              sum[c * 16 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, sum[c * 16 + i]);
-          }
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
+      for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+      // scales of this block and the next two, x's of this row and w's of these columns
+      const float* sx = p.sx + (row < p.m ? row : 0);
+      const float* sw = p.sw + col0 / FB * p.num_k_blocks;
+      const int last = p.num_k_blocks - 1;
+      float x0 = __ldg(sx), w0 = __ldg(sw);
+      float x1 = __ldg(sx + (int64_t)min(1, last) * p.m), w1 = __ldg(sw + min(1, last));
+      full();
+      if (!ok) break;
+      ld_start(tsub + (use % F_ACCS) * ACC_COLS, ra);
+      for (int kb = 0; kb <= last; ++kb) {
+        const int k2 = min(kb + 2, last);
+        const float x2 = __ldg(sx + (int64_t)k2 * p.m), w2 = __ldg(sw + k2);
+        const uint32_t ta = tsub + (use % F_ACCS) * ACC_COLS;
+        const float s = x0 * w0;
+        ld_wait(ra);
+        ld_start(ta + 32, rb);
+        add32(sum, ra, s);
+        ld_wait(rb);
+        ld_start(ta + 64, ra);
+        add32(sum + 16, rb, s);
+        ld_wait(ra);
+        ld_start(ta + 96, rb);
+        add32(sum + 32, ra, s);
+        ld_wait(rb);
+        hand_back();
+        if (kb < last) {
+          full();
+          if (!ok) break;
+          ld_start(tsub + (use % F_ACCS) * ACC_COLS, ra);
         }
+        add32(sum + 48, rb, s);
         x0 = x1; w0 = w1;
         x1 = x2; w1 = w2;
       }
-      if (!ok || !live) continue;
+      if (!ok) break;
       // ---- out: 64 bytes of a row at a time through shared memory ----
 #pragma unroll
-      for (int c = 0; c < F_COLS / COLS; ++c) {
+      for (int c = 0; c < 128 / COLS; ++c) {
+        const int64_t cc = col0 + c * COLS;
+        if (cc >= p.n) break;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
         uint4* srow = reinterpret_cast<uint4*>(srow0 + lane * 64);
@@ -252,12 +311,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             srow[u] = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y),
                                  __float_as_uint(q[1].x), __float_as_uint(q[1].y));
         }
-        const int64_t cc = col0 + c * COLS;
         if (p.use_tma) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (cc < p.n) tma_store_2d(&tmO, smem_u32(srow0), (int32_t)cc, (int32_t)row0);
+            tma_store_2d(&tmO, smem_u32(srow0), (int32_t)cc, (int32_t)row0);
             bulk_commit();
           }
         } else {
@@ -474,7 +532,8 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
   p.num_k_blocks = (int)L.blocks;
   p.m_units = (int)mblocks;
   p.num_units = (int)(mblocks * nblocks);
-  int64_t gm = (32ll << 20) / ((int64_t)BM * k);  // bands of about 32 MB of x, as for bf16
+  // bands of about 32 MB of x, as for bf16
+  const int64_t gm = (32ll << 20) / ((int64_t)BM * k);
   p.group_m = (int)(gm < 1 ? 1 : gm > mblocks ? mblocks : gm);
   p.sx = sx; p.sw = w_scales; p.out = out; p.ldo = ldo;
   p.use_tma = aligned(out, 16) && (ldo * dsize(out_dtype)) % 16 == 0 && (n * dsize(out_dtype)) % 16 == 0;
@@ -495,11 +554,12 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
                  out_dtype == FLJSD_BF16, status};
   cudaError_t e;
   trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
+  const bool b16 = out_dtype == FLJSD_BF16;
   if (skinny_supported(few))
     e = launch_skinny(few, st);
   else
-    e = out_dtype == FLJSD_BF16 ? launch_product<__nv_bfloat16>(ma, mb, mo, p, st)
-                                                : launch_product<float>(ma, mb, mo, p, st);
+    e = b16 ? launch_product<__nv_bfloat16>(ma, mb, mo, p, st)
+            : launch_product<float>(ma, mb, mo, p, st);
   trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
   return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
 }
