@@ -6,8 +6,10 @@
 //   lse = m / T + ln2 log2 d,  log p_j = ln2 (t_j - log2 d),
 //   entropy = -sum p_j log p_j = ln2 (log2 d - s / d).
 // A row is cut into parts (128 columns of a product's tile, or a segment of
-// given logits); each part writes (m, d, s) and at most k candidates for the
-// row's k largest logits, and k_lp_join combines them. The entropy comes from
+// given logits); each part writes (m, d, s), and k_lp_join combines them. For the k
+// largest it has, from the product, at most k candidates of each part, and from given
+// logits the maximum of each 1024 of them: the k-th largest of those maxima says
+// which few have to be read again. The entropy comes from
 // sums centred on the maximum: lse - sum p_j s_j would cancel all digits of a
 // peaked row. The difference z - m is taken before the scale, so that a row of
 // the type's lowest value (a mask that leaves nothing) does not overflow, and
@@ -22,6 +24,7 @@ namespace fljsd {
 constexpr int LP_MAX_TOP = 32;
 constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product
 constexpr int LP_SEG = 8192;       // elements of a part of given logits
+constexpr int LP_CHUNKS = 8;       // maxima kept of each such part
 // Parts of a row of given logits: segments are counted from the 16-byte boundary
 // at or before the row, so a row that starts off one may need one part more.
 inline int64_t lp_row_parts(int64_t v) { return (v + 7 + LP_SEG - 1) / LP_SEG; }
@@ -38,12 +41,18 @@ struct LpJoinArgs {
   float *logp, *entropy, *lse;  // [bt]; logp null without labels
   float2* norm;        // [bt] (m, log2 d)
   int k;
-  const int2* cand;    // [rows x cap] (value bits, column); column < 0: none
+  // from the product:
+  const int2* cand;    // [rows x cap] (value bits, column)
   int64_t cap;
-  const int* count;    // [rows] candidates of each row, or null: all cap of them
-  const unsigned* gmax;  // [rows x k] group maxima (see lp_head_tc.cu), or null
+  const int* count;    // [rows] candidates of each row
+  const unsigned* gmax;  // [rows x k] group maxima (see lp_head_tc.cu)
   const float* dump;   // [rows x dump_cols] logits of the first columns, or null
   int64_t dump_cols;
+  // from given logits:
+  const void* z;       // [rows x ld], or null
+  int z_dtype;
+  int64_t ld;
+  const float* cmax;   // [rows x parts * LP_CHUNKS]
   float* top_logp;     // [bt x k]
   int64_t* top_id;     // [bt x k]
 };
@@ -56,8 +65,7 @@ struct LpRowsArgs {
   const int64_t* labels;
   float4* part;        // [rows x parts], parts = lp_row_parts(v)
   float* zy;
-  int k;
-  int2* cand;          // [rows x parts * k]
+  float* cmax;         // [rows x parts * LP_CHUNKS], or null
   int* status;         // set to 0, or null
 };
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st);

@@ -39,7 +39,7 @@ struct LpLayout {
   // zeroed: status, count, gmax (in one piece, [zero, zero + zero_bytes))
   size_t zero, zero_bytes, status, count, gmax;
   int dump_blocks;
-  size_t part, zy, cand, dump, z, dz, acc32, splitk, splitk_bytes, total, logits_bytes, stats_bytes;
+  size_t part, zy, cand, cmax, dump, z, dz, acc32, splitk, splitk_bytes, total, logits_bytes, stats_bytes;
 };
 
 LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
@@ -64,7 +64,8 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.zero_bytes = at - L.zero;
   L.part = take(rows * L.parts * sizeof(float4));
   L.zy = take(rows * sizeof(float));
-  L.cand = take(rows * L.cap * sizeof(int2));
+  L.cand = take(fused ? rows * L.cap * sizeof(int2) : 0);
+  L.cmax = take(!fused && p.top_k ? rows * L.parts * LP_CHUNKS * sizeof(float) : 0);
   L.dump_blocks = fused ? lp_head_dump_blocks(c, p.v, p.h, p.top_k) : 0;
   L.dump = take(rows * L.dump_blocks * 256 * sizeof(float));
   L.stats_bytes = at;
@@ -171,8 +172,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
   r.z = z; r.ld = L.ld; r.v = p.v; r.rows = rows; r.c = c; r.labels = labels;
   r.part = reinterpret_cast<float4*>(ws + L.part);
   r.zy = reinterpret_cast<float*>(ws + L.zy);
-  r.k = top;
-  r.cand = reinterpret_cast<int2*>(ws + L.cand);
+  r.cmax = top ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
   return launch_lp_rows(FLJSD_F32, r, st);
 }
 
@@ -189,15 +189,15 @@ fljsd_status lp_plan_check(const fljsd_lp_problem* p, const fljsd_plan_t* plan,
 
 struct LogitsLayout {
   int64_t parts;
-  size_t part, zy, cand, total;
+  size_t part, zy, cmax, total;
 };
 LogitsLayout logits_layout(int64_t rows, int64_t v, int k) {
   LogitsLayout L{};
   L.parts = lp_row_parts(v);
   L.part = kAlign;  // after the status word
   L.zy = L.part + align_up((size_t)rows * L.parts * sizeof(float4));
-  L.cand = L.zy + align_up((size_t)rows * sizeof(float));
-  L.total = L.cand + align_up((size_t)rows * L.parts * k * sizeof(int2));
+  L.cmax = L.zy + align_up((size_t)rows * sizeof(float));
+  L.total = L.cmax + (k > 0 ? align_up((size_t)rows * L.parts * LP_CHUNKS * sizeof(float)) : 0);
   return L;
 }
 
@@ -291,12 +291,17 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
     j.status = reinterpret_cast<int*>(ws + L.status);
     j.logp = logp; j.entropy = entropy; j.lse = lse; j.norm = reinterpret_cast<float2*>(norm);
     j.k = p->top_k;
-    j.cand = reinterpret_cast<const int2*>(ws + L.cand);
-    j.cap = L.cap;
-    j.count = L.path == kFused ? reinterpret_cast<const int*>(ws + L.count) : nullptr;
-    j.gmax = L.path == kFused ? reinterpret_cast<const unsigned*>(ws + L.gmax) : nullptr;
-    j.dump = L.dump_blocks ? reinterpret_cast<const float*>(ws + L.dump) : nullptr;
-    j.dump_cols = (int64_t)L.dump_blocks * 256;
+    if (L.path == kFused) {
+      j.cand = reinterpret_cast<const int2*>(ws + L.cand);
+      j.cap = L.cap;
+      j.count = reinterpret_cast<const int*>(ws + L.count);
+      j.gmax = reinterpret_cast<const unsigned*>(ws + L.gmax);
+      j.dump = L.dump_blocks ? reinterpret_cast<const float*>(ws + L.dump) : nullptr;
+      j.dump_cols = (int64_t)L.dump_blocks * 256;
+    } else {
+      j.z = ws + L.z; j.z_dtype = FLJSD_F32; j.ld = L.ld;
+      j.cmax = reinterpret_cast<const float*>(ws + L.cmax);
+    }
     j.top_logp = top_logp; j.top_id = top_id;
     if (launch_lp_join(j, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   }
@@ -393,8 +398,7 @@ fljsd_status fljsd_logits_lp(int64_t rows, int64_t v, int64_t ld, int32_t dtype,
   r.labels = labels;
   r.part = reinterpret_cast<float4*>(ws + L.part);
   r.zy = reinterpret_cast<float*>(ws + L.zy);
-  r.k = top_k;
-  r.cand = reinterpret_cast<int2*>(ws + L.cand);
+  r.cmax = top_k > 0 ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
   if (launch_lp_rows(dtype, r, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   LpJoinArgs j{};
   j.rows = rows; j.v = v; j.part = r.part; j.parts = L.parts; j.c = r.c; j.inv_t = 1.f / temperature;
@@ -402,7 +406,7 @@ fljsd_status fljsd_logits_lp(int64_t rows, int64_t v, int64_t ld, int32_t dtype,
   j.labels = labels; j.ignore_index = ignore_index;
   j.status = reinterpret_cast<int*>(ws);
   j.logp = logp; j.entropy = entropy; j.lse = lse; j.norm = reinterpret_cast<float2*>(norm);
-  j.k = top_k; j.cand = r.cand; j.cap = L.parts * top_k;
+  j.k = top_k; j.z = logits; j.z_dtype = dtype; j.ld = ld; j.cmax = r.cmax;
   j.top_logp = top_logp; j.top_id = top_id;
   return launch_lp_join(j, stream) == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
 }

@@ -15,14 +15,15 @@
 // (bf16 here made the gradients' error 1.5 times that of one rounding, fp16 1.4).
 // Keeping the logits instead would need fp32 for the same error.
 //
-// The k largest: every thread keeps a sorted list of its part in registers. What
-// keeps this rare is a threshold for each row: the parts are dealt into k groups
-// (part index mod k), gmax[row][g] is the largest logit seen in group g, and at
-// least k logits of the row reach the least of the k group maxima, so anything
-// below it can be skipped. A chunk of 32 columns whose maximum is below every
-// lane's threshold costs one vote. The order in which parts arrive changes how
-// much is skipped, never the result: candidates equal to the threshold are
-// kept, and k_lp_join orders them by value and column.
+// The k largest: what reaches the row's threshold is appended to the row's
+// candidates. The threshold: the parts are dealt into k groups (part index mod k),
+// gmax[row][g] is the largest logit seen in group g, and at least k logits of the
+// row reach the least of the k group maxima. A chunk of 32 columns whose maximum is
+// below every lane's threshold costs one vote. Where more than k of a part's logits
+// reach it (equal logits, or a threshold that came late), its k largest are found
+// with a sorted list in registers (list_part). The order in which parts arrive
+// changes how much is skipped, never the result: candidates equal to the threshold
+// are kept, and k_lp_join orders them by value and column.
 // The first columns, whose tiles run before there is a threshold, are not listed:
 // their logits are written out (about one tile for each SM) and k_lp_join reads
 // them against the final threshold. Listing them took longer than their products:
@@ -111,7 +112,37 @@ __device__ __forceinline__ float below(unsigned key) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-template <bool PAIR, int KT, bool KEEP>
+// The `top` largest of a part for the lanes with `mine` (a warp's, all its lanes
+// together), appended to their rows' candidates. Out of line: rare, and its list
+// would take the registers of the loop around it.
+static __device__ __noinline__ void list_part(uint32_t tacc, int ncols, int col0, int top, bool mine,
+                                              int* count, int2* cand) {
+  TopList<LP_MAX_TOP> list;
+  list.clear(-INFINITY);
+#pragma unroll 1
+  for (int c = 0; c < ncols; c += 32) {
+    float v[32];
+    tmem_ld32(tacc + c, v);
+#pragma unroll 1
+    for (int e = 0; e < 32; ++e) {
+      float x = v[0];
+#pragma unroll
+      for (int i = 0; i + 1 < 32; ++i) v[i] = v[i + 1];  // v[e] in front, without an index
+      if (mine && c + e < ncols && x > list.v[LP_MAX_TOP - 1]) list.insert(x, col0 + c + e);
+    }
+  }
+  if (mine) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < LP_MAX_TOP; ++j) n += (j < top && list.id[j] >= 0) ? 1 : 0;
+    int2* dst = cand + atomicAdd(count, n);
+#pragma unroll
+    for (int j = 0; j < LP_MAX_TOP; ++j)
+      if (j < n) dst[j] = make_int2(__float_as_int(list.v[j]), list.id[j]);
+  }
+}
+
+template <bool PAIR, bool TOP, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     k_lp_head(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmE, const HeadParams p) {
@@ -257,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ew = warp - 2;
     int local = 0;
     int sbuf = 0;
-    TopList<KT ? KT : 1> list;
     for (int t = unit0; t < p.num_units; t += unit_step, ++local) {
       int mb, nb;
       tile_coords(t, mb, nb);
@@ -268,19 +298,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ncols = (int)min((int64_t)LP_PART_COLS, p.n - col0);
       const bool live = row0 < p.m && ncols > 0;  // of this warp
       int lab = -1;
-      float thr = -INFINITY;
       if (live && row_ok) {
         if (p.labels) {
           const int64_t y = p.labels[row];
           if (y >= col0 && y < col0 + ncols) lab = (int)(y - col0);
         }
-        if (KT && nb >= p.dump_blocks) {  // the least of the row's group maxima, read from L2
-          unsigned least = 0xffffffffu;
-          const unsigned* g = p.gmax + row * p.top;
-          for (int j = 0; j < p.top; ++j) least = min(least, __ldcg(g + j));
-          thr = below(least);
-        }
       }
+      const bool listed = TOP && live && nb >= p.dump_blocks;
+      // the least of the row's group maxima, read from L2 (0: a group has none yet)
+      auto least = [&]() {
+        unsigned l = 0xffffffffu;
+        if (row_ok)
+          for (int j = 0; j < p.top; ++j) l = min(l, __ldcg(p.gmax + row * p.top + j));
+        return l;
+      };
+      unsigned low = listed ? least() : 0xffffffffu;
       bool ok = true;
       if (lane == 0) {
         ok = wait_bar<PAIR>(cb, smem_u32(&cb->tmem_full[acc]), (local >> 1) & 1, p.status);
@@ -291,58 +323,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (live) {
+        // (the tiles that fill the groups may have ended since)
+        if (listed && __any_sync(0xffffffffu, low == 0)) low = least();
         const uint32_t tacc = tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS +
                               grp * LP_PART_COLS;
-        // ---- the maximum, the label's logit, the candidates ----
+        // ---- the maximum and the label's logit; the columns that reach thr ----
         float mx = -INFINITY;
-        if (KT) list.clear(thr);
+        unsigned hit[4] = {0u, 0u, 0u, 0u};  // by chunk of 32 columns
+        auto scan = [&](float thr, bool again) {
 #pragma unroll 1
-        for (int c = 0; c < ncols; c += 32) {
-          float v[32];
-          tmem_ld32(tacc + c, v);
-          if (ncols - c < 32) {
+          for (int c = 0; c < ncols; c += 32) {
+            float v[32];
+            tmem_ld32(tacc + c, v);
+            if (ncols - c < 32) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e >= ncols) v[e] = -INFINITY;
-          }
-          float cm = v[0];
-#pragma unroll
-          for (int e = 1; e < 32; ++e) cm = fmaxf(cm, v[e]);
-          mx = fmaxf(mx, cm);
-          const bool has = lab >= c && lab < c + 32;
-          if (__any_sync(0xffffffffu, has)) {
-            float z = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) z = c + e == lab ? v[e] : z;
-            if (has) p.zy[row] = z;
-          }
-          if (KT && nb < p.dump_blocks) {
-            if (row_ok) {
-              float4* o = reinterpret_cast<float4*>(p.dump + row * p.dump_blocks * BN + col0 + c);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              for (int e = 0; e < 32; ++e)
+                if (c + e >= ncols) v[e] = -INFINITY;
             }
-          } else if (KT) {
-            // rows past the last hold zeros and list nothing
-            const bool want = row_ok && cm > list.v[KT ? KT - 1 : 0];
-            if (__any_sync(0xffffffffu, want)) {
-              float mem[32];  // indexed by the loop: in local memory
+            float cm = v[0];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mem[e] = v[e];
-              unsigned left = 0;
+            for (int e = 1; e < 32; ++e) cm = fmaxf(cm, v[e]);
+            mx = fmaxf(mx, cm);
+            const bool has = lab >= c && lab < c + 32;
+            if (!again && __any_sync(0xffffffffu, has)) {
+              float z = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) left |= (want && v[e] > list.v[KT ? KT - 1 : 0]) ? 1u << e : 0u;
-#pragma unroll 1
-              while (__any_sync(0xffffffffu, left != 0)) {
-                if (left) {
-                  const int e = __ffs(left) - 1;
-                  left &= left - 1;
-                  list.insert(mem[e], col0 + c + e);
-                }
+              for (int e = 0; e < 32; ++e) z = c + e == lab ? v[e] : z;
+              if (has) p.zy[row] = z;
+            }
+            if (listed) {
+              // rows past the last hold zeros and list nothing
+              const bool want = row_ok && cm > thr;
+              if (again || __any_sync(0xffffffffu, want)) {
+                unsigned w = 0;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w |= v[e] > thr ? 1u << e : 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (c == q * 32) hit[q] = want ? w : 0u;
               }
             }
           }
+        };
+        auto hits = [&]() { return __popc(hit[0]) + __popc(hit[1]) + __popc(hit[2]) + __popc(hit[3]); };
+        scan(listed ? below(low) : -INFINITY, false);
+        const int part = nb * 2 + grp;
+        // (at once: the tiles that come next are waiting for a threshold)
+        if (TOP && row_ok && mx > -INFINITY)
+          atomicMax(p.gmax + row * p.top + part % p.top, lp_key(mx));
+        int2* dst = nullptr;
+        if (listed) {
+          int n = hits();
+          if (__any_sync(0xffffffffu, n > p.top)) {  // the threshold may have risen since
+            scan(below(least()), true);
+            n = hits();
+          }
+          const bool many = n > p.top;
+          int2* cand = p.cand + (row_ok ? row : 0) * p.parts * p.top;
+          if (__any_sync(0xffffffffu, many)) {
+            list_part(tacc, ncols, col0, p.top, many, p.count + (row_ok ? row : 0), cand);
+            if (many) hit[0] = hit[1] = hit[2] = hit[3] = 0u;
+          }
+          if (n > 0 && !many) dst = cand + atomicAdd(p.count + row, n);
         }
         // ---- sums relative to the maximum ----
         const float ref = mx == -INFINITY ? 0.f : mx;
@@ -356,6 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c + e >= ncols) v[e] = -INFINITY;
+          }
+          if (TOP && !listed) {
+            if (row_ok) {
+              float4* o = reinterpret_cast<float4*>(p.dump + row * p.dump_blocks * BN + col0 + c);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+          } else if (TOP) {
+            unsigned w = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w = c == q * 32 ? hit[q] : w;
+            if (__any_sync(0xffffffffu, w != 0)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (w >> e & 1) *dst++ = make_int2(__float_as_int(v[e]), col0 + c + e);
+            }
           }
           if (KEEP && (c & 32) == 0) {
             // the store that last used this buffer has read it
@@ -394,22 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (row_ok) {
-          const int part = nb * 2 + grp;
           p.part[row * p.parts + part] =
               make_float4(mx, d.x + d.y, s.x + s.y, 0.f);
-          if (KT) {
-            if (mx > -INFINITY) atomicMax(p.gmax + row * p.top + part % p.top, lp_key(mx));
-            int cnt = 0;
-#pragma unroll
-            for (int j = 0; j < KT; ++j) cnt += (j < p.top && list.id[j] >= 0) ? 1 : 0;
-            if (cnt) {
-              const int64_t cap = p.parts * p.top;
-              int2* dst = p.cand + row * cap + atomicAdd(p.count + row, cnt);
-#pragma unroll
-              for (int j = 0; j < KT; ++j)
-                if (j < cnt) dst[j] = make_int2(__float_as_int(list.v[j]), list.id[j]);
-            }
-          }
         }
       }
       tc_fence_before();
@@ -434,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool PAIR, int KT, bool KEEP>
+template <bool PAIR, bool TOP, bool KEEP>
 cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
                      const HeadParams& p, cudaStream_t st) {
-  auto kern = k_lp_head<PAIR, KT, KEEP>;
+  auto kern = k_lp_head<PAIR, TOP, KEEP>;
   const int smem = head_smem(p.nst, PAIR, KEEP);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
   if (e != cudaSuccess) return e;
@@ -473,9 +518,8 @@ cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
 template <bool PAIR, bool KEEP>
 cudaError_t launch_k(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
                      const HeadParams& p, cudaStream_t st) {
-  if (p.top == 0) return launch_v<PAIR, 0, KEEP>(ma, mb, me, p, st);
-  if (p.top <= 8) return launch_v<PAIR, 8, KEEP>(ma, mb, me, p, st);
-  return launch_v<PAIR, LP_MAX_TOP, KEEP>(ma, mb, me, p, st);
+  return p.top ? launch_v<PAIR, true, KEEP>(ma, mb, me, p, st)
+               : launch_v<PAIR, false, KEEP>(ma, mb, me, p, st);
 }
 
 }  // namespace

@@ -1,15 +1,18 @@
 // Token log probabilities: parts of given logits, the join of a row's parts,
 // and the gradient in the logits. The formulas are in lp.cuh.
 //
-// k_lp_rows cuts each row into segments of 8192 logits, one CTA each: the
-// segment stays in registers (32 values a thread) between the maximum, the sums
-// and the candidates, so logits are read once whatever k is, and a single row
-// of 128256 still runs on 16 CTAs. k_lp_grad is elementwise. Both are bound by
-// HBM.
+// k_lp_rows cuts each row into segments of 8192 logits, one CTA each, so that a
+// single row of 128256 still runs on 16 CTAs; the next row's segment is on its way
+// while one is reduced. The k largest are left to k_lp_join, which reads again the
+// few 1024s whose maxima reach the k-th largest of them (choosing candidates here
+// took three times as long as the sums). k_lp_grad is elementwise. Both are bound by
+// HBM: ROWS_FIGURES.
 #include "lp.cuh"
 #include "jsd_math.cuh"
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 namespace fljsd {
 namespace {
@@ -20,36 +23,18 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = LP_SEG / kThreads;  // logits a thread holds
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kGroups = kThreads / 4;  // groups of threads whose maxima are ranked
-constexpr int kList = 512;             // candidates of a segment ranked in shared memory
-static_assert(LP_MAX_TOP <= kGroups, "the k-th of the groups' maxima");
-constexpr int kJoinThreads = 256;
+static_assert(kWarps == LP_CHUNKS, "a maximum for each warp");
+// Threads of a row's join: few rows are bound by one CTA's way through its loads,
+// many by how many CTAs an SM holds (JOIN_FIGURES).
+constexpr int kJoinFew = 512, kJoinMany = 128;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
-static_assert(kJoinThreads <= kJoinCap && kJoinThreads >= LP_MAX_TOP, "the threads' largest");
+static_assert(kJoinFew <= kJoinCap && kJoinMany >= LP_MAX_TOP, "the threads' largest");
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
 __device__ __forceinline__ float val(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float val(const __half* p) { return __half2float(*p); }
 
 // Eight values, 16-byte aligned.
-__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-  o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&o)[8]) {
-  Vec<__nv_bfloat16>::load(p, o);
-}
-__device__ __forceinline__ void load8(const __half* p, float (&o)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    o[2 * i] = f.x;
-    o[2 * i + 1] = f.y;
-  }
-}
 __device__ __forceinline__ void store8(float* p, const float (&o)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
@@ -57,6 +42,88 @@ __device__ __forceinline__ void store8(float* p, const float (&o)[8]) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&o)[8]) {
   Vec<__nv_bfloat16>::store(p, o);
 }
+
+// 16 bytes of logits as they lie in memory, and their values.
+template <typename T>
+struct Raw {
+  uint4 w;
+};
+template <typename T>
+__device__ __forceinline__ void values(const Raw<T>& q, float* z);
+template <>
+__device__ __forceinline__ void values(const Raw<float>& q, float* z) {
+  z[0] = __uint_as_float(q.w.x);
+  z[1] = __uint_as_float(q.w.y);
+  z[2] = __uint_as_float(q.w.z);
+  z[3] = __uint_as_float(q.w.w);
+}
+template <>
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16>& q, float* z) {
+  const uint32_t w[4] = {q.w.x, q.w.y, q.w.z, q.w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    z[2 * i] = __uint_as_float(w[i] << 16);
+    z[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void values(const Raw<__half>& q, float* z) {
+  const uint32_t w[4] = {q.w.x, q.w.y, q.w.z, q.w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    z[2 * i] = f.x;
+    z[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint32_t bits_of(const float* p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+__device__ __forceinline__ uint32_t bits_of(const __half* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+// The 16 bytes at element j of a segment whose elements [first, n) exist; the others
+// read as `none` (the bits of one element).
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* zs, int j, int first, int n, uint32_t none) {
+  constexpr int N = 16 / sizeof(T);
+  Raw<T> q;
+  if (j >= first && j + N <= n) {
+    q.w = *reinterpret_cast<const uint4*>(zs + j);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 4) {
+        w[i] = j + i >= first && j + i < n ? bits_of(zs + j + i) : none;
+      } else {
+        const int a = j + 2 * i, b = a + 1;
+        w[i] = (a >= first && a < n ? bits_of(zs + a) : none) |
+               ((b >= first && b < n ? bits_of(zs + b) : none) << 16);
+      }
+    }
+    q.w = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return q;
+}
+
+// Where a segment of a row lies: elements [first, n) of zs, which starts on a 16-byte
+// boundary (lead elements before the row in its first segment).
+template <typename T>
+struct Segment {
+  const T* zs;
+  int64_t e0;  // the row's element at zs
+  int first, n;
+  __device__ __forceinline__ Segment(const void* z, int64_t ld, int64_t r, int64_t v, int64_t part) {
+    const T* zr = reinterpret_cast<const T*>(z) + r * ld;
+    const int lead = (int)((((uintptr_t)zr) & 15u) / sizeof(T));
+    e0 = part * LP_SEG - lead;
+    n = (int)(v - e0 < LP_SEG ? (v > e0 ? v - e0 : 0) : LP_SEG);
+    first = e0 < 0 ? lead : 0;
+    zs = zr + e0;
+  }
+};
 
 // Value first, then the lower column: one key for each candidate.
 __device__ __forceinline__ unsigned long long cand_key(int2 c) {
@@ -127,125 +194,67 @@ __device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
 // first element may lie anywhere) and the one that crosses its end are read one
 // element at a time. Sums are taken relative to each thread's own maximum, so
 // that one reduction serves maximum and sums.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) k_lp_rows(LpRowsArgs a, int64_t parts) {
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(LpRowsArgs a, int64_t parts) {
   constexpr int N = Vec<T>::N;
   constexpr int V = kPer / N;
   __shared__ Mds shm[kWarps];
-  __shared__ unsigned long long sh64[kWarps];
-  __shared__ float gmax[kGroups];
-  __shared__ unsigned long long list[kList];
-  __shared__ int n_list;
-  __shared__ float s_thr;
   const int tid = threadIdx.x;
   const int64_t part = blockIdx.x;
+  constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80u;  // -inf
   if (a.status && part == 0 && blockIdx.y == 0 && tid == 0) *a.status = 0;
+  Raw<T> raw[V];
+  auto load = [&](int64_t r) {
+    const Segment<T> g(a.z, a.ld, r, a.v, part);
+#pragma unroll
+    for (int u = 0; u < V; ++u) raw[u] = load_raw(g.zs, (u * kThreads + tid) * N, g.first, g.n, kNone);
+  };
+  if (blockIdx.y < a.rows) load(blockIdx.y);
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    const T* zr = reinterpret_cast<const T*>(a.z) + r * a.ld;
-    const int lead = (int)((((uintptr_t)zr) & 15u) / sizeof(T));
-    const int64_t e0 = part * LP_SEG - lead;  // first element, may be before the row
-    const int n = (int)(a.v - e0 < LP_SEG ? (a.v > e0 ? a.v - e0 : 0) : LP_SEG);
-    const int first = e0 < 0 ? lead : 0;      // elements [first, n) of the segment count
-    const T* zs = zr + e0;
     float z[kPer];
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int j = (u * kThreads + tid) * N;
-      if (j >= first && j + N <= n) {
-        float o[N];
-        Vec<T>::load(zs + j, o);
-#pragma unroll
-        for (int e = 0; e < N; ++e) z[u * N + e] = o[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          z[u * N + e] = (j + e >= first && j + e < n) ? val(zs + j + e) : -INFINITY;
-      }
-    }
+    for (int u = 0; u < V; ++u) values(raw[u], z + u * N);
+    // the next row's segment is on its way while this one is reduced
+    if (r + gridDim.y < a.rows) load(r + gridDim.y);
     Mds x{-INFINITY, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kPer; ++i) x.m = fmaxf(x.m, z[i]);  // (skips NaN)
     {
+      // t = c z - c ref in one operation: c ref = hi + lo, hi rounded, and the sums
+      // are put right for lo once (2^-lo, and s - lo d)
       const float ref = x.m == -INFINITY ? 0.f : x.m;
-      const float2 c2 = make_float2(a.c, a.c), nref = make_float2(-ref, -ref);
+      const float hi = __fmul_rn(ref, a.c), lo = __fmaf_rn(ref, a.c, -hi);
+      const float2 c2 = make_float2(a.c, a.c), nhi = make_float2(-hi, -hi);
       float2 d = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kPer; i += 2) {
-        const float2 q = __fmul2_rn(__fadd2_rn(make_float2(z[i], z[i + 1]), nref), c2);
+        const float2 q = __ffma2_rn(make_float2(z[i], z[i + 1]), c2, nhi);
         const float2 y = make_float2(ex2(q.x), ex2(q.y));
         d = __fadd2_rn(d, y);
-        // a logit of -inf adds 0, NaN stays
-        t = __ffma2_rn(y, make_float2(fmaxf(q.x, -1024.f), fmaxf(q.y, -1024.f)), t);
+        t = __ffma2_rn(y, q, t);
       }
-      x.d = d.x + d.y;
-      x.s = t.x + t.y;
+      const float f = ex2(-lo);
+      x.d = (d.x + d.y) * f;
+      x.s = __fmaf_rn(-lo, d.x + d.y, t.x + t.y) * f;
+      if (!(fabsf(x.s) < INFINITY)) {
+        // a logit of -inf or near the type's lowest (0 times -inf above), a maximum
+        // that overflows c, or NaN, which stays: with the difference taken first
+        x.d = x.s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float q = __fmul_rn(z[i] - ref, a.c), y = ex2(q);
+          x.d += y;
+          x.s = __fmaf_rn(y, fmaxf(q, -1024.f), x.s);
+        }
+      }
     }
-    const float tm = x.m;
     x = block_mds<kWarps>(x, a.c, shm);
+    if (a.cmax && tid < kWarps) a.cmax[(r * parts + part) * kWarps + tid] = shm[tid].m;
     if (tid == 0) {
       a.part[r * parts + part] = make_float4(x.m, x.d, x.s, 0.f);
       if (a.labels && part == 0) {
         const int64_t y = a.labels[a.row0 + r];
-        if (y >= 0 && y < a.v) a.zy[r] = val(zr + y);
-      }
-    }
-    if (TOP) {
-      // The k-th largest of 64 groups' maxima (four threads each) bounds the k-th
-      // largest logit from below: what reaches it is listed and ranked. A list
-      // that overflows (many equal logits) is replaced by k rounds of the largest
-      // remaining key.
-      float g = tm;
-      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-      if ((tid & 3) == 0) gmax[tid >> 2] = g;
-      if (tid == 0) n_list = 0;
-      __syncthreads();
-      if (tid < kGroups) {
-        const float o = gmax[tid];
-        int rank = 0;
-#pragma unroll 16
-        for (int j = 0; j < kGroups; ++j) rank += (gmax[j] > o || (gmax[j] == o && j < tid)) ? 1 : 0;
-        if (rank == a.k - 1) s_thr = o;
-      }
-      __syncthreads();
-      const float thr = s_thr;
-      if (tm >= thr) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (z[i] >= thr && z[i] > -INFINITY) {
-            const int at = atomicAdd(&n_list, 1);
-            const int col = (int)e0 + ((i / N) * kThreads + tid) * N + i % N;
-            if (at < kList) list[at] = cand_key(make_int2(__float_as_int(z[i]), col));
-          }
-        }
-      }
-      __syncthreads();
-      const int n_all = n_list;
-      int2* out = a.cand + (r * parts + part) * a.k;
-      if (n_all <= kList) {
-        for (int i = tid; i < n_all; i += kThreads) {
-          const unsigned long long key = list[i];
-          int above = 0;
-          for (int j = 0; j < n_all; ++j) above += list[j] > key ? 1 : 0;
-          if (above < a.k) out[above] = make_int2(__float_as_int(key_value(key)), key_col(key));
-        }
-        for (int i = n_all + tid; i < a.k; i += kThreads) out[i] = make_int2(0, -1);
-      } else {
-        unsigned long long last = ~0ull;
-        for (int q = 0; q < a.k; ++q) {
-          unsigned long long best = 0;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int col = (int)e0 + ((i / N) * kThreads + tid) * N + i % N;
-            const unsigned long long key =
-                z[i] > -INFINITY ? cand_key(make_int2(__float_as_int(z[i]), col)) : 0ull;
-            best = key < last && key > best ? key : best;
-          }
-          best = block_max64<kWarps>(best, sh64);
-          if (tid == 0)
-            out[q] = best ? make_int2(__float_as_int(key_value(best)), key_col(best)) : make_int2(0, -1);
-          last = best;
-        }
+        if (y >= 0 && y < a.v) a.zy[r] = val(reinterpret_cast<const T*>(a.z) + r * a.ld + y);
       }
     }
     __syncthreads();  // the shared results are written again by the next row
@@ -253,8 +262,11 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) k_lp_rows(LpRowsArgs a,
 }
 
 // One CTA to a row: its parts into the row's results, its candidates into the
-// k largest.
+// k largest. SRC: where the candidates are; void: lists and written-out logits of
+// the product, else given logits of that type.
+template <typename SRC, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
+  constexpr bool kRowsSrc = !std::is_same<SRC, void>::value;
   constexpr int W = kJoinThreads / 32;
   __shared__ Mds shm[W];
   __shared__ float2 sh_norm;
@@ -307,50 +319,100 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   }
   if (a.k == 0) return;
   // ---- the k largest candidates ----
-  const int2* cand = a.cand + r * a.cap;
-  const int64_t n_cand = a.count ? (int64_t)a.count[r] : a.cap;
+  // the k-th largest of the first n threads' values (0 if fewer are above 0)
+  auto kth_of_threads = [&](unsigned mine, int n) {
+    unsigned* keys = reinterpret_cast<unsigned*>(list);
+    keys[tid] = mine;
+    if (tid == 0) sh_least = 0;
+    __syncthreads();
+    int gt = 0, ge = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      gt += keys[j] > mine ? 1 : 0;
+      ge += keys[j] >= mine ? 1 : 0;
+    }
+    if (tid < n && gt < a.k && a.k <= ge) sh_least = mine;  // (equal threads write the same)
+    __syncthreads();
+    return sh_least;
+  };
   unsigned least = 0;
-  if (a.gmax) {
+  const int64_t chunks = a.parts * LP_CHUNKS;
+  const float* cmax = a.cmax + r * chunks;
+  const int64_t n_cand = kRowsSrc ? 0 : (int64_t)a.count[r];
+  const int2* cand = a.cand + r * a.cap;
+  const float* dump = a.dump + r * a.dump_cols;
+  const int64_t n_dump = !kRowsSrc && a.dump ? (a.dump_cols < a.v ? a.dump_cols : a.v) : 0;
+  if (kRowsSrc) {
+    unsigned mine = 0;
+    for (int64_t i = tid; i < chunks; i += kJoinThreads) {
+      const float m1 = cmax[i];
+      if (m1 > -INFINITY) mine = max(mine, lp_key(m1));
+    }
+    least = kth_of_threads(mine, (int)(chunks < kJoinThreads ? chunks : kJoinThreads));
+  } else {
     least = 0xffffffffu;
     for (int j = 0; j < a.k; ++j) least = min(least, a.gmax[r * a.k + j]);
   }
-  const float* dump = a.dump + r * a.dump_cols;
-  const int64_t n_dump = a.dump ? (a.dump_cols < a.v ? a.dump_cols : a.v) : 0;
-  auto dump_key = [&](int64_t i) {
-    const float z = dump[i];
-    return z > -INFINITY ? cand_key(make_int2(__float_as_int(z), (int)i)) : 0ull;
-  };
-  // every candidate's key, four loads in flight a thread
+  // every candidate's key that reaches `least`
   auto each = [&](auto&& f) {
+    const float lo = least > 0x007fffffu ? key_value((unsigned long long)least << 32) : -INFINITY;
+    auto give = [&](float z, int64_t col) {
+      if (z >= lo && z > -INFINITY) f(cand_key(make_int2(__float_as_int(z), (int)col)));
+    };
+    if constexpr (kRowsSrc) {
+      constexpr int N = 16 / sizeof(SRC);
+      constexpr uint32_t kNone = sizeof(SRC) == 4 ? 0xff800000u : 0xff80u;  // -inf
+      for (int64_t c = tid >> 5; c < chunks; c += W) {
+        const float m1 = cmax[c];
+        if (!(m1 > -INFINITY) || lp_key(m1) < least) continue;
+        const Segment<SRC> g(a.z, a.ld, r, a.v, c / LP_CHUNKS);
+        const int j0 = ((int)(c % LP_CHUNKS) * 32 + (tid & 31)) * N;
+        Raw<SRC> raw[kPer / N];
+#pragma unroll
+        for (int u = 0; u < kPer / N; ++u)
+          raw[u] = load_raw(g.zs, u * kThreads * N + j0, g.first, g.n, kNone);
+#pragma unroll
+        for (int u = 0; u < kPer / N; ++u) {
+          float z[N];
+          values(raw[u], z);
+#pragma unroll
+          for (int i = 0; i < N; ++i) give(z[i], g.e0 + u * kThreads * N + j0 + i);
+        }
+      }
+    } else {
 #pragma unroll 4
-    for (int64_t i = tid; i < n_cand; i += kJoinThreads) f(cand_key(cand[i]));
+      for (int64_t i = tid; i < n_cand; i += kJoinThreads) {
+        const int2 q = cand[i];
+        give(__int_as_float(q.x), q.y);
+      }
+      // (whole 256-column blocks; columns past the vocabulary hold nothing)
 #pragma unroll 4
-    for (int64_t i = tid; i < n_dump; i += kJoinThreads) f(dump_key(i));
+      for (int64_t i = tid * 4; i < n_dump; i += kJoinThreads * 4) {
+        const float4 q = *reinterpret_cast<const float4*>(dump + i);
+        give(q.x, i);
+        if (i + 1 < n_dump) give(q.y, i + 1);
+        if (i + 2 < n_dump) give(q.z, i + 2);
+        if (i + 3 < n_dump) give(q.w, i + 3);
+      }
+    }
   };
   auto gather = [&]() {
     each([&](unsigned long long key) {
-      if (key != 0 && (unsigned)(key >> 32) >= least) {
-        const int at = atomicAdd(&n_list, 1);
-        if (at < kJoinCap) list[at] = key;
-      }
+      const int at = atomicAdd(&n_list, 1);
+      if (at < kJoinCap) list[at] = key;
     });
   };
   gather();
   __syncthreads();
   if (n_list > kJoinCap) {
     // no threshold, or many equal logits: the k-th largest of the threads' own
-    // largest keys bounds the k-th largest from below, ties apart
+    // largest bounds the k-th largest from below, ties apart
     unsigned long long mine = 0;
     each([&](unsigned long long key) { mine = key > mine ? key : mine; });
     __syncthreads();
-    list[tid] = mine;
-    __syncthreads();
-    int rank = 0;
-    for (int j = 0; j < kJoinThreads; ++j) rank += (list[j] > mine || (list[j] == mine && j < tid)) ? 1 : 0;
-    if (rank == a.k - 1) sh_least = (unsigned)(mine >> 32);
+    least = max(least, kth_of_threads((unsigned)(mine >> 32), kJoinThreads));
     if (tid == 0) n_list = 0;
     __syncthreads();
-    least = sh_least;
     gather();
     __syncthreads();
   }
@@ -382,22 +444,37 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
   }
 }
 
-// dz of one logit; lp2 = log2 p. -inf: p = 0 and p log p = 0.
-//   -p (a + b (log p + entropy)) = -p (b ln2 log2 p + (a + b entropy))
-__device__ __forceinline__ float grad_of(float lp2, float bl, float ab) {
-  return -ex2(lp2) * __fmaf_rn(bl, fmaxf(lp2, -1024.f), ab);
-}
-
 // One CTA to a segment of a row, in vectors of eight where the logits and their
 // gradient lie alike relative to a 16-byte boundary (rows of odd length start
-// anywhere, but both at the same place), else one element at a time. All loads of
-// a thread are issued before the first is used.
+// anywhere, but both at the same place), else one element at a time.
+//   dz_j = -p (a + b (log p + entropy)) = -p (b ln2 log2 p + (a + b entropy))
+// with log2 p = c (z - m) - log2 d, or, from 2^t, t + c (m of its part - m) - log2 d.
+// All loads of a thread are issued before the first is used, and the next row's
+// before this one's arithmetic.
 template <typename TI, typename TO, bool FROM_E>
-__global__ void __launch_bounds__(kThreads) k_lp_grad(LpGradArgs a) {
-  constexpr int N = 8, U = LP_SEG / (kThreads * N);
+__global__ void __launch_bounds__(kThreads, 3) k_lp_grad(LpGradArgs a) {
+  constexpr int N = 8, U = LP_SEG / (kThreads * N), R = N * sizeof(TI) / 16;
   const int tid = threadIdx.x;
-  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+  Raw<TI> raw[U][R];
+  float top[U];  // (FROM_E) the maximum of the vector's part
+  auto lies_alike = [&](int64_t r) {
     const TI* zr = reinterpret_cast<const TI*>(a.z) + r * a.ldz;
+    const TO* orow = reinterpret_cast<const TO*>(a.out) + r * a.ldo;
+    return ((uintptr_t)zr & 15u) / sizeof(TI) == ((uintptr_t)orow & 15u) / sizeof(TO);
+  };
+  auto load = [&](int64_t r) {
+    if (!lies_alike(r)) return;
+    const Segment<TI> g(a.z, a.ldz, r, a.v, blockIdx.x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = (u * kThreads + tid) * N;
+#pragma unroll
+      for (int q = 0; q < R; ++q) raw[u][q] = load_raw(g.zs, j + q * (N / R), g.first, g.n, 0u);
+      if (FROM_E) top[u] = j < g.n ? a.part[r * a.parts + (g.e0 + j) / LP_PART_COLS].x : 0.f;
+    }
+  };
+  if (blockIdx.y < a.rows) load(blockIdx.y);
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     TO* orow = reinterpret_cast<TO*>(a.out) + r * a.ldo;
     const int64_t row = a.row0 + r;
     const int64_t y = a.labels ? a.labels[row] : -1;
@@ -408,50 +485,60 @@ __global__ void __launch_bounds__(kThreads) k_lp_grad(LpGradArgs a) {
     const float ga = a.grad_logp && a.labels ? a.grad_logp[row] * a.inv_t : 0.f;
     const float gb = a.grad_entropy ? a.grad_entropy[row] * a.inv_t : 0.f;
     const float ent = a.entropy[row];
-    const float bl = gb * kLn2, ab = __fmaf_rn(gb, ent, ga);
-    const bool same = ((uintptr_t)zr & 15u) / sizeof(TI) == ((uintptr_t)orow & 15u) / sizeof(TO);
-    const int lead = same ? (int)(((uintptr_t)zr & 15u) / sizeof(TI)) : 0;
-    const int64_t e0 = (int64_t)blockIdx.x * LP_SEG - lead;
-    const int n = (int)(a.v - e0 < LP_SEG ? (a.v > e0 ? a.v - e0 : 0) : LP_SEG);
-    const int first = e0 < 0 ? lead : 0;  // elements [first, n) of the segment count
-    const TI* zs = zr + e0;
+    const float bl = -gb * kLn2, ab = -__fmaf_rn(gb, ent, ga);
+    const bool alike = lies_alike(r);
+    const Segment<TI> g(a.z, a.ldz, r, a.v, blockIdx.x);
+    // (rows that do not lie alike: segments from the row's own start)
+    const int64_t e0 = alike ? g.e0 : (int64_t)blockIdx.x * LP_SEG;
+    const int n = alike ? g.n : (int)(a.v - e0 < LP_SEG ? (a.v > e0 ? a.v - e0 : 0) : LP_SEG);
+    const int first = alike ? g.first : 0;
     TO* os = orow + e0;
-    // log2 p = c (z - m) - log2 d; from 2^t, log2 p = t + c (m of its part - m) - log2 d
-    auto one = [&](float z, float ref) {
-      const float lp2 = FROM_E ? lg2(z) + ref : __fmul_rn(z - norm.x, a.c) - norm.y;
-      return grad_of(lp2, bl, ab);
+    // two at a time; -inf: p = 0 and p log p = 0
+    auto two = [&](float za, float zb, float ref) {
+      float2 lp2;
+      if (FROM_E)
+        lp2 = __fadd2_rn(make_float2(lg2(za), lg2(zb)), make_float2(ref, ref));
+      else
+        lp2 = __ffma2_rn(__fadd2_rn(make_float2(za, zb), make_float2(-norm.x, -norm.x)),
+                         make_float2(a.c, a.c), make_float2(-norm.y, -norm.y));
+      const float2 t = __ffma2_rn(make_float2(fmaxf(lp2.x, -1024.f), fmaxf(lp2.y, -1024.f)),
+                                  make_float2(bl, bl), make_float2(ab, ab));
+      return __fmul2_rn(make_float2(ex2(lp2.x), ex2(lp2.y)), t);
     };
-    auto ref_of = [&](int j) {  // (FROM_E: lead is 0)
-      return FROM_E ? __fmul_rn(a.part[r * a.parts + (e0 + j) / LP_PART_COLS].x - norm.x, a.c) - norm.y
-                    : 0.f;
-    };
-    if (same) {
+    if (alike) {
       float z[U][N], ref[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int j = (u * kThreads + tid) * N;
-        ref[u] = 0.f;
-        if (live && j >= first && j + N <= n) {
-          load8(zs + j, z[u]);
-          ref[u] = ref_of(j);
-        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) values(raw[u][q], z[u] + q * (N / R));
+        ref[u] = FROM_E ? __fmul_rn(top[u] - norm.x, a.c) - norm.y : 0.f;
       }
+      // (the gradient may overwrite the logits: only rows that this CTA reads later)
+      if (r + gridDim.y < a.rows) load(r + gridDim.y);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = (u * kThreads + tid) * N;
-        if (j >= first && j + N <= n) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) z[u][e] = live ? one(z[u][e], ref[u]) : 0.f;
+        for (int e = 0; e < N; e += 2) {
+          const float2 o = two(z[u][e], z[u][e + 1], ref[u]);
+          z[u][e] = live ? o.x : 0.f;
+          z[u][e + 1] = live ? o.y : 0.f;
+        }
+        if (j >= first && j + N <= n) {
           store8(os + j, z[u]);
         } else {
+#pragma unroll
           for (int e = 0; e < N; ++e)
-            if (j + e >= first && j + e < n)
-              Vec<TO>::put(os + j + e, live ? one(val(zs + j + e), ref_of(j + e)) : 0.f);
+            if (j + e >= first && j + e < n) Vec<TO>::put(os + j + e, z[u][e]);
         }
       }
     } else {
-      for (int j = tid; j < n; j += kThreads)
-        Vec<TO>::put(os + j, live ? one(val(zs + j), ref_of(j)) : 0.f);
+      const TI* zs = reinterpret_cast<const TI*>(a.z) + r * a.ldz + e0;
+      for (int j = tid; j < n; j += kThreads) {
+        const float z = val(zs + j);
+        Vec<TO>::put(os + j, live ? two(z, z, 0.f).x : 0.f);
+      }
+      if (r + gridDim.y < a.rows) load(r + gridDim.y);
     }
     // The label's own element from its fp32 log probability (1 - p_y would lose its
     // digits to a rounded p_y), written over what the loop left there.
@@ -473,12 +560,26 @@ dim3 row_grid(int64_t segs, int64_t rows) {
   return dim3((unsigned)segs, (unsigned)(y < 65535 ? y : 65535));
 }
 
+template <int THREADS>
+void launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)a.rows;
+  if (!a.z)
+    k_lp_join<void, THREADS><<<grid, THREADS, 0, st>>>(a);
+  else if (a.z_dtype == FLJSD_BF16)
+    k_lp_join<__nv_bfloat16, THREADS><<<grid, THREADS, 0, st>>>(a);
+  else
+    k_lp_join<float, THREADS><<<grid, THREADS, 0, st>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  k_lp_join<<<(unsigned)a.rows, kJoinThreads, 0, st>>>(a);
+  if (a.rows <= num_sms() * 2)
+    launch_join_t<kJoinFew>(a, st);
+  else
+    launch_join_t<kJoinMany>(a, st);
   trace_end(FLJSD_KERNEL_SMALL, st);
   return cudaGetLastError();
 }
@@ -488,17 +589,10 @@ cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
   const int64_t parts = lp_row_parts(a.v);
   const dim3 grid = row_grid(parts, a.rows);
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
-  if (dtype == FLJSD_BF16) {
-    if (a.k > 0)
-      k_lp_rows<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a, parts);
-    else
-      k_lp_rows<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a, parts);
-  } else {
-    if (a.k > 0)
-      k_lp_rows<float, true><<<grid, kThreads, 0, st>>>(a, parts);
-    else
-      k_lp_rows<float, false><<<grid, kThreads, 0, st>>>(a, parts);
-  }
+  if (dtype == FLJSD_BF16)
+    k_lp_rows<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, parts);
+  else
+    k_lp_rows<float><<<grid, kThreads, 0, st>>>(a, parts);
   trace_end(FLJSD_KERNEL_JSD_ROWS, st);
   return cudaGetLastError();
 }
