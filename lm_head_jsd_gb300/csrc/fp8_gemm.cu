@@ -26,6 +26,7 @@
 // codes are the nearest to x (448 (1 / amax)).
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
+#include "tensor_map.cuh"
 
 #include <cuda_fp8.h>
 
@@ -540,12 +541,13 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
   p.timeout_ns = kTimeoutNs;
   p.status = status;
   CUtensorMap ma, mb, mo;
-  if (!tc_make_map_u8(&ma, ws + L.codes, k, m, L.ldq, FB, BM) ||
-      !tc_make_map_u8(&mb, w_codes, k, n, ldw, FB, BN))
+  if (!make_tensor_map(&ma, MapType::kU8, ws + L.codes, k, m, L.ldq, FB, BM) ||
+      !make_tensor_map(&mb, MapType::kU8, w_codes, k, n, ldw, FB, BN))
     return FLJSD_ERR_CUDA;
   mo = ma;
-  if (p.use_tma && !tc_make_map(&mo, out, n, m, ldo, out_dtype == FLJSD_BF16 ? 32 : 16, 32,
-                                out_dtype == FLJSD_F32, false))
+  const bool b16 = out_dtype == FLJSD_BF16;
+  if (p.use_tma && !make_tensor_map(&mo, b16 ? MapType::kBf16 : MapType::kF32, out, n, m, ldo,
+                                    b16 ? 32 : 16, 32, false))
     return FLJSD_ERR_CUDA;
   if (quantise(m, k, x_dtype, 1, x, ldx, ws + L.codes, L.ldq, sx, status, st) != cudaSuccess)
     return FLJSD_ERR_CUDA;
@@ -554,7 +556,6 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
                  out_dtype == FLJSD_BF16, status};
   cudaError_t e;
   trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
-  const bool b16 = out_dtype == FLJSD_BF16;
   if (skinny_supported(few))
     e = launch_skinny(few, st);
   else

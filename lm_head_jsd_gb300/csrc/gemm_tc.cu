@@ -74,9 +74,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // 2-D tensor map (bf16, or fp32 when f32) over a row-major [outer x inner]
 // matrix with row stride ld elements; box = box_inner x box_outer; 128-byte
-// swizzle (or none); zero fill.
+// swizzle; zero fill.
 bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-              int box_inner, int box_outer, bool f32 = false, bool swizzle = true) {
+              int box_inner, int box_outer, bool f32 = false) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
@@ -85,8 +85,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void*>(ptr), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -102,25 +101,6 @@ cudaError_t launch_layout(bool a_mn, bool b_mn, bool pair, const CUtensorMap& ma
 }
 
 }  // namespace
-
-bool tc_make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-                 int box_inner, int box_outer, bool f32, bool swizzle) {
-  return make_map(m, ptr, inner, outer, ld, box_inner, box_outer, f32, swizzle);
-}
-
-bool tc_make_map_u8(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-                    int box_inner, int box_outer) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  cuuint64_t strides[1] = {(cuuint64_t)ld};
-  cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 size_t tc_splitk_bytes(int64_t m, int64_t n, int64_t k, int ctas) {
   const int s = splitk_factor(m, n, k, ctas);

@@ -1,7 +1,6 @@
 // Tensor-core GEMM interface (internal). See gemm_tc.cu.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -57,15 +56,6 @@ constexpr int TC_STATS_COLS = 128;  // columns per pass-1 partial
 constexpr int TC_PLAN_CTAS = 152;
 // Scratch bytes the split-K schedule of this contraction would use.
 size_t tc_splitk_bytes(int64_t m, int64_t n, int64_t k, int ctas);
-
-// 2-D tensor map over a row-major [outer x inner] bf16 (or fp32) matrix with row
-// stride ld elements: box_inner x box_outer boxes, 128-byte swizzle (or none), zero
-// fill.
-bool tc_make_map(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-                 int box_inner, int box_outer, bool f32 = false, bool swizzle = true);
-// The same over 8-bit elements.
-bool tc_make_map_u8(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
-                    int box_inner, int box_outer);
 
 bool tc_gemm_supported(const TcGemmArgs& g);
 cudaError_t launch_gemm_tc(const TcGemmArgs& g, cudaStream_t st);

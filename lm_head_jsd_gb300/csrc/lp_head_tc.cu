@@ -30,6 +30,7 @@
 // 333 rows of H = 2048, V = 40960 with 20 alternatives 150 us, DUMP_US so.
 #include "gemm_tc_kernel.cuh"
 #include "lp.cuh"
+#include "tensor_map.cuh"
 
 #include <cuda_fp16.h>
 
@@ -567,11 +568,11 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms());
   const bool pair = h.pair, keep = a.e != nullptr;
   CUtensorMap ma, mb, me;
-  if (!tc_make_map(&ma, a.x, a.k, a.m, a.ldx, BK, BM) ||
-      !tc_make_map(&mb, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
+  if (!make_tensor_map(&ma, MapType::kBf16, a.x, a.k, a.m, a.ldx, BK, BM) ||
+      !make_tensor_map(&mb, MapType::kBf16, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
     return cudaErrorInvalidValue;
   me = ma;
-  if (keep && !tc_make_map(&me, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
+  if (keep && !make_tensor_map(&me, MapType::kBf16, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
   HeadParams p{};
   p.m = a.m; p.n = a.n;
   p.num_n_blocks = (int)h.nblocks;

@@ -14,6 +14,7 @@
 // ring of eight, and is scaled and added in fp32 registers.
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
+#include "tensor_map.cuh"
 
 namespace fljsd {
 namespace {
@@ -313,10 +314,9 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;
   CUtensorMap mx, mw;
-  const bool ok = a.e4m3 ? tc_make_map_u8(&mx, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&
-                               tc_make_map_u8(&mw, a.w, a.k, a.n, a.ldw, ke, BM)
-                         : tc_make_map(&mx, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&
-                               tc_make_map(&mw, a.w, a.k, a.n, a.ldw, ke, BM);
+  const MapType mt = a.e4m3 ? MapType::kU8 : MapType::kBf16;
+  const bool ok = make_tensor_map(&mx, mt, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&
+                  make_tensor_map(&mw, mt, a.w, a.k, a.n, a.ldw, ke, BM);
   if (!ok) return cudaErrorInvalidValue;
   const int smem = (p.resident ? (int)xb : 0) + p.nst * sb + kCtrl + 1024;
   if (a.e4m3)

@@ -105,7 +105,8 @@ def _limit(xq, wq, k, out_dtype, ref):
 @gpu
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 1000, 64), (3, 257, 130), (128, 256, 128), (129, 512, 1000),
-                                   (300, 1027, 512), (65, 2056, 2048), (2, 40960, 384)])
+                                   (300, 1027, 512), (65, 2056, 2048), (2, 40960, 384),
+                                   (16, 300, 8200), (3, 130, 40000), (17, 300, 8200), (1300, 2304, 256)])
 def test_linear(m, n, k, out_dtype):
     from lm_head_jsd_gb300 import fp8_linear, fp8_quantize
 

@@ -196,10 +196,12 @@ def _fused(x, w, y, dev="cuda", **kw):
     return run, args, run.forward(*args)
 
 
-# one token to several tiles, odd vocabularies, rows that fill half a pair, hidden sizes
+# one token to several tiles (up to 16 rows by the product for few rows, its x kept in
+# shared memory up to h of about 4300), odd vocabularies, rows that fill half a pair, hidden sizes
 # of less than one k-block; (_, 12, _) and fp32 run on the CUDA cores
 SHAPES = [(1, 64, 1000), (1, 512, 32000), (2, 8, 33), (7, 136, 129), (33, 64, 4099), (128, 256, 2048),
-          (129, 320, 1027), (257, 512, 513), (300, 1024, 5000), (5, 12, 777), (3, 16, 1)]
+          (129, 320, 1027), (257, 512, 513), (300, 1024, 5000), (5, 12, 777), (3, 16, 1),
+          (16, 4096, 700), (17, 4096, 700), (15, 8200, 300)]
 
 
 @gpu
@@ -237,6 +239,22 @@ def test_fused_alternatives_ties_and_order(k):
     assert r.logp is None
     assert np.array_equal(r.top_id.cpu().numpy(), ref[4])
     _check_rows(r, ref, _logit_bound(x, w, 1.0), "ties")
+
+
+@gpu
+@pytest.mark.parametrize("bt,v", [(1, 128256), (5, 70001), (130, 50000), (300, 40960)])
+def test_fused_alternatives_at_length(bt, v):
+    """Thresholds, written-out columns and read-again chunks at a vocabulary's length,
+    the largest logits all in one place or spread out."""
+    h, k = 64, 20
+    x, w, y = _inputs(bt, h, v, torch.bfloat16, 40 + bt, grid=True)
+    w[v - 90:] = w[v - 90:] * 2  # the last part holds most of them
+    w[1000:1040, 0] = 8.0
+    x[0, 0] = 4.0  # one row: equal logits far above the rest
+    x[0, 1:] = 0
+    _, _, r = _fused(x, w, y, top_k=k)
+    ref = lp_rows_ref(f64(x) @ f64(w).T, y.numpy(), top_k=k)
+    _check_rows(r, ref, _logit_bound(x, w, 1.0), f"{bt}x{v}")
 
 
 @gpu
