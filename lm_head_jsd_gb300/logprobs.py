@@ -27,10 +27,9 @@ class Logprobs(NamedTuple):
 
 
 def _results(rows, top_k, with_logp, device) -> Logprobs:
-    logp, entropy, lse = torch.empty((3, rows), dtype=torch.float32, device=device).unbind()
-    return Logprobs(logp if with_logp else None, entropy, lse,
-                    torch.empty((rows, 2), dtype=torch.float32, device=device),
-                    torch.empty((rows, top_k), dtype=torch.float32, device=device) if top_k else None,
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
+    return Logprobs(f32(rows) if with_logp else None, f32(rows), f32(rows), f32(rows, 2),
+                    f32(rows, top_k) if top_k else None,
                     torch.empty((rows, top_k), dtype=torch.int64, device=device) if top_k else None)
 
 

@@ -120,8 +120,11 @@ class AdamW:
             self._at = at
             t["param"] = at
         live, sizes = grads, self._sizes
-        if any(g is None for g in grads):
+        try:
+            t["grad"] = _ptrs(grads)
+        except TypeError:  # some are None: those parameters stay as they are
             t = t.copy()
+            t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
             t["n"] = [0 if g is None else n for g, n in zip(grads, sizes)]
             live = [g for g in grads if g is not None]
             sizes = [n for g, n in zip(grads, sizes) if g is not None]
@@ -137,10 +140,6 @@ class AdamW:
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one fp32 value on {dev}")
-        if live is grads:
-            t["grad"] = _ptrs(grads)
-        else:
-            t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
         o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay,
                                     self.steps + 1, _DT[self.dtype], _DT[dt], self.state_bits,
                                     int(self.master is not None))
