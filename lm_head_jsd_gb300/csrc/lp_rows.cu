@@ -5,8 +5,12 @@
 // single row of 128256 still runs on 16 CTAs; the next row's segment is on its way
 // while one is reduced. The k largest are left to k_lp_join, which reads again the
 // few 1024s whose maxima reach the k-th largest of them (choosing candidates here
-// took three times as long as the sums). k_lp_grad is elementwise. Both are bound by
-// HBM: ROWS_FIGURES.
+// took three times as long as the sums: 361 us where the sums took 117 and the join
+// now takes 38, 2047 x 128255 bf16). k_lp_grad is elementwise. HBM bounds both for
+// fp32 (1023 x 128255: 81 us = 6.5 TB/s, the gradient 160 us = 6.5 TB/s, 0.96 of a
+// copy's rate); for bf16 k_lp_rows, with twice the elements to a byte, is bound by
+// issue (2047 x 128255: 96 us = 5.5 TB/s, about nine instructions an element), the
+// gradient by HBM (165 us = 6.3 TB/s).
 #include "lp.cuh"
 #include "jsd_math.cuh"
 
@@ -24,8 +28,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPer = LP_SEG / kThreads;  // logits a thread holds
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kWarps == LP_CHUNKS, "a maximum for each warp");
-// Threads of a row's join: few rows are bound by one CTA's way through its loads,
-// many by how many CTAs an SM holds (JOIN_FIGURES).
+// Threads of a row's join: few rows are bound by one CTA's way through its loads (333
+// fused rows, 20 alternatives: 512 threads 16 us, 256 threads 19), many by how many
+// CTAs an SM holds (2047 rows of given logits, 8 alternatives: 128 threads 38 us, 256
+// threads 58).
 constexpr int kJoinFew = 512, kJoinMany = 128;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
 static_assert(kJoinFew <= kJoinCap && kJoinMany >= LP_MAX_TOP, "the threads' largest");
@@ -170,21 +176,29 @@ __device__ __forceinline__ Mds merge(const Mds& a, const Mds& b, float c) {
              __fmaf_rn(fa, __fmaf_rn(a.d, fmaxf(ta, -1024.f), a.s),
                        fb * __fmaf_rn(b.d, fmaxf(tb, -1024.f), b.s))};
 }
+// The warp's: its maximum in one instruction (exact, so order-free), every lane's sums
+// rescaled to it once and added in a fixed order.
+__device__ __forceinline__ Mds warp_mds(Mds x, float c) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x.m));
+  const float t = x.m == -INFINITY ? 0.f : __fmul_rn(x.m - m, c);
+  const float f = ex2(t);
+  float2 ds = make_float2(x.d * f, f * __fmaf_rn(x.d, fmaxf(t, -1024.f), x.s));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    ds = __fadd2_rn(ds, make_float2(__shfl_xor_sync(0xffffffffu, ds.x, o),
+                                    __shfl_xor_sync(0xffffffffu, ds.y, o)));
+  return Mds{m, ds.x, ds.y};
+}
 // The block's, in a fixed order (in every thread of the first warp).
 template <int W>
 __device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    x = merge(x, Mds{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.d, o),
-                     __shfl_xor_sync(0xffffffffu, x.s, o)}, c);
+  x = warp_mds(x, c);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
   __syncthreads();
   if (threadIdx.x < 32) {
     x = threadIdx.x < W ? sh[threadIdx.x] : Mds{-INFINITY, 0.f, 0.f};
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-      x = merge(x, Mds{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.d, o),
-                       __shfl_xor_sync(0xffffffffu, x.s, o)}, c);
+    x = warp_mds(x, c);
   }
   return x;
 }
@@ -206,8 +220,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
   Raw<T> raw[V];
   auto load = [&](int64_t r) {
     const Segment<T> g(a.z, a.ld, r, a.v, part);
+    if (g.first == 0 && g.n == LP_SEG) {
 #pragma unroll
-    for (int u = 0; u < V; ++u) raw[u] = load_raw(g.zs, (u * kThreads + tid) * N, g.first, g.n, kNone);
+      for (int u = 0; u < V; ++u)
+        raw[u].w = *reinterpret_cast<const uint4*>(g.zs + (u * kThreads + tid) * N);
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        raw[u] = load_raw(g.zs, (u * kThreads + tid) * N, g.first, g.n, kNone);
+    }
   };
   if (blockIdx.y < a.rows) load(blockIdx.y);
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
@@ -449,10 +470,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
 // anywhere, but both at the same place), else one element at a time.
 //   dz_j = -p (a + b (log p + entropy)) = -p (b ln2 log2 p + (a + b entropy))
 // with log2 p = c (z - m) - log2 d, or, from 2^t, t + c (m of its part - m) - log2 d.
-// All loads of a thread are issued before the first is used, and the next row's
-// before this one's arithmetic.
+// All loads of a thread are issued before the first is used; four CTAs an SM keep
+// enough of them in flight (the next row's loads before this one's arithmetic, with
+// three CTAs: 190 us where this takes 167, 2047 x 128255 bf16, 0.93 of HBM).
 template <typename TI, typename TO, bool FROM_E>
-__global__ void __launch_bounds__(kThreads, 3) k_lp_grad(LpGradArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_lp_grad(LpGradArgs a) {
   constexpr int N = 8, U = LP_SEG / (kThreads * N), R = N * sizeof(TI) / 16;
   const int tid = threadIdx.x;
   Raw<TI> raw[U][R];
@@ -468,13 +490,19 @@ __global__ void __launch_bounds__(kThreads, 3) k_lp_grad(LpGradArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = (u * kThreads + tid) * N;
+      if (g.first == 0 && g.n == LP_SEG) {
 #pragma unroll
-      for (int q = 0; q < R; ++q) raw[u][q] = load_raw(g.zs, j + q * (N / R), g.first, g.n, 0u);
+        for (int q = 0; q < R; ++q)
+          raw[u][q].w = *reinterpret_cast<const uint4*>(g.zs + j + q * (N / R));
+      } else {
+#pragma unroll
+        for (int q = 0; q < R; ++q) raw[u][q] = load_raw(g.zs, j + q * (N / R), g.first, g.n, 0u);
+      }
       if (FROM_E) top[u] = j < g.n ? a.part[r * a.parts + (g.e0 + j) / LP_PART_COLS].x : 0.f;
     }
   };
-  if (blockIdx.y < a.rows) load(blockIdx.y);
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    load(r);
     TO* orow = reinterpret_cast<TO*>(a.out) + r * a.ldo;
     const int64_t row = a.row0 + r;
     const int64_t y = a.labels ? a.labels[row] : -1;
@@ -513,16 +541,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_lp_grad(LpGradArgs a) {
         for (int q = 0; q < R; ++q) values(raw[u][q], z[u] + q * (N / R));
         ref[u] = FROM_E ? __fmul_rn(top[u] - norm.x, a.c) - norm.y : 0.f;
       }
-      // (the gradient may overwrite the logits: only rows that this CTA reads later)
-      if (r + gridDim.y < a.rows) load(r + gridDim.y);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = (u * kThreads + tid) * N;
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-          const float2 o = two(z[u][e], z[u][e + 1], ref[u]);
-          z[u][e] = live ? o.x : 0.f;
-          z[u][e + 1] = live ? o.y : 0.f;
+          const float2 o = live ? two(z[u][e], z[u][e + 1], ref[u]) : make_float2(0.f, 0.f);
+          z[u][e] = o.x;
+          z[u][e + 1] = o.y;
         }
         if (j >= first && j + N <= n) {
           store8(os + j, z[u]);
@@ -538,7 +564,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_lp_grad(LpGradArgs a) {
         const float z = val(zs + j);
         Vec<TO>::put(os + j, live ? two(z, z, 0.f).x : 0.f);
       }
-      if (r + gridDim.y < a.rows) load(r + gridDim.y);
     }
     // The label's own element from its fp32 log probability (1 - p_y would lose its
     // digits to a rounded p_y), written over what the loop left there.
@@ -576,7 +601,7 @@ void launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  if (a.rows <= num_sms() * 2)
+  if (a.rows <= num_sms() * 4)  // 512 threads, four CTAs an SM: one round
     launch_join_t<kJoinFew>(a, st);
   else
     launch_join_t<kJoinMany>(a, st);
