@@ -391,7 +391,7 @@ fljsd_status fljsd_ce_forward(const fljsd_ce_problem* problem, const fljsd_plan_
  *
  * Errors: FLJSD_ERR_INVALID_ARG for a dimension <= 0, a stride below v, an
  * unknown dtype or flag, top_k outside [0, v], a temperature that is not
- * positive and finite, grad_logp without labels, a null or unaligned pointer, or
+ * positive and finite (with a finite log2(e) / temperature), grad_logp without labels, a null or unaligned pointer, or
  * kept = 1 with more than one chunk; FLJSD_ERR_UNSUPPORTED for top_k above 32,
  * bt, rows or v above 2^30 or h above 2^20; FLJSD_ERR_WORKSPACE for a workspace
  * below the plan's (or, in fljsd_lp_plan, when not even one row fits the

@@ -84,21 +84,23 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   return L;
 }
 
+float log2_scale(float temperature) {
+  return (float)(1.4426950408889634 / (double)temperature);
+}
+// Positive, finite, and so is what the logits are multiplied by.
+bool temperature_ok(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(log2_scale(t)); }
+
 fljsd_status lp_check(const fljsd_lp_problem* p) {
   if (!p) return FLJSD_ERR_INVALID_ARG;
   if (p->bt <= 0 || p->h <= 0 || p->v <= 0 || p->chunk_rows < 0) return FLJSD_ERR_INVALID_ARG;
   if (p->dtype != FLJSD_F32 && p->dtype != FLJSD_BF16) return FLJSD_ERR_INVALID_ARG;
   if (p->top_k < 0 || p->top_k > p->v) return FLJSD_ERR_INVALID_ARG;
-  if (!(p->temperature > 0.f) || !std::isfinite(p->temperature)) return FLJSD_ERR_INVALID_ARG;
+  if (!temperature_ok(p->temperature)) return FLJSD_ERR_INVALID_ARG;
   if ((p->flags & ~(FLJSD_LP_BACKWARD | FLJSD_FLAG_ACCUM_FP32)) != 0) return FLJSD_ERR_INVALID_ARG;
   if (p->top_k > LP_MAX_TOP || p->v > (int64_t)1 << 30 || p->bt > (int64_t)1 << 30 ||
       p->h > (int64_t)1 << 20)
     return FLJSD_ERR_UNSUPPORTED;
   return FLJSD_OK;
-}
-
-float log2_scale(float temperature) {
-  return (float)(1.4426950408889634 / (double)temperature);
 }
 
 // D[m x n] (+)= A . B^T in dtype, on the tensor cores where they take it.
@@ -206,7 +208,7 @@ fljsd_status logits_check(int64_t rows, int64_t v, int64_t ld, int32_t dtype, in
   if (rows <= 0 || v <= 0 || ld < v) return FLJSD_ERR_INVALID_ARG;
   if (dtype != FLJSD_F32 && dtype != FLJSD_BF16) return FLJSD_ERR_INVALID_ARG;
   if (top_k < 0 || top_k > v) return FLJSD_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !std::isfinite(temperature)) return FLJSD_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature)) return FLJSD_ERR_INVALID_ARG;
   if (top_k > LP_MAX_TOP || rows > (int64_t)1 << 30 || v > (int64_t)1 << 30)
     return FLJSD_ERR_UNSUPPORTED;
   return FLJSD_OK;

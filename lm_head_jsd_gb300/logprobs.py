@@ -142,7 +142,12 @@ class _FusedLinearLogprobsFunction(torch.autograd.Function):
 def fused_linear_logprobs(x, w, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
                           chunk_rows=0) -> Logprobs:
     """:class:`Logprobs` of the logits x.w^T without forming them, differentiable in x
-    and w through logp and entropy. 2-D tensors on one CUDA device, fp32 or bf16."""
+    and w through logp and entropy. 2-D tensors on one CUDA device, fp32 or bf16.
+
+    To capture a backward pass into a CUDA graph, use :class:`FusedLinearLogprobs`, or
+    leaves of its own (``x.detach().requires_grad_()``): autograd delivers a leaf's
+    gradient on the stream of whatever eager graph of that leaf is still alive, which a
+    capture forbids."""
     need = torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)
     return Logprobs(*_FusedLinearLogprobsFunction.apply(x, w, labels, int(top_k), float(temperature),
                                                         int(ignore_index), int(chunk_rows), need))
@@ -205,8 +210,8 @@ class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, labels, top_k, temperature, ignore_index):
         z = logits.detach()
-        if z.dim() == 2 and z.stride(1) != 1:
-            z = z.contiguous()
+        if z.dim() == 2 and (z.stride(1) != 1 or z.stride(0) < z.shape[1]):
+            z = z.contiguous()  # columns apart, or rows that share memory
         lab = None if labels is None else labels.contiguous()
         r = logits_logprobs(z, lab, top_k=top_k, temperature=temperature, ignore_index=ignore_index)
         ctx.set_materialize_grads(False)

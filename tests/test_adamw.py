@@ -273,3 +273,17 @@ def test_step_in_a_graph_on_another_stream(bits):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(p, q) and torch.equal(a.exp_avg[0].float(), b.exp_avg[0].float())
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(bits):
+    from lm_head_jsd_gb300 import AdamW
+
+    n, tail = (1 << 31) + 3001, 3001 + 128 * 7
+    p = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(0, 0.02)
+    g = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(0, 0.01)
+    small = AdamW([p[-tail:].clone()], state_bits=bits, **HY)
+    AdamW([p], state_bits=bits, **HY).step([g])
+    small.step([g[-tail:].clone()])
+    assert torch.equal(p[-tail:], small.params[0])

@@ -157,3 +157,14 @@ def test_linear_special_values_and_streams():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(cap.nan_to_num(), out.nan_to_num())
+
+
+@gpu
+def test_linear_offsets_past_32_bits():
+    from lm_head_jsd_gb300 import fp8_linear, fp8_quantize
+
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(17000, 64, device="cuda", generator=g).bfloat16()
+    wq, ws = fp8_quantize(torch.randn(128257, 64, device="cuda", generator=g))
+    out = fp8_linear(x, wq, ws)
+    assert torch.equal(out[-300:], fp8_linear(x[-300:], wq, ws))

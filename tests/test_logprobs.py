@@ -121,7 +121,7 @@ def L():
 @pytest.mark.parametrize("kw,status", [
     (dict(bt=0), 1), (dict(h=-1), 1), (dict(v=0), 1), (dict(top_k=-1), 1), (dict(top_k=101), 1),
     (dict(temperature=0.0), 1), (dict(temperature=float("nan")), 1),
-    (dict(temperature=float("inf")), 1), (dict(dtype=7), 1), (dict(chunk_rows=-1), 1),
+    (dict(temperature=float("inf")), 1), (dict(temperature=1e-40), 1), (dict(dtype=7), 1), (dict(chunk_rows=-1), 1),
     (dict(v=1 << 31), 2), (dict(v=1000, top_k=33), 2), (dict(h=1 << 21), 2)])
 def test_plan_refusals(L, kw, status):
     base = dict(bt=4, h=64, v=100, dtype="bf16")
@@ -386,7 +386,77 @@ def test_fused_step_in_a_graph():
     assert all(torch.equal(p, q) for p, q in zip(r, rg)) and all(torch.equal(p, q) for p, q in zip(g, gg))
 
 
+@gpu
+def test_fused_autograd_in_a_graph_beside_an_eager_one():
+    from lm_head_jsd_gb300 import fused_linear_logprobs
+
+    x, w, y = _inputs(50, 64, 400, torch.bfloat16, 35, ignored=0.1)
+    xr, wr, yc = x.cuda().requires_grad_(), w.cuda().requires_grad_(), y.cuda()
+    eager = fused_linear_logprobs(xr, wr, yc)  # its graph stays alive
+    want = torch.autograd.grad(fused_linear_logprobs(xr, wr, yc).logp.sum(), (xr, wr))
+    def step():
+        leaves = xr.detach().requires_grad_(), wr.detach().requires_grad_()  # of the capture's own
+        return torch.autograd.grad(fused_linear_logprobs(*leaves, yc).logp.sum(), leaves)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for t in got:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    eager.logp.sum().backward()
+    assert torch.equal(xr.grad, want[0]) and torch.equal(wr.grad, want[1])
+
+
+@gpu
+def test_fused_offsets_past_32_bits():
+    """More than 2^31 probabilities kept for the backward pass; rows and gradients of the
+    end are those of the end alone."""
+    from lm_head_jsd_gb300 import FusedLinearLogprobs
+
+    bt, h, v, last = 17000, 64, 130000, 700  # (as many rows as are joined in the same order)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(bt, h, device="cuda", generator=g).bfloat16()
+    w = torch.randn(v, h, device="cuda", generator=g).div_(2).bfloat16()
+    y = torch.randint(0, v, (bt,), device="cuda", generator=g)
+    a = torch.randn(bt, device="cuda", generator=g)
+    run = FusedLinearLogprobs(bt, h, v, top_k=4, keep_for_backward=True)
+    assert run.plan.num_chunks == 1
+    r = run.forward(x, w, y)
+    gx, _ = run.backward(x, w, y, r, a, need=(True, False))
+    tail = FusedLinearLogprobs(last, h, v, top_k=4, keep_for_backward=True)
+    s = slice(bt - last, bt)
+    q = tail.forward(x[s], w, y[s])
+    hx, _ = tail.backward(x[s], w, y[s], q, a[s].contiguous(), need=(True, False))
+    assert all(torch.equal(t[s], u) for t, u in zip(r, q))
+    # (the product over v may be split differently for few rows)
+    assert rel_fro(f64(gx[s]), f64(hx)) <= 2.0 ** -8
+
+
 # ---- GPU: given logits ----
+@gpu
+def test_logits_offsets_past_32_bits():
+    from lm_head_jsd_gb300 import logits_logprobs, logits_logprobs_backward
+
+    rows, v = 17000, 128256
+    z = torch.empty(rows, v, dtype=torch.bfloat16, device="cuda").normal_(0, 3)
+    y = torch.randint(0, v, (rows,), device="cuda")
+    r = logits_logprobs(z, y, top_k=3)
+    n = 700  # (as many rows as are joined in the same order)
+    q = logits_logprobs(z[-n:], y[-n:], top_k=3)
+    assert all(torch.equal(t[-n:], u) for t, u in zip(r, q))
+    a = torch.randn(rows, device="cuda")
+    want = logits_logprobs_backward(z[-n:], y[-n:], q, a[-n:].contiguous())
+    assert torch.equal(logits_logprobs_backward(z, y, r, a, out=z)[-n:], want)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("rows,v,k", [(1, 1, 1), (1, 8190, 8), (2, 8192, 32), (3, 8193, 20), (5, 8191, 0),
@@ -457,6 +527,11 @@ def test_logits_autograd_and_refusals():
     (r.logp.sum() * 2 - r.entropy.mean()).backward()  # (the upstream gradients are expanded scalars)
     ref = lp_grad_ref(z.float().numpy(), y.numpy(), np.full(6, 2.0), np.full(6, -1 / 6))
     assert rel_fro(f64(zr.grad), ref) <= 1e-5
+    one = z.float().cuda()[:1].requires_grad_()
+    wide = token_logprobs(one.expand(3, 50), torch.tensor([1, 2, 3]).cuda())  # rows share memory
+    wide.logp.sum().backward()
+    refw = lp_grad_ref(z[:1].expand(3, 50).float().numpy(), np.array([1, 2, 3]), np.ones(3), None)
+    assert rel_fro(f64(one.grad), refw.sum(0, keepdims=True)) <= 1e-5
     zt = z.float().cuda().T.contiguous().T.requires_grad_()  # columns contiguous
     r2 = token_logprobs(zt, y.cuda())
     r2.logp.sum().backward()
