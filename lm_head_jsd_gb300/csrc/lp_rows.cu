@@ -9,7 +9,7 @@
 // now takes 38, 2047 x 128255 bf16). k_lp_grad is elementwise. HBM bounds both for
 // fp32 (1023 x 128255: 81 us = 6.5 TB/s, the gradient 160 us = 6.5 TB/s, 0.96 of a
 // copy's rate); for bf16 k_lp_rows, with twice the elements to a byte, is bound by
-// issue (2047 x 128255: 96 us = 5.5 TB/s, about nine instructions an element), the
+// issue (2047 x 128255: 96 us = 5.5 TB/s, ten instructions an element), the
 // gradient by HBM (165 us = 6.3 TB/s).
 #include "lp.cuh"
 #include "jsd_math.cuh"

@@ -10,6 +10,8 @@
 //    slices of L2; read again for every tile by every SM, it held the stream up
 //    (one row took 220 us where sixteen took 175 us; H = 4096, V = 128256);
 //  - the rest of shared memory is the ring of w's tiles, 16 KB each.
+// H = 4096, V = 128256: bf16 163 us = 6.4 TB/s, e4m3 86 us = 6.1 TB/s (0.95 and 0.90 of
+// a copy's rate).
 // e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
 // ring of eight, and is scaled and added in fp32 registers.
 #include "gemm_tc_kernel.cuh"
