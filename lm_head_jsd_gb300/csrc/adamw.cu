@@ -147,15 +147,16 @@ template <typename P, typename G, int BITS, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table<CAP> t,
                                                     const Hyper h) {
   const float scale = h.scale ? *h.scale : 1.f;
+  int at = 0;  // the last tensor that starts at or before chunk c (it only rises)
   for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    int at = 0;  // the last tensor that starts at or before chunk c
-    for (int end = t.count; end - at > 1;) {
-      const int mid = (at + end) / 2;
-      if (c >= t.first[mid])
-        at = mid;
-      else
-        end = mid;
-    }
+    if (c >= t.first[at + 1])
+      for (int end = t.count; end - at > 1;) {
+        const int mid = (at + end) / 2;
+        if (c >= t.first[mid])
+          at = mid;
+        else
+          end = mid;
+      }
     const Entry& e = t.e[at];
     const int64_t i0 = (c - t.first[at]) * kChunk + threadIdx.x * kPer;
     const int n = (int)max((int64_t)0, min((int64_t)kPer, e.n - i0));  // this thread's elements

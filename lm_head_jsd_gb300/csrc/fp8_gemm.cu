@@ -10,17 +10,20 @@
 // form one block's sums, eight warps add the other's, scaled, to 128 fp32 registers
 // a thread (one row, half of the columns). A scale that is no power of two cannot be
 // applied by the tensor cores, and folding it into the codes would round them again.
-// Scales are read two blocks ahead: their way from L2 is longer than a block's
-// products (read one block ahead: 650 ns a block instead of 572).
+// Two more warps bring the scales: they multiply x's of each row with w's of each
+// half of the columns into shared memory as soon as an accumulator is free, long
+// before its products are done, and what the epilogue waits for is all three. (Loaded
+// by the epilogue itself, however far ahead, they cost it 90 ns a block.)
 //
 // What bounds it, in ns for each 128 x 256 x 128 block of a tile (4096 x 32768 x
-// 4096): 547 as it is; 457 with the products left out, of which the additions alone
-// are 151; 439 with the accumulators handed back unread; 347 for the products with
-// nothing but the copies' barriers. So the additions' pass over the accumulator,
-// 2.6 cycles for each FFMA2 and about 2 for each column read, sets the pace, and the
-// hand-overs between two accumulators add a fifth. Tried and slower: CTA pairs on
-// 256 x 256 tiles (570), sixteen epilogue warps of 64 columns (598), four
-// accumulators of 128 columns (857), loads of 64 columns at once (667).
+// 4096): 500 as it is = 2.55 PFLOP/s; 376 with the products left out; 439 with the
+// accumulators handed back unread; 347 for the products with nothing but the copies'
+// barriers. The additions alone (2.6 cycles for each FFMA2) are 151 and reading the
+// accumulator about as much; what the two accumulators add is the way from commit to
+// hand-back and on to the next products. Tried and slower, before the scales had their
+// own warps (then 547): CTA pairs on 256 x 256 tiles (570), sixteen epilogue warps of
+// 64 columns (598), three accumulators of 160 columns (770), four of 128 (857), loads
+// of 64 columns at once (667).
 //
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).
@@ -46,7 +49,9 @@ constexpr int F_REGS_LOW = 40, F_REGS_HIGH = 232;
 constexpr int F_THREADS = 128 + 32 * F_EPI;
 constexpr int F_STAGES = 4;
 constexpr int F_STAGE_BYTES = (BM + BN) * FB;
-constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * F_OUT_BYTES + 1024 + CTRL_BYTES;
+constexpr int F_SCALES = F_ACCS * 2 * BM;  // of each accumulator: column half x row
+constexpr int F_SMEM = F_STAGES * F_STAGE_BYTES + F_EPI * F_OUT_BYTES +
+                       F_SCALES * (int)sizeof(float) + 1024 + CTRL_BYTES;
 static_assert(F_SMEM <= SMEM_MAX && F_STAGES <= STAGES && F_ACCS == 2, "control block and memory");
 
 // fp32 accumulator, e4m3 operands (format 0), both K-major
@@ -116,7 +121,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* stg = smem_raw + (base - raw) + F_STAGES * F_STAGE_BYTES;
-  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + F_EPI * F_OUT_BYTES);
+  float* scales = reinterpret_cast<float*>(stg + F_EPI * F_OUT_BYTES);
+  Ctrl* cb = reinterpret_cast<Ctrl*>(scales + F_SCALES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < F_STAGES; ++s) {
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       mbar_init(smem_u32(&cb->empty[s]), 1);
     }
     for (int a = 0; a < F_ACCS; ++a) {
-      mbar_init(smem_u32(&cb->tmem_full[a]), 1);
+      mbar_init(smem_u32(&cb->tmem_full[a]), 3);  // the products, and two warps of scales
       mbar_init(smem_u32(&cb->tmem_empty[a]), F_EPI);
     }
     mbar_init(smem_u32(&cb->drain), 1);
@@ -222,6 +228,36 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         wait_bar(cb, smem_u32(&cb->drain), 0, p.status);
       }
     }
+    // ---------------- scales: rows 32 (warp - 2) + lane and 64 more ----------------
+    if (warp >= 2) {
+      const int r0 = (warp - 2) * 32 + lane;
+      uint32_t use = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
+        int mb, nb;
+        tile_coords(t, mb, nb);
+        const int64_t row = (int64_t)mb * BM + r0;
+        const float* sx0 = p.sx + (row < p.m ? row : 0);
+        const float* sx1 = p.sx + (row + 64 < p.m ? row + 64 : 0);
+        const float* sw0 = p.sw + (int64_t)nb * 2 * p.num_k_blocks;
+        const float* sw1 = sw0 + ((int64_t)nb * BN + 128 < p.n ? p.num_k_blocks : 0);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++use) {
+          const float x0 = __ldg(sx0 + (int64_t)kb * p.m), x1 = __ldg(sx1 + (int64_t)kb * p.m);
+          const float w0 = __ldg(sw0 + kb), w1 = __ldg(sw1 + kb);
+          const int acc = use & 1;
+          ok = wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use >> 1) & 1) ^ 1u, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float* to = scales + acc * 2 * BM + r0;
+          to[0] = x0 * w0;
+          to[64] = x1 * w0;
+          to[BM] = x0 * w1;
+          to[BM + 64] = x1 * w1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&cb->tmem_full[acc]));
+        }
+      }
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F_REGS_HIGH));
     // ---------------- epilogue: one row of 128 columns to a thread ----------------
@@ -246,7 +282,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
       int mb, nb;
       tile_coords(t, mb, nb);
-      const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
+      const int64_t row0 = (int64_t)mb * BM + sub * 32;
       const int64_t col0 = (int64_t)nb * BN + grp * 128;
       const bool live = row0 < p.m && col0 < p.n;  // of this warp
       if (!live) {
@@ -259,20 +295,13 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       float2 sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
-      // scales of this block and the next two, x's of this row and w's of these columns
-      const float* sx = p.sx + (row < p.m ? row : 0);
-      const float* sw = p.sw + col0 / FB * p.num_k_blocks;
       const int last = p.num_k_blocks - 1;
-      float x0 = __ldg(sx), w0 = __ldg(sw);
-      float x1 = __ldg(sx + (int64_t)min(1, last) * p.m), w1 = __ldg(sw + min(1, last));
       full();
       if (!ok) break;
       ld_start(tsub + (use % F_ACCS) * ACC_COLS, ra);
       for (int kb = 0; kb <= last; ++kb) {
-        const int k2 = min(kb + 2, last);
-        const float x2 = __ldg(sx + (int64_t)k2 * p.m), w2 = __ldg(sw + k2);
         const uint32_t ta = tsub + (use % F_ACCS) * ACC_COLS;
-        const float s = x0 * w0;
+        const float s = scales[((use % F_ACCS) * 2 + grp) * BM + sub * 32 + lane];
         ld_wait(ra);
         ld_start(ta + 32, rb);
         add32(sum, ra, s);
@@ -290,8 +319,6 @@ __global__ void __launch_bounds__(F_THREADS, 1)
           ld_start(tsub + (use % F_ACCS) * ACC_COLS, ra);
         }
         add32(sum + 48, rb, s);
-        x0 = x1; w0 = w1;
-        x1 = x2; w1 = w2;
       }
       if (!ok) break;
       // ---- out: 64 bytes of a row at a time through shared memory ----
