@@ -15,10 +15,13 @@
 // before its products are done, and what the epilogue waits for is all three. (Loaded
 // by the epilogue itself, however far ahead, they cost it 90 ns a block.)
 //
-// What bounds it, in ns for each 128 x 256 x 128 block of a tile (4096 x 32768 x
-// 4096): 500 as it is = 2.55 PFLOP/s; 376 with the products left out; 439 with the
-// accumulators handed back unread; 347 for the products with nothing but the copies'
-// barriers. The additions alone (2.6 cycles for each FFMA2) are 151 and reading the
+// What bounds it: at full clocks a 128 x 256 x 128 block of a tile takes 960 cycles
+// (4096 x 32768 x 4096 of zeros, 403 us = 2.73 PFLOP/s), where the products alone would
+// take 512 and shared memory 768 (96 KB written and read again); with random codes the
+// card's power limit lowers the clock to 1.8 GHz (465 us). In ns for a block, before the
+// issuing warps stayed together (elect.cuh): 500; 376 with the products left out; 439
+// with the accumulators handed back unread; 347 for the products with nothing but the
+// copies' barriers. The additions alone (2.6 cycles for each FFMA2) are 151 and reading the
 // accumulator about as much; what the two accumulators add is the way from commit to
 // hand-back and on to the next products. Tried and slower, before the scales had their
 // own warps (then 547): CTA pairs on 256 x 256 tiles (570), sixteen epilogue warps of
@@ -27,6 +30,7 @@
 //
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).
+#include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
 #include "tensor_map.cuh"
@@ -158,8 +162,12 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F_REGS_LOW));
+    // (all lanes wait, one issues: elect.cuh)
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar(cb, bar, parity, p.status)) != 0;
+    };
     // ---------------- TMA producer ----------------
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t filled = 0;  // stages filled since the start
@@ -168,15 +176,18 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         int mb, nb;
         tile_coords(t, mb, nb);
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!wait_bar(cb, smem_u32(&cb->empty[stage]), phase ^ 1u, p.status)) {
+          if (!wait_all(smem_u32(&cb->empty[stage]), phase ^ 1u)) {
             ok = false;
             break;
           }
-          const uint32_t sa = base + stage * F_STAGE_BYTES;
-          const uint32_t fb = smem_u32(&cb->full[stage]);
-          mbar_arrive_expect_tx(fb, F_STAGE_BYTES);
-          tma_load_2d(sa, &tmA, fb, kb * FB, mb * BM);
-          tma_load_2d(sa + BM * FB, &tmB, fb, kb * FB, nb * BN);
+          if (elect_one()) {
+            const uint32_t sa = base + stage * F_STAGE_BYTES;
+            const uint32_t fb = smem_u32(&cb->full[stage]);
+            mbar_arrive_expect_tx(fb, F_STAGE_BYTES);
+            tma_load_2d(sa, &tmA, fb, kb * FB, mb * BM);
+            tma_load_2d(sa + BM * FB, &tmB, fb, kb * FB, nb * BN);
+          }
+          __syncwarp();
           ++filled;
           if (++stage == F_STAGES) {
             stage = 0;
@@ -191,32 +202,31 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       }
     }
     // ---------------- MMA issuer: one accumulator for each 128-deep block ----------------
-    if (warp == 1 && lane == 0) {
+    if (warp == 1) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t use = 0;  // accumulators handed out
       bool ok = true;
       for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
-        for (int kb = 0; ok && kb < p.num_k_blocks; ++kb) {
-          if (!wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
-            ok = false;
-            break;
-          }
+        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
           const uint32_t acc = use % F_ACCS;
-          if (!wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use / F_ACCS) & 1u) ^ 1u,
-                             p.status)) {
+          if (!wait_all(smem_u32(&cb->full[stage]), phase) ||
+              !wait_all(smem_u32(&cb->tmem_empty[acc]), ((use / F_ACCS) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
           ++use;
           tc_fence_after();
-          const uint32_t sa = base + stage * F_STAGE_BYTES, sb = sa + BM * FB;
+          if (elect_one()) {
+            const uint32_t sa = base + stage * F_STAGE_BYTES, sb = sa + BM * FB;
 #pragma unroll
-          for (int kk = 0; kk < FB / F_UMMA_K; ++kk)
-            mma_e4m3(tmem_base + acc * ACC_COLS, smem_desc(sa + kk * F_UMMA_K, 16, 1024),
-                           smem_desc(sb + kk * F_UMMA_K, 16, 1024), kk > 0 ? 1u : 0u);
-          mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
-          mma_commit<false>(smem_u32(&cb->empty[stage]));
+            for (int kk = 0; kk < FB / F_UMMA_K; ++kk)
+              mma_e4m3(tmem_base + acc * ACC_COLS, smem_desc(sa + kk * F_UMMA_K, 16, 1024),
+                       smem_desc(sb + kk * F_UMMA_K, 16, 1024), kk > 0 ? 1u : 0u);
+            mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
+            mma_commit<false>(smem_u32(&cb->empty[stage]));
+          }
+          __syncwarp();
           if (++stage == F_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -224,7 +234,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         }
       }
       if (use > 0) {
-        mma_commit<false>(smem_u32(&cb->drain));
+        if (elect_one()) mma_commit<false>(smem_u32(&cb->drain));
+        __syncwarp();
         wait_bar(cb, smem_u32(&cb->drain), 0, p.status);
       }
     }

@@ -35,6 +35,7 @@
 // = 1.90 PFLOP/s, 0.96 of the measured burst rate (power-capped: 1.10 of the sustained
 // one). Bound by the tensor cores down to H of about 1024; at H = 512 by the epilogue
 // (4096 rows, V = 40960: 118 us, 232 with 8 alternatives, for 87 us of products).
+#include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "lp.cuh"
 #include "tensor_map.cuh"
@@ -202,25 +203,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     mb = PAIR ? 2 * mu + (int)rank : mu;
   };
 
+  // (all lanes wait, one issues: elect.cuh)
+  auto wait_all = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bar(cb, bar, parity, p.status)) != 0;
+  };
   if (warp == 0) {
     // ---------------- TMA producer (hand-over of a pair's stages: gemm_tc_kernel.cuh) ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued_parity[STAGES];
-      bool issued[STAGES];
-      for (int s = 0; s < STAGES; ++s) issued[s] = false;
-      bool ok = true;
-      const uint32_t flip = (PAIR && !leader) ? 0u : 1u;
-      for (int t = unit0; ok && t < p.num_units; t += unit_step) {
-        int mb, nb;
-        tile_coords(t, mb, nb);
-        const int nrow = nb * BN + (PAIR ? (int)rank * (BN / 2) : 0);
-        for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!wait_bar(cb, smem_u32(&cb->empty[stage]), phase ^ flip, p.status)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t filled = 0;  // stages filled since the start
+    bool ok = true;
+    const uint32_t flip = (PAIR && !leader) ? 0u : 1u;
+    for (int t = unit0; ok && t < p.num_units; t += unit_step) {
+      int mb, nb;
+      tile_coords(t, mb, nb);
+      const int nrow = nb * BN + (PAIR ? (int)rank * (BN / 2) : 0);
+      for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+        if (!wait_all(smem_u32(&cb->empty[stage]), phase ^ flip)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t sa = base + stage * SB;
           uint32_t fb;
           if (PAIR) {
@@ -235,21 +238,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tma_operand<PAIR>(sa, &tmA, fb, kb * BK, mb * BM);
           tma_operand<PAIR>(sa + A_BYTES, &tmB, fb, kb * BK, nrow);
-          issued[stage] = true;
-          issued_parity[stage] = phase;
-          if (++stage == p.nst) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++stage == p.nst) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!PAIR || leader)
-        for (int s = 0; s < STAGES; ++s)
-          if (issued[s]) wait_bar(cb, smem_u32(&cb->full[s]), issued_parity[s], p.status);
     }
+    // every copy has landed before the CTA may exit: the last fill of each stage
+    if (!PAIR || leader)
+      for (int s = 0; s < p.nst; ++s) {
+        const uint32_t fills = filled / p.nst + ((uint32_t)s < filled % p.nst ? 1u : 0u);
+        if (fills > 0) wait_bar(cb, smem_u32(&cb->full[s]), (fills - 1) & 1u, p.status);
+      }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0 && leader) {
+    if (leader) {
       constexpr uint32_t idesc = instr_desc(false, false, PAIR);
       int stage = 0;
       uint32_t phase = 0;
@@ -258,23 +264,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;
       for (int t = unit0; ok && t < p.num_units; t += unit_step, ++local) {
         const int acc = local & 1;
-        if (!wait_bar<PAIR>(cb, smem_u32(&cb->tmem_empty[acc]), ((local >> 1) & 1) ^ 1u, p.status))
+        if (!__all_sync(0xffffffffu, wait_bar<PAIR>(cb, smem_u32(&cb->tmem_empty[acc]),
+                                                    ((local >> 1) & 1) ^ 1u, p.status)))
           break;
         tc_fence_after();
         const uint32_t tmem_d = tmem_base + acc * ACC_COLS;
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-          if (!wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
+          if (!wait_all(smem_u32(&cb->full[stage]), phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + stage * SB;
+          if (elect_one()) {
+            const uint32_t sa = base + stage * SB;
 #pragma unroll
-          for (int kk = 0; kk < BK / UMMA_K; ++kk)
-            mma_bf16<PAIR>(tmem_d, smem_desc(sa + kk * (UMMA_K * 2), 16, 1024),
-                           smem_desc(sa + A_BYTES + kk * (UMMA_K * 2), 16, 1024), idesc,
-                           (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit<PAIR>(smem_u32(&cb->empty[stage]));
+            for (int kk = 0; kk < BK / UMMA_K; ++kk)
+              mma_bf16<PAIR>(tmem_d, smem_desc(sa + kk * (UMMA_K * 2), 16, 1024),
+                             smem_desc(sa + A_BYTES + kk * (UMMA_K * 2), 16, 1024), idesc,
+                             (kb > 0 || kk > 0) ? 1u : 0u);
+            mma_commit<PAIR>(smem_u32(&cb->empty[stage]));
+          }
+          __syncwarp();
           any = true;
           if (++stage == p.nst) {
             stage = 0;
@@ -282,10 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        mma_commit<PAIR>(smem_u32(&cb->tmem_full[acc]));
+        if (elect_one()) mma_commit<PAIR>(smem_u32(&cb->tmem_full[acc]));
+        __syncwarp();
       }
       if (any) {
-        mma_commit<PAIR>(smem_u32(&cb->drain));
+        if (elect_one()) mma_commit<PAIR>(smem_u32(&cb->drain));
+        __syncwarp();
         wait_bar(cb, smem_u32(&cb->drain), 0, p.status);
       }
     }
@@ -316,8 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the least of the row's group maxima, read from L2 (0: a group has none yet)
       auto least = [&]() {
         unsigned l = 0xffffffffu;
-        if (row_ok)
+        if (row_ok) {
+#pragma unroll 8
           for (int j = 0; j < p.top; ++j) l = min(l, __ldcg(p.gmax + row * p.top + j));
+        }
         return l;
       };
       unsigned low = listed ? least() : 0xffffffffu;

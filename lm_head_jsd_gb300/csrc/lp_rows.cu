@@ -282,11 +282,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
   }
 }
 
+// CTAs an SM that the registers leave room for. The product's lists take 40 registers at
+// no loss (333 rows, 20 alternatives: three CTAs of 512 threads 14 us, two 17; 4096 rows:
+// twelve of 128 threads 29 us, eight 33); the loads from given logits would spill.
+template <typename SRC, int THREADS>
+constexpr int kJoinCtas = std::is_same<SRC, void>::value ? (THREADS == kJoinFew ? 3 : 12)
+                                                         : (THREADS == kJoinFew ? 2 : 8);
 // One CTA to a row: its parts into the row's results, its candidates into the
 // k largest. SRC: where the candidates are; void: lists and written-out logits of
 // the product, else given logits of that type.
 template <typename SRC, int kJoinThreads>
-__global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) k_lp_join(LpJoinArgs a) {
   constexpr bool kRowsSrc = !std::is_same<SRC, void>::value;
   constexpr int W = kJoinThreads / 32;
   __shared__ Mds shm[W];
@@ -347,12 +353,32 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
     if (tid == 0) sh_least = 0;
     __syncthreads();
     int gt = 0, ge = 0;
+    if constexpr (kJoinThreads == kJoinFew) {
+      // four threads to a value, each against a quarter of them: 2 us less
+      const unsigned quad = 0xfu << (tid & 28);
+      for (int i = tid >> 2; i < n; i += kJoinThreads / 4) {
+        const unsigned x = keys[i];
+        gt = ge = 0;
 #pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      gt += keys[j] > mine ? 1 : 0;
-      ge += keys[j] >= mine ? 1 : 0;
+        for (int j = tid & 3; j < n; j += 4) {
+          gt += keys[j] > x ? 1 : 0;
+          ge += keys[j] >= x ? 1 : 0;
+        }
+#pragma unroll
+        for (int o = 2; o > 0; o >>= 1) {
+          gt += __shfl_xor_sync(quad, gt, o);
+          ge += __shfl_xor_sync(quad, ge, o);
+        }
+        if ((tid & 3) == 0 && gt < a.k && a.k <= ge) sh_least = x;  // (equal ones write the same)
+      }
+    } else {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        gt += keys[j] > mine ? 1 : 0;
+        ge += keys[j] >= mine ? 1 : 0;
+      }
+      if (tid < n && gt < a.k && a.k <= ge) sh_least = mine;
     }
-    if (tid < n && gt < a.k && a.k <= ge) sh_least = mine;  // (equal threads write the same)
     __syncthreads();
     return sh_least;
   };
@@ -371,8 +397,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(LpJoinArgs a) {
     }
     least = kth_of_threads(mine, (int)(chunks < kJoinThreads ? chunks : kJoinThreads));
   } else {
-    least = 0xffffffffu;
-    for (int j = 0; j < a.k; ++j) least = min(least, a.gmax[r * a.k + j]);
+    const int lane = tid & 31;  // (k is at most 32)
+    least = __reduce_min_sync(0xffffffffu, lane < a.k ? a.gmax[r * a.k + lane] : 0xffffffffu);
   }
   // every candidate's key that reaches `least`
   auto each = [&](auto&& f) {
@@ -601,7 +627,7 @@ void launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  if (a.rows <= num_sms() * 4)  // 512 threads, four CTAs an SM: one round
+  if (a.rows <= num_sms() * 4)  // 512 threads
     launch_join_t<kJoinFew>(a, st);
   else
     launch_join_t<kJoinMany>(a, st);

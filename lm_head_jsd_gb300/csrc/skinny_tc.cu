@@ -14,6 +14,7 @@
 // a copy's rate).
 // e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
 // ring of eight, and is scaled and added in fp32 registers.
+#include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
 #include "tensor_map.cuh"
@@ -152,66 +153,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = cb->tmem_base;
 
+  // (all lanes wait, one issues: elect.cuh)
+  auto wait_all = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, sk_wait(cb, bar, parity, p.status)) != 0;
+  };
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t filled = 0;  // stages filled since the start
-      bool ok = true;
-      if (p.resident && (int)blockIdx.x < p.num_tiles) {
-        const uint32_t xb = smem_u32(&cb->x_full);
-        mbar_arrive_expect_tx(xb, nkb * kXBlock);
-        for (int kb = 0; kb < nkb; ++kb) tma_load_2d(xbase + kb * kXBlock, &tmX, xb, kb * KE, 0);
-      }
-      for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!sk_wait(cb, smem_u32(&cb->empty[stage]), phase ^ 1u, p.status)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t filled = 0;  // stages filled since the start
+    bool ok = true;
+    if (p.resident && (int)blockIdx.x < p.num_tiles && elect_one()) {
+      const uint32_t xb = smem_u32(&cb->x_full);
+      mbar_arrive_expect_tx(xb, nkb * kXBlock);
+      for (int kb = 0; kb < nkb; ++kb) tma_load_2d(xbase + kb * kXBlock, &tmX, xb, kb * KE, 0);
+    }
+    __syncwarp();
+    for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!wait_all(smem_u32(&cb->empty[stage]), phase ^ 1u)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t dst = wbase + stage * sb, fb = smem_u32(&cb->full[stage]);
           mbar_arrive_expect_tx(fb, sb);
           tma_load_2d(dst, &tmW, fb, kb * KE, t * BM);
           if (!p.resident) tma_load_2d(dst + kStage, &tmX, fb, kb * KE, 0);
-          ++filled;
-          if (++stage == p.nst) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++stage == p.nst) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every copy has landed before the CTA may exit: the last fill of each stage
-      if (p.resident && (int)blockIdx.x < p.num_tiles)
-        sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
-      for (int s = 0; s < p.nst; ++s) {
-        const uint32_t fills = filled / p.nst + ((uint32_t)s < filled % p.nst ? 1u : 0u);
-        if (fills > 0) sk_wait(cb, smem_u32(&cb->full[s]), (fills - 1) & 1u, p.status);
-      }
+    }
+    // every copy has landed before the CTA may exit: the last fill of each stage
+    if (p.resident && (int)blockIdx.x < p.num_tiles)
+      sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
+    for (int s = 0; s < p.nst; ++s) {
+      const uint32_t fills = filled / p.nst + ((uint32_t)s < filled % p.nst ? 1u : 0u);
+      if (fills > 0) sk_wait(cb, smem_u32(&cb->full[s]), (fills - 1) & 1u, p.status);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t use = 0;  // accumulators handed out
-      bool any = false;
-      bool ok = true;
-      if (p.resident && (int)blockIdx.x < p.num_tiles)
-        ok = sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
-      for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int acc = use % kAccs;
-          if ((E4M3 || kb == 0) && !sk_wait(cb, smem_u32(&cb->tmem_empty[acc]),
-                                            ((use / kAccs) & 1u) ^ 1u, p.status)) {
-            ok = false;
-            break;
-          }
-          if (!sk_wait(cb, smem_u32(&cb->full[stage]), phase, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t use = 0;  // accumulators handed out
+    bool any = false;
+    bool ok = true;
+    if (p.resident && (int)blockIdx.x < p.num_tiles) ok = wait_all(smem_u32(&cb->x_full), 0);
+    for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int acc = use % kAccs;
+        if (((E4M3 || kb == 0) &&
+             !wait_all(smem_u32(&cb->tmem_empty[acc]), ((use / kAccs) & 1u) ^ 1u)) ||
+            !wait_all(smem_u32(&cb->full[stage]), phase)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool last = E4M3 || kb == nkb - 1;  // of this accumulator
+        if (elect_one()) {
           const uint32_t sa = wbase + stage * sb;
           const uint32_t sx = p.resident ? xbase + kb * kXBlock : sa + kStage;
 #pragma unroll
@@ -219,21 +223,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma16<E4M3>(tmem_base + acc * kAccCols, smem_desc(sa + kk * 32, 16, 1024),
                         smem_desc(sx + kk * 32, 16, 1024), (kk > 0 || (!E4M3 && kb > 0)) ? 1u : 0u);
           mma_commit<false>(smem_u32(&cb->empty[stage]));
-          any = true;
-          if (E4M3 || kb == nkb - 1) {
-            mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
-            ++use;
-          }
-          if (++stage == p.nst) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (last) mma_commit<false>(smem_u32(&cb->tmem_full[acc]));
+        }
+        __syncwarp();
+        any = true;
+        if (last) ++use;
+        if (++stage == p.nst) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (any) {
-        mma_commit<false>(smem_u32(&cb->drain));
-        sk_wait(cb, smem_u32(&cb->drain), 0, p.status);
-      }
+    }
+    if (any) {
+      if (elect_one()) mma_commit<false>(smem_u32(&cb->drain));
+      __syncwarp();
+      sk_wait(cb, smem_u32(&cb->drain), 0, p.status);
     }
   } else {
     // ---------------- epilogue: one row of w (a column of out) to a thread ----------------
