@@ -45,7 +45,7 @@ struct LpJoinArgs {
   const int2* cand;    // [rows x cap] (value bits, column)
   int64_t cap;
   const int* count;    // [rows] candidates of each row
-  const unsigned* gmax;  // [rows x k] group maxima (see lp_head_tc.cu)
+  const unsigned* gmax;  // [k x rows] group maxima (see lp_head_tc.cu)
   const float* dump;   // [rows x dump_cols] logits of the first columns, or null
   int64_t dump_cols;
   // from given logits:
@@ -100,7 +100,7 @@ struct LpHeadArgs {
   int64_t parts;
   float* zy;
   int top;
-  unsigned* gmax;      // [m x top], zeroed
+  unsigned* gmax;      // [top x m], zeroed
   int* count;          // [m], zeroed
   int2* cand;          // [m x parts * top]
   float* dump;         // [m x 256 dump_blocks] logits of the first 256-column blocks

@@ -63,23 +63,27 @@ struct HeadParams {
   unsigned* gmax;
   int* count;
   int2* cand;
-  float* dump;
   int dump_blocks;
   unsigned long long timeout_ns;
   int* status;
 };
 
-__host__ __device__ constexpr int head_smem(int nst, bool pair, bool keep) {
-  return nst * stage_bytes(pair) + (keep ? kEpiWarps * kKeepBufs * OUT_BUF_BYTES : 0) + 1024 +
+// Staging buffers of an epilogue warp: of 2^t two, one of which the first columns'
+// logits borrow.
+__host__ __device__ constexpr int stage_bufs(bool top, bool keep) {
+  return keep ? kKeepBufs : top ? 1 : 0;
+}
+__host__ __device__ constexpr int head_smem(int nst, bool pair, bool top, bool keep) {
+  return nst * stage_bytes(pair) + kEpiWarps * stage_bufs(top, keep) * OUT_BUF_BYTES + 1024 +
          CTRL_BYTES;
 }
 __host__ __device__ constexpr int head_stages(bool pair, bool keep) {
   return pair ? (keep ? 5 : 6) : (keep ? 3 : 4);
 }
-static_assert(head_smem(head_stages(true, true), true, true) <= SMEM_MAX &&
-                  head_smem(head_stages(true, false), true, false) <= SMEM_MAX &&
-                  head_smem(head_stages(false, true), false, true) <= SMEM_MAX &&
-                  head_smem(head_stages(false, false), false, false) <= SMEM_MAX,
+static_assert(head_smem(head_stages(true, true), true, true, true) <= SMEM_MAX &&
+                  head_smem(head_stages(true, false), true, true, false) <= SMEM_MAX &&
+                  head_smem(head_stages(false, true), false, true, true) <= SMEM_MAX &&
+                  head_smem(head_stages(false, false), false, true, false) <= SMEM_MAX,
               "shared memory");
 
 // A thread's list of its part's largest logits, in descending order; ties keep
@@ -154,13 +158,14 @@ static __device__ __noinline__ void list_part(uint32_t tacc, int ncols, int col0
 template <bool PAIR, bool TOP, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     k_lp_head(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmE, const HeadParams p) {
+              const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmD,
+              const HeadParams p) {
   constexpr int SB = stage_bytes(PAIR);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* stg = smem_raw + (base - raw) + p.nst * SB;
-  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + (KEEP ? kEpiWarps * kKeepBufs * OUT_BUF_BYTES : 0));
+  Ctrl* cb = reinterpret_cast<Ctrl*>(stg + kEpiWarps * stage_bufs(TOP, KEEP) * OUT_BUF_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -181,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
     if (KEEP) prefetch_tensormap(&tmE);
+    if (TOP) prefetch_tensormap(&tmD);
   }
   if (PAIR) cluster_sync_all();
   if (warp == 1) tmem_alloc<PAIR>(smem_u32(&cb->tmem_base), TMEM_COLS);
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned l = 0xffffffffu;
         if (row_ok) {
 #pragma unroll 8
-          for (int j = 0; j < p.top; ++j) l = min(l, __ldcg(p.gmax + row * p.top + j));
+          for (int j = 0; j < p.top; ++j) l = min(l, __ldcg(p.gmax + j * p.m + row));
         }
         return l;
       };
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part = nb * 2 + grp;
         // (at once: the tiles that come next are waiting for a threshold)
         if (TOP && row_ok && mx > -INFINITY)
-          atomicMax(p.gmax + row * p.top + part % p.top, lp_key(mx));
+          atomicMax(p.gmax + (part % p.top) * p.m + row, lp_key(mx));
         int2* dst = nullptr;
         if (listed) {
           int n = hits();
@@ -422,11 +428,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c + e >= ncols) v[e] = -INFINITY;
           }
           if (TOP && !listed) {
-            if (row_ok) {
-              float4* o = reinterpret_cast<float4*>(p.dump + row * p.dump_blocks * BN + col0 + c);
+            // 32 rows of 128 bytes; of 2^t's buffers the one that is not being filled
+            uint8_t* buf = stg + (ew * stage_bufs(TOP, KEEP) + (KEEP ? sbuf ^ 1 : 0)) * OUT_BUF_BYTES;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmD, smem_u32(buf), col0 + c, (int32_t)row0);
+              bulk_commit();
             }
           } else if (TOP) {
             unsigned w = 0;
@@ -488,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&cb->tmem_empty[acc]));
       }
     }
-    if (KEEP && lane == 0) bulk_wait_all();
+    if ((KEEP || TOP) && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -503,13 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool PAIR, bool TOP, bool KEEP>
 cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
-                     const HeadParams& p, cudaStream_t st) {
+                     const CUtensorMap& md, const HeadParams& p, cudaStream_t st) {
   auto kern = k_lp_head<PAIR, TOP, KEEP>;
-  const int smem = head_smem(p.nst, PAIR, KEEP);
+  const int smem = head_smem(p.nst, PAIR, TOP, KEEP);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
   if (e != cudaSuccess) return e;
   if (!PAIR) {
-    kern<<<p.num_units < num_sms() ? p.num_units : num_sms(), kThreads, smem, st>>>(ma, mb, me, p);
+    kern<<<p.num_units < num_sms() ? p.num_units : num_sms(), kThreads, smem, st>>>(ma, mb, me, md, p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -533,15 +547,15 @@ cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
     if (dev >= 0 && dev < 64) resident[dev] = most;
   }
   cfg.gridDim = dim3(2 * (p.num_units < most ? p.num_units : most));
-  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, me, p);
+  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, me, md, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool PAIR, bool KEEP>
 cudaError_t launch_k(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
-                     const HeadParams& p, cudaStream_t st) {
-  return p.top ? launch_v<PAIR, true, KEEP>(ma, mb, me, p, st)
-               : launch_v<PAIR, false, KEEP>(ma, mb, me, p, st);
+                     const CUtensorMap& md, const HeadParams& p, cudaStream_t st) {
+  return p.top ? launch_v<PAIR, true, KEEP>(ma, mb, me, md, p, st)
+               : launch_v<PAIR, false, KEEP>(ma, mb, me, md, p, st);
 }
 
 }  // namespace
@@ -588,12 +602,16 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   if (!lp_head_supported(a)) return cudaErrorInvalidValue;
   const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms());
   const bool pair = h.pair, keep = a.e != nullptr;
-  CUtensorMap ma, mb, me;
+  CUtensorMap ma, mb, me, md;
   if (!make_tensor_map(&ma, MapType::kBf16, a.x, a.k, a.m, a.ldx, BK, BM) ||
       !make_tensor_map(&mb, MapType::kBf16, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
     return cudaErrorInvalidValue;
   me = ma;
   if (keep && !make_tensor_map(&me, MapType::kBf16, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
+  md = ma;
+  if (a.top > 0 && !make_tensor_map(&md, MapType::kF32, a.dump, (int64_t)a.dump_blocks * BN, a.m,
+                                 (int64_t)a.dump_blocks * BN, 32, 32))
+    return cudaErrorInvalidValue;
   HeadParams p{};
   p.m = a.m; p.n = a.n;
   p.num_n_blocks = (int)h.nblocks;
@@ -604,12 +622,12 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   p.group_m = (int)h.group_m;
   p.nst = head_stages(pair, keep);
   p.c = a.c; p.labels = a.labels; p.part = a.part; p.parts = a.parts; p.zy = a.zy;
-  p.dump = a.dump; p.dump_blocks = a.dump_blocks;
+  p.dump_blocks = a.dump_blocks;
   p.top = a.top; p.gmax = a.gmax; p.count = a.count; p.cand = a.cand;
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;
-  if (pair) return keep ? launch_k<true, true>(ma, mb, me, p, st) : launch_k<true, false>(ma, mb, me, p, st);
-  return keep ? launch_k<false, true>(ma, mb, me, p, st) : launch_k<false, false>(ma, mb, me, p, st);
+  if (pair) return keep ? launch_k<true, true>(ma, mb, me, md, p, st) : launch_k<true, false>(ma, mb, me, md, p, st);
+  return keep ? launch_k<false, true>(ma, mb, me, md, p, st) : launch_k<false, false>(ma, mb, me, md, p, st);
 }
 
 }  // namespace fljsd

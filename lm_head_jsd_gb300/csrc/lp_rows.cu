@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
     least = kth_of_threads(mine, (int)(chunks < kJoinThreads ? chunks : kJoinThreads));
   } else {
     const int lane = tid & 31;  // (k is at most 32)
-    least = __reduce_min_sync(0xffffffffu, lane < a.k ? a.gmax[r * a.k + lane] : 0xffffffffu);
+    least = __reduce_min_sync(0xffffffffu, lane < a.k ? a.gmax[lane * a.rows + r] : 0xffffffffu);
   }
   // every candidate's key that reaches `least`
   auto each = [&](auto&& f) {
