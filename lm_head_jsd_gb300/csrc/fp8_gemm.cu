@@ -30,6 +30,7 @@
 //
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).
+#include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
@@ -401,6 +402,7 @@ __global__ void __launch_bounds__(256) k_quantise_rows(const T* x, int64_t ldx, 
                                                        int64_t cols, int64_t blocks, uint8_t* q,
                                                        int64_t ldq, float* scales, int* status) {
   const int lane = threadIdx.x & 31;
+  let_next_launch();
   if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const int64_t units = rows * blocks;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * 8) {
@@ -591,7 +593,7 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
     return FLJSD_ERR_CUDA;
   // a few rows are bound by reading w: the product arranged around that
   SkinnyArgs few{1, ws + L.codes, L.ldq, w_codes, ldw, m, n, k, sx, w_scales, out, ldo,
-                 out_dtype == FLJSD_BF16, status};
+                 out_dtype == FLJSD_BF16, status, true};
   cudaError_t e;
   trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
   if (skinny_supported(few))

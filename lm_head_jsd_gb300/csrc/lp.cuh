@@ -67,6 +67,7 @@ struct LpRowsArgs {
   float* zy;
   float* cmax;         // [rows x parts * LP_CHUNKS], or null
   int* status;         // set to 0, or null
+  bool own_logits;     // fp32, from the kernel launched just before
 };
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st);
 

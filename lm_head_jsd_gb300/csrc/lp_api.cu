@@ -175,6 +175,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
   r.part = reinterpret_cast<float4*>(ws + L.part);
   r.zy = reinterpret_cast<float*>(ws + L.zy);
   r.cmax = top ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
+  r.own_logits = true;
   return launch_lp_rows(FLJSD_F32, r, st);
 }
 

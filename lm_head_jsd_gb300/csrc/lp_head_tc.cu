@@ -35,6 +35,7 @@
 // = 1.90 PFLOP/s, 0.96 of the measured burst rate (power-capped: 1.10 of the sustained
 // one). Bound by the tensor cores down to H of about 1024; at H = 512 by the epilogue
 // (4096 rows, V = 40960: 118 us, 232 with 8 alternatives, for 87 us of products).
+#include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "lp.cuh"
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
+  let_next_launch();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {

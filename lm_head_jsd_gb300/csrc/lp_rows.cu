@@ -11,6 +11,7 @@
 // copy's rate); for bf16 k_lp_rows, with twice the elements to a byte, is bound by
 // issue (2047 x 128255: 96 us = 5.5 TB/s, ten instructions an element), the
 // gradient by HBM (165 us = 6.3 TB/s).
+#include "dependent.cuh"
 #include "lp.cuh"
 #include "jsd_math.cuh"
 
@@ -216,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
   const int tid = threadIdx.x;
   const int64_t part = blockIdx.x;
   constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80u;  // -inf
+  let_next_launch();
+  wait_for_previous();
   if (a.status && part == 0 && blockIdx.y == 0 && tid == 0) *a.status = 0;
   Raw<T> raw[V];
   auto load = [&](int64_t r) {
@@ -303,6 +306,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   __shared__ unsigned sh_least;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x, out = a.row0 + r;
+  wait_for_previous();
   const float4* ps = a.part + r * a.parts;
   // four parts in flight a thread
   Mds x{-INFINITY, 0.f, 0.f};
@@ -612,14 +616,13 @@ dim3 row_grid(int64_t segs, int64_t rows) {
 }
 
 template <int THREADS>
-void launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
+cudaError_t launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)a.rows;
   if (!a.z)
-    k_lp_join<void, THREADS><<<grid, THREADS, 0, st>>>(a);
-  else if (a.z_dtype == FLJSD_BF16)
-    k_lp_join<__nv_bfloat16, THREADS><<<grid, THREADS, 0, st>>>(a);
-  else
-    k_lp_join<float, THREADS><<<grid, THREADS, 0, st>>>(a);
+    return launch_dependent(k_lp_join<void, THREADS>, grid, THREADS, 0, st, a);
+  if (a.z_dtype == FLJSD_BF16)
+    return launch_dependent(k_lp_join<__nv_bfloat16, THREADS>, grid, THREADS, 0, st, a);
+  return launch_dependent(k_lp_join<float, THREADS>, grid, THREADS, 0, st, a);
 }
 
 }  // namespace
@@ -627,12 +630,10 @@ void launch_join_t(const LpJoinArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  if (a.rows <= num_sms() * 4)  // 512 threads
-    launch_join_t<kJoinFew>(a, st);
-  else
-    launch_join_t<kJoinMany>(a, st);
+  const cudaError_t e = a.rows <= num_sms() * 4 ? launch_join_t<kJoinFew>(a, st)  // 512 threads
+                                                : launch_join_t<kJoinMany>(a, st);
   trace_end(FLJSD_KERNEL_SMALL, st);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
@@ -640,12 +641,15 @@ cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
   const int64_t parts = lp_row_parts(a.v);
   const dim3 grid = row_grid(parts, a.rows);
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
-  if (dtype == FLJSD_BF16)
+  cudaError_t e = cudaSuccess;
+  if (a.own_logits)  // (fp32)
+    e = launch_dependent(k_lp_rows<float>, grid, kThreads, 0, st, a, parts);
+  else if (dtype == FLJSD_BF16)
     k_lp_rows<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, parts);
   else
     k_lp_rows<float><<<grid, kThreads, 0, st>>>(a, parts);
   trace_end(FLJSD_KERNEL_JSD_ROWS, st);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_lp_grad(int z_dtype, int out_dtype, bool from_e, const LpGradArgs& a,

@@ -14,6 +14,7 @@
 // a copy's rate).
 // e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
 // ring of eight, and is scaled and added in fp32 registers.
+#include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "skinny_tc.cuh"
@@ -47,6 +48,7 @@ static_assert(sizeof(SkCtrl) <= kCtrl, "control block");
 struct SkParams {
   int64_t m, n;
   int num_tiles, num_k_blocks, nst, resident;
+  bool own_x;
   const float *sx, *sw;
   void* out;
   int64_t ldo;
@@ -123,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t wbase = base + (p.resident ? nkb * kXBlock : 0);
   SkCtrl* cb = reinterpret_cast<SkCtrl*>(smem_raw + (wbase - raw) + p.nst * sb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_launch();
   constexpr int KE = E4M3 ? 128 : 64;  // elements in 128 bytes
 
   if (threadIdx.x == 0) {
@@ -143,11 +146,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmW);
   }
   if (warp == 1) tmem_alloc<false>(smem_u32(&cb->tmem_base), kTmemCols);
-  if (E4M3)
-    for (int i = threadIdx.x; i < nkb * SK_ROWS; i += kThreads) {
-      const int j = i % SK_ROWS;
-      s_sx[i] = j < p.m ? p.sx[(int64_t)(i / SK_ROWS) * p.m + j] : 0.f;
-    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -163,14 +161,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     uint32_t filled = 0;  // stages filled since the start
     bool ok = true;
-    if (p.resident && (int)blockIdx.x < p.num_tiles && elect_one()) {
-      const uint32_t xb = smem_u32(&cb->x_full);
-      mbar_arrive_expect_tx(xb, nkb * kXBlock);
-      for (int kb = 0; kb < nkb; ++kb) tma_load_2d(xbase + kb * kXBlock, &tmX, xb, kb * KE, 0);
-    }
-    __syncwarp();
+    // x is asked for once the stages are full of w (which x, where it shares them, cannot be)
+    bool have_x = false;
+    auto ask_x = [&]() {
+      wait_for_previous();
+      if (p.resident && (int)blockIdx.x < p.num_tiles && elect_one()) {
+        const uint32_t xb = smem_u32(&cb->x_full);
+        mbar_arrive_expect_tx(xb, nkb * kXBlock);
+        for (int kb = 0; kb < nkb; ++kb) tma_load_2d(xbase + kb * kXBlock, &tmX, xb, kb * KE, 0);
+      }
+      __syncwarp();
+      have_x = true;
+    };
+    if (!p.resident || !p.own_x) ask_x();
     for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
       for (int kb = 0; kb < nkb; ++kb) {
+        if (!have_x && filled == (uint32_t)p.nst) ask_x();
         if (!wait_all(smem_u32(&cb->empty[stage]), phase ^ 1u)) {
           ok = false;
           break;
@@ -189,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (!have_x) ask_x();
     // every copy has landed before the CTA may exit: the last fill of each stage
     if (p.resident && (int)blockIdx.x < p.num_tiles)
       sk_wait(cb, smem_u32(&cb->x_full), 0, p.status);
@@ -244,6 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = warp & 3;
     uint32_t use = 0;
     bool ok = true;
+    wait_for_previous();
+    if (E4M3) {
+      for (int i = threadIdx.x - 64; i < nkb * SK_ROWS; i += 128) {
+        const int j = i % SK_ROWS;
+        s_sx[i] = j < p.m ? p.sx[(int64_t)(i / SK_ROWS) * p.m + j] : 0.f;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
     for (int t = blockIdx.x; ok && t < p.num_tiles; t += gridDim.x) {
       const int64_t col = (int64_t)t * BM + sub * 32 + lane;
       float sum[SK_ROWS];
@@ -289,7 +304,9 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const SkParams&
   auto kern = k_skinny<E4M3, T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<p.num_tiles < num_sms() ? p.num_tiles : num_sms(), kThreads, smem, st>>>(mx, mw, p);
+  const int grid = p.num_tiles < num_sms() ? p.num_tiles : num_sms();
+  if (p.own_x) return launch_dependent(kern, grid, kThreads, smem, st, mx, mw, p);
+  kern<<<grid, kThreads, smem, st>>>(mx, mw, p);
   return cudaGetLastError();
 }
 
@@ -319,6 +336,7 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.sx = a.sx; p.sw = a.sw; p.out = a.out; p.ldo = a.ldo;
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;
+  p.own_x = a.own_x;
   CUtensorMap mx, mw;
   const MapType mt = a.e4m3 ? MapType::kU8 : MapType::kBf16;
   const bool ok = make_tensor_map(&mx, mt, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&

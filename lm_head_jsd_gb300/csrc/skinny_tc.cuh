@@ -20,6 +20,9 @@ struct SkinnyArgs {
   void* out; int64_t ldo;
   int out_bf16;
   int* status;
+  // x and sx come from the kernel launched just before, which does not write w or sw:
+  // w is on its way before that kernel has ended.
+  bool own_x;
 };
 // Whether the kernel takes the shape (alignment as for the tensor maps).
 bool skinny_supported(const SkinnyArgs& a);
