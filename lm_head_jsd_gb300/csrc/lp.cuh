@@ -57,6 +57,8 @@ struct LpJoinArgs {
   int64_t* top_id;     // [bt x k]
 };
 cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st);
+// Zeros over whole 16-byte units, by a kernel that the next may be launched behind.
+cudaError_t launch_zero(void* to, size_t bytes, cudaStream_t st);
 
 struct LpRowsArgs {
   const void* z;       // [rows x ld]
@@ -109,6 +111,7 @@ struct LpHeadArgs {
   void* e;             // [m x lde] fp16: 2^t_j relative to each part's maximum, or null
   int64_t lde;
   int* status;
+  bool own_zeros;      // count, gmax and status were zeroed by the kernel launched just before
 };
 bool lp_head_supported(const LpHeadArgs& a);
 // Blocks of 256 columns whose logits are best written out instead of listed.

@@ -129,10 +129,11 @@ cudaError_t lp_gemm(int kind, int dtype, bool tc, const void* a, int64_t lda, in
 }
 
 // The parts of one chunk's rows (and, with `keep`, 2^t or the logits) into the
-// workspace; `top` candidates of each row.
+// workspace; `top` candidates of each row. zeroed: launch_zero came just before;
+// first: the product of a few rows clears the status word.
 cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x, const void* w,
-                     const int64_t* labels, int64_t rows, int top, bool keep, char* ws,
-                     cudaStream_t st) {
+                     const int64_t* labels, int64_t rows, int top, bool keep, bool zeroed,
+                     bool first, char* ws, cudaStream_t st) {
   const float c = log2_scale(p.temperature);
   if (L.path == kFused) {
     LpHeadArgs h{};
@@ -150,6 +151,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     h.e = keep ? ws + L.z : nullptr;
     h.lde = L.ld;
     h.status = reinterpret_cast<int*>(ws + L.status);
+    h.own_zeros = zeroed;
     trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
     const cudaError_t e = launch_lp_head(h, st);
     trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
@@ -162,6 +164,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     k.x = x; k.ldx = p.h; k.w = w; k.ldw = p.h; k.m = rows; k.n = p.v; k.k = p.h;
     k.out = z; k.ldo = L.ld;
     k.status = reinterpret_cast<int*>(ws + L.status);
+    k.zero_status = first;
     trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
     e = launch_skinny(k, st);
     trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
@@ -276,12 +279,14 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
   char* ws = static_cast<char*>(workspace);
   for (int64_t r0 = 0; r0 < p->bt; r0 += c) {
     const int64_t rows = p->bt - r0 < c ? p->bt - r0 : c;
-    // the status word is reset once, the counts and thresholds for each chunk
+    // the status word is reset once (by the product of a few rows itself), the counts and
+    // thresholds for each chunk
     const size_t z0 = r0 == 0 ? L.zero : L.count, zb = L.zero + L.zero_bytes - z0;
-    if (zb && cudaMemsetAsync(ws + z0, 0, zb, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
+    const bool zeros = L.path != kFew && zb > 0;
+    if (zeros && launch_zero(ws + z0, zb, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
     const char* xc = static_cast<const char*>(x) + (size_t)r0 * p->h * dsize(p->dtype);
-    if (lp_chunk(*p, L, xc, w, labels ? labels + r0 : nullptr, rows, p->top_k, keep, ws, stream) !=
-        cudaSuccess)
+    if (lp_chunk(*p, L, xc, w, labels ? labels + r0 : nullptr, rows, p->top_k, keep, zeros, r0 == 0,
+                 ws, stream) != cudaSuccess)
       return FLJSD_ERR_CUDA;
     LpJoinArgs j{};
     j.rows = rows; j.row0 = r0; j.v = p->v;
@@ -341,7 +346,8 @@ fljsd_status fljsd_lp_backward(const fljsd_lp_problem* p, const fljsd_plan_t* pl
   for (int64_t r0 = 0; r0 < p->bt; r0 += c) {
     const int64_t rows = p->bt - r0 < c ? p->bt - r0 : c;
     const char* xc = static_cast<const char*>(x) + (size_t)r0 * p->h * s;
-    if (!kept && lp_chunk(*p, L, xc, w, nullptr, rows, 0, true, ws, stream) != cudaSuccess)
+    if (!kept &&
+        lp_chunk(*p, L, xc, w, nullptr, rows, 0, true, false, false, ws, stream) != cudaSuccess)
       return FLJSD_ERR_CUDA;
     LpGradArgs g{};
     g.z = ws + L.z; g.ldz = L.ld;

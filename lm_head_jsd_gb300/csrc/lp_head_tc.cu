@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ew = warp - 2;
     int local = 0;
     int sbuf = 0;
+    wait_for_previous();  // (the zeroed counts; the products need nothing of it)
     for (int t = unit0; t < p.num_units; t += unit_step, ++local) {
       int mb, nb;
       tile_coords(t, mb, nb);
@@ -519,17 +520,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool PAIR, bool TOP, bool KEEP>
 cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
-                     const CUtensorMap& md, const HeadParams& p, cudaStream_t st) {
+                     const CUtensorMap& md, const HeadParams& p, bool after, cudaStream_t st) {
   auto kern = k_lp_head<PAIR, TOP, KEEP>;
   const int smem = head_smem(p.nst, PAIR, TOP, KEEP);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
   if (e != cudaSuccess) return e;
   if (!PAIR) {
-    kern<<<p.num_units < num_sms() ? p.num_units : num_sms(), kThreads, smem, st>>>(ma, mb, me, md, p);
+    const int grid = p.num_units < num_sms() ? p.num_units : num_sms();
+    if (after) return launch_dependent(kern, grid, kThreads, smem, st, ma, mb, me, md, p);
+    kern<<<grid, kThreads, smem, st>>>(ma, mb, me, md, p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -549,15 +554,16 @@ cudaError_t launch_v(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
     if (dev >= 0 && dev < 64) resident[dev] = most;
   }
   cfg.gridDim = dim3(2 * (p.num_units < most ? p.num_units : most));
+  if (after) cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, ma, mb, me, md, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool PAIR, bool KEEP>
 cudaError_t launch_k(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& me,
-                     const CUtensorMap& md, const HeadParams& p, cudaStream_t st) {
-  return p.top ? launch_v<PAIR, true, KEEP>(ma, mb, me, md, p, st)
-               : launch_v<PAIR, false, KEEP>(ma, mb, me, md, p, st);
+                     const CUtensorMap& md, const HeadParams& p, bool after, cudaStream_t st) {
+  return p.top ? launch_v<PAIR, true, KEEP>(ma, mb, me, md, p, after, st)
+               : launch_v<PAIR, false, KEEP>(ma, mb, me, md, p, after, st);
 }
 
 }  // namespace
@@ -603,7 +609,7 @@ int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top) {
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   if (!lp_head_supported(a)) return cudaErrorInvalidValue;
   const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms());
-  const bool pair = h.pair, keep = a.e != nullptr;
+  const bool pair = h.pair, keep = a.e != nullptr, after = a.own_zeros;
   CUtensorMap ma, mb, me, md;
   if (!make_tensor_map(&ma, MapType::kBf16, a.x, a.k, a.m, a.ldx, BK, BM) ||
       !make_tensor_map(&mb, MapType::kBf16, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
@@ -628,8 +634,8 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   p.top = a.top; p.gmax = a.gmax; p.count = a.count; p.cand = a.cand;
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;
-  if (pair) return keep ? launch_k<true, true>(ma, mb, me, md, p, st) : launch_k<true, false>(ma, mb, me, md, p, st);
-  return keep ? launch_k<false, true>(ma, mb, me, md, p, st) : launch_k<false, false>(ma, mb, me, md, p, st);
+  if (pair) return keep ? launch_k<true, true>(ma, mb, me, md, p, after, st) : launch_k<true, false>(ma, mb, me, md, p, after, st);
+  return keep ? launch_k<false, true>(ma, mb, me, md, p, after, st) : launch_k<false, false>(ma, mb, me, md, p, after, st);
 }
 
 }  // namespace fljsd

@@ -608,6 +608,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_lp_grad(LpGradArgs a) {
   }
 }
 
+__global__ void __launch_bounds__(kThreads) k_zero(uint4* to, int64_t n) {
+  let_next_launch();
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads)
+    to[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // x: segments of a row; y: rows, up to what keeps the GPU full (a CTA then walks on)
 dim3 row_grid(int64_t segs, int64_t rows) {
   const int64_t most = ((int64_t)num_sms() * 32 + segs - 1) / segs;
@@ -634,6 +640,15 @@ cudaError_t launch_lp_join(const LpJoinArgs& a, cudaStream_t st) {
                                                 : launch_join_t<kJoinMany>(a, st);
   trace_end(FLJSD_KERNEL_SMALL, st);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_zero(void* to, size_t bytes, cudaStream_t st) {
+  if (bytes == 0) return cudaSuccess;
+  const int64_t n = (int64_t)(bytes / sizeof(uint4)), blocks = (n + kThreads - 1) / kThreads;
+  k_zero<<<(unsigned)(blocks < num_sms() ? blocks : num_sms()), kThreads, 0, st>>>(
+      static_cast<uint4*>(to), n);
+  count_extra_launch();
+  return cudaGetLastError();
 }
 
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {

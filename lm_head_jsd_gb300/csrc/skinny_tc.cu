@@ -48,7 +48,7 @@ static_assert(sizeof(SkCtrl) <= kCtrl, "control block");
 struct SkParams {
   int64_t m, n;
   int num_tiles, num_k_blocks, nst, resident;
-  bool own_x;
+  bool own_x, zero_status;
   const float *sx, *sw;
   void* out;
   int64_t ldo;
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KE = E4M3 ? 128 : 64;  // elements in 128 bytes
 
   if (threadIdx.x == 0) {
+    if (p.zero_status && blockIdx.x == 0) *p.status = 0;  // (long before a wait runs out)
     for (int s = 0; s < p.nst; ++s) {
       mbar_init(smem_u32(&cb->full[s]), 1);
       mbar_init(smem_u32(&cb->empty[s]), 1);
@@ -337,6 +338,7 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.timeout_ns = kTimeoutNs;
   p.status = a.status;
   p.own_x = a.own_x;
+  p.zero_status = a.zero_status;
   CUtensorMap mx, mw;
   const MapType mt = a.e4m3 ? MapType::kU8 : MapType::kBf16;
   const bool ok = make_tensor_map(&mx, mt, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&

@@ -23,6 +23,7 @@ struct SkinnyArgs {
   // x and sx come from the kernel launched just before, which does not write w or sw:
   // w is on its way before that kernel has ended.
   bool own_x;
+  bool zero_status;  // *status is set to 0 first
 };
 // Whether the kernel takes the shape (alignment as for the tensor maps).
 bool skinny_supported(const SkinnyArgs& a);
