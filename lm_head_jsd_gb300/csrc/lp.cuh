@@ -23,6 +23,7 @@ namespace fljsd {
 
 constexpr int LP_MAX_TOP = 32;
 constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product
+constexpr int LP_FEW_COLS = 32;    // behind a kept maximum of the product of a few rows
 constexpr int LP_SEG = 8192;       // elements of a part of given logits
 constexpr int LP_CHUNKS = 8;       // maxima kept of each such part
 // Parts of a row of given logits: segments are counted from the 16-byte boundary
@@ -52,7 +53,8 @@ struct LpJoinArgs {
   const void* z;       // [rows x ld], or null
   int z_dtype;
   int64_t ld;
-  const float* cmax;   // [rows x parts * LP_CHUNKS]
+  const float* cmax;   // [rows x chunks]: parts * LP_CHUNKS, or few_chunks
+  int64_t few_chunks;  // of LP_FEW_COLS columns, from the product of a few rows; else 0
   float* top_logp;     // [bt x k]
   int64_t* top_id;     // [bt x k]
 };

@@ -22,15 +22,18 @@ bool on_tensor_cores(const fljsd_lp_problem& p) { return p.dtype == FLJSD_BF16 &
 
 // How the logits of a plan's chunks are reduced.
 //  kFused: in the product's epilogue.
-//  kFew:   a forward of up to 16 rows, bound by reading w: the product for few rows
-//          (skinny_tc.cu) and the row kernels over its fp32 logits, 4 bytes for
-//          every 2 h of w.
+//  kFew:   a forward of up to 16 rows, bound by reading w: in the epilogue of the
+//          product for few rows (skinny_tc.cu), which writes the fp32 logits beside
+//          where alternatives are asked for, 4 bytes for every 2 h of w.
 //  kRows:  the CUDA-core product and the row kernels.
 enum Path { kFused, kFew, kRows };
 Path path_of(const fljsd_lp_problem& p) {
   if (!on_tensor_cores(p)) return kRows;
   return !(p.flags & FLJSD_LP_BACKWARD) && p.bt <= SK_ROWS ? kFew : kFused;
 }
+
+// Chunks of a row whose maxima the product of a few rows keeps.
+int64_t few_chunks(int64_t v) { return (v + 127) / 128 * (128 / LP_FEW_COLS); }
 
 struct LpLayout {
   Path path;
@@ -49,7 +52,9 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.path = path_of(p);
   const bool fused = L.path == kFused;
   L.ld = (p.v + 7) / 8 * 8;
-  L.parts = fused ? (p.v + LP_PART_COLS - 1) / LP_PART_COLS : lp_row_parts(p.v);
+  L.parts = fused             ? (p.v + LP_PART_COLS - 1) / LP_PART_COLS
+            : L.path == kFew ? few_chunks(p.v)  // (at most)
+                             : lp_row_parts(p.v);
   L.cap = L.parts * p.top_k;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -65,7 +70,7 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.part = take(rows * L.parts * sizeof(float4));
   L.zy = take(rows * sizeof(float));
   L.cand = take(fused ? rows * L.cap * sizeof(int2) : 0);
-  L.cmax = take(!fused && p.top_k ? rows * L.parts * LP_CHUNKS * sizeof(float) : 0);
+  L.cmax = take(fused || !p.top_k ? 0 : rows * L.parts * (L.path == kFew ? 1 : LP_CHUNKS) * sizeof(float));
   L.dump_blocks = fused ? lp_head_dump_blocks(c, p.v, p.h, p.top_k) : 0;
   L.dump = take(rows * L.dump_blocks * 256 * sizeof(float));
   L.stats_bytes = at;
@@ -158,20 +163,23 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     return e;
   }
   float* z = reinterpret_cast<float*>(ws + L.z);
-  cudaError_t e;
   if (L.path == kFew) {
     SkinnyArgs k{};
     k.x = x; k.ldx = p.h; k.w = w; k.ldw = p.h; k.m = rows; k.n = p.v; k.k = p.h;
-    k.out = z; k.ldo = L.ld;
+    k.out = top ? z : nullptr; k.ldo = L.ld;  // (alternatives are ranked from them)
     k.status = reinterpret_cast<int*>(ws + L.status);
     k.zero_status = first;
+    k.part = reinterpret_cast<float4*>(ws + L.part);
+    k.cmax = top ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
+    k.c = c; k.labels = labels;
+    k.zy = reinterpret_cast<float*>(ws + L.zy);
     trace_begin(FLJSD_KERNEL_GEMM_LOGITS, st);
-    e = launch_skinny(k, st);
+    const cudaError_t e = launch_skinny(k, st);
     trace_end(FLJSD_KERNEL_GEMM_LOGITS, st);
-  } else {
-    e = lp_gemm(FLJSD_KERNEL_GEMM_LOGITS, p.dtype, false, x, p.h, 0, w, p.h, 0, z, L.ld, rows, p.v,
-                p.h, 0, z, 0, nullptr, nullptr, 0, st);
+    return e;
   }
+  const cudaError_t e = lp_gemm(FLJSD_KERNEL_GEMM_LOGITS, p.dtype, false, x, p.h, 0, w, p.h, 0, z,
+                                L.ld, rows, p.v, p.h, 0, z, 0, nullptr, nullptr, 0, st);
   if (e != cudaSuccess) return e;
   LpRowsArgs r{};
   r.z = z; r.ld = L.ld; r.v = p.v; r.rows = rows; r.c = c; r.labels = labels;
@@ -309,6 +317,10 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
     } else {
       j.z = ws + L.z; j.z_dtype = FLJSD_F32; j.ld = L.ld;
       j.cmax = reinterpret_cast<const float*>(ws + L.cmax);
+      if (L.path == kFew) {
+        j.parts = skinny_parts(p->v);
+        j.few_chunks = few_chunks(p->v);
+      }
     }
     j.top_logp = top_logp; j.top_id = top_id;
     if (launch_lp_join(j, stream) != cudaSuccess) return FLJSD_ERR_CUDA;

@@ -13,6 +13,7 @@
 // gradient by HBM (165 us = 6.3 TB/s).
 #include "dependent.cuh"
 #include "lp.cuh"
+#include "lp_mds.cuh"
 #include "jsd_math.cuh"
 
 #include <cuda_fp16.h>
@@ -162,35 +163,6 @@ __device__ __forceinline__ unsigned long long block_max64(unsigned long long x,
   return x;
 }
 
-// (m, d, s) of two sets, each relative to its own maximum (lp.cuh); a set without a
-// finite value has m = -inf and d = s = 0, or NaN where it holds one.
-struct Mds {
-  float m, d, s;
-};
-__device__ __forceinline__ Mds merge(const Mds& a, const Mds& b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float ta = a.m == -INFINITY ? 0.f : __fmul_rn(a.m - m, c);
-  const float tb = b.m == -INFINITY ? 0.f : __fmul_rn(b.m - m, c);
-  const float fa = ex2(ta), fb = ex2(tb);
-  // 2^t (s + d t): both vanish where 2^t does
-  return Mds{m, __fmaf_rn(a.d, fa, b.d * fb),
-             __fmaf_rn(fa, __fmaf_rn(a.d, fmaxf(ta, -1024.f), a.s),
-                       fb * __fmaf_rn(b.d, fmaxf(tb, -1024.f), b.s))};
-}
-// The warp's: its maximum in one instruction (exact, so order-free), every lane's sums
-// rescaled to it once and added in a fixed order.
-__device__ __forceinline__ Mds warp_mds(Mds x, float c) {
-  float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x.m));
-  const float t = x.m == -INFINITY ? 0.f : __fmul_rn(x.m - m, c);
-  const float f = ex2(t);
-  float2 ds = make_float2(x.d * f, f * __fmaf_rn(x.d, fmaxf(t, -1024.f), x.s));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    ds = __fadd2_rn(ds, make_float2(__shfl_xor_sync(0xffffffffu, ds.x, o),
-                                    __shfl_xor_sync(0xffffffffu, ds.y, o)));
-  return Mds{m, ds.x, ds.y};
-}
 // The block's, in a fixed order (in every thread of the first warp).
 template <int W>
 __device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
@@ -350,19 +322,25 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   }
   if (a.k == 0) return;
   // ---- the k largest candidates ----
-  // the k-th largest of the first n threads' values (0 if fewer are above 0)
+  // a value that at least k of the first n threads' values reach: the k-th largest of
+  // them, or, of more than 128, of the largest of each four (0 if fewer are above 0)
   auto kth_of_threads = [&](unsigned mine, int n) {
     unsigned* keys = reinterpret_cast<unsigned*>(list);
-    keys[tid] = mine;
     if (tid == 0) sh_least = 0;
-    __syncthreads();
     int gt = 0, ge = 0;
     if constexpr (kJoinThreads == kJoinFew) {
-      // four threads to a value, each against a quarter of them: 2 us less
-      const unsigned quad = 0xfu << (tid & 28);
-      for (int i = tid >> 2; i < n; i += kJoinThreads / 4) {
-        const unsigned x = keys[i];
-        gt = ge = 0;
+      if (n > kJoinFew / 4) {
+        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+        if ((tid & 3) == 0) keys[tid >> 2] = mine;
+        n = (n + 3) / 4;
+      } else if (tid < n) {
+        keys[tid] = mine;
+      }
+      __syncthreads();
+      // four threads to a value, each against a quarter of them
+      if ((tid >> 2) < n) {
+        const unsigned quad = 0xfu << (tid & 28), x = keys[tid >> 2];
 #pragma unroll 8
         for (int j = tid & 3; j < n; j += 4) {
           gt += keys[j] > x ? 1 : 0;
@@ -376,6 +354,8 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
         if ((tid & 3) == 0 && gt < a.k && a.k <= ge) sh_least = x;  // (equal ones write the same)
       }
     } else {
+      keys[tid] = mine;
+      __syncthreads();
 #pragma unroll 8
       for (int j = 0; j < n; ++j) {
         gt += keys[j] > mine ? 1 : 0;
@@ -387,7 +367,8 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
     return sh_least;
   };
   unsigned least = 0;
-  const int64_t chunks = a.parts * LP_CHUNKS;
+  const bool few = kRowsSrc && a.few_chunks > 0;  // chunks: 32 columns of a product of few rows
+  const int64_t chunks = few ? a.few_chunks : a.parts * LP_CHUNKS;
   const float* cmax = a.cmax + r * chunks;
   const int64_t n_cand = kRowsSrc ? 0 : (int64_t)a.count[r];
   const int2* cand = a.cand + r * a.cap;
@@ -395,6 +376,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   const int64_t n_dump = !kRowsSrc && a.dump ? (a.dump_cols < a.v ? a.dump_cols : a.v) : 0;
   if (kRowsSrc) {
     unsigned mine = 0;
+#pragma unroll 4
     for (int64_t i = tid; i < chunks; i += kJoinThreads) {
       const float m1 = cmax[i];
       if (m1 > -INFINITY) mine = max(mine, lp_key(m1));
@@ -413,6 +395,27 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
     if constexpr (kRowsSrc) {
       constexpr int N = 16 / sizeof(SRC);
       constexpr uint32_t kNone = sizeof(SRC) == 4 ? 0xff800000u : 0xff80u;  // -inf
+      if (few) {
+        const SRC* zr = reinterpret_cast<const SRC*>(a.z) + r * a.ld;
+        // every lane a chunk's maximum, the warp those chunks that reach it
+        for (int64_t c0 = (tid >> 5) * 32; c0 < chunks; c0 += 4 * kJoinThreads) {
+          float m1[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int64_t c = c0 + u * kJoinThreads + (tid & 31);
+            m1[u] = c < chunks ? cmax[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            unsigned hit = __ballot_sync(0xffffffffu, m1[u] > -INFINITY && lp_key(m1[u]) >= least);
+            for (; hit; hit &= hit - 1) {
+              const int64_t col = (c0 + u * kJoinThreads + __ffs(hit) - 1) * LP_FEW_COLS + (tid & 31);
+              if (col < a.v) give(val(zr + col), col);
+            }
+          }
+        }
+        return;
+      }
       for (int64_t c = tid >> 5; c < chunks; c += W) {
         const float m1 = cmax[c];
         if (!(m1 > -INFINITY) || lp_key(m1) < least) continue;

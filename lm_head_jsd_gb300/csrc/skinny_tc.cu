@@ -10,6 +10,10 @@
 //    slices of L2; read again for every tile by every SM, it held the stream up
 //    (one row took 220 us where sixteen took 175 us; H = 4096, V = 128256);
 //  - the rest of shared memory is the ring of w's tiles, 16 KB each.
+// For token log probabilities the epilogue reduces what it holds: each warp its 32
+// columns of each row, over all of the CTA's tiles, in some 500 instructions of a tile's
+// 25 us (one row of H = 4096, V = 128256, with the join: 161 us, 166 with the logits read
+// again by the row kernels; H = 512, V = 40960: 14.4 and 16.5).
 // H = 4096, V = 128256: bf16 163 us = 6.4 TB/s, e4m3 86 us = 6.1 TB/s (0.95 and 0.90 of
 // a copy's rate).
 // e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
@@ -17,6 +21,7 @@
 #include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
+#include "lp_mds.cuh"
 #include "skinny_tc.cuh"
 #include "tensor_map.cuh"
 
@@ -54,6 +59,11 @@ struct SkParams {
   int64_t ldo;
   unsigned long long timeout_ns;
   int* status;
+  float4* part;
+  float* cmax;
+  float c;
+  const int64_t* labels;
+  float* zy;
 };
 
 __device__ __forceinline__ bool sk_wait(SkCtrl* cb, uint32_t bar, uint32_t parity, int* status) {
@@ -252,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = warp & 3;
     uint32_t use = 0;
     bool ok = true;
+    Mds all{-INFINITY, 0.f, 0.f};  // of the tiles so far
     wait_for_previous();
     if (E4M3) {
       for (int i = threadIdx.x - 64; i < nkb * SK_ROWS; i += 128) {
@@ -282,13 +293,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < SK_ROWS; ++j)
           sum[j] = E4M3 ? __fmaf_rn(v[j], s_sx[kb * SK_ROWS + j] * sw, sum[j]) : v[j];
       }
-      if (ok && col < p.n) {
+      // (m, d, s) of this warp's columns, row by row; lane j keeps row j's
+      if (!E4M3 && ok && p.part) {
+        Mds mine{-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int j0 = 0; j0 < SK_ROWS; j0 += 4) {  // four rows' reductions side by side
+          if (j0 >= p.m) break;
+          Mds x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float z = col < p.n ? sum[j0 + i] : -INFINITY;
+            // (NaN is no maximum, but stays in the sums)
+            x[i] = warp_mds(Mds{fmaxf(z, -INFINITY), z == -INFINITY ? 0.f : z != z ? z : 1.f, 0.f},
+                            p.c);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (lane == j0 + i) mine = x[i];
+        }
+        if (p.labels && col < p.n) {
+#pragma unroll
+          for (int j = 0; j < SK_ROWS; ++j)
+            if (j < p.m && p.labels[j] == col) p.zy[j] = sum[j];
+        }
+        if (p.cmax && lane < p.m) p.cmax[((int64_t)lane * p.num_tiles + t) * 4 + sub] = mine.m;
+        all = merge(all, mine, p.c);
+      }
+      if (ok && col < p.n && p.out) {
         T* o = reinterpret_cast<T*>(p.out) + col;
 #pragma unroll
         for (int j = 0; j < SK_ROWS; ++j)
           if (j < p.m) put(o + j * p.ldo, sum[j]);
       }
     }
+    if (!E4M3 && p.part && lane < p.m)
+      p.part[((int64_t)lane * gridDim.x + blockIdx.x) * 4 + sub] = make_float4(all.m, all.d, all.s, 0.f);
   }
   tc_fence_before();
   __syncthreads();
@@ -321,6 +360,11 @@ bool skinny_supported(const SkinnyArgs& a) {
          (!a.e4m3 || a.k <= (int64_t)kScaleBlocks * 128);
 }
 
+int64_t skinny_parts(int64_t n) {
+  const int64_t tiles = (n + BM - 1) / BM;
+  return 4 * (tiles < num_sms() ? tiles : num_sms());
+}
+
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   if (!skinny_supported(a)) return cudaErrorInvalidValue;
   SkParams p{};
@@ -339,6 +383,7 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.status = a.status;
   p.own_x = a.own_x;
   p.zero_status = a.zero_status;
+  p.part = a.part; p.cmax = a.cmax; p.c = a.c; p.labels = a.labels; p.zy = a.zy;
   CUtensorMap mx, mw;
   const MapType mt = a.e4m3 ? MapType::kU8 : MapType::kBf16;
   const bool ok = make_tensor_map(&mx, mt, a.x, a.k, a.m, a.ldx, ke, SK_ROWS) &&

@@ -24,9 +24,19 @@ struct SkinnyArgs {
   // w is on its way before that kernel has ended.
   bool own_x;
   bool zero_status;  // *status is set to 0 first
+  // bf16: parts (m, d, s) as in lp.cuh, [m x skinny_parts(n)], with c = log2(e) / T; the
+  // logit of each row's label; the maxima of 32 columns each, [m x 4 ceil(n / 128)], or
+  // null. out may then be null.
+  float4* part;
+  float* cmax;
+  float c;
+  const int64_t* labels;
+  float* zy;
 };
 // Whether the kernel takes the shape (alignment as for the tensor maps).
 bool skinny_supported(const SkinnyArgs& a);
+// Parts of a row: one for each epilogue warp.
+int64_t skinny_parts(int64_t n);
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st);
 
 }  // namespace fljsd
