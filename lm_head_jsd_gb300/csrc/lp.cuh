@@ -22,7 +22,7 @@
 namespace fljsd {
 
 constexpr int LP_MAX_TOP = 32;
-constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product
+constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product (at most)
 constexpr int LP_FEW_COLS = 32;    // behind a kept maximum of the product of a few rows
 constexpr int LP_SEG = 8192;       // elements of a part of given logits
 constexpr int LP_CHUNKS = 8;       // maxima kept of each such part
@@ -47,8 +47,9 @@ struct LpJoinArgs {
   int64_t cap;
   const int* count;    // [rows] candidates of each row
   const unsigned* gmax;  // [k x rows] group maxima (see lp_head_tc.cu)
-  const float* dump;   // [rows x dump_cols] logits of the first columns, or null
-  int64_t dump_cols;
+  const float* dump;   // [rows x dump_cols] logits of the first columns, or null: of each
+  int64_t dump_cols;   // LP_PART_COLS the first part_cols, one part's
+  int part_cols;
   // from given logits:
   const void* z;       // [rows x ld], or null
   int z_dtype;
@@ -108,7 +109,8 @@ struct LpHeadArgs {
   unsigned* gmax;      // [top x m], zeroed
   int* count;          // [m], zeroed
   int2* cand;          // [m x parts * top]
-  float* dump;         // [m x 256 dump_blocks] logits of the first 256-column blocks
+  int bn;              // columns of a tile (two parts): lp_head_tile_cols, or 256
+  float* dump;         // [m x 256 dump_blocks] logits of the first tiles' columns (LpJoinArgs)
   int dump_blocks;
   void* e;             // [m x lde] fp16: 2^t_j relative to each part's maximum, or null
   int64_t lde;
@@ -116,8 +118,11 @@ struct LpHeadArgs {
   bool own_zeros;      // count, gmax and status were zeroed by the kernel launched just before
 };
 bool lp_head_supported(const LpHeadArgs& a);
-// Blocks of 256 columns whose logits are best written out instead of listed.
-int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top);
+// Columns of a tile, a multiple of 16 up to 256: as few as the rounds of tiles over the
+// SMs allow, so that the last round is as full as the others.
+int lp_head_tile_cols(int64_t m, int64_t n, int64_t k);
+// Tiles in a row of them whose logits are best written out instead of listed.
+int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top, int bn);
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st);
 
 // Floats as integers in their order (0 is below every value).

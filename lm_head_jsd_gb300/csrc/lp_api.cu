@@ -41,7 +41,7 @@ struct LpLayout {
   int64_t ld, parts, cap;
   // zeroed: status, count, gmax (in one piece, [zero, zero + zero_bytes))
   size_t zero, zero_bytes, status, count, gmax;
-  int dump_blocks;
+  int dump_blocks, bn;
   size_t part, zy, cand, cmax, dump, z, dz, acc32, splitk, splitk_bytes, total, logits_bytes, stats_bytes;
 };
 
@@ -52,7 +52,9 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.path = path_of(p);
   const bool fused = L.path == kFused;
   L.ld = (p.v + 7) / 8 * 8;
-  L.parts = fused             ? (p.v + LP_PART_COLS - 1) / LP_PART_COLS
+  // (a backward pass reads parts of 128 columns)
+  L.bn = fused && !bwd ? lp_head_tile_cols(c, p.v, p.h) : 2 * LP_PART_COLS;
+  L.parts = fused             ? (p.v + L.bn / 2 - 1) / (L.bn / 2)
             : L.path == kFew ? few_chunks(p.v)  // (at most)
                              : lp_row_parts(p.v);
   L.cap = L.parts * p.top_k;
@@ -71,7 +73,7 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.zy = take(rows * sizeof(float));
   L.cand = take(fused ? rows * L.cap * sizeof(int2) : 0);
   L.cmax = take(fused || !p.top_k ? 0 : rows * L.parts * (L.path == kFew ? 1 : LP_CHUNKS) * sizeof(float));
-  L.dump_blocks = fused ? lp_head_dump_blocks(c, p.v, p.h, p.top_k) : 0;
+  L.dump_blocks = fused ? lp_head_dump_blocks(c, p.v, p.h, p.top_k, L.bn) : 0;
   L.dump = take(rows * L.dump_blocks * 256 * sizeof(float));
   L.stats_bytes = at;
   // 2^t in fp16 that the backward pass turns into dz in place, or fp32 logits (and their
@@ -153,6 +155,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
     h.cand = reinterpret_cast<int2*>(ws + L.cand);
     h.dump = reinterpret_cast<float*>(ws + L.dump);
     h.dump_blocks = top ? L.dump_blocks : 0;
+    h.bn = L.bn;
     h.e = keep ? ws + L.z : nullptr;
     h.lde = L.ld;
     h.status = reinterpret_cast<int*>(ws + L.status);
@@ -313,7 +316,8 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
       j.count = reinterpret_cast<const int*>(ws + L.count);
       j.gmax = reinterpret_cast<const unsigned*>(ws + L.gmax);
       j.dump = L.dump_blocks ? reinterpret_cast<const float*>(ws + L.dump) : nullptr;
-      j.dump_cols = (int64_t)L.dump_blocks * 256;
+      j.dump_cols = (int64_t)L.dump_blocks * 2 * LP_PART_COLS;
+      j.part_cols = L.bn / 2;
     } else {
       j.z = ws + L.z; j.z_dtype = FLJSD_F32; j.ld = L.ld;
       j.cmax = reinterpret_cast<const float*>(ws + L.cmax);

@@ -55,6 +55,7 @@ constexpr int kKeepBufs = 2;   // staging buffers of an epilogue warp
 struct HeadParams {
   int64_t m, n;
   int num_n_blocks, num_k_blocks, m_units, num_units, group_m, nst;
+  int bn;  // columns of a tile, two parts
   float c;
   const int64_t* labels;
   float4* part;
@@ -222,10 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t filled = 0;  // stages filled since the start
     bool ok = true;
     const uint32_t flip = (PAIR && !leader) ? 0u : 1u;
+    const uint32_t copied = A_BYTES + (PAIR ? p.bn / 2 : p.bn) * (BK * 2);  // of a stage's SB
     for (int t = unit0; ok && t < p.num_units; t += unit_step) {
       int mb, nb;
       tile_coords(t, mb, nb);
-      const int nrow = nb * BN + (PAIR ? (int)rank * (BN / 2) : 0);
+      const int nrow = nb * p.bn + (PAIR ? (int)rank * (p.bn / 2) : 0);
       for (int kb = 0; kb < p.num_k_blocks; ++kb) {
         if (!wait_all(smem_u32(&cb->empty[stage]), phase ^ flip)) {
           ok = false;
@@ -237,12 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (PAIR) {
             fb = map_to_cta(smem_u32(&cb->full[stage]), 0);
             if (leader) {
-              mbar_arrive_expect_tx(smem_u32(&cb->full[stage]), 2 * SB);
+              mbar_arrive_expect_tx(smem_u32(&cb->full[stage]), 2 * copied);
               mbar_arrive_remote_relaxed(map_to_cta(smem_u32(&cb->empty[stage]), 1));
             }
           } else {
             fb = smem_u32(&cb->full[stage]);
-            mbar_arrive_expect_tx(fb, SB);
+            mbar_arrive_expect_tx(fb, copied);
           }
           tma_operand<PAIR>(sa, &tmA, fb, kb * BK, mb * BM);
           tma_operand<PAIR>(sa + A_BYTES, &tmB, fb, kb * BK, nrow);
@@ -264,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (leader) {
-      constexpr uint32_t idesc = instr_desc(false, false, PAIR);
+      // (N, from bit 17 on, is the tile's columns)
+      const uint32_t idesc = instr_desc(false, false, PAIR) - ((uint32_t)((BN - p.bn) >> 3) << 17);
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
@@ -323,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int acc = local & 1;
       const int64_t row0 = (int64_t)mb * BM + sub * 32, row = row0 + lane;
       const bool row_ok = row < p.m;
-      const int col0 = nb * BN + grp * LP_PART_COLS;
-      const int ncols = (int)min((int64_t)LP_PART_COLS, p.n - col0);
+      const int col0 = nb * p.bn + grp * (p.bn / 2);
+      const int ncols = (int)min((int64_t)(p.bn / 2), p.n - col0);
       const bool live = row0 < p.m && ncols > 0;  // of this warp
       int lab = -1;
       if (live && row_ok) {
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the tiles that fill the groups may have ended since)
         if (listed && __any_sync(0xffffffffu, low == 0)) low = least();
         const uint32_t tacc = tmem_base + ((uint32_t)(sub * 32) << 16) + acc * ACC_COLS +
-                              grp * LP_PART_COLS;
+                              grp * (p.bn / 2);
         // ---- the maximum and the label's logit; the columns that reach thr ----
         float mx = -INFINITY;
         unsigned hit[4] = {0u, 0u, 0u, 0u};  // by chunk of 32 columns
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmD, smem_u32(buf), col0 + c, (int32_t)row0);
+              tma_store_2d(&tmD, smem_u32(buf), (nb * 2 + grp) * LP_PART_COLS + c, (int32_t)row0);
               bulk_commit();
             }
           } else if (TOP) {
@@ -570,7 +573,8 @@ cudaError_t launch_k(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
 
 bool lp_head_supported(const LpHeadArgs& a) {
   auto al = [](const void* q) { return ((uintptr_t)q & 15u) == 0; };
-  return a.m > 0 && a.n > 0 && a.k > 0 && al(a.x) && al(a.w) && a.ldx % 8 == 0 && a.ldw % 8 == 0 &&
+  return a.m > 0 && a.n > 0 && a.k > 0 && a.bn >= BN / 2 && a.bn <= BN && a.bn % 16 == 0 &&
+         (a.e == nullptr || a.bn == BN) && al(a.x) && al(a.w) && a.ldx % 8 == 0 && a.ldw % 8 == 0 &&
          (a.e == nullptr || (al(a.e) && a.lde % 8 == 0)) && a.m < (1ll << 31) - 512 &&
          a.n < (1ll << 31) - 512 && a.k < (1ll << 31);
 }
@@ -580,15 +584,21 @@ struct HeadSchedule {
   bool pair;
   int64_t nblocks, m_units, group_m;
 };
+int64_t up(int64_t x, int64_t q) { return (x + q - 1) / q; }
+// rounds of tiles: one CTA each | CTA pairs
+int64_t rounds(int64_t mblocks, int64_t nblocks, int64_t sms, bool pair) {
+  return pair ? up(up(mblocks, 2) * nblocks, sms >= 2 ? sms / 2 : 1) : up(mblocks * nblocks, sms);
+}
 // the schedule rule of launch_gemm_tc (gemm_tc.cu)
-HeadSchedule head_schedule(int64_t m, int64_t n, int64_t k, int64_t sms) {
+bool use_pair(int64_t m, int64_t k, int64_t pair_cost, int64_t one_cost) {
+  return m > BM && up(k, BK) >= 4 && pair_cost * 100 <= one_cost * 112;
+}
+HeadSchedule head_schedule(int64_t m, int64_t n, int64_t k, int64_t sms, int bn) {
   HeadSchedule h;
-  const int64_t mblocks = (m + BM - 1) / BM, clusters = sms >= 2 ? sms / 2 : 1;
-  h.nblocks = (n + BN - 1) / BN;
-  const int64_t waves_one = (mblocks * h.nblocks + sms - 1) / sms;
-  const int64_t waves_pair = ((mblocks + 1) / 2 * h.nblocks + clusters - 1) / clusters;
-  h.pair = mblocks >= 2 && (k + BK - 1) / BK >= 4 && waves_pair * 100 <= waves_one * 112;
-  h.m_units = h.pair ? (mblocks + 1) / 2 : mblocks;
+  const int64_t mblocks = up(m, BM);
+  h.nblocks = up(n, bn);
+  h.pair = use_pair(m, k, rounds(mblocks, h.nblocks, sms, true), rounds(mblocks, h.nblocks, sms, false));
+  h.m_units = h.pair ? up(mblocks, 2) : mblocks;
   // bands of about 32 MB of X, as for the logits product
   const int64_t gm = (32ll << 20) / ((int64_t)BM * (h.pair ? 2 : 1) * k * 2);
   h.group_m = gm < 1 ? 1 : gm > h.m_units ? h.m_units : gm;
@@ -596,9 +606,27 @@ HeadSchedule head_schedule(int64_t m, int64_t n, int64_t k, int64_t sms) {
 }
 }  // namespace
 
-int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top) {
+int lp_head_tile_cols(int64_t m, int64_t n, int64_t k) {
+  // More tiles read X more often; where it lies in few slices of L2, that costs more than
+  // the rounds gain (H = 2048, V = 40960: 24 rows 57 us instead of 45, 32 rows 36 instead
+  // of 42; H = 512: 17 rows 19 instead of 15, 96 rows 14 instead of 15).
+  if (m * k * 2 < (128 << 10)) return BN;
+  const int64_t sms = TC_PLAN_CTAS, mblocks = up(m, BM);
+  int64_t cols[2], cost[2];
+  for (int pair = 0; pair < 2; ++pair) {
+    const int64_t units = pair ? up(mblocks, 2) : mblocks, at_once = pair ? sms / 2 : sms;
+    const int64_t r = rounds(mblocks, up(n, BN), sms, pair != 0);
+    const int64_t most = r * at_once / units;  // tiles of a row of tiles in r rounds
+    cols[pair] = up(up(n, most > 0 ? most : 1), 16) * 16;
+    cols[pair] = cols[pair] < BN / 2 ? BN / 2 : cols[pair] > BN ? BN : cols[pair];
+    cost[pair] = r * cols[pair];
+  }
+  return (int)cols[use_pair(m, k, cost[1], cost[0]) ? 1 : 0];
+}
+
+int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top, int bn) {
   if (top == 0 || m <= 0) return 0;
-  const HeadSchedule h = head_schedule(m, n, k, TC_PLAN_CTAS);
+  const HeadSchedule h = head_schedule(m, n, k, TC_PLAN_CTAS, bn);
   const int64_t at_once = h.pair ? TC_PLAN_CTAS / 2 : TC_PLAN_CTAS;
   int64_t blocks = (at_once + h.group_m - 1) / h.group_m;
   // the threshold needs a part in each of the k groups
@@ -608,11 +636,11 @@ int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top) {
 
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
   if (!lp_head_supported(a)) return cudaErrorInvalidValue;
-  const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms());
+  const HeadSchedule h = head_schedule(a.m, a.n, a.k, num_sms(), a.bn);
   const bool pair = h.pair, keep = a.e != nullptr, after = a.own_zeros;
   CUtensorMap ma, mb, me, md;
   if (!make_tensor_map(&ma, MapType::kBf16, a.x, a.k, a.m, a.ldx, BK, BM) ||
-      !make_tensor_map(&mb, MapType::kBf16, a.w, a.k, a.n, a.ldw, BK, pair ? BN / 2 : BN))
+      !make_tensor_map(&mb, MapType::kBf16, a.w, a.k, a.n, a.ldw, BK, pair ? a.bn / 2 : a.bn))
     return cudaErrorInvalidValue;
   me = ma;
   if (keep && !make_tensor_map(&me, MapType::kBf16, a.e, a.lde, a.m, a.lde, 64, 32)) return cudaErrorInvalidValue;
@@ -621,7 +649,7 @@ cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st) {
                                  (int64_t)a.dump_blocks * BN, 32, 32))
     return cudaErrorInvalidValue;
   HeadParams p{};
-  p.m = a.m; p.n = a.n;
+  p.m = a.m; p.n = a.n; p.bn = a.bn;
   p.num_n_blocks = (int)h.nblocks;
   p.num_k_blocks = (int)((a.k + BK - 1) / BK);
   p.m_units = (int)h.m_units;

@@ -36,6 +36,7 @@ static_assert(kWarps == LP_CHUNKS, "a maximum for each warp");
 // threads 58).
 constexpr int kJoinFew = 512, kJoinMany = 128;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
+constexpr int kJoinMost = 192;  // as they are; more are sifted first (2000 x 1003, 20: 359 us without, 25 with)
 static_assert(kJoinFew <= kJoinCap && kJoinMany >= LP_MAX_TOP, "the threads' largest");
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   __shared__ float2 sh_norm;
   __shared__ unsigned long long sh64[W];
   __shared__ unsigned long long list[kJoinCap];
+  __shared__ unsigned keys[kJoinThreads];
   __shared__ int n_list;
   __shared__ unsigned sh_least;
   const int tid = threadIdx.x;
@@ -325,7 +327,6 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   // a value that at least k of the first n threads' values reach: the k-th largest of
   // them, or, of more than 128, of the largest of each four (0 if fewer are above 0)
   auto kth_of_threads = [&](unsigned mine, int n) {
-    unsigned* keys = reinterpret_cast<unsigned*>(list);
     if (tid == 0) sh_least = 0;
     int gt = 0, ge = 0;
     if constexpr (kJoinThreads == kJoinFew) {
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   const int64_t n_cand = kRowsSrc ? 0 : (int64_t)a.count[r];
   const int2* cand = a.cand + r * a.cap;
   const float* dump = a.dump + r * a.dump_cols;
-  const int64_t n_dump = !kRowsSrc && a.dump ? (a.dump_cols < a.v ? a.dump_cols : a.v) : 0;
+  const unsigned n_dump = !kRowsSrc && a.dump ? (unsigned)a.dump_cols : 0u;
   if (kRowsSrc) {
     unsigned mine = 0;
 #pragma unroll 4
@@ -439,14 +440,16 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
         const int2 q = cand[i];
         give(__int_as_float(q.x), q.y);
       }
-      // (whole 256-column blocks; columns past the vocabulary hold nothing)
+      // (columns past the part's or the vocabulary's hold nothing)
 #pragma unroll 4
-      for (int64_t i = tid * 4; i < n_dump; i += kJoinThreads * 4) {
+      for (unsigned i = tid * 4; i < n_dump; i += kJoinThreads * 4) {
         const float4 q = *reinterpret_cast<const float4*>(dump + i);
-        give(q.x, i);
-        if (i + 1 < n_dump) give(q.y, i + 1);
-        if (i + 2 < n_dump) give(q.z, i + 2);
-        if (i + 3 < n_dump) give(q.w, i + 3);
+        const unsigned off = i % LP_PART_COLS, col = i / LP_PART_COLS * (unsigned)a.part_cols + off;
+        if (off >= (unsigned)a.part_cols) continue;  // (a multiple of 8)
+        if (col < a.v) give(q.x, col);
+        if (col + 1 < a.v) give(q.y, col + 1);
+        if (col + 2 < a.v) give(q.z, col + 2);
+        if (col + 3 < a.v) give(q.w, col + 3);
       }
     }
   };
@@ -468,6 +471,25 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
     if (tid == 0) n_list = 0;
     __syncthreads();
     gather();
+    __syncthreads();
+  }
+  if (n_list > kJoinMost && n_list <= kJoinCap) {
+    // ranking takes each against each: first leave out what cannot be among the k largest
+    constexpr int PER = kJoinCap / kJoinThreads;
+    const int have = n_list;
+    unsigned long long mine[PER], best = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = u * kJoinThreads + tid;
+      mine[u] = i < have ? list[i] : 0;
+      best = mine[u] > best ? mine[u] : best;
+    }
+    const unsigned lo = kth_of_threads((unsigned)(best >> 32), have < kJoinThreads ? have : kJoinThreads);
+    if (tid == 0) n_list = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (mine[u] != 0 && (unsigned)(mine[u] >> 32) >= lo) list[atomicAdd(&n_list, 1)] = mine[u];
     __syncthreads();
   }
   const int n = n_list;
