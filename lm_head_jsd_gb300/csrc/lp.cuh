@@ -26,9 +26,9 @@ constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product (at
 constexpr int LP_FEW_COLS = 32;    // behind a kept maximum of the product of a few rows
 constexpr int LP_SEG = 8192;       // elements of a part of given logits
 constexpr int LP_CHUNKS = 8;       // maxima kept of each such part
-// Parts of a row of given logits: segments are counted from the 16-byte boundary
-// at or before the row, so a row that starts off one may need one part more.
-inline int64_t lp_row_parts(int64_t v) { return (v + 7 + LP_SEG - 1) / LP_SEG; }
+// Segments of a row of given logits: they are counted from the 16-byte boundary
+// at or before the row, so a row that starts off one may need one more.
+inline int64_t lp_row_segs(int64_t v) { return (v + 7 + LP_SEG - 1) / LP_SEG; }
 
 struct LpJoinArgs {
   int64_t rows, row0, v;
@@ -54,7 +54,8 @@ struct LpJoinArgs {
   const void* z;       // [rows x ld], or null
   int z_dtype;
   int64_t ld;
-  const float* cmax;   // [rows x chunks]: parts * LP_CHUNKS, or few_chunks
+  int64_t segs;        // lp_row_segs
+  const float* cmax;   // [rows x chunks]: segs * LP_CHUNKS, or few_chunks
   int64_t few_chunks;  // of LP_FEW_COLS columns, from the product of a few rows; else 0
   float* top_logp;     // [bt x k]
   int64_t* top_id;     // [bt x k]
@@ -68,12 +69,15 @@ struct LpRowsArgs {
   int64_t ld, v, rows, row0;
   float c;
   const int64_t* labels;
-  float4* part;        // [rows x parts], parts = lp_row_parts(v)
+  int segs, group;     // lp_row_segs(v), and how many of them make a part
+  float4* part;        // [rows x ceil(segs / group)]
   float* zy;
-  float* cmax;         // [rows x parts * LP_CHUNKS], or null
+  float* cmax;         // [rows x segs * LP_CHUNKS], or null
   int* status;         // set to 0, or null
   bool own_logits;     // fp32, from the kernel launched just before
 };
+// How many of a row's segments one CTA reduces into a part.
+int lp_row_group(int dtype, int64_t rows, int64_t segs);
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st);
 
 // dz = (a (1[j = y] - p_j) - b p_j (log p_j + entropy)) / T from logits

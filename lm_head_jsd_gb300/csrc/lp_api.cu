@@ -56,7 +56,7 @@ LpLayout lp_layout(const fljsd_lp_problem& p, int64_t c) {
   L.bn = fused && !bwd ? lp_head_tile_cols(c, p.v, p.h) : 2 * LP_PART_COLS;
   L.parts = fused             ? (p.v + L.bn / 2 - 1) / (L.bn / 2)
             : L.path == kFew ? few_chunks(p.v)  // (at most)
-                             : lp_row_parts(p.v);
+                             : lp_row_segs(p.v);
   L.cap = L.parts * p.top_k;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -190,6 +190,7 @@ cudaError_t lp_chunk(const fljsd_lp_problem& p, const LpLayout& L, const char* x
   r.zy = reinterpret_cast<float*>(ws + L.zy);
   r.cmax = top ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
   r.own_logits = true;
+  r.segs = (int)L.parts; r.group = 1;
   return launch_lp_rows(FLJSD_F32, r, st);
 }
 
@@ -210,7 +211,7 @@ struct LogitsLayout {
 };
 LogitsLayout logits_layout(int64_t rows, int64_t v, int k) {
   LogitsLayout L{};
-  L.parts = lp_row_parts(v);
+  L.parts = lp_row_segs(v);
   L.part = kAlign;  // after the status word
   L.zy = L.part + align_up((size_t)rows * L.parts * sizeof(float4));
   L.cmax = L.zy + align_up((size_t)rows * sizeof(float));
@@ -324,6 +325,8 @@ fljsd_status fljsd_lp_forward(const fljsd_lp_problem* p, const fljsd_plan_t* pla
       if (L.path == kFew) {
         j.parts = skinny_parts(p->v);
         j.few_chunks = few_chunks(p->v);
+      } else {
+        j.segs = L.parts;
       }
     }
     j.top_logp = top_logp; j.top_id = top_id;
@@ -424,9 +427,11 @@ fljsd_status fljsd_logits_lp(int64_t rows, int64_t v, int64_t ld, int32_t dtype,
   r.part = reinterpret_cast<float4*>(ws + L.part);
   r.zy = reinterpret_cast<float*>(ws + L.zy);
   r.cmax = top_k > 0 ? reinterpret_cast<float*>(ws + L.cmax) : nullptr;
+  r.segs = (int)L.parts; r.group = lp_row_group(dtype, rows, L.parts);
   if (launch_lp_rows(dtype, r, stream) != cudaSuccess) return FLJSD_ERR_CUDA;
   LpJoinArgs j{};
-  j.rows = rows; j.v = v; j.part = r.part; j.parts = L.parts; j.c = r.c; j.inv_t = 1.f / temperature;
+  j.rows = rows; j.v = v; j.part = r.part; j.segs = L.parts; j.c = r.c;
+  j.parts = (r.segs + r.group - 1) / r.group; j.inv_t = 1.f / temperature;
   j.zy = r.zy;
   j.labels = labels; j.ignore_index = ignore_index;
   j.status = reinterpret_cast<int*>(ws);

@@ -2,15 +2,15 @@
 // and the gradient in the logits. The formulas are in lp.cuh.
 //
 // k_lp_rows cuts each row into segments of 8192 logits, one CTA each, so that a
-// single row of 128256 still runs on 16 CTAs; the next row's segment is on its way
-// while one is reduced. The k largest are left to k_lp_join, which reads again the
-// few 1024s whose maxima reach the k-th largest of them (choosing candidates here
-// took three times as long as the sums: 361 us where the sums took 117 and the join
-// now takes 38, 2047 x 128255 bf16). k_lp_grad is elementwise. HBM bounds both for
-// fp32 (1023 x 128255: 81 us = 6.5 TB/s, the gradient 160 us = 6.5 TB/s, 0.96 of a
-// copy's rate); for bf16 k_lp_rows, with twice the elements to a byte, is bound by
-// issue (2047 x 128255: 96 us = 5.5 TB/s, ten instructions an element), the
-// gradient by HBM (165 us = 6.3 TB/s).
+// single row of 128256 still runs on 16 CTAs (of many rows of bf16 a CTA takes up to
+// four segments: k_lp_rows_many); the next segment is on its way while one is
+// reduced. The k largest are left to k_lp_join, which reads again the few 1024s whose
+// maxima reach the k-th largest of them (choosing candidates here took three times as
+// long as the sums: 361 us, 2047 x 128255 bf16, where the sums then took 117 and the
+// join now takes 35). k_lp_grad is elementwise. HBM bounds both for
+// fp32 (1023 x 128255: 80 us = 6.6 TB/s, the gradient 160 us = 6.5 TB/s, 0.97 of a
+// copy's rate) and nearly so for bf16, with twice the elements to a byte (2047 x 128255:
+// 84 us = 6.2 TB/s, the gradient 165 us = 6.3 TB/s).
 #include "dependent.cuh"
 #include "lp.cuh"
 #include "lp_mds.cuh"
@@ -32,11 +32,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kWarps == LP_CHUNKS, "a maximum for each warp");
 // Threads of a row's join: few rows are bound by one CTA's way through its loads (333
 // fused rows, 20 alternatives: 512 threads 16 us, 256 threads 19), many by how many
-// CTAs an SM holds (2047 rows of given logits, 8 alternatives: 128 threads 38 us, 256
+// CTAs an SM holds (2047 rows of given logits, 8 alternatives, then: 128 threads 38 us, 256
 // threads 58).
 constexpr int kJoinFew = 512, kJoinMany = 128;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
-constexpr int kJoinMost = 192;  // as they are; more are sifted first (2000 x 1003, 20: 359 us without, 25 with)
+// as they are; more are sifted first (2000 x 1003, 20 alternatives: 359 us, sifted 25)
+constexpr int kJoinMost = 192;
 static_assert(kJoinFew <= kJoinCap && kJoinMany >= LP_MAX_TOP, "the threads' largest");
 
 __device__ __forceinline__ float val(const float* p) { return *p; }
@@ -177,6 +178,37 @@ __device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
   return x;
 }
 
+// {sum 2^t, sum 2^t t} of a thread's logits, t = c (z - m).
+__device__ __forceinline__ float2 sums_of(const float (&z)[kPer], float m, float c) {
+  // t = c z - c ref in one operation: c ref = hi + lo, hi rounded, and the sums
+  // are put right for lo once (2^-lo, and s - lo d)
+  const float ref = m == -INFINITY ? 0.f : m;
+  const float hi = __fmul_rn(ref, c), lo = __fmaf_rn(ref, c, -hi);
+  const float2 c2 = make_float2(c, c), nhi = make_float2(-hi, -hi);
+  float2 d = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2) {
+    const float2 q = __ffma2_rn(make_float2(z[i], z[i + 1]), c2, nhi);
+    const float2 y = make_float2(ex2(q.x), ex2(q.y));
+    d = __fadd2_rn(d, y);
+    t = __ffma2_rn(y, q, t);
+  }
+  const float f = ex2(-lo);
+  float2 o = make_float2((d.x + d.y) * f, __fmaf_rn(-lo, d.x + d.y, t.x + t.y) * f);
+  if (!(fabsf(o.y) < INFINITY)) {
+    // a logit of -inf or near the type's lowest (0 times -inf above), a maximum
+    // that overflows c, or NaN, which stays: with the difference taken first
+    o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float q = __fmul_rn(z[i] - ref, c), y = ex2(q);
+      o.x += y;
+      o.y = __fmaf_rn(y, fmaxf(q, -1024.f), o.y);
+    }
+  }
+  return o;
+}
+
 // A segment's logits, 32 to a thread: vectors of N elements, kThreads vectors
 // apart, from a 16-byte boundary. The vector that starts before the row (whose
 // first element may lie anywhere) and the one that crosses its end are read one
@@ -216,35 +248,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
     Mds x{-INFINITY, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kPer; ++i) x.m = fmaxf(x.m, z[i]);  // (skips NaN)
-    {
-      // t = c z - c ref in one operation: c ref = hi + lo, hi rounded, and the sums
-      // are put right for lo once (2^-lo, and s - lo d)
-      const float ref = x.m == -INFINITY ? 0.f : x.m;
-      const float hi = __fmul_rn(ref, a.c), lo = __fmaf_rn(ref, a.c, -hi);
-      const float2 c2 = make_float2(a.c, a.c), nhi = make_float2(-hi, -hi);
-      float2 d = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 q = __ffma2_rn(make_float2(z[i], z[i + 1]), c2, nhi);
-        const float2 y = make_float2(ex2(q.x), ex2(q.y));
-        d = __fadd2_rn(d, y);
-        t = __ffma2_rn(y, q, t);
-      }
-      const float f = ex2(-lo);
-      x.d = (d.x + d.y) * f;
-      x.s = __fmaf_rn(-lo, d.x + d.y, t.x + t.y) * f;
-      if (!(fabsf(x.s) < INFINITY)) {
-        // a logit of -inf or near the type's lowest (0 times -inf above), a maximum
-        // that overflows c, or NaN, which stays: with the difference taken first
-        x.d = x.s = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const float q = __fmul_rn(z[i] - ref, a.c), y = ex2(q);
-          x.d += y;
-          x.s = __fmaf_rn(y, fmaxf(q, -1024.f), x.s);
-        }
-      }
-    }
+    const float2 ds = sums_of(z, x.m, a.c);
+    x.d = ds.x;
+    x.s = ds.y;
     x = block_mds<kWarps>(x, a.c, shm);
     if (a.cmax && tid < kWarps) a.cmax[(r * parts + part) * kWarps + tid] = shm[tid].m;
     if (tid == 0) {
@@ -252,6 +258,89 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
       if (a.labels && part == 0) {
         const int64_t y = a.labels[a.row0 + r];
         if (y >= 0 && y < a.v) a.zy[r] = val(reinterpret_cast<const T*>(a.z) + r * a.ld + y);
+      }
+    }
+    __syncthreads();  // the shared results are written again by the next row
+  }
+}
+
+// The same for many rows of bf16, where the block's reduction took a third of the
+// instructions: a CTA takes `group` segments of a row into each thread's running sums and
+// reduces them once (2047 x 128255: 84 us = 6.2 TB/s with four, 99.5 with a reduction for
+// each; fp32, bound by HBM, 84 and 80). 64 registers a thread are all but full, and a few
+// values that do not fit cost more than the reductions did: rows are counted in 32 bits.
+__global__ void __launch_bounds__(kThreads, 4) k_lp_rows_many(LpRowsArgs a) {
+  using T = __nv_bfloat16;
+  constexpr int N = Vec<T>::N;
+  constexpr int V = kPer / N;
+  __shared__ Mds shm[kWarps];
+  const int tid = threadIdx.x;
+  const unsigned part = blockIdx.x;
+  constexpr uint32_t kNone = 0xff80u;  // -inf
+  let_next_launch();
+  if (a.status && part == 0 && blockIdx.y == 0 && tid == 0) *a.status = 0;
+  const int seg0 = part * a.group;
+  const int count = seg0 + a.group < a.segs ? a.group : a.segs - seg0;
+  // the next segment to ask for: its elements [lead, left) lie from zs on
+  const int rows = (int)a.rows;
+  int rl = blockIdx.y;
+  const T* zs = nullptr;
+  int lead = 0, left = 0, more = 0;
+  Raw<T> raw[V];
+  auto ask = [&]() {
+    if (rl < rows) {
+      if (more == 0) {
+        const T* zr = reinterpret_cast<const T*>(a.z) + (int64_t)rl * a.ld;
+        const int before = (int)((((uintptr_t)zr) & 15u) / sizeof(T));
+        zs = zr - before + (int64_t)seg0 * LP_SEG;
+        lead = seg0 == 0 ? before : 0;
+        left = (int)a.v + before - seg0 * LP_SEG;
+        more = count;
+      }
+      if (lead == 0 && left >= LP_SEG) {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+          raw[u].w = *reinterpret_cast<const uint4*>(zs + (u * kThreads + tid) * N);
+      } else {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+          raw[u] = load_raw(zs, (u * kThreads + tid) * N, lead, left < LP_SEG ? left : LP_SEG, kNone);
+      }
+      zs += LP_SEG;
+      left -= LP_SEG;
+      lead = 0;
+      if (--more == 0) rl += gridDim.y;
+    }
+  };
+  ask();
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    Mds x{-INFINITY, 0.f, 0.f};
+    for (int seg = 0; seg < count; ++seg) {
+      float z[kPer];
+#pragma unroll
+      for (int u = 0; u < V; ++u) values(raw[u], z + u * N);
+      ask();
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) m = fmaxf(m, z[i]);  // (skips NaN)
+      if (a.cmax) {
+        float w;
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
+        if ((tid & 31) == 0) a.cmax[((int64_t)r * a.segs + seg0 + seg) * kWarps + (tid >> 5)] = w;
+      }
+      m = fmaxf(m, x.m);
+      const float2 ds = sums_of(z, m, a.c);
+      // the thread's sums so far, relative to the new maximum
+      const float u = x.m == -INFINITY ? 0.f : __fmul_rn(x.m - m, a.c), fu = ex2(u);
+      x = Mds{m, __fmaf_rn(x.d, fu, ds.x), __fmaf_rn(fu, __fmaf_rn(x.d, fmaxf(u, -1024.f), x.s), ds.y)};
+      __syncwarp();  // (keeps the loads and conversions of the next one behind these sums)
+    }
+    x = block_mds<kWarps>(x, a.c, shm);
+    if (tid == 0) {
+      a.part[(int64_t)r * gridDim.x + part] = make_float4(x.m, x.d, x.s, 0.f);
+      if (a.labels && part == 0) {
+        const int64_t y = a.labels[a.row0 + r];
+        if (y >= 0 && y < a.v) a.zy[r] = val(reinterpret_cast<const T*>(a.z) + (int64_t)r * a.ld + y);
       }
     }
     __syncthreads();  // the shared results are written again by the next row
@@ -369,7 +458,7 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
   };
   unsigned least = 0;
   const bool few = kRowsSrc && a.few_chunks > 0;  // chunks: 32 columns of a product of few rows
-  const int64_t chunks = few ? a.few_chunks : a.parts * LP_CHUNKS;
+  const int64_t chunks = few ? a.few_chunks : a.segs * LP_CHUNKS;
   const float* cmax = a.cmax + r * chunks;
   const int64_t n_cand = kRowsSrc ? 0 : (int64_t)a.count[r];
   const int2* cand = a.cand + r * a.cap;
@@ -417,21 +506,26 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
         }
         return;
       }
-      for (int64_t c = tid >> 5; c < chunks; c += W) {
-        const float m1 = cmax[c];
-        if (!(m1 > -INFINITY) || lp_key(m1) < least) continue;
-        const Segment<SRC> g(a.z, a.ld, r, a.v, c / LP_CHUNKS);
-        const int j0 = ((int)(c % LP_CHUNKS) * 32 + (tid & 31)) * N;
-        Raw<SRC> raw[kPer / N];
+      // every lane a chunk's maximum, the warp those chunks that reach it
+      for (int64_t c0 = tid >> 5; c0 < chunks; c0 += 32 * W) {
+        const int64_t cl = c0 + (tid & 31) * W;
+        const float m1 = cl < chunks ? cmax[cl] : -INFINITY;
+        unsigned hit = __ballot_sync(0xffffffffu, m1 > -INFINITY && lp_key(m1) >= least);
+        for (; hit; hit &= hit - 1) {
+          const int64_t c = c0 + (__ffs(hit) - 1) * W;
+          const Segment<SRC> g(a.z, a.ld, r, a.v, c / LP_CHUNKS);
+          const int j0 = ((int)(c % LP_CHUNKS) * 32 + (tid & 31)) * N;
+          Raw<SRC> raw[kPer / N];
 #pragma unroll
-        for (int u = 0; u < kPer / N; ++u)
-          raw[u] = load_raw(g.zs, u * kThreads * N + j0, g.first, g.n, kNone);
+          for (int u = 0; u < kPer / N; ++u)
+            raw[u] = load_raw(g.zs, u * kThreads * N + j0, g.first, g.n, kNone);
 #pragma unroll
-        for (int u = 0; u < kPer / N; ++u) {
-          float z[N];
-          values(raw[u], z);
+          for (int u = 0; u < kPer / N; ++u) {
+            float z[N];
+            values(raw[u], z);
 #pragma unroll
-          for (int i = 0; i < N; ++i) give(z[i], g.e0 + u * kThreads * N + j0 + i);
+            for (int i = 0; i < N; ++i) give(z[i], g.e0 + u * kThreads * N + j0 + i);
+          }
         }
       }
     } else {
@@ -676,14 +770,22 @@ cudaError_t launch_zero(void* to, size_t bytes, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+int lp_row_group(int dtype, int64_t rows, int64_t segs) {
+  if (dtype != FLJSD_BF16) return 1;
+  const int64_t g = rows * segs / ((int64_t)num_sms() * 16);  // (16 parts for each SM are left)
+  return g > 4 ? 4 : g > 1 ? (int)g : 1;
+}
+
 cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  const int64_t parts = lp_row_parts(a.v);
+  const int64_t parts = (a.segs + a.group - 1) / a.group;
   const dim3 grid = row_grid(parts, a.rows);
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
   cudaError_t e = cudaSuccess;
   if (a.own_logits)  // (fp32)
     e = launch_dependent(k_lp_rows<float>, grid, kThreads, 0, st, a, parts);
+  else if (a.group > 1)
+    k_lp_rows_many<<<grid, kThreads, 0, st>>>(a);
   else if (dtype == FLJSD_BF16)
     k_lp_rows<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, parts);
   else
@@ -695,7 +797,7 @@ cudaError_t launch_lp_rows(int dtype, const LpRowsArgs& a, cudaStream_t st) {
 cudaError_t launch_lp_grad(int z_dtype, int out_dtype, bool from_e, const LpGradArgs& a,
                            cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  const dim3 grid = row_grid(from_e ? (a.v + LP_SEG - 1) / LP_SEG : lp_row_parts(a.v), a.rows);
+  const dim3 grid = row_grid(from_e ? (a.v + LP_SEG - 1) / LP_SEG : lp_row_segs(a.v), a.rows);
   using bf = __nv_bfloat16;
   trace_begin(FLJSD_KERNEL_JSD_ROWS, st);
   if (from_e)
