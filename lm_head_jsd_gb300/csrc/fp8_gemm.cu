@@ -211,8 +211,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
       for (int t = blockIdx.x; ok && t < p.num_units; t += gridDim.x) {
         for (int kb = 0; kb < p.num_k_blocks; ++kb) {
           const uint32_t acc = use % F_ACCS;
-          if (!wait_all(smem_u32(&cb->full[stage]), phase) ||
-              !wait_all(smem_u32(&cb->tmem_empty[acc]), ((use / F_ACCS) & 1u) ^ 1u)) {
+          // (one vote for both: the way from a free accumulator to its products counts)
+          const bool have = wait_bar(cb, smem_u32(&cb->full[stage]), phase, p.status);
+          const bool room = wait_bar(cb, smem_u32(&cb->tmem_empty[acc]), ((use / F_ACCS) & 1u) ^ 1u,
+                                     p.status);
+          if (!__all_sync(0xffffffffu, have && room)) {
             ok = false;
             break;
           }
