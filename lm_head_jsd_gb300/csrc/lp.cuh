@@ -5,11 +5,12 @@
 //   m = max z_j,  t_j = c (z_j - m),  d = sum 2^t_j,  s = sum 2^t_j t_j,
 //   lse = m / T + ln2 log2 d,  log p_j = ln2 (t_j - log2 d),
 //   entropy = -sum p_j log p_j = ln2 (log2 d - s / d).
-// A row is cut into parts (128 columns of a product's tile, or a segment of
-// given logits); each part writes (m, d, s), and k_lp_join combines them. For the k
-// largest it has, from the product, at most k candidates of each part, and from given
-// logits the maximum of each 1024 of them: the k-th largest of those maxima says
-// which few have to be read again. The entropy comes from
+// A row is cut into parts (up to 128 columns of a product's tile, what a warp sees of
+// the product of a few rows, or up to four segments of given logits); each part writes
+// (m, d, s), and k_lp_join combines them. For the k largest it has, from the product, at
+// most k candidates of each part, and from logits that lie in memory the maximum of each
+// 1024 of them (32 from the product of a few rows): the k-th largest of those maxima
+// says which few have to be read again. The entropy comes from
 // sums centred on the maximum: lse - sum p_j s_j would cancel all digits of a
 // peaked row. The difference z - m is taken before the scale, so that a row of
 // the type's lowest value (a mask that leaves nothing) does not overflow, and

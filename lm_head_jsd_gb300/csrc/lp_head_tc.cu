@@ -25,16 +25,21 @@
 // changes how much is skipped, never the result: candidates equal to the threshold
 // are kept, and k_lp_join orders them by value and column.
 // The first columns, whose tiles run before there is a threshold, are not listed:
-// their logits are written out (about one tile for each SM) and k_lp_join reads
+// their logits are written out (about one tile for each SM, through shared memory: a
+// thread's own stores, 32 rows to an instruction, took 4 us a tile) and k_lp_join reads
 // them against the final threshold. Sorted lists of every part took longer than the
-// products they came from: 333 rows of H = 2048, V = 40960, 20 alternatives: 133 us;
-// the first columns written out instead 109; appending, with the maxima published
-// before a part's sums, 75, of which 65 are the products' alone (no alternatives).
+// products they came from: 333 rows of H = 2048, V = 40960, 20 alternatives: 133 us; with
+// the first columns written out 109; appending, with the maxima published before a part's
+// sums, 75; written out by copies, with the maxima of neighbouring rows side by side, 64,
+// of which 57 are the products' alone (no alternatives).
 //
-// Measured, with the join: 4096 rows of H = 4096, V = 128256 and 8 alternatives 2.26 ms
-// = 1.90 PFLOP/s, 0.96 of the measured burst rate (power-capped: 1.10 of the sustained
-// one). Bound by the tensor cores down to H of about 1024; at H = 512 by the epilogue
-// (4096 rows, V = 40960: 118 us, 232 with 8 alternatives, for 87 us of products).
+// Tiles are as narrow as the rounds over the SMs allow (lp_head_tile_cols); a plan with a
+// backward pass keeps 256 columns.
+//
+// Measured, with the join: 4096 rows of H = 4096, V = 128256 and 8 alternatives 2.07 ms
+// = 2.08 PFLOP/s, 1.05 of the measured burst rate of a library product, 1.2 of the
+// sustained one. Bound by the tensor cores down to H of about 1024; at H = 512 by the
+// epilogue (4096 rows, V = 40960: 97 us, 214 with 8 alternatives, for 87 us of products).
 #include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"

@@ -14,8 +14,8 @@
 // columns of each row, over all of the CTA's tiles, in some 500 instructions of a tile's
 // 25 us (one row of H = 4096, V = 128256, with the join: 161 us, 166 with the logits read
 // again by the row kernels; H = 512, V = 40960: 14.4 and 16.5).
-// H = 4096, V = 128256: bf16 163 us = 6.4 TB/s, e4m3 86 us = 6.1 TB/s (0.95 and 0.90 of
-// a copy's rate).
+// H = 4096, V = 128256: bf16 160 us = 6.6 TB/s, e4m3 with the quantisation of x in front
+// 84 us = 6.2 TB/s (0.97 and 0.92 of a copy's rate).
 // e4m3 (see fp8_gemm.cu): every 128-deep block has an accumulator of its own in a
 // ring of eight, and is scaled and added in fp32 registers.
 #include "dependent.cuh"
