@@ -154,3 +154,19 @@ def test_captured_calls_follow_each_other(bt):
     torch.cuda.synchronize()
     want, wo = run.forward(x2, w, y2), fp8_linear(x2, *q)
     assert all(torch.equal(a, b) for a, b in zip(r, want)) and torch.equal(o, wo)
+
+
+@gpu
+@pytest.mark.parametrize("bt,v", [(100, 20011), (333, 40960), (700, 9000)])
+def test_alternatives_beside_a_kept_forward(bt, v):
+    # the first columns' logits go out through the buffers that 2^t leaves by: neither
+    # changes the other
+    x, w, y = base._inputs(bt, 512, v, torch.bfloat16, 120 + bt, grid=True, ignored=0.1)
+    a = torch.randn(bt, generator=torch.Generator().manual_seed(1)).cuda()
+    run, args, r = base._fused(x, w, y, top_k=20, keep_for_backward=True)
+    plain, _, r0 = base._fused(x, w, y, keep_for_backward=True)
+    ref = lp_rows_ref(f64(x) @ f64(w).T, y.numpy(), top_k=20)
+    base._check_rows(r, ref, base._logit_bound(x, w, 1.0), f"{bt}x{v}")
+    assert torch.equal(r.logp, r0.logp) and torch.equal(r.entropy, r0.entropy)
+    got, want = run.backward(*args, r, a, a), plain.backward(*args, r0, a, a)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
