@@ -9,7 +9,7 @@
 // the product of a few rows, or up to four segments of given logits); each part writes
 // (m, d, s), and k_lp_join combines them. For the k largest it has, from the product, at
 // most k candidates of each part, and from logits that lie in memory the maximum of each
-// 1024 of them (32 from the product of a few rows): the k-th largest of those maxima
+// 256 of them (32 from the product of a few rows): the k-th largest of those maxima
 // says which few have to be read again. The entropy comes from
 // sums centred on the maximum: lse - sum p_j s_j would cancel all digits of a
 // peaked row. The difference z - m is taken before the scale, so that a row of
@@ -26,7 +26,7 @@ constexpr int LP_MAX_TOP = 32;
 constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product (at most)
 constexpr int LP_FEW_COLS = 32;    // behind a kept maximum of the product of a few rows
 constexpr int LP_SEG = 8192;       // elements of a part of given logits
-constexpr int LP_CHUNKS = 8;       // maxima kept of each such part
+constexpr int LP_CHUNKS = 32;      // maxima kept of each such part: of 256 logits each
 // Segments of a row of given logits: they are counted from the 16-byte boundary
 // at or before the row, so a row that starts off one may need one more.
 inline int64_t lp_row_segs(int64_t v) { return (v + 7 + LP_SEG - 1) / LP_SEG; }

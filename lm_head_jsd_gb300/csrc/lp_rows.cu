@@ -4,10 +4,10 @@
 // k_lp_rows cuts each row into segments of 8192 logits, one CTA each, so that a
 // single row of 128256 still runs on 16 CTAs (of many rows of bf16 a CTA takes up to
 // four segments: k_lp_rows_many); the next segment is on its way while one is
-// reduced. The k largest are left to k_lp_join, which reads again the few 1024s whose
+// reduced. The k largest are left to k_lp_join, which reads again the few 256s whose
 // maxima reach the k-th largest of them (choosing candidates here took three times as
 // long as the sums: 361 us, 2047 x 128255 bf16, where the sums then took 117 and the
-// join now takes 35). k_lp_grad is elementwise. HBM bounds both for
+// join now takes 28). k_lp_grad is elementwise. HBM bounds both for
 // fp32 (1023 x 128255: 80 us = 6.6 TB/s, the gradient 160 us = 6.5 TB/s, 0.97 of a
 // copy's rate) and nearly so for bf16, with twice the elements to a byte (2047 x 128255:
 // 84 us = 6.2 TB/s, the gradient 165 us = 6.3 TB/s).
@@ -29,7 +29,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = LP_SEG / kThreads;  // logits a thread holds
 constexpr float kLn2 = 0.6931471805599453f;
-static_assert(kWarps == LP_CHUNKS, "a maximum for each warp");
+constexpr int kQuarters = LP_CHUNKS / kWarps;  // of a warp's vectors, a maximum for each
+static_assert(kQuarters == 4, "one 16-byte store");
 // Threads of a row's join: few rows are bound by one CTA's way through its loads (333
 // fused rows, 20 alternatives: 512 threads 16 us, 256 threads 19), many by how many
 // CTAs an SM holds (2047 rows of given logits, 8 alternatives, then: 128 threads 38 us, 256
@@ -178,6 +179,26 @@ __device__ __forceinline__ Mds block_mds(Mds x, float c, Mds* sh) {
   return x;
 }
 
+// The largest of a thread's logits (NaN passed over) and, where `keep` is set, the warp's
+// largest of each quarter of them.
+__device__ __forceinline__ float largest(const float (&z)[kPer], float* keep) {
+  float m[kQuarters];
+#pragma unroll
+  for (int q = 0; q < kQuarters; ++q) {
+    m[q] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer / kQuarters; ++i) m[q] = fmaxf(m[q], z[q * (kPer / kQuarters) + i]);
+  }
+  const float all = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  if (keep) {
+#pragma unroll
+    for (int q = 0; q < kQuarters; ++q)
+      asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m[q]) : "f"(m[q]));
+    if ((threadIdx.x & 31) == 0) *reinterpret_cast<float4*>(keep) = make_float4(m[0], m[1], m[2], m[3]);
+  }
+  return all;
+}
+
 // {sum 2^t, sum 2^t t} of a thread's logits, t = c (z - m).
 __device__ __forceinline__ float2 sums_of(const float (&z)[kPer], float m, float c) {
   // t = c z - c ref in one operation: c ref = hi + lo, hi rounded, and the sums
@@ -245,14 +266,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_lp_rows(Lp
     for (int u = 0; u < V; ++u) values(raw[u], z + u * N);
     // the next row's segment is on its way while this one is reduced
     if (r + gridDim.y < a.rows) load(r + gridDim.y);
-    Mds x{-INFINITY, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x.m = fmaxf(x.m, z[i]);  // (skips NaN)
+    float* keep = a.cmax ? a.cmax + ((r * parts + part) * kWarps + (tid >> 5)) * kQuarters : nullptr;
+    Mds x{largest(z, keep), 0.f, 0.f};
     const float2 ds = sums_of(z, x.m, a.c);
     x.d = ds.x;
     x.s = ds.y;
     x = block_mds<kWarps>(x, a.c, shm);
-    if (a.cmax && tid < kWarps) a.cmax[(r * parts + part) * kWarps + tid] = shm[tid].m;
     if (tid == 0) {
       a.part[r * parts + part] = make_float4(x.m, x.d, x.s, 0.f);
       if (a.labels && part == 0) {
@@ -320,14 +339,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_lp_rows_many(LpRowsArgs a) {
 #pragma unroll
       for (int u = 0; u < V; ++u) values(raw[u], z + u * N);
       ask();
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) m = fmaxf(m, z[i]);  // (skips NaN)
-      if (a.cmax) {
-        float w;
-        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
-        if ((tid & 31) == 0) a.cmax[((int64_t)r * a.segs + seg0 + seg) * kWarps + (tid >> 5)] = w;
-      }
+      float* keep = a.cmax ? a.cmax + (((int64_t)r * a.segs + seg0 + seg) * kWarps + (tid >> 5)) * kQuarters
+                           : nullptr;
+      float m = largest(z, keep);
       m = fmaxf(m, x.m);
       const float2 ds = sums_of(z, m, a.c);
       // the thread's sums so far, relative to the new maximum
@@ -485,46 +499,40 @@ __global__ void __launch_bounds__(kJoinThreads, (kJoinCtas<SRC, kJoinThreads>)) 
     if constexpr (kRowsSrc) {
       constexpr int N = 16 / sizeof(SRC);
       constexpr uint32_t kNone = sizeof(SRC) == 4 ? 0xff800000u : 0xff80u;  // -inf
-      if (few) {
-        const SRC* zr = reinterpret_cast<const SRC*>(a.z) + r * a.ld;
-        // every lane a chunk's maximum, the warp those chunks that reach it
-        for (int64_t c0 = (tid >> 5) * 32; c0 < chunks; c0 += 4 * kJoinThreads) {
-          float m1[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int64_t c = c0 + u * kJoinThreads + (tid & 31);
-            m1[u] = c < chunks ? cmax[c] : -INFINITY;
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            unsigned hit = __ballot_sync(0xffffffffu, m1[u] > -INFINITY && lp_key(m1[u]) >= least);
-            for (; hit; hit &= hit - 1) {
-              const int64_t col = (c0 + u * kJoinThreads + __ffs(hit) - 1) * LP_FEW_COLS + (tid & 31);
-              if (col < a.v) give(val(zr + col), col);
-            }
-          }
-        }
-        return;
-      }
+      constexpr int V = kPer / N / kQuarters;  // vectors behind a kept maximum
+      const SRC* zr = reinterpret_cast<const SRC*>(a.z) + r * a.ld;
       // every lane a chunk's maximum, the warp those chunks that reach it
-      for (int64_t c0 = tid >> 5; c0 < chunks; c0 += 32 * W) {
-        const int64_t cl = c0 + (tid & 31) * W;
-        const float m1 = cl < chunks ? cmax[cl] : -INFINITY;
-        unsigned hit = __ballot_sync(0xffffffffu, m1 > -INFINITY && lp_key(m1) >= least);
-        for (; hit; hit &= hit - 1) {
-          const int64_t c = c0 + (__ffs(hit) - 1) * W;
-          const Segment<SRC> g(a.z, a.ld, r, a.v, c / LP_CHUNKS);
-          const int j0 = ((int)(c % LP_CHUNKS) * 32 + (tid & 31)) * N;
-          Raw<SRC> raw[kPer / N];
+      for (int64_t c0 = tid >> 5; c0 < chunks; c0 += 4 * 32 * W) {
+        float m1[4];
 #pragma unroll
-          for (int u = 0; u < kPer / N; ++u)
-            raw[u] = load_raw(g.zs, u * kThreads * N + j0, g.first, g.n, kNone);
+        for (int u = 0; u < 4; ++u) {
+          const int64_t c = c0 + (u * 32 + (tid & 31)) * W;
+          m1[u] = c < chunks ? cmax[c] : -INFINITY;
+        }
 #pragma unroll
-          for (int u = 0; u < kPer / N; ++u) {
-            float z[N];
-            values(raw[u], z);
+        for (int u = 0; u < 4; ++u) {
+          unsigned hit = __ballot_sync(0xffffffffu, m1[u] > -INFINITY && lp_key(m1[u]) >= least);
+          for (; hit; hit &= hit - 1) {
+            const int64_t c = c0 + (u * 32 + __ffs(hit) - 1) * W;
+            if (few) {
+              const int64_t col = c * LP_FEW_COLS + (tid & 31);
+              if (col < a.v) give(val(zr + col), col);
+              continue;
+            }
+            const Segment<SRC> g(a.z, a.ld, r, a.v, c / LP_CHUNKS);
+            const int w = (int)(c % LP_CHUNKS);  // warp w / 4's vectors, quarter w % 4
+            const int j0 = ((w % kQuarters) * V * kThreads + w / kQuarters * 32 + (tid & 31)) * N;
+            Raw<SRC> raw[V];
 #pragma unroll
-            for (int i = 0; i < N; ++i) give(z[i], g.e0 + u * kThreads * N + j0 + i);
+            for (int v = 0; v < V; ++v)
+              raw[v] = load_raw(g.zs, v * kThreads * N + j0, g.first, g.n, kNone);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              float z[N];
+              values(raw[v], z);
+#pragma unroll
+              for (int i = 0; i < N; ++i) give(z[i], g.e0 + v * kThreads * N + j0 + i);
+            }
           }
         }
       }
