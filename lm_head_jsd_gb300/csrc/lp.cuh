@@ -25,8 +25,8 @@ namespace fljsd {
 constexpr int LP_MAX_TOP = 32;
 constexpr int LP_PART_COLS = 128;  // columns of a part of the fused product (at most)
 constexpr int LP_FEW_COLS = 32;    // behind a kept maximum of the product of a few rows
-constexpr int LP_SEG = 8192;       // elements of a part of given logits
-constexpr int LP_CHUNKS = 32;      // maxima kept of each such part: of 256 logits each
+constexpr int LP_SEG = 8192;       // elements of a segment of given logits
+constexpr int LP_CHUNKS = 32;      // maxima kept of a segment: of 256 logits each
 // Segments of a row of given logits: they are counted from the 16-byte boundary
 // at or before the row, so a row that starts off one may need one more.
 inline int64_t lp_row_segs(int64_t v) { return (v + 7 + LP_SEG - 1) / LP_SEG; }

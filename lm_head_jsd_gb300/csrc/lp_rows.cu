@@ -33,8 +33,8 @@ constexpr int kQuarters = LP_CHUNKS / kWarps;  // of a warp's vectors, a maximum
 static_assert(kQuarters == 4, "one 16-byte store");
 // Threads of a row's join: few rows are bound by one CTA's way through its loads (333
 // fused rows, 20 alternatives: 512 threads 16 us, 256 threads 19), many by how many
-// CTAs an SM holds (2047 rows of given logits, 8 alternatives, then: 128 threads 38 us, 256
-// threads 58).
+// CTAs an SM holds (given logits, 8 alternatives: 2047 rows of 128255 with 64, 128 and
+// 256 threads 26, 34 and 45 us, 1000 rows of 50001 21, 18 and 22).
 constexpr int kJoinFew = 512, kJoinMany = 128;
 constexpr int kJoinCap = 1024;  // candidates ranked in shared memory
 // as they are; more are sifted first (2000 x 1003, 20 alternatives: 359 us, sifted 25)
