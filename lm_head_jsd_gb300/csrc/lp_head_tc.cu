@@ -125,10 +125,11 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The largest value below x (-inf stays): candidates must exceed it.
+// The largest value below x (-inf stays): candidates must exceed it. Below +0.0 that is the
+// least negative value, for -0.0, the next key, is equal to it.
 __device__ __forceinline__ float below(unsigned key) {
   if (key <= 0x00800000u) return -INFINITY;  // no value yet, or -inf
-  const unsigned k = key - 1;
+  const unsigned k = key - (key == 0x80000000u ? 2u : 1u);
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
