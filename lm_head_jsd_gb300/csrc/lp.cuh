@@ -130,8 +130,9 @@ int lp_head_tile_cols(int64_t m, int64_t n, int64_t k);
 int lp_head_dump_blocks(int64_t m, int64_t n, int64_t k, int top, int bn);
 cudaError_t launch_lp_head(const LpHeadArgs& a, cudaStream_t st);
 
-// Floats as integers in their order (0 is below every value).
+// Floats as integers in their order (0 is below every value); -0.0 becomes +0.0, its equal.
 __host__ __device__ inline unsigned lp_key(float x) {
+  x += 0.f;
 #ifdef __CUDA_ARCH__
   const unsigned u = __float_as_uint(x);
 #else

@@ -126,7 +126,7 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 
 // The largest value below x (-inf stays): candidates must exceed it. Below +0.0 that is the
-// least negative value, for -0.0, the next key, is equal to it.
+// least negative value (the key between them is no value's: -0.0 has +0.0's).
 __device__ __forceinline__ float below(unsigned key) {
   if (key <= 0x00800000u) return -INFINITY;  // no value yet, or -inf
   const unsigned k = key - (key == 0x80000000u ? 2u : 1u);
