@@ -216,9 +216,10 @@ __device__ __forceinline__ float2 sums_of(const float (&z)[kPer], float m, float
   }
   const float f = ex2(-lo);
   float2 o = make_float2((d.x + d.y) * f, __fmaf_rn(-lo, d.x + d.y, t.x + t.y) * f);
-  if (!(fabsf(o.y) < INFINITY)) {
+  if (!(fabsf(o.y) < INFINITY && fabsf(lo) <= 64.f)) {
     // a logit of -inf or near the type's lowest (0 times -inf above), a maximum
-    // that overflows c, or NaN, which stays: with the difference taken first
+    // that overflows c, a maximum so far out (2^30 and more) that 2^lo may vanish
+    // beside a finite 2^-lo, or NaN, which stays: with the difference taken first
     o = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
