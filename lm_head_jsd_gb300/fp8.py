@@ -5,6 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from ._streams import hand_over, on
 from .api import _DT
 
 BLOCK = 128
@@ -27,11 +28,12 @@ def fp8_quantize(w, *, block_rows=BLOCK, stream=None):
         raise ValueError(f"w has dtype {w.dtype}, expected one of {list(_DT)}")
     rows, cols = w.shape
     ldq, kb = -(-cols // 16) * 16, -(-cols // BLOCK)
-    codes = torch.empty((rows, ldq), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((-(-rows // BLOCK), kb) if block_rows == BLOCK else (kb, rows),
-                         dtype=torch.float32, device=w.device)
-    _lib.fljsd_fp8_quantize(rows, cols, _DT[w.dtype], block_rows, w, ld, codes, ldq, scales,
-                            stream=stream)
+    with on(stream, w.device):
+        codes = torch.empty((rows, ldq), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((-(-rows // BLOCK), kb) if block_rows == BLOCK else (kb, rows),
+                             dtype=torch.float32, device=w.device)
+        _lib.fljsd_fp8_quantize(rows, cols, _DT[w.dtype], block_rows, w, ld, codes, ldq, scales)
+    hand_over((codes, scales), stream, w.device)
     return codes.view(torch.float8_e4m3fn)[:, :cols], scales
 
 
@@ -48,16 +50,16 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stre
     if (w_scales.dtype != torch.float32 or not w_scales.is_contiguous() or w_scales.device != dev
             or tuple(w_scales.shape) != (-(-n // BLOCK), -(-k // BLOCK))):
         raise ValueError(f"w_scales must be fp32 [{-(-n // BLOCK)}, {-(-k // BLOCK)}] on {dev}")
-    if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    elif out.dtype != out_dtype or tuple(out.shape) != (m, n) or out.device != dev:
+    if out is not None and (out.dtype != out_dtype or tuple(out.shape) != (m, n) or out.device != dev):
         raise ValueError(f"out must be {out_dtype} [{m}, {n}] on {dev}")
-    ws = torch.empty(_lib.fljsd_fp8_linear_workspace_bytes(m, k), dtype=torch.uint8, device=dev)
-    _lib.fljsd_fp8_linear(m, n, k, _DT[x.dtype], x, ldx, w_codes, ldw, w_scales, _DT[out_dtype],
-                          out, _check_rows("out", out), ws, stream=stream)
-    if stream is not None and not isinstance(stream, int):
-        ws.record_stream(stream)
-    return out
+    with on(stream, dev):
+        y = out if out is not None else torch.empty((m, n), dtype=out_dtype, device=dev)
+        ws = torch.empty(_lib.fljsd_fp8_linear_workspace_bytes(m, k), dtype=torch.uint8, device=dev)
+        _lib.fljsd_fp8_linear(m, n, k, _DT[x.dtype], x, ldx, w_codes, ldw, w_scales, _DT[out_dtype],
+                              y, _check_rows("out", y), ws)
+    if out is None:
+        hand_over((y,), stream, dev)
+    return y
 
 
 __all__ = ["fp8_linear", "fp8_quantize"]

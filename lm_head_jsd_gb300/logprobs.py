@@ -9,6 +9,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
+from ._streams import Memory, hand_over, on
 from .api import _DT, _check
 
 
@@ -64,6 +65,7 @@ class FusedLinearLogprobs:
         self.plan = _lib.fljsd_lp_plan(self.problem, int(free_hbm_bytes))
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8,
                                      device=self.device)
+        self._memory = Memory([self.workspace])
         self._kept = None  # the result whose probabilities the workspace holds
 
     def forward(self, x, w, labels=None, out=None, stream=None) -> Logprobs:
@@ -72,10 +74,14 @@ class FusedLinearLogprobs:
         _check("w", w, self.dtype, self.device, (p.v, p.h))
         if labels is not None:
             _check("labels", labels, torch.int64, self.device, (p.bt,))
-        r = _results(p.bt, p.top_k, labels is not None, self.device) if out is None else out
         self._kept = None
-        _lib.fljsd_lp_forward(p, self.plan, x, w, labels, r.logp, r.entropy, r.lse, r.norm,
-                              r.top_logp, r.top_id, self.workspace, stream=stream)
+        with on(stream, self.device):
+            self._memory.use()
+            r = _results(p.bt, p.top_k, labels is not None, self.device) if out is None else out
+            _lib.fljsd_lp_forward(p, self.plan, x, w, labels, r.logp, r.entropy, r.lse, r.norm,
+                                  r.top_logp, r.top_id, self.workspace)
+        if out is None:
+            hand_over(r, stream, self.device)
         if p.flags & _lib.FLJSD_LP_BACKWARD and self.plan.num_chunks == 1:
             self._kept = r
         return r
@@ -91,14 +97,18 @@ class FusedLinearLogprobs:
             _check("labels", labels, torch.int64, self.device, (p.bt,))
         _check_grad("grad_logp", grad_logp, p.bt, self.device)
         _check_grad("grad_entropy", grad_entropy, p.bt, self.device)
-        if out is None:
-            out = (torch.empty_like(x) if need[0] else None, torch.empty_like(w) if need[1] else None)
         kept = self._kept is result
         self._kept = None
-        _lib.fljsd_lp_backward(p, self.plan, x, w, labels, result.logp, result.entropy, result.norm,
-                               grad_logp, grad_entropy, int(kept), out[0], out[1], self.workspace,
-                               stream=stream)
-        return out
+        with on(stream, self.device):
+            self._memory.use()
+            g = out if out is not None else (torch.empty_like(x) if need[0] else None,
+                                             torch.empty_like(w) if need[1] else None)
+            _lib.fljsd_lp_backward(p, self.plan, x, w, labels, result.logp, result.entropy,
+                                   result.norm, grad_logp, grad_entropy, int(kept), g[0], g[1],
+                                   self.workspace)
+        if out is None:
+            hand_over(g, stream, self.device)
+        return g
 
 
 def _outputs(ctx, r):
@@ -175,14 +185,14 @@ def logits_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_ind
     stride apart). For a differentiable form see :func:`token_logprobs`."""
     _logits_check(logits, labels)
     rows, v = logits.shape
-    r = _results(rows, top_k, labels is not None, logits.device)
-    ws = torch.empty(_lib.fljsd_logits_lp_workspace_bytes(rows, v, top_k), dtype=torch.uint8,
-                     device=logits.device)
-    _lib.fljsd_logits_lp(rows, v, _row_stride(logits), _DT[logits.dtype], top_k, temperature,
-                         ignore_index, logits, labels, r.logp, r.entropy, r.lse, r.norm,
-                         r.top_logp, r.top_id, ws, stream=stream)
-    if stream is not None and not isinstance(stream, int):
-        ws.record_stream(stream)
+    with on(stream, logits.device):
+        r = _results(rows, top_k, labels is not None, logits.device)
+        ws = torch.empty(_lib.fljsd_logits_lp_workspace_bytes(rows, v, top_k), dtype=torch.uint8,
+                         device=logits.device)
+        _lib.fljsd_logits_lp(rows, v, _row_stride(logits), _DT[logits.dtype], top_k, temperature,
+                             ignore_index, logits, labels, r.logp, r.entropy, r.lse, r.norm,
+                             r.top_logp, r.top_id, ws)
+    hand_over(r, stream, logits.device)
     return r
 
 
@@ -194,16 +204,19 @@ def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entrop
     rows, v = logits.shape
     _check_grad("grad_logp", grad_logp, rows, logits.device)
     _check_grad("grad_entropy", grad_entropy, rows, logits.device)
-    if out is None:
-        out = torch.empty((rows, v), dtype=logits.dtype, device=logits.device)
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device or (
-            out.stride(1) != 1 and v > 1):
+    if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype or
+                            out.device != logits.device or (out.stride(1) != 1 and v > 1)):
         raise ValueError("out must be like the logits, with contiguous rows")
-    _lib.fljsd_logits_lp_backward(rows, v, _row_stride(logits), _row_stride(out),
-                                  _DT[logits.dtype], temperature, ignore_index, logits, labels,
-                                  result.logp, result.entropy, result.norm, grad_logp, grad_entropy,
-                                  out, stream=stream)
-    return out
+    with on(stream, logits.device):
+        g = out if out is not None else torch.empty((rows, v), dtype=logits.dtype,
+                                                    device=logits.device)
+        _lib.fljsd_logits_lp_backward(rows, v, _row_stride(logits), _row_stride(g),
+                                      _DT[logits.dtype], temperature, ignore_index, logits, labels,
+                                      result.logp, result.entropy, result.norm, grad_logp,
+                                      grad_entropy, g)
+    if out is None:
+        hand_over((g,), stream, logits.device)
+    return g
 
 
 class _TokenLogprobsFunction(torch.autograd.Function):

@@ -7,6 +7,7 @@ import numpy as np
 import torch
 
 from . import _lib
+from ._streams import Memory, on
 from .api import _DT
 
 _BLOCK = 128  # elements of one 8-bit state block
@@ -53,7 +54,8 @@ class AdamW:
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits, self.steps = state_bits, int(step)
         self._check("params", self.params, self.dtype)
-        if master is True:
+        own_master = master is True
+        if own_master:
             master = [p.detach().float() for p in self.params]
         self.master = list(master) if master else None
         if self.master and self.dtype != torch.bfloat16:
@@ -78,6 +80,10 @@ class AdamW:
                 ("exp_avg_sq_scale", self.exp_avg_sq_scale, torch.float32, None)):
             if ts is not None:
                 self._check(name, ts, dt, want or [-(-n // _BLOCK) for n in sizes])
+        made = [] if exp_avg is not None else [*self.exp_avg, *self.exp_avg_sq,
+                                               *(self.exp_avg_scale or ()), *(self.exp_avg_sq_scale or ())]
+        made += self.master if own_master else []
+        self._memory = Memory(made) if made and self.device.type == "cuda" else None
         self._sizes = sizes
         self._table = np.zeros(len(sizes), dtype=_ENTRY)
         t = self._table
@@ -143,7 +149,10 @@ class AdamW:
         o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay,
                                     self.steps + 1, _DT[self.dtype], _DT[dt], self.state_bits,
                                     int(self.master is not None))
-        _lib.fljsd_adamw_step(o, t.ctypes.data, len(t), grad_scale, stream=stream)
+        with on(stream, dev):
+            if self._memory is not None:
+                self._memory.use()
+            _lib.fljsd_adamw_step(o, t.ctypes.data, len(t), grad_scale)
         self.steps += 1
 
 
