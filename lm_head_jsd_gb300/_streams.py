@@ -1,4 +1,4 @@
-"""Memory of calls that run on a stream other than the current one."""
+"""The device and stream a call runs on, and its memory there."""
 from __future__ import annotations
 
 from contextlib import nullcontext
@@ -10,12 +10,17 @@ from . import _lib
 _HERE = nullcontext()
 
 
+def require_cuda(name, device):
+    if device.type != "cuda":
+        raise ValueError(f"{name} is on {device}, expected a CUDA device")
+
+
 def on(stream, device):
     """Where a call allocates and launches: on ``stream`` (a Stream or its handle), so that
     what it takes is free there and what it drops is not handed out before that stream has
-    passed the call; None: where the caller is."""
+    passed the call; None: on the current stream of its tensors' device."""
     if stream is None:
-        return _HERE
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream if isinstance(stream, int) else stream.cuda_stream
         # (0 and 1 are the default stream's)

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._streams import hand_over, on
+from ._streams import hand_over, on, require_cuda
 from .api import _DT
 
 BLOCK = 128
@@ -26,6 +26,7 @@ def fp8_quantize(w, *, block_rows=BLOCK, stream=None):
     ld = _check_rows("w", w)
     if w.dtype not in _DT:
         raise ValueError(f"w has dtype {w.dtype}, expected one of {list(_DT)}")
+    require_cuda("w", w.device)
     rows, cols = w.shape
     ldq, kb = -(-cols // 16) * 16, -(-cols // BLOCK)
     with on(stream, w.device):
@@ -43,6 +44,7 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stre
     ldx = _check_rows("x", x)
     ldw = _check_rows("w_codes", w_codes)
     (m, k), n, dev = x.shape, w_codes.shape[0], x.device
+    require_cuda("x", dev)
     if x.dtype not in _DT or out_dtype not in _DT:
         raise ValueError(f"x and out_dtype must be one of {list(_DT)}")
     if w_codes.dtype != torch.float8_e4m3fn or w_codes.shape[1] != k or w_codes.device != dev:

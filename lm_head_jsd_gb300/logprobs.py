@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._streams import Memory, hand_over, on
+from ._streams import Memory, hand_over, on, require_cuda
 from .api import _DT, _check
 
 
@@ -53,7 +53,8 @@ class FusedLinearLogprobs:
                  ignore_index=-100, chunk_rows=0, keep_for_backward=False, accum_fp32=False,
                  device="cuda", free_hbm_bytes=None):
         self.device = torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
+        require_cuda("the plan", self.device)
+        if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         if dtype not in _DT:
             raise ValueError(f"dtype {dtype} is not one of {list(_DT)}")
@@ -170,6 +171,7 @@ def _logits_check(logits, labels):
         raise ValueError(f"logits have dtype {logits.dtype}, expected one of {list(_DT)}")
     if logits.stride(1) != 1 and logits.shape[1] > 1:
         raise ValueError("the rows of logits must be contiguous")
+    require_cuda("logits", logits.device)
     if labels is not None:
         _check("labels", labels, torch.int64, logits.device, (logits.shape[0],))
 

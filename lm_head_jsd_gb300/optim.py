@@ -7,7 +7,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._streams import Memory, on
+from ._streams import Memory, on, require_cuda
 from .api import _DT
 
 _BLOCK = 128  # elements of one 8-bit state block
@@ -137,6 +137,7 @@ class AdamW:
             if not live:
                 return
         dt, dev = live[0].dtype, self.device
+        require_cuda("the optimizer", dev)
         # (whole-list checks: a step of many small tensors is bound by this function)
         if (dt not in _DT or set(map(_DTYPE, live)) != {dt} or set(map(_DEVICE, live)) != {dev}
                 or not all(map(torch.Tensor.is_contiguous, live))
