@@ -34,6 +34,18 @@ def _results(rows, top_k, with_logp, device) -> Logprobs:
                     torch.empty((rows, top_k), dtype=torch.int64, device=device) if top_k else None)
 
 
+def _check_result(r, rows, with_logp, device, top_k=None):
+    """That a result is one of ``rows`` rows (and of ``top_k`` alternatives, to be written)."""
+    need = [("logp", torch.float32, (rows,))] if with_logp else []
+    need += [("entropy", torch.float32, (rows,)), ("norm", torch.float32, (rows, 2))]
+    if top_k is not None:
+        need.append(("lse", torch.float32, (rows,)))
+        if top_k:
+            need += [("top_logp", torch.float32, (rows, top_k)), ("top_id", torch.int64, (rows, top_k))]
+    for name, dtype, shape in need:
+        _check(f"the result's {name}", getattr(r, name), dtype, device, shape)
+
+
 def _check_grad(name, t, rows, device):
     if t is not None:
         _check(name, t, torch.float32, device, (rows,))
@@ -42,11 +54,11 @@ def _check_grad(name, t, rows, device):
 class FusedLinearLogprobs:
     """Plans one problem shape and keeps its workspace for repeated calls.
 
-    ``forward`` returns :class:`Logprobs`; with ``keep_for_backward`` the plan also
-    serves ``backward``, which takes the upstream gradients of logp and entropy.
-    A forward whose plan is one chunk leaves the probabilities (bt x v bf16) in the
-    workspace for the first backward of its result; any other backward computes
-    them again.
+    ``forward`` returns :class:`Logprobs` (``out``: a result to be written instead); with
+    ``keep_for_backward`` the plan also serves ``backward``, which takes the upstream
+    gradients of logp and entropy. A forward whose plan is one chunk leaves the
+    probabilities (bt x v fp16) in the workspace for the first backward of its result; any
+    other backward computes them again.
     """
 
     def __init__(self, bt, h, v, dtype=torch.bfloat16, *, top_k=0, temperature=1.0,
@@ -75,6 +87,8 @@ class FusedLinearLogprobs:
         _check("w", w, self.dtype, self.device, (p.v, p.h))
         if labels is not None:
             _check("labels", labels, torch.int64, self.device, (p.bt,))
+        if out is not None:
+            _check_result(out, p.bt, labels is not None, self.device, p.top_k)
         self._kept = None
         with on(stream, self.device):
             self._memory.use()
@@ -98,7 +112,13 @@ class FusedLinearLogprobs:
             _check("labels", labels, torch.int64, self.device, (p.bt,))
         _check_grad("grad_logp", grad_logp, p.bt, self.device)
         _check_grad("grad_entropy", grad_entropy, p.bt, self.device)
+        if out is not None:
+            for name, t, like in zip(("grad_input", "grad_weight"), out, (x, w), strict=True):
+                if t is not None:
+                    _check(name, t, self.dtype, self.device, like.shape)
         kept = self._kept is result
+        if not kept:
+            _check_result(result, p.bt, labels is not None, self.device)
         self._kept = None
         with on(stream, self.device):
             self._memory.use()
@@ -206,6 +226,7 @@ def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entrop
     rows, v = logits.shape
     _check_grad("grad_logp", grad_logp, rows, logits.device)
     _check_grad("grad_entropy", grad_entropy, rows, logits.device)
+    _check_result(result, rows, labels is not None, logits.device)
     if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype or
                             out.device != logits.device or (out.stride(1) != 1 and v > 1)):
         raise ValueError("out must be like the logits, with contiguous rows")

@@ -54,3 +54,70 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     ctx = _streams.on(None, torch.device("cuda", 1))
     assert isinstance(ctx, torch.cuda.device) and ctx.idx == 1
     assert not isinstance(_streams.on(None, torch.device("cuda", 0)), torch.cuda.device)
+
+
+# ---- results and outputs that are given ----
+def _result(rows=4, k=2, device="cpu", **other):
+    f = lambda *s: torch.zeros(s, device=device)  # noqa: E731
+    r = dict(logp=f(rows), entropy=f(rows), lse=f(rows), norm=f(rows, 2), top_logp=f(rows, k),
+             top_id=f(rows, k).long())
+    return fl.Logprobs(**{**r, **other})
+
+
+def _bad_results(device):
+    f = lambda *s: torch.zeros(s, device=device)  # noqa: E731
+    return [dict(entropy=f(3)), dict(norm=f(4)), dict(norm=f(4, 4)[:, ::2]), dict(entropy=f(4).double()),
+            dict(logp=f(4).half()), dict(logp=None), dict(norm=None),
+            dict(entropy=torch.zeros(4, device="meta"))]
+
+
+def _bad_outs(device):
+    f = lambda *s: torch.zeros(s, device=device)  # noqa: E731
+    return _bad_results(device) + [dict(lse=f(5)), dict(top_logp=f(4, 1)), dict(top_id=None),
+                                   dict(top_id=f(4, 2)), dict(top_id=f(4, 3).long()[:, :2])]
+
+
+def test_results_are_checked():
+    from lm_head_jsd_gb300.logprobs import _check_result
+
+    cpu = torch.device("cpu")
+    _check_result(_result(), 4, True, cpu, 2)
+    _check_result(_result(logp=None), 4, False, cpu, 2)
+    _check_result(_result(lse=None, top_logp=None, top_id=None), 4, True, cpu)
+    _check_result(_result(top_logp=None, top_id=None), 4, True, cpu, 0)
+    for bad in _bad_outs(cpu):
+        with pytest.raises((ValueError, TypeError)):
+            _check_result(_result(**bad), 4, True, cpu, 2)
+    for bad in _bad_results(cpu):
+        with pytest.raises((ValueError, TypeError)):
+            _check_result(_result(**bad), 4, True, cpu)
+
+
+@gpu
+def test_given_results_and_outputs_are_refused_on_the_host():
+    """Nothing is launched: each of these would be written or read past its end."""
+    x, w = torch.randn(4, 64).bfloat16().cuda(), torch.randn(50, 64).bfloat16().cuda()
+    y = torch.tensor([0, 1, 2, 49]).cuda()
+    g = torch.ones(4, device="cuda")
+    run = fl.FusedLinearLogprobs(4, 64, 50, top_k=2, keep_for_backward=True)
+    r = run.forward(x, w, y)
+    launched = fl.fljsd_launch_count()
+    for bad in _bad_outs("cuda"):
+        with pytest.raises((ValueError, TypeError)):
+            run.forward(x, w, y, out=_result(device="cuda", **bad))
+    for bad in _bad_results("cuda"):
+        q = _result(device="cuda", **bad)
+        with pytest.raises((ValueError, TypeError)):
+            run.backward(x, w, y, q, g)
+        with pytest.raises((ValueError, TypeError)):
+            fl.logits_logprobs_backward(x.float() @ w.float().T, y, q, g)
+    e = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    for bad in ((e(3, 64), e(50, 64)), (e(4, 64), e(49, 64)), (e(64, 4).T, None), (None, e(50, 65)[:, :64]),
+                (e(4, 64, dtype=torch.float32), None), (None,)):
+        with pytest.raises(ValueError):
+            run.backward(x, w, y, r, g, out=bad)
+    assert fl.fljsd_launch_count() == launched
+    # what was refused leaves the plan as it was
+    gx, gw = torch.empty_like(x), torch.empty_like(w)
+    assert run.backward(x, w, y, r, g, out=(gx, gw))[0] is gx
+    assert torch.equal(gw, run.backward(x, w, y, r, g)[1])
