@@ -40,7 +40,10 @@ def fp8_quantize(w, *, block_rows=BLOCK, stream=None):
 
 def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stream=None):
     """x.w^T of x [m, k] (fp32 or bf16, quantised on the way) and a weight from
-    :func:`fp8_quantize`. Carries no gradient."""
+    :func:`fp8_quantize`. Carries no gradient: an x that would need one is refused (pass
+    ``x.detach()``, or call under ``torch.no_grad()``)."""
+    if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
+        raise ValueError("x requires a gradient, which fp8_linear does not give: pass x.detach()")
     ldx = _check_rows("x", x)
     ldw = _check_rows("w_codes", w_codes)
     (m, k), n, dev = x.shape, w_codes.shape[0], x.device

@@ -121,3 +121,27 @@ def test_given_results_and_outputs_are_refused_on_the_host():
     gx, gw = torch.empty_like(x), torch.empty_like(w)
     assert run.backward(x, w, y, r, g, out=(gx, gw))[0] is gx
     assert torch.equal(gw, run.backward(x, w, y, r, g)[1])
+
+
+# ---- what carries no gradient ----
+def test_fp8_linear_does_not_cut_a_graph_silently():
+    x, w, s = _fp8()
+    with pytest.raises(ValueError, match="requires a gradient"):
+        fl.fp8_linear(x.requires_grad_(), w, s)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        fl.fp8_linear(x * 2, w, s)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+        fl.fp8_linear(x, w, s)
+    with pytest.raises(ValueError, match="CUDA device"):
+        fl.fp8_linear(x.detach(), w, s)
+
+
+@gpu
+def test_fp8_linear_without_a_graph():
+    x = torch.randn(3, 64, device="cuda", requires_grad=True)
+    q = fl.fp8_quantize(torch.randn(200, 64, device="cuda"))
+    want = fl.fp8_linear(x.detach(), *q)
+    with torch.no_grad():
+        assert torch.equal(fl.fp8_linear(x, *q), want)
+    with torch.inference_mode():
+        assert torch.equal(fl.fp8_linear(x, *q), want)
