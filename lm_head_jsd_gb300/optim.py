@@ -5,6 +5,7 @@ from operator import attrgetter
 
 import numpy as np
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._streams import Memory, on, require_cuda
@@ -18,7 +19,7 @@ _ENTRY = np.dtype([(n, np.uint64) for n in ("grad", "param", "master", "exp_avg"
                   [("n", np.int64)])
 
 
-_DTYPE, _DEVICE = attrgetter("dtype"), attrgetter("device")
+_DTYPE, _DEVICE = attrgetter("dtype"), torch.Tensor.get_device  # (-1 off the GPUs)
 
 
 def _ptrs(ts):
@@ -85,6 +86,7 @@ class AdamW:
         made += self.master if own_master else []
         self._memory = Memory(made) if made and self.device.type == "cuda" else None
         self._sizes = sizes
+        self._stepped = self.params + (self.master or [])
         self._table = np.zeros(len(sizes), dtype=_ENTRY)
         t = self._table
         self._at = _ptrs(self.params)
@@ -125,7 +127,7 @@ class AdamW:
             self._check("params", self.params, self.dtype, self._sizes)
             self._at = at
             t["param"] = at
-        live, sizes = grads, self._sizes
+        live, sizes, stepped = grads, self._sizes, self._stepped
         try:
             t["grad"] = _ptrs(grads)
         except TypeError:  # some are None: those parameters stay as they are
@@ -134,12 +136,13 @@ class AdamW:
             t["n"] = [0 if g is None else n for g, n in zip(grads, sizes)]
             live = [g for g in grads if g is not None]
             sizes = [n for g, n in zip(grads, sizes) if g is not None]
+            stepped = [x for x, g in zip(stepped, grads * 2) if g is not None]
             if not live:
                 return
         dt, dev = live[0].dtype, self.device
         require_cuda("the optimizer", dev)
         # (whole-list checks: a step of many small tensors is bound by this function)
-        if (dt not in _DT or set(map(_DTYPE, live)) != {dt} or set(map(_DEVICE, live)) != {dev}
+        if (dt not in _DT or set(map(_DTYPE, live)) != {dt} or set(map(_DEVICE, live)) != {dev.index}
                 or not all(map(torch.Tensor.is_contiguous, live))
                 or list(map(torch.Tensor.numel, live)) != sizes):
             raise ValueError(f"gradients must be contiguous, of one dtype of {list(_DT)}, on {dev}, "
@@ -154,6 +157,8 @@ class AdamW:
             if self._memory is not None:
                 self._memory.use()
             _lib.fljsd_adamw_step(o, t.ctypes.data, len(t), grad_scale)
+        # autograd's own check of what it saved: these have changed
+        increment_version(stepped)
         self.steps += 1
 
 

@@ -1,0 +1,39 @@
+"""The operators inside autograd: what they write in place is seen by the graphs that saved
+it, and a graph's own values are those of its forward."""
+import pytest
+import torch
+
+gpu = pytest.mark.gpu
+
+
+def _problem(dtype=torch.bfloat16, bt=20, h=64, v=300):
+    g = torch.Generator().manual_seed(bt)
+    x, w = torch.randn(bt, h, generator=g), torch.randn(v, h, generator=g) / 8
+    y = torch.randint(0, v, (bt,), generator=g).cuda()
+    return x.to(dtype).cuda().requires_grad_(), w.to(dtype).cuda().requires_grad_(), y
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("master", [None, True])
+def test_a_step_is_seen_by_the_graphs_before_it(bits, master):
+    from lm_head_jsd_gb300 import AdamW, fused_linear_logprobs
+
+    x, w, y = _problem()
+    other = torch.ones(5, dtype=torch.bfloat16, device="cuda").requires_grad_()
+    square = (other * other).sum()
+    opt = AdamW([w, other], lr=0.1, state_bits=bits, master=master)
+    loss = fused_linear_logprobs(x, w, y).logp.sum()
+    loss.backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    square.backward()  # had no gradient: not stepped
+    version = w._version
+    w.grad = None
+    opt.step()
+    assert w._version == version and other._version > 0
+    with torch.inference_mode():  # (tensors without a version)
+        p = torch.ones(5, device="cuda")
+        AdamW([p]).step([torch.ones(5, device="cuda")])
+        assert (p != 1).all()

@@ -145,3 +145,16 @@ def test_fp8_linear_without_a_graph():
         assert torch.equal(fl.fp8_linear(x, *q), want)
     with torch.inference_mode():
         assert torch.equal(fl.fp8_linear(x, *q), want)
+
+
+@gpu
+def test_adamw_gradients_elsewhere_are_refused():
+    opt = fl.AdamW([torch.zeros(4, device="cuda"), torch.zeros(3, device="cuda")])
+    good = [torch.ones(4, device="cuda"), torch.ones(3, device="cuda")]
+    for bad in ([good[0], good[1].cpu()], [good[0].cpu(), good[1].cpu()], [good[0], good[1].to("meta")],
+                [None, good[1].cpu()]):
+        with pytest.raises((ValueError, RuntimeError)):
+            opt.step(bad)
+    assert opt.steps == 0 and not opt.params[0].any()
+    opt.step(good)
+    assert opt.params[0].all()
