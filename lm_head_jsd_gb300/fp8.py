@@ -3,6 +3,7 @@ of 128 (the C entry points fljsd_fp8_*)."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._streams import hand_over, on, require_cuda
@@ -64,6 +65,8 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stre
                               y, _check_rows("out", y), ws)
     if out is None:
         hand_over((y,), stream, dev)
+    else:  # autograd's own check of what it saved: this has changed
+        increment_version(out)
     return y
 
 

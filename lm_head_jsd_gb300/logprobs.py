@@ -7,6 +7,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._streams import Memory, hand_over, on, require_cuda
@@ -97,6 +98,8 @@ class FusedLinearLogprobs:
                                   r.top_logp, r.top_id, self.workspace)
         if out is None:
             hand_over(r, stream, self.device)
+        else:  # autograd's own check of what it saved: these have changed
+            increment_version([t for t in out if t is not None])
         if p.flags & _lib.FLJSD_LP_BACKWARD and self.plan.num_chunks == 1:
             self._kept = r
         return r
@@ -129,6 +132,8 @@ class FusedLinearLogprobs:
                                    self.workspace)
         if out is None:
             hand_over(g, stream, self.device)
+        else:
+            increment_version([t for t in out if t is not None])
         return g
 
 
@@ -239,6 +244,8 @@ def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entrop
                                       grad_entropy, g)
     if out is None:
         hand_over((g,), stream, logits.device)
+    else:
+        increment_version(out)
     return g
 
 

@@ -37,3 +37,33 @@ def test_a_step_is_seen_by_the_graphs_before_it(bits, master):
         p = torch.ones(5, device="cuda")
         AdamW([p]).step([torch.ones(5, device="cuda")])
         assert (p != 1).all()
+
+
+@gpu
+def test_given_outputs_are_seen_by_the_graphs_that_saved_them():
+    import lm_head_jsd_gb300 as fl
+
+    x, w, y = (t.detach() for t in _problem())
+    z = (x.float() @ w.float().T)
+    q = fl.fp8_quantize(w)
+    leaf = torch.ones((), device="cuda", requires_grad=True)
+    saved = lambda t: (leaf * t).sum()  # (the product saves t)  # noqa: E731
+    run = fl.FusedLinearLogprobs(20, 64, 300, keep_for_backward=True)
+    r = run.forward(x, w, y)
+    gx, gw = torch.empty_like(x), torch.empty_like(w)
+    a = torch.ones(20, device="cuda")
+    zl = fl.logits_logprobs(z, y)
+    out = torch.empty(20, 300, device="cuda", dtype=torch.bfloat16)
+    graph = fl.token_logprobs(z.requires_grad_(), y).logp.sum()  # keeps z for its gradient
+    z = z.detach()
+    for write, t in ((lambda: run.forward(x, w, y, out=r), r.lse),
+                     (lambda: run.backward(x, w, y, r, a, out=(gx, gw)), gx),
+                     (lambda: run.backward(x, w, y, r, a, out=(None, gw)), gw),
+                     (lambda: fl.fp8_linear(x, *q, out=out), out),
+                     (lambda: fl.logits_logprobs_backward(z, y, zl, a, out=z), z)):
+        loss = saved(t)
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        graph.backward()
