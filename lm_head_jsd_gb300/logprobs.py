@@ -161,14 +161,15 @@ class _FusedLinearLogprobsFunction(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         if need:
             ctx.run, ctx.result = run, r
-            ctx.save_for_backward(xc, wc, lab)
+            # (of the result, for the check that nothing has been written over it)
+            ctx.save_for_backward(xc, wc, lab, r.logp, r.entropy, r.norm)
         return _outputs(ctx, r)
 
     @staticmethod
     def backward(ctx, g_logp, g_entropy, *_):
         if g_logp is None and g_entropy is None:
             return (None,) * 8
-        x, w, labels = ctx.saved_tensors
+        x, w, labels, *_ = ctx.saved_tensors
         need = ctx.needs_input_grad[:2]
         gx, gw = ctx.run.backward(x, w, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                   need=need)
@@ -258,7 +259,7 @@ class _TokenLogprobsFunction(torch.autograd.Function):
         lab = None if labels is None else labels.contiguous()
         r = logits_logprobs(z, lab, top_k=top_k, temperature=temperature, ignore_index=ignore_index)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(z, lab)
+        ctx.save_for_backward(z, lab, r.logp, r.entropy, r.norm)
         ctx.result, ctx.opts = r, (temperature, ignore_index)
         return _outputs(ctx, r)
 
@@ -266,7 +267,7 @@ class _TokenLogprobsFunction(torch.autograd.Function):
     def backward(ctx, g_logp, g_entropy, *_):
         if g_logp is None and g_entropy is None:
             return (None,) * 5
-        z, labels = ctx.saved_tensors
+        z, labels, *_ = ctx.saved_tensors
         g = logits_logprobs_backward(z, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                      temperature=ctx.opts[0], ignore_index=ctx.opts[1])
         return g, None, None, None, None

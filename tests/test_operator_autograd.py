@@ -67,3 +67,52 @@ def test_given_outputs_are_seen_by_the_graphs_that_saved_them():
             loss.backward()
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         graph.backward()
+
+
+@gpu
+@pytest.mark.parametrize("form", ["fused", "token"])
+@pytest.mark.parametrize("name", ["logp", "entropy", "norm"])
+def test_results_written_over_before_their_backward(form, name):
+    from lm_head_jsd_gb300 import fused_linear_logprobs, token_logprobs
+
+    x, w, y = _problem()
+
+    def graph():
+        r = (fused_linear_logprobs(x, w, y) if form == "fused" else token_logprobs(x @ w.T, y))
+        return r, r.logp.sum() + r.entropy.sum()
+
+    _, loss = graph()
+    want = torch.autograd.grad(loss, (x, w))
+    r, loss = graph()
+    changed = getattr(r, name).detach().clone()  # a copy may be changed
+    changed.zero_()
+    got = torch.autograd.grad(loss, (x, w), retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    getattr(r, name).detach().zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+@gpu
+def test_a_dropped_graph_frees_its_memory():
+    import gc
+
+    from lm_head_jsd_gb300 import fused_linear_logprobs, token_logprobs
+
+    x, w, y = _problem()
+    torch.autograd.grad(fused_linear_logprobs(x, w, y).logp.sum(), x)
+    gc.collect()
+    gc.disable()
+    try:
+        before = torch.cuda.memory_allocated()
+        for _ in range(3):
+            r, t = fused_linear_logprobs(x, w, y, top_k=2), token_logprobs(x @ w.T, y)
+            loss = r.logp.sum() + t.entropy.sum()
+            del r, t, loss
+        assert torch.cuda.memory_allocated() == before
+        loss = fused_linear_logprobs(x, w, y).logp.sum()
+        torch.autograd.grad(loss, (x, w))
+        del loss
+        assert torch.cuda.memory_allocated() == before
+    finally:
+        gc.enable()
