@@ -149,20 +149,36 @@ def _upstream(g):
     return None if g is None else g.detach().to(torch.float32).contiguous()
 
 
+class _Once(torch.autograd.Function):
+    """Gradients as functions of what they come from, whose derivative is not provided."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(None if g is None else g.view_as(g) for g in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("token log probabilities are differentiable once: the derivative of "
+                           "their gradient is not provided")
+
+
+def _once(grads, of):
+    """Under create_graph=True the gradients depend on ``of``; otherwise as they are."""
+    return _Once.apply(len(grads), *grads, *of) if torch.is_grad_enabled() else grads
+
+
 class _FusedLinearLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, labels, top_k, temperature, ignore_index, chunk_rows, need):
         run = FusedLinearLogprobs(x.shape[0], x.shape[1], w.shape[0], x.dtype, top_k=top_k,
                                   temperature=temperature, ignore_index=ignore_index,
                                   chunk_rows=chunk_rows, keep_for_backward=need, device=x.device)
-        xc, wc = x.detach().contiguous(), w.detach().contiguous()
-        lab = None if labels is None else labels.contiguous()
-        r = run.forward(xc, wc, lab)
+        r = run.forward(x, w, labels)
         ctx.set_materialize_grads(False)
         if need:
             ctx.run, ctx.result = run, r
             # (of the result, for the check that nothing has been written over it)
-            ctx.save_for_backward(xc, wc, lab, r.logp, r.entropy, r.norm)
+            ctx.save_for_backward(x, w, labels, r.logp, r.entropy, r.norm)
         return _outputs(ctx, r)
 
     @staticmethod
@@ -173,19 +189,21 @@ class _FusedLinearLogprobsFunction(torch.autograd.Function):
         need = ctx.needs_input_grad[:2]
         gx, gw = ctx.run.backward(x, w, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                   need=need)
-        return gx, gw, None, None, None, None, None, None
+        return *_once((gx, gw), (x, w, g_logp, g_entropy)), None, None, None, None, None, None
 
 
 def fused_linear_logprobs(x, w, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
                           chunk_rows=0) -> Logprobs:
     """:class:`Logprobs` of the logits x.w^T without forming them, differentiable in x
-    and w through logp and entropy. 2-D tensors on one CUDA device, fp32 or bf16.
+    and w through logp and entropy, once. 2-D tensors on one CUDA device, fp32 or bf16.
 
     To capture a backward pass into a CUDA graph, use :class:`FusedLinearLogprobs`, or
     leaves of its own (``x.detach().requires_grad_()``): autograd delivers a leaf's
     gradient on the stream of whatever eager graph of that leaf is still alive, which a
     capture forbids."""
     need = torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)
+    x, w = x.contiguous(), w.contiguous()
+    labels = None if labels is None else labels.contiguous()
     return Logprobs(*_FusedLinearLogprobsFunction.apply(x, w, labels, int(top_k), float(temperature),
                                                         int(ignore_index), int(chunk_rows), need))
 
@@ -253,13 +271,10 @@ def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entrop
 class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, labels, top_k, temperature, ignore_index):
-        z = logits.detach()
-        if z.dim() == 2 and (z.stride(1) != 1 or z.stride(0) < z.shape[1]):
-            z = z.contiguous()  # columns apart, or rows that share memory
-        lab = None if labels is None else labels.contiguous()
-        r = logits_logprobs(z, lab, top_k=top_k, temperature=temperature, ignore_index=ignore_index)
+        r = logits_logprobs(logits, labels, top_k=top_k, temperature=temperature,
+                            ignore_index=ignore_index)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(z, lab, r.logp, r.entropy, r.norm)
+        ctx.save_for_backward(logits, labels, r.logp, r.entropy, r.norm)
         ctx.result, ctx.opts = r, (temperature, ignore_index)
         return _outputs(ctx, r)
 
@@ -270,11 +285,14 @@ class _TokenLogprobsFunction(torch.autograd.Function):
         z, labels, *_ = ctx.saved_tensors
         g = logits_logprobs_backward(z, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                      temperature=ctx.opts[0], ignore_index=ctx.opts[1])
-        return g, None, None, None, None
+        return *_once((g,), (z, g_logp, g_entropy)), None, None, None, None
 
 
 def token_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100) -> Logprobs:
-    """:func:`logits_logprobs`, differentiable in the logits through logp and entropy."""
+    """:func:`logits_logprobs`, differentiable in the logits through logp and entropy, once."""
+    if logits.dim() == 2 and (logits.stride(1) != 1 or logits.stride(0) < logits.shape[1]):
+        logits = logits.contiguous()  # columns apart, or rows that share memory
+    labels = None if labels is None else labels.contiguous()
     return Logprobs(*_TokenLogprobsFunction.apply(logits, labels, int(top_k), float(temperature),
                                                   int(ignore_index)))
 

@@ -116,3 +116,44 @@ def test_a_dropped_graph_frees_its_memory():
         assert torch.cuda.memory_allocated() == before
     finally:
         gc.enable()
+
+
+@gpu
+@pytest.mark.parametrize("form", ["fused", "token"])
+def test_a_second_derivative_is_refused(form):
+    from lm_head_jsd_gb300 import fused_linear_logprobs, token_logprobs
+
+    x, w, y = _problem(torch.float32)
+    z = (x @ w.T).detach().requires_grad_()
+    to = x if form == "fused" else z
+    loss = (fused_linear_logprobs(x, w, y) if form == "fused" else token_logprobs(z, y)).logp.sum()
+    (want,) = torch.autograd.grad(loss, to, retain_graph=True)
+    (g,) = torch.autograd.grad(loss, to, create_graph=True)
+    assert torch.equal(g, want)
+    other = (to * to).sum()  # (a term that the derivative could be taken of)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(other + (g * g).sum(), to)
+
+
+@gpu
+@pytest.mark.parametrize("form", ["fused", "token"])
+def test_inputs_that_were_copied_may_change(form):
+    """Inputs of other strides are copied; writing over the originals leaves the gradient."""
+    from lm_head_jsd_gb300 import fused_linear_logprobs, token_logprobs
+
+    x, w, y = _problem(torch.float32)
+    z = (x @ w.T).detach()
+    y2 = torch.stack([y, y], 1)[:, 0]
+    x2, z2 = x.detach().T.contiguous().T.requires_grad_(), z.T.contiguous().T.requires_grad_()
+    if form == "fused":
+        want = torch.autograd.grad(fused_linear_logprobs(x, w, y).logp.sum(), (x, w))
+        loss, to, base = fused_linear_logprobs(x2, w, y2).logp.sum(), (x2, w), x2
+    else:
+        z.requires_grad_()
+        want = torch.autograd.grad(token_logprobs(z, y).logp.sum(), (z,))
+        loss, to, base = token_logprobs(z2, y2).logp.sum(), (z2,), z2
+    with torch.no_grad():
+        base.zero_()
+        y2.zero_()
+    got = torch.autograd.grad(loss, to)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
