@@ -436,7 +436,8 @@ fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64
 /*
  * fljsd_adamw_step -- one AdamW step over `count` tensors, in place. Per element,
  * in fp32, each operation rounded once, t = options->step (the number of this
- * step, from 1):
+ * step, from 1, for all tensors of the call: tensors that have taken other numbers of
+ * steps take calls of their own):
  *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,
  *   v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay)

@@ -33,11 +33,13 @@ class AdamW:
     second's root, one fp32 scale for 128 elements). ``master``: True to keep fp32
     weights beside bf16 parameters, or a list of them. The states may be given
     (``exp_avg``, ``exp_avg_sq`` and, in 8 bits, their scales, with ``step`` the number
-    of steps they have taken), e.g. from a checkpoint: they are stepped in place.
+    of steps they have taken, or a list of each parameter's), e.g. from a checkpoint: they
+    are stepped in place.
 
     ``step(grads)`` takes the gradients in the parameters' order, or the parameters'
-    ``.grad``; a gradient of None leaves its parameter as it is. ``lr`` and
-    ``weight_decay`` may be changed between steps.
+    ``.grad``; a gradient of None leaves its parameter, its states and its number of steps
+    (``param_steps``) as they are. ``steps`` is the number of steps that moved any. ``lr``
+    and ``weight_decay`` may be changed between steps.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, *,
@@ -53,7 +55,13 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits is {state_bits}, expected 8 or 32")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
-        self.state_bits, self.steps = state_bits, int(step)
+        self.state_bits = state_bits
+        counts = np.array(step, dtype=np.int64) if isinstance(step, (list, tuple, np.ndarray)) else None
+        if counts is not None and counts.shape != (len(self.params),):
+            raise ValueError(f"step has {counts.size} numbers, expected {len(self.params)}")
+        self.steps = int(step) if counts is None else int(counts.max())
+        # steps that a parameter has not taken part in (None: all have in each)
+        self._missed = None if counts is None or (counts == self.steps).all() else self.steps - counts
         self._check("params", self.params, self.dtype)
         own_master = master is True
         if own_master:
@@ -98,6 +106,13 @@ class AdamW:
             t["exp_avg_scale"] = _ptrs(self.exp_avg_scale)
             t["exp_avg_sq_scale"] = _ptrs(self.exp_avg_sq_scale)
 
+    @property
+    def param_steps(self):
+        """The number of steps that each parameter has taken."""
+        if self._missed is None:
+            return [self.steps] * len(self.params)
+        return (self.steps - self._missed).tolist()
+
     def _zeros(self, dtype):
         return [torch.zeros(p.numel(), dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
                             device=self.device).view(dtype) for p in self.params]
@@ -127,18 +142,18 @@ class AdamW:
             self._check("params", self.params, self.dtype, self._sizes)
             self._at = at
             t["param"] = at
-        live, sizes, stepped = grads, self._sizes, self._stepped
+        live, sizes, stepped, out = grads, self._sizes, self._stepped, None
         try:
             t["grad"] = _ptrs(grads)
         except TypeError:  # some are None: those parameters stay as they are
-            t = t.copy()
-            t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
-            t["n"] = [0 if g is None else n for g, n in zip(grads, sizes)]
+            out = np.array([g is None for g in grads])
+            t = t[~out]
             live = [g for g in grads if g is not None]
             sizes = [n for g, n in zip(grads, sizes) if g is not None]
             stepped = [x for x, g in zip(stepped, grads * 2) if g is not None]
             if not live:
                 return
+            t["grad"] = _ptrs(live)
         dt, dev = live[0].dtype, self.device
         require_cuda("the optimizer", dev)
         # (whole-list checks: a step of many small tensors is bound by this function)
@@ -150,16 +165,23 @@ class AdamW:
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one fp32 value on {dev}")
-        o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay,
-                                    self.steps + 1, _DT[self.dtype], _DT[dt], self.state_bits,
-                                    int(self.master is not None))
+        groups = ((t, self.steps + 1),)
+        if self._missed is not None:  # parameters of one number of steps to a call
+            missed = self._missed if out is None else self._missed[~out]
+            groups = [(t[missed == m], self.steps + 1 - int(m)) for m in np.unique(missed)]
         with on(stream, dev):
             if self._memory is not None:
                 self._memory.use()
-            _lib.fljsd_adamw_step(o, t.ctypes.data, len(t), grad_scale)
+            for part, step in groups:
+                o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay, step,
+                                            _DT[self.dtype], _DT[dt], self.state_bits,
+                                            int(self.master is not None))
+                _lib.fljsd_adamw_step(o, part.ctypes.data, len(part), grad_scale)
         # autograd's own check of what it saved: these have changed
         increment_version(stepped)
         self.steps += 1
+        if out is not None:
+            self._missed = out + (0 if self._missed is None else self._missed)
 
 
 __all__ = ["AdamW"]

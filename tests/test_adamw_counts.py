@@ -1,0 +1,96 @@
+"""AdamW over parameters that have taken different numbers of steps: each is stepped as it
+would be alone."""
+import numpy as np
+import pytest
+import torch
+
+gpu = pytest.mark.gpu
+HY = dict(lr=3e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.1)
+
+
+def _run(opt_of, sizes, dtype, steps, skip, seed=0):
+    """One optimizer over all, and one of each parameter alone, the same gradients."""
+    g = torch.Generator().manual_seed(seed)
+    ps = [(torch.randn(n, generator=g) * 0.02).to(dtype).cuda() for n in sizes]
+    joint, alone = opt_of([p.clone() for p in ps]), [opt_of([p.clone()]) for p in ps]
+    for t in range(steps):
+        grads = [None if skip(t, i) else (torch.randn(n, generator=g) * 1e-2).to(dtype).cuda()
+                 for i, n in enumerate(sizes)]
+        joint.step(grads)
+        for one, gr in zip(alone, grads):
+            if gr is not None:
+                one.step([gr])
+    return joint, alone
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype,master", [(torch.float32, None), (torch.bfloat16, None), (torch.bfloat16, True)])
+@pytest.mark.parametrize("sizes", [[5, 300, 2049], [(i * 37) % 300 + 1 for i in range(450)]],
+                         ids=["three", "many"])
+def test_each_as_it_would_be_alone(bits, dtype, master, sizes):
+    from lm_head_jsd_gb300 import AdamW
+
+    def skip(t, i):  # 0: never, 1: from the third step on, 2: every other step
+        return i % 3 == 1 and t < 3 or i % 3 == 2 and t % 2 == 1
+
+    joint, alone = _run(lambda ps: AdamW(ps, state_bits=bits, master=master, **HY), sizes, dtype, 5, skip)
+    for name in ("params", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
+        if getattr(joint, name) is not None:
+            for a, one in zip(getattr(joint, name), alone):
+                assert torch.equal(a.float(), getattr(one, name)[0].float()), name
+    assert joint.steps == 5 and joint.param_steps == [one.steps for one in alone]
+
+
+@gpu
+def test_late_parameter_against_torch():
+    from lm_head_jsd_gb300 import AdamW
+
+    g = torch.Generator().manual_seed(1)
+    start = [torch.randn(40, generator=g) for _ in range(2)]
+    ours = AdamW([p.cuda() for p in start], **HY)
+    ref = [torch.nn.Parameter(p.double()) for p in start]
+    theirs = torch.optim.AdamW(ref, **HY)
+    for t in range(60):
+        grads = [torch.randn(40, generator=g), torch.randn(40, generator=g) if t >= 50 else None]
+        ours.step([None if x is None else x.cuda() for x in grads])
+        for p, x in zip(ref, grads):
+            p.grad = None if x is None else x.double()
+        theirs.step()
+    # each step: two roundings of p and six of an update of at most lr (1 + a few)
+    lim = 60 * (2 ** -23 * 5 + 2 ** -21 * 4 * HY["lr"])
+    for a, b in zip(ours.params, ref):
+        assert (a.cpu().double() - b.detach()).abs().max().item() <= lim
+    assert ours.steps == 60 and ours.param_steps == [60, 10]
+
+
+@gpu
+def test_counts_go_on_from_a_checkpoint():
+    from lm_head_jsd_gb300 import AdamW
+
+    sizes = [129, 300, 7]
+    opt = lambda ps, **kw: AdamW(ps, state_bits=8, **HY, **kw)  # noqa: E731
+    joint, _ = _run(opt, sizes, torch.float32, 4, lambda t, i: i == 1 and t != 2)
+    again = opt([p.clone() for p in joint.params], exp_avg=[t.clone() for t in joint.exp_avg],
+                exp_avg_sq=[t.clone() for t in joint.exp_avg_sq],
+                exp_avg_scale=[t.clone() for t in joint.exp_avg_scale],
+                exp_avg_sq_scale=[t.clone() for t in joint.exp_avg_sq_scale], step=joint.param_steps)
+    assert again.param_steps == [4, 1, 4] and again.steps == 4
+    grads = [torch.ones(n, device="cuda") for n in sizes]
+    joint.step(grads)
+    again.step(grads)
+    assert all(torch.equal(a, b) for a, b in zip(joint.params, again.params))
+    assert joint.param_steps == again.param_steps == [5, 2, 5]
+
+
+def test_counts_without_a_gpu():
+    from lm_head_jsd_gb300 import AdamW
+
+    p = [torch.zeros(4), torch.zeros(3)]
+    assert AdamW(p).param_steps == [0, 0]
+    assert AdamW(p, step=7).param_steps == [7, 7]
+    assert AdamW(p, step=[7, 2]).param_steps == [7, 2] and AdamW(p, step=(7, 2)).steps == 7
+    assert AdamW(p, step=np.array([3, 3])).param_steps == [3, 3]
+    for bad in ([1], [1, 2, 3], [[1, 2]]):
+        with pytest.raises(ValueError):
+            AdamW(p, step=bad)
