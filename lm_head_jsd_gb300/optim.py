@@ -66,7 +66,7 @@ class AdamW:
         own_master = master is True
         if own_master:
             master = [p.detach().float() for p in self.params]
-        self.master = list(master) if master else None
+        self._master = tuple(master) if master else None
         if self.master and self.dtype != torch.bfloat16:
             raise ValueError("master weights are kept beside bf16 parameters")
         sd = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
@@ -74,13 +74,13 @@ class AdamW:
                  exp_avg_sq_scale is not None)
         if any(given) and given != (True, True, state_bits == 8, state_bits == 8):
             raise ValueError("states are given all together, with scales in 8 bits")
-        self.exp_avg = list(exp_avg) if exp_avg is not None else self._zeros(sd)
-        self.exp_avg_sq = list(exp_avg_sq) if exp_avg_sq is not None else self._zeros(sd)
-        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        self._exp_avg = tuple(exp_avg) if exp_avg is not None else self._zeros(sd)
+        self._exp_avg_sq = tuple(exp_avg_sq) if exp_avg_sq is not None else self._zeros(sd)
+        self._exp_avg_scale = self._exp_avg_sq_scale = None
         if state_bits == 8:
-            self.exp_avg_scale = list(exp_avg_scale) if exp_avg_scale is not None else self._scales()
-            self.exp_avg_sq_scale = (list(exp_avg_sq_scale) if exp_avg_sq_scale is not None
-                                     else self._scales())
+            self._exp_avg_scale = tuple(exp_avg_scale) if exp_avg_scale is not None else self._scales()
+            self._exp_avg_sq_scale = (tuple(exp_avg_sq_scale) if exp_avg_sq_scale is not None
+                                      else self._scales())
         sizes = [p.numel() for p in self.params]
         for name, ts, dt, want in (
                 ("master", self.master, torch.float32, sizes), ("exp_avg", self.exp_avg, sd, sizes),
@@ -91,10 +91,14 @@ class AdamW:
                 self._check(name, ts, dt, want or [-(-n // _BLOCK) for n in sizes])
         made = [] if exp_avg is not None else [*self.exp_avg, *self.exp_avg_sq,
                                                *(self.exp_avg_scale or ()), *(self.exp_avg_sq_scale or ())]
-        made += self.master if own_master else []
+        made += self.master if own_master else ()
         self._memory = Memory(made) if made and self.device.type == "cuda" else None
         self._sizes = sizes
-        self._stepped = self.params + (self.master or [])
+        # (what the table points at is kept, whatever becomes of the tensors)
+        self._storages = [t.untyped_storage() for ts in (self.master, self.exp_avg, self.exp_avg_sq,
+                                                         self.exp_avg_scale, self.exp_avg_sq_scale)
+                          for t in ts or ()]
+        self._stepped = [*self.params, *(self.master or ())]
         self._table = np.zeros(len(sizes), dtype=_ENTRY)
         t = self._table
         self._at = _ptrs(self.params)
@@ -106,6 +110,14 @@ class AdamW:
             t["exp_avg_scale"] = _ptrs(self.exp_avg_scale)
             t["exp_avg_sq_scale"] = _ptrs(self.exp_avg_sq_scale)
 
+    # The weights and states that are stepped, where they lay at construction: their contents
+    # may be written, but no other tensor put in their place.
+    master = property(lambda self: self._master)
+    exp_avg = property(lambda self: self._exp_avg)
+    exp_avg_sq = property(lambda self: self._exp_avg_sq)
+    exp_avg_scale = property(lambda self: self._exp_avg_scale)
+    exp_avg_sq_scale = property(lambda self: self._exp_avg_sq_scale)
+
     @property
     def param_steps(self):
         """The number of steps that each parameter has taken."""
@@ -114,12 +126,12 @@ class AdamW:
         return (self.steps - self._missed).tolist()
 
     def _zeros(self, dtype):
-        return [torch.zeros(p.numel(), dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
-                            device=self.device).view(dtype) for p in self.params]
+        return tuple(torch.zeros(p.numel(), dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
+                                 device=self.device).view(dtype) for p in self.params)
 
     def _scales(self):
-        return [torch.zeros(-(-p.numel() // _BLOCK), dtype=torch.float32, device=self.device)
-                for p in self.params]
+        return tuple(torch.zeros(-(-p.numel() // _BLOCK), dtype=torch.float32, device=self.device)
+                     for p in self.params)
 
     def _check(self, name, ts, dtype, sizes=None):
         if sizes is not None and len(ts) != len(sizes):
@@ -142,6 +154,7 @@ class AdamW:
             self._check("params", self.params, self.dtype, self._sizes)
             self._at = at
             t["param"] = at
+            self._stepped = [*self.params, *(self.master or ())]
         live, sizes, stepped, out = grads, self._sizes, self._stepped, None
         try:
             t["grad"] = _ptrs(grads)

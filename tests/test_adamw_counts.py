@@ -1,5 +1,5 @@
 """AdamW over parameters that have taken different numbers of steps: each is stepped as it
-would be alone."""
+would be alone. And which tensors of an optimizer may be replaced."""
 import numpy as np
 import pytest
 import torch
@@ -94,3 +94,46 @@ def test_counts_without_a_gpu():
     for bad in ([1], [1, 2, 3], [[1, 2]]):
         with pytest.raises(ValueError):
             AdamW(p, step=bad)
+
+
+def test_states_are_not_replaced():
+    """The kernel's table holds the addresses of the tensors of the construction: another
+    tensor in their place would be left as it is, and the old one's memory written when it
+    may be another's."""
+    from lm_head_jsd_gb300 import AdamW
+
+    p = [torch.zeros(4).bfloat16(), torch.zeros(300).bfloat16()]
+    opt = AdamW(p, state_bits=8, master=True)
+    for name in ("master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
+        ts = getattr(opt, name)
+        with pytest.raises(TypeError):
+            ts[0] = ts[0].clone()
+        with pytest.raises(AttributeError):
+            setattr(opt, name, [t.clone() for t in ts])
+        ts[0].view(torch.uint8).zero_()  # (contents may be written)
+
+
+@gpu
+def test_replaced_parameters_and_storages():
+    from lm_head_jsd_gb300 import AdamW
+
+    g = torch.ones(300, device="cuda")
+    opt = AdamW([torch.ones(300, device="cuda") for _ in range(2)], **HY)
+    ref = AdamW([torch.ones(300, device="cuda") for _ in range(2)], **HY)
+    opt.step([g, g])
+    ref.step([g, g])
+    old = opt.params[0]
+    opt.params[0] = old.clone()  # another tensor in a parameter's place is stepped
+    kept, version = old.clone(), opt.params[0]._version
+    opt.step([g, g])
+    ref.step([g, g])
+    assert torch.equal(opt.params[0], ref.params[0]) and torch.equal(old, kept)
+    assert opt.params[0]._version > version
+    # a state whose storage is replaced: the old memory is still the optimizer's own
+    at = opt.exp_avg[0].data_ptr()
+    opt.exp_avg[0].data = opt.exp_avg[0].clone()
+    later = [torch.full((300,), 5.0, device="cuda") for _ in range(20)]
+    assert at not in [t.data_ptr() for t in later]
+    opt.step([g, g])
+    torch.cuda.synchronize()
+    assert all((t == 5).all() for t in later)
