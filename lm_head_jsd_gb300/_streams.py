@@ -39,6 +39,18 @@ def hand_over(tensors, stream, device):
                 t.record_stream(caller)
 
 
+def report(status, workspace, offset=0):
+    """A call's status word into the caller's ``status``, on the current stream."""
+    if status is not None:
+        status.copy_(workspace[offset:offset + 4].view(torch.int32).view(status.shape))
+
+
+def check_status(status, device):
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1
+                               or status.device != device):
+        raise ValueError(f"status must be one int32 value on {device}")
+
+
 class Memory:
     """Tensors that an object keeps from call to call, made on the stream that is current
     now: another stream's first use waits for what that one still does with their memory

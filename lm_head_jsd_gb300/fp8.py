@@ -6,7 +6,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from ._streams import hand_over, on, require_cuda
+from ._streams import check_status, hand_over, on, report, require_cuda
 from .api import _DT
 
 BLOCK = 128
@@ -39,16 +39,18 @@ def fp8_quantize(w, *, block_rows=BLOCK, stream=None):
     return codes.view(torch.float8_e4m3fn)[:, :cols], scales
 
 
-def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stream=None):
+def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, status=None, stream=None):
     """x.w^T of x [m, k] (fp32 or bf16, quantised on the way) and a weight from
     :func:`fp8_quantize`. Carries no gradient: an x that would need one is refused (pass
-    ``x.detach()``, or call under ``torch.no_grad()``)."""
+    ``x.detach()``, or call under ``torch.no_grad()``). ``status``: an int32 on the device
+    that receives the call's status word (0, or FLJSD_ERR_TIMEOUT)."""
     if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
         raise ValueError("x requires a gradient, which fp8_linear does not give: pass x.detach()")
     ldx = _check_rows("x", x)
     ldw = _check_rows("w_codes", w_codes)
     (m, k), n, dev = x.shape, w_codes.shape[0], x.device
     require_cuda("x", dev)
+    check_status(status, dev)
     if x.dtype not in _DT or out_dtype not in _DT:
         raise ValueError(f"x and out_dtype must be one of {list(_DT)}")
     if w_codes.dtype != torch.float8_e4m3fn or w_codes.shape[1] != k or w_codes.device != dev:
@@ -63,6 +65,7 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stre
         ws = torch.empty(_lib.fljsd_fp8_linear_workspace_bytes(m, k), dtype=torch.uint8, device=dev)
         _lib.fljsd_fp8_linear(m, n, k, _DT[x.dtype], x, ldx, w_codes, ldw, w_scales, _DT[out_dtype],
                               y, _check_rows("out", y), ws)
+        report(status, ws)
     if out is None:
         hand_over((y,), stream, dev)
     else:  # autograd's own check of what it saved: this has changed

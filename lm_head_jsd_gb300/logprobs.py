@@ -10,7 +10,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from ._streams import Memory, hand_over, on, require_cuda
+from ._streams import Memory, check_status, hand_over, on, report, require_cuda
 from .api import _DT, _check
 
 
@@ -104,6 +104,12 @@ class FusedLinearLogprobs:
             self._kept = r
         return r
 
+    def report(self, status):
+        """The status word of the calls so far (since the last forward) into an int32 on the
+        device, on the current stream (None: nothing)."""
+        check_status(status, self.device)
+        report(status, self.workspace, self.plan.status_offset)
+
     def backward(self, x, w, labels, result, grad_logp=None, grad_entropy=None, out=None,
                  need=(True, True), stream=None):
         """(grad_input, grad_weight) for the upstream gradients of ``result``'s logp
@@ -169,14 +175,16 @@ def _once(grads, of):
 
 class _FusedLinearLogprobsFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, labels, top_k, temperature, ignore_index, chunk_rows, need):
+    def forward(ctx, x, w, labels, top_k, temperature, ignore_index, chunk_rows, need, status):
+        check_status(status, x.device)
         run = FusedLinearLogprobs(x.shape[0], x.shape[1], w.shape[0], x.dtype, top_k=top_k,
                                   temperature=temperature, ignore_index=ignore_index,
                                   chunk_rows=chunk_rows, keep_for_backward=need, device=x.device)
         r = run.forward(x, w, labels)
+        run.report(status)
         ctx.set_materialize_grads(False)
         if need:
-            ctx.run, ctx.result = run, r
+            ctx.run, ctx.result, ctx.status = run, r, status
             # (of the result, for the check that nothing has been written over it)
             ctx.save_for_backward(x, w, labels, r.logp, r.entropy, r.norm)
         return _outputs(ctx, r)
@@ -184,18 +192,22 @@ class _FusedLinearLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_logp, g_entropy, *_):
         if g_logp is None and g_entropy is None:
-            return (None,) * 8
+            return (None,) * 9
         x, w, labels, *_ = ctx.saved_tensors
         need = ctx.needs_input_grad[:2]
         gx, gw = ctx.run.backward(x, w, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                   need=need)
-        return *_once((gx, gw), (x, w, g_logp, g_entropy)), None, None, None, None, None, None
+        ctx.run.report(ctx.status)
+        return *_once((gx, gw), (x, w, g_logp, g_entropy)), *(None,) * 7
 
 
 def fused_linear_logprobs(x, w, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
-                          chunk_rows=0) -> Logprobs:
+                          chunk_rows=0, status=None) -> Logprobs:
     """:class:`Logprobs` of the logits x.w^T without forming them, differentiable in x
     and w through logp and entropy, once. 2-D tensors on one CUDA device, fp32 or bf16.
+    ``status``: an int32 on the device that receives the forward's status word, and again
+    after a backward pass (0; FLJSD_ERR_INVALID_ARG for a label outside [0, V) other than
+    ignore_index; FLJSD_ERR_TIMEOUT).
 
     To capture a backward pass into a CUDA graph, use :class:`FusedLinearLogprobs`, or
     leaves of its own (``x.detach().requires_grad_()``): autograd delivers a leaf's
@@ -205,7 +217,7 @@ def fused_linear_logprobs(x, w, labels=None, *, top_k=0, temperature=1.0, ignore
     x, w = x.contiguous(), w.contiguous()
     labels = None if labels is None else labels.contiguous()
     return Logprobs(*_FusedLinearLogprobsFunction.apply(x, w, labels, int(top_k), float(temperature),
-                                                        int(ignore_index), int(chunk_rows), need))
+                                                        int(ignore_index), int(chunk_rows), need, status))
 
 
 def _logits_check(logits, labels):
@@ -226,10 +238,13 @@ def _row_stride(t):
 
 
 def logits_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
-                    stream=None) -> Logprobs:
+                    status=None, stream=None) -> Logprobs:
     """:class:`Logprobs` of given logits [rows x V], fp32 or bf16 (rows may be any
-    stride apart). For a differentiable form see :func:`token_logprobs`."""
+    stride apart). For a differentiable form see :func:`token_logprobs`. ``status``: an
+    int32 on the device that receives the call's status word (0, or FLJSD_ERR_INVALID_ARG
+    for a label outside [0, V) other than ignore_index)."""
     _logits_check(logits, labels)
+    check_status(status, logits.device)
     rows, v = logits.shape
     with on(stream, logits.device):
         r = _results(rows, top_k, labels is not None, logits.device)
@@ -238,6 +253,7 @@ def logits_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_ind
         _lib.fljsd_logits_lp(rows, v, _row_stride(logits), _DT[logits.dtype], top_k, temperature,
                              ignore_index, logits, labels, r.logp, r.entropy, r.lse, r.norm,
                              r.top_logp, r.top_id, ws)
+        report(status, ws)
     hand_over(r, stream, logits.device)
     return r
 
@@ -270,9 +286,9 @@ def logits_logprobs_backward(logits, labels, result, grad_logp=None, grad_entrop
 
 class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, labels, top_k, temperature, ignore_index):
+    def forward(ctx, logits, labels, top_k, temperature, ignore_index, status):
         r = logits_logprobs(logits, labels, top_k=top_k, temperature=temperature,
-                            ignore_index=ignore_index)
+                            ignore_index=ignore_index, status=status)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(logits, labels, r.logp, r.entropy, r.norm)
         ctx.result, ctx.opts = r, (temperature, ignore_index)
@@ -281,20 +297,21 @@ class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g_logp, g_entropy, *_):
         if g_logp is None and g_entropy is None:
-            return (None,) * 5
+            return (None,) * 6
         z, labels, *_ = ctx.saved_tensors
         g = logits_logprobs_backward(z, labels, ctx.result, _upstream(g_logp), _upstream(g_entropy),
                                      temperature=ctx.opts[0], ignore_index=ctx.opts[1])
-        return *_once((g,), (z, g_logp, g_entropy)), None, None, None, None
+        return *_once((g,), (z, g_logp, g_entropy)), *(None,) * 5
 
 
-def token_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100) -> Logprobs:
+def token_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_index=-100,
+                   status=None) -> Logprobs:
     """:func:`logits_logprobs`, differentiable in the logits through logp and entropy, once."""
     if logits.dim() == 2 and (logits.stride(1) != 1 or logits.stride(0) < logits.shape[1]):
         logits = logits.contiguous()  # columns apart, or rows that share memory
     labels = None if labels is None else labels.contiguous()
     return Logprobs(*_TokenLogprobsFunction.apply(logits, labels, int(top_k), float(temperature),
-                                                  int(ignore_index)))
+                                                  int(ignore_index), status))
 
 
 __all__ = ["FusedLinearLogprobs", "Logprobs", "fused_linear_logprobs", "logits_logprobs",
