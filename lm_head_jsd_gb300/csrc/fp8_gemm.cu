@@ -399,6 +399,11 @@ __device__ __forceinline__ uint32_t code4(const float (&x)[4], float inv) {
   return lo | (hi << 16);
 }
 
+// Zeros from the end of a row's last block on (ldq may be any length).
+__device__ __forceinline__ void zero_tail(uint8_t* row, int64_t from, int64_t ldq) {
+  for (int64_t j = from; j < ldq; j += FB) *reinterpret_cast<uint32_t*>(row + j) = 0u;
+}
+
 // One warp to a 1 x 128 block, four consecutive elements a lane. `scales` is
 // [blocks x rows], so that the product's threads (one row each) read it whole.
 template <typename T>
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(256) k_quantise_rows(const T* x, int64_t ldx, 
     a = fmaxf(a, kAmaxFloor);
     const uint32_t c = code4(v, __fmul_rn(__frcp_rn(a), 448.f));
     if (j < ldq) *reinterpret_cast<uint32_t*>(q + r * ldq + j) = c;  // (ldq: whole 16-byte units)
+    if (b == blocks - 1) zero_tail(q + r * ldq, j + FB, ldq);
     if (lane == 0) scales[b * rows + r] = __fmul_rn(a, 1.f / 448.f);
   }
 }
@@ -457,6 +463,7 @@ __global__ void __launch_bounds__(256) k_quantise_blocks(const T* x, int64_t ldx
   for (int i = 0; i < 16; ++i) {
     const int64_t r = rb * FB + i * 8 + warp;
     if (r < rows && j < ldq) *reinterpret_cast<uint32_t*>(q + r * ldq + j) = code4(v[i], inv);
+    if (r < rows && b == blocks - 1) zero_tail(q + r * ldq, j + FB, ldq);
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = __fmul_rn(a, 1.f / 448.f);
 }
