@@ -372,17 +372,18 @@ fljsd_status fljsd_ce_forward(const fljsd_ce_problem* problem, const fljsd_plan_
  * found on the host before anything is launched. x [bt x h] and w [v x h] in
  * dtype, 16-byte aligned; labels [bt] int64 or NULL (then no logp); logp,
  * entropy, lse [bt] fp32; norm [bt x 2] fp32, for the backward pass (the row's
- * largest logit and log2 of the sum of e^{s_j} relative to it); top_logp [bt x top_k] fp32 and top_id [bt x top_k]
- * int64 (NULL with top_k 0). bf16 with h a multiple of 8 runs on the tensor
- * cores, everything else on the CUDA cores.
+ * largest logit and log2 of the sum of e^{s_j} relative to it); top_logp
+ * [bt x top_k] fp32 and top_id [bt x top_k] int64 (NULL with top_k 0). bf16 with h
+ * a multiple of 8 runs on the tensor cores, everything else on the CUDA cores.
  *
  * FLJSD_LP_BACKWARD sizes the workspace for fljsd_lp_backward, and lets the
  * forward of a one-chunk plan leave there what the backward would otherwise
  * compute again: pass kept = 1 when the workspace is as the forward of the same
- * problem and inputs left it (a backward pass uses it up), kept = 0 to compute
- * it again. logp, entropy and norm are the forward's results; grad_logp
- * (needs labels) and grad_entropy may be NULL (zero). grad_input and grad_weight are
- * written in full, as by fljsd_forward; one of them may be NULL and is left out.
+ * problem and inputs left it (a backward pass uses it up, at each replay where it
+ * was captured), kept = 0 to compute it again. logp, entropy and norm are the
+ * forward's results; grad_logp (needs labels) and grad_entropy may be NULL (zero).
+ * grad_input and grad_weight are written in full, as by fljsd_forward; one of them
+ * may be NULL and is left out.
  *
  * fljsd_logits_lp / fljsd_logits_lp_backward are the same of given logits
  * [rows x v] in dtype with row stride ld (elements, any alignment) and of their
@@ -521,6 +522,11 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
                               int64_t ldx, const void* w_codes, int64_t ldw, const float* w_scales,
                               int32_t out_dtype, void* out, int64_t ldo, void* workspace,
                               size_t workspace_bytes, fljsd_stream_t stream);
+
+/* Id of the capture into a CUDA graph that `stream` is in, unique in the process; 0 where
+ * it is in none (or on an error). A caller that passes kept = 1 to fljsd_lp_backward needs
+ * it: the two calls belong to one capture, or to none. */
+uint64_t fljsd_capture_id(fljsd_stream_t stream);
 
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fljsd_status_string(fljsd_status status);

@@ -21,6 +21,7 @@ from ._lib import (  # noqa: F401
     fljsd_fp8_linear,
     fljsd_fp8_linear_workspace_bytes,
     fljsd_fp8_quantize,
+    fljsd_capture_id,
     fljsd_launch_count,
     fljsd_logits_lp,
     fljsd_logits_lp_backward,

@@ -145,6 +145,8 @@ def _load():
     lib.fljsd_fp8_linear.restype = ctypes.c_int
     lib.fljsd_status_string.argtypes = [ctypes.c_int]
     lib.fljsd_status_string.restype = ctypes.c_char_p
+    lib.fljsd_capture_id.argtypes = [P]
+    lib.fljsd_capture_id.restype = ctypes.c_uint64
     lib.fljsd_launch_count.argtypes = []
     lib.fljsd_launch_count.restype = ctypes.c_int64
     lib.fljsd_launch_count_reset.argtypes = []
@@ -447,6 +449,10 @@ def fljsd_fp8_linear(m, n, k, x_dtype, x, ldx, w_codes, ldw, w_scales, out_dtype
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_fp8_linear")
     return st
+
+
+def fljsd_capture_id(stream=None) -> int:
+    return lib.fljsd_capture_id(_stream(stream))
 
 
 def fljsd_launch_count() -> int:

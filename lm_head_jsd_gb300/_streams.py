@@ -39,6 +39,13 @@ def hand_over(tensors, stream, device):
                 t.record_stream(caller)
 
 
+def capture_id():
+    """Of the capture that the current stream is in; 0: none."""
+    if not torch.cuda.is_current_stream_capturing():
+        return 0
+    return _lib.fljsd_capture_id()
+
+
 def report(status, workspace, offset=0):
     """A call's status word into the caller's ``status``, on the current stream."""
     if status is not None:

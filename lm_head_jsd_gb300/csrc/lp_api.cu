@@ -397,6 +397,16 @@ fljsd_status fljsd_lp_backward(const fljsd_lp_problem* p, const fljsd_plan_t* pl
   return FLJSD_OK;
 }
 
+uint64_t fljsd_capture_id(fljsd_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 size_t fljsd_logits_lp_workspace_bytes(int64_t rows, int64_t v, int32_t top_k) {
   if (logits_check(rows, v, v, FLJSD_F32, top_k, 1.f) != FLJSD_OK) return 0;
   return logits_layout(rows, v, top_k).total;

@@ -10,7 +10,8 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from ._streams import Memory, check_status, hand_over, on, report, require_cuda
+from ._streams import (Memory, capture_id, check_status, hand_over, on, report,
+                       require_cuda)
 from .api import _DT, _check
 
 
@@ -59,7 +60,8 @@ class FusedLinearLogprobs:
     ``keep_for_backward`` the plan also serves ``backward``, which takes the upstream
     gradients of logp and entropy. A forward whose plan is one chunk leaves the
     probabilities (bt x v fp16) in the workspace for the first backward of its result; any
-    other backward computes them again.
+    other backward computes them again (so do captured calls, but for a backward in the
+    capture of its forward, and eager ones of a plan that has been captured).
     """
 
     def __init__(self, bt, h, v, dtype=torch.bfloat16, *, top_k=0, temperature=1.0,
@@ -80,7 +82,8 @@ class FusedLinearLogprobs:
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8,
                                      device=self.device)
         self._memory = Memory([self.workspace])
-        self._kept = None  # the result whose probabilities the workspace holds
+        # the result whose probabilities the workspace holds, and the capture it was made in
+        self._kept, self._captured = (None, 0), False
 
     def forward(self, x, w, labels=None, out=None, stream=None) -> Logprobs:
         p = self.problem
@@ -90,9 +93,11 @@ class FusedLinearLogprobs:
             _check("labels", labels, torch.int64, self.device, (p.bt,))
         if out is not None:
             _check_result(out, p.bt, labels is not None, self.device, p.top_k)
-        self._kept = None
+        self._kept = None, 0
         with on(stream, self.device):
             self._memory.use()
+            capture = capture_id()
+            self._captured |= capture != 0
             r = _results(p.bt, p.top_k, labels is not None, self.device) if out is None else out
             _lib.fljsd_lp_forward(p, self.plan, x, w, labels, r.logp, r.entropy, r.lse, r.norm,
                                   r.top_logp, r.top_id, self.workspace)
@@ -101,7 +106,7 @@ class FusedLinearLogprobs:
         else:  # autograd's own check of what it saved: these have changed
             increment_version([t for t in out if t is not None])
         if p.flags & _lib.FLJSD_LP_BACKWARD and self.plan.num_chunks == 1:
-            self._kept = r
+            self._kept = r, capture
         return r
 
     def report(self, status):
@@ -125,12 +130,16 @@ class FusedLinearLogprobs:
             for name, t, like in zip(("grad_input", "grad_weight"), out, (x, w), strict=True):
                 if t is not None:
                     _check(name, t, self.dtype, self.device, like.shape)
-        kept = self._kept is result
-        if not kept:
+        (r, made), self._kept = self._kept, (None, 0)
+        if r is not result:
             _check_result(result, p.bt, labels is not None, self.device)
-        self._kept = None
         with on(stream, self.device):
             self._memory.use()
+            capture = capture_id()
+            # A captured backward runs once for each replay, and replays of a captured
+            # forward or backward write the workspace unseen.
+            kept = r is result and made == capture and (capture != 0 or not self._captured)
+            self._captured |= capture != 0
             g = out if out is not None else (torch.empty_like(x) if need[0] else None,
                                              torch.empty_like(w) if need[1] else None)
             _lib.fljsd_lp_backward(p, self.plan, x, w, labels, result.logp, result.entropy,
