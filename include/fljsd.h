@@ -352,8 +352,10 @@ fljsd_status fljsd_ce_forward(const fljsd_ce_problem* problem, const fljsd_plan_
  * Upstream gradients a (grad_logp) and b (grad_entropy), [bt] fp32 each, give
  *   dz_j = (a (1[j = y] - p_j) - b p_j (log p_j + entropy)) / temperature,
  *   grad_input = dz . w,  grad_weight = dz^T . x.
- * All of it is computed in fp32 from unrounded logits (the fused form never
- * writes them); the top alternatives carry no gradient.
+ * All of it is computed in fp32 from unrounded logits; the top alternatives carry
+ * no gradient. The fused form does not write the logits, but its workspace has room
+ * for the alternatives' candidates, about v top_k / 16 bytes a row (top_k 32: what
+ * bf16 logits take), and with FLJSD_LP_BACKWARD for the kept 2 v bytes a row.
  *
  * Rows and values outside the ordinary:
  *  - a row whose label is ignore_index, or outside [0, v), has logp 0, entropy 0
@@ -449,7 +451,11 @@ fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64
  * exp_avg and exp_avg_sq are e4m3 codes [n] of m and of sqrt(v), with one fp32
  * scale for every 128 consecutive elements ([ceil(n / 128)] each): value = code
  * * scale, scale = amax * (1 / 448) (amax of the block, not below 2^-100), code =
- * the nearest to value * (448 * (1 / amax)). States may start as zeros.
+ * the nearest to value * (448 * (1 / amax)). States may start as zeros. There is no
+ * floor under the codes: what is below about 2^-19 of its block's amax is held as 0,
+ * and m and sqrt(v) have scales of their own, so that a sqrt(v) may be held as 0 whose
+ * m is not. What that parameter's next step divides by is then its new gradient's part
+ * of v and eps alone: choose eps so that lr m / eps is a step that may be taken.
  * grad_scale: device fp32 scalar or NULL (1), e.g. 1 / loss scale, or the factor
  * of a clipped gradient norm.
  * `tensors` is host memory, read before the call returns; the tensors' memory is

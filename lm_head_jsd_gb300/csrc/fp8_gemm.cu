@@ -19,15 +19,9 @@
 // (4096 x 32768 x 4096 of zeros, 412 us = 2.67 PFLOP/s), where the products alone would
 // take 512 and shared memory 768 (96 KB written and read again); with random codes the
 // card's power limit lowers the clock to 1.75 to 1.85 GHz (460 to 480 us), and what saves
-// cycles saves less time than it should: CTA pairs on 256 x 256 tiles 427 and 462 to 467,
-// sixteen epilogue warps of 64 columns 439 and 480, the votes after the waits left to a
-// tile's end 407 and the same. In ns for a block, before the issuing warps stayed together
-// (elect.cuh): 500; 376 with the products left out; 439 with the accumulators handed back
-// unread; 347 for the products with nothing but the copies' barriers. The additions alone
-// (2.6 cycles for each FFMA2) are 151 and reading the accumulator about as much; what the
-// two accumulators add is the way from commit to hand-back and on to the next products.
-// Tried and slower, before the scales had their own warps (then 547): three accumulators
-// of 160 columns (770), four of 128 (857), loads of 64 columns at once (667).
+// cycles saves less time than it should. The additions (2.6 cycles for each FFMA2) take
+// some 150 ns a block and reading the accumulator about as much; what the two accumulators
+// add is the way from commit to hand-back and on to the next products.
 //
 // Quantisation: one scale for 1 x 128 of x (or 128 x 128 of a weight), amax / 448;
 // codes are the nearest to x (448 (1 / amax)).

@@ -25,13 +25,10 @@
 // changes how much is skipped, never the result: candidates equal to the threshold
 // are kept, and k_lp_join orders them by value and column.
 // The first columns, whose tiles run before there is a threshold, are not listed:
-// their logits are written out (about one tile for each SM, through shared memory: a
-// thread's own stores, 32 rows to an instruction, took 4 us a tile) and k_lp_join reads
-// them against the final threshold. Sorted lists of every part took longer than the
-// products they came from: 333 rows of H = 2048, V = 40960, 20 alternatives: 133 us; with
-// the first columns written out 109; appending, with the maxima published before a part's
-// sums, 75; written out by copies, with the maxima of neighbouring rows side by side, 64,
-// of which 57 are the products' alone (no alternatives).
+// their logits are written out (about one tile for each SM, through shared memory, whose
+// copies write whole rows) and k_lp_join reads them against the final threshold. With 333
+// rows of H = 2048, V = 40960 and 20 alternatives the listing takes 7 of 64 us; a sorted
+// list of every part would take longer than the products it comes from.
 //
 // Tiles are as narrow as the rounds over the SMs allow (lp_head_tile_cols); a plan with a
 // backward pass keeps 256 columns.

@@ -5,12 +5,10 @@
 // single row of 128256 still runs on 16 CTAs (of many rows of bf16 a CTA takes up to
 // four segments: k_lp_rows_many); the next segment is on its way while one is
 // reduced. The k largest are left to k_lp_join, which reads again the few 256s whose
-// maxima reach the k-th largest of them (choosing candidates here took three times as
-// long as the sums: 361 us, 2047 x 128255 bf16, where the sums then took 117 and the
-// join now takes 28). k_lp_grad is elementwise. HBM bounds both for
-// fp32 (1023 x 128255: 80 us = 6.6 TB/s, the gradient 160 us = 6.5 TB/s, 0.97 of a
-// copy's rate) and nearly so for bf16, with twice the elements to a byte (2047 x 128255:
-// 84 us = 6.2 TB/s, the gradient 165 us = 6.3 TB/s).
+// maxima reach the k-th largest of them (2047 x 128255 bf16, 8 alternatives: 28 us).
+// k_lp_grad is elementwise. HBM bounds both for fp32 (1023 x 128255: 80 us = 6.6 TB/s, the
+// gradient 160 us = 6.5 TB/s, 0.97 of a copy's rate) and nearly so for bf16, with twice
+// the elements to a byte (2047 x 128255: 84 us = 6.2 TB/s, the gradient 165 us = 6.3 TB/s).
 #include "dependent.cuh"
 #include "lp.cuh"
 #include "lp_mds.cuh"

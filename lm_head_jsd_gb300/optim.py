@@ -30,7 +30,9 @@ class AdamW:
     """AdamW for a list of parameters of one dtype (fp32 or bf16) on one device.
 
     ``state_bits``: 32 (fp32 moments) or 8 (e4m3 codes of the first moment and of the
-    second's root, one fp32 scale for 128 elements). ``master``: True to keep fp32
+    second's root, one fp32 scale for 128 elements; a root below about 2^-19 of its block's
+    largest is held as 0, and the next step then divides by the new gradient's part and
+    ``eps`` alone, so ``eps`` bounds it). ``master``: True to keep fp32
     weights beside bf16 parameters, or a list of them. The states may be given
     (``exp_avg``, ``exp_avg_sq`` and, in 8 bits, their scales, with ``step`` the number
     of steps they have taken, or a list of each parameter's), e.g. from a checkpoint: they
