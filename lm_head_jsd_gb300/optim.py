@@ -103,6 +103,7 @@ class AdamW:
         self._stepped = [*self.params, *(self.master or ())]
         self._table = np.zeros(len(sizes), dtype=_ENTRY)
         t = self._table
+        self._table_at = t.ctypes.data
         self._at = _ptrs(self.params)
         t["param"], t["n"] = self._at, sizes
         t["exp_avg"], t["exp_avg_sq"] = _ptrs(self.exp_avg), _ptrs(self.exp_avg_sq)
@@ -180,18 +181,19 @@ class AdamW:
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one fp32 value on {dev}")
-        groups = ((t, self.steps + 1),)
+        groups = ((self._table_at if out is None else t.ctypes.data, len(t), self.steps + 1),)
         if self._missed is not None:  # parameters of one number of steps to a call
             missed = self._missed if out is None else self._missed[~out]
-            groups = [(t[missed == m], self.steps + 1 - int(m)) for m in np.unique(missed)]
+            parts = [(t[missed == m], self.steps + 1 - int(m)) for m in np.unique(missed)]
+            groups = [(part.ctypes.data, len(part), step) for part, step in parts]
         with on(stream, dev):
             if self._memory is not None:
                 self._memory.use()
-            for part, step in groups:
+            for at, count, step in groups:
                 o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay, step,
                                             _DT[self.dtype], _DT[dt], self.state_bits,
                                             int(self.master is not None))
-                _lib.fljsd_adamw_step(o, part.ctypes.data, len(part), grad_scale)
+                _lib.fljsd_adamw_step(o, at, count, grad_scale)
         # autograd's own check of what it saved: these have changed
         increment_version(stepped)
         self.steps += 1
