@@ -22,7 +22,7 @@
 // 8-bit states: four elements a thread (402 us against 376, one tensor), the next
 // chunk's loads under way while one is stepped (391), five CTAs an SM (427). The
 // tensors' table is a kernel parameter: no copy to the device, nothing that must
-// outlive the call. Many small tensors are bound by the host (64 tensors 38 us a step,
+// outlive the call. Many small tensors are bound by the host (64 tensors 39 us a step,
 // 7 of them the kernel's).
 #include "internal.cuh"
 
