@@ -439,8 +439,8 @@ fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64
 /*
  * fljsd_adamw_step -- one AdamW step over `count` tensors, in place. Per element,
  * in fp32, each operation rounded once, t = options->step (the number of this
- * step, from 1, for all tensors of the call: tensors that have taken other numbers of
- * steps take calls of their own):
+ * step, from 1, for all tensors of the call; fljsd_adamw_step_each: steps[i], host memory,
+ * for tensor i):
  *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,
  *   v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay)
@@ -464,7 +464,7 @@ fljsd_status fljsd_logits_lp_backward(int64_t rows, int64_t v, int64_t ld, int64
  * Hyperparameters are taken at the call: a captured call repeats its step number.
  * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for an unknown
  * dtype, state_bits other than 8 and 32, beta outside [0, 1), a negative or
- * non-finite eps, a non-finite lr or weight_decay, step < 1, n < 0, a null or
+ * non-finite eps, a non-finite lr or weight_decay, a step < 1, n < 0, a null or
  * misaligned pointer, master with fp32 params, a master pointer without master;
  * FLJSD_ERR_UNSUPPORTED for n above 2^40; FLJSD_ERR_CUDA when a launch fails.
  */
@@ -491,6 +491,10 @@ typedef struct {
 fljsd_status fljsd_adamw_step(const fljsd_adamw_options* options,
                               const fljsd_adamw_tensor* tensors, int32_t count,
                               const float* grad_scale, fljsd_stream_t stream);
+fljsd_status fljsd_adamw_step_each(const fljsd_adamw_options* options,
+                                   const fljsd_adamw_tensor* tensors, const int64_t* steps,
+                                   int32_t count, const float* grad_scale,
+                                   fljsd_stream_t stream);
 
 /*
  * Product in 8-bit floating point with a scale for each block of 128, for a frozen

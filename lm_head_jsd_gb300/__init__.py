@@ -18,6 +18,7 @@ from ._lib import (  # noqa: F401
     fljsd_scale,
     fljsd_tvd,
     fljsd_adamw_step,
+    fljsd_adamw_step_each,
     fljsd_fp8_linear,
     fljsd_fp8_linear_workspace_bytes,
     fljsd_fp8_quantize,

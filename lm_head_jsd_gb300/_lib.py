@@ -137,6 +137,8 @@ def _load():
     lib.fljsd_logits_lp_backward.restype = ctypes.c_int
     lib.fljsd_adamw_step.argtypes = [ctypes.POINTER(fljsd_adamw_options), P, i32, P, P]
     lib.fljsd_adamw_step.restype = ctypes.c_int
+    lib.fljsd_adamw_step_each.argtypes = [ctypes.POINTER(fljsd_adamw_options), P, P, i32, P, P]
+    lib.fljsd_adamw_step_each.restype = ctypes.c_int
     lib.fljsd_fp8_quantize.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P]
     lib.fljsd_fp8_quantize.restype = ctypes.c_int
     lib.fljsd_fp8_linear_workspace_bytes.argtypes = [i64, i64]
@@ -423,6 +425,17 @@ def fljsd_adamw_step(options, tensors, count, grad_scale=None, stream=None, chec
                               _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_adamw_step")
+    return st
+
+
+def fljsd_adamw_step_each(options, tensors, steps, count, grad_scale=None, stream=None,
+                          check=True) -> int:
+    """``tensors``, ``steps``: addresses of ``count`` fljsd_adamw_tensor and int64 in host
+    memory."""
+    st = lib.fljsd_adamw_step_each(ctypes.byref(options), tensors, steps, count, _ptr(grad_scale),
+                                   _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_adamw_step_each")
     return st
 
 

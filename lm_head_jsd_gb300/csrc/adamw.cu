@@ -55,12 +55,13 @@ struct Entry {
 template <int CAP>
 struct Table {
   Entry e[CAP];
+  float2 bias[CAP];  // by the tensor's own step t: {1 / sqrt(1 - beta2^t), lr / (1 - beta1^t)}
   int64_t first[CAP + 1];
   unsigned char vec[CAP];  // every pointer allows vector accesses
   int count;
 };
 struct Hyper {
-  float b1, omb1, b2, omb2, inv_bc2, eps, keep, step;
+  float b1, omb1, b2, omb2, eps, keep;
   const float* scale;
 };
 
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
           end = mid;
       }
     const Entry& e = t.e[at];
+    const float2 bias = t.bias[at];
     const int64_t i0 = (c - t.first[at]) * kChunk + threadIdx.x * kPer;
     const int n = (int)max((int64_t)0, min((int64_t)kPer, e.n - i0));  // this thread's elements
     const bool vec = t.vec[at] && n == kPer;
@@ -222,11 +224,11 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
       const float2 vi = add2(mul2(make_float2(v[i], v[i + 1]), both(h.b2)),
                                    mul2(mul2(gi, both(h.omb2)), gi));
       const float2 ri = make_float2(__fsqrt_rn(vi.x), __fsqrt_rn(vi.y));
-      const float2 den = add2(mul2(ri, both(h.inv_bc2)), both(h.eps));
+      const float2 den = add2(mul2(ri, both(bias.x)), both(h.eps));
       const float2 u = make_float2(__fdiv_rn(mi.x, den.x), __fdiv_rn(mi.y, den.y));
       // (p keep) - (u step): a sum with the negated product, which rounds the same
       const float2 pi = add2(mul2(make_float2(p[i], p[i + 1]), both(h.keep)),
-                                   mul2(u, both(-h.step)));
+                                   mul2(u, both(-bias.y)));
       m[i] = mi.x; m[i + 1] = mi.y;
       v[i] = vi.x; v[i + 1] = vi.y;
       r[i] = ri.x; r[i + 1] = ri.y;
@@ -298,11 +300,19 @@ cudaError_t launch_pg(int bits, bool master, const Table<CAP>& t, const Hyper& h
 
 using bf = __nv_bfloat16;
 
+float2 bias_of(const fljsd_adamw_options& o, int64_t step) {
+  const double t = (double)step;
+  return make_float2((float)(1.0 / std::sqrt(1.0 - std::pow(o.beta2, t))),
+                     (float)(o.lr / (1.0 - std::pow(o.beta1, t))));
+}
+
 // Launches of up to CAP tensors each.
 template <int CAP>
-cudaError_t run(const fljsd_adamw_tensor* ts, int count, const fljsd_adamw_options& o,
-                const Hyper& h, cudaStream_t st) {
+cudaError_t run(const fljsd_adamw_tensor* ts, const int64_t* steps, int count,
+                const fljsd_adamw_options& o, const Hyper& h, cudaStream_t st) {
   Table<CAP> t;
+  int64_t last = 0;  // the step of `bias` (most tensors share it)
+  float2 bias{};
   for (int at = 0; at < count;) {
     t.count = 0;
     t.first[0] = 0;
@@ -312,6 +322,9 @@ cudaError_t run(const fljsd_adamw_tensor* ts, int count, const fljsd_adamw_optio
       const int i = t.count++;
       t.e[i] = Entry{x.grad, x.param, x.master, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale,
                      x.exp_avg_sq_scale, x.n};
+      const int64_t step = steps ? steps[at] : o.step;
+      if (step != last) bias = bias_of(o, last = step);
+      t.bias[i] = bias;
       t.first[i + 1] = t.first[i] + (x.n + kChunk - 1) / kChunk;
       uintptr_t bits = (uintptr_t)x.grad | (uintptr_t)x.param | (uintptr_t)x.master;
       const uintptr_t state = (uintptr_t)x.exp_avg | (uintptr_t)x.exp_avg_sq;
@@ -342,6 +355,13 @@ using namespace fljsd;
 extern "C" fljsd_status fljsd_adamw_step(const fljsd_adamw_options* o,
                                          const fljsd_adamw_tensor* tensors, int32_t count,
                                          const float* grad_scale, fljsd_stream_t stream) {
+  return fljsd_adamw_step_each(o, tensors, nullptr, count, grad_scale, stream);
+}
+
+extern "C" fljsd_status fljsd_adamw_step_each(const fljsd_adamw_options* o,
+                                              const fljsd_adamw_tensor* tensors,
+                                              const int64_t* steps, int32_t count,
+                                              const float* grad_scale, fljsd_stream_t stream) {
   if (!o || count < 0 || (count > 0 && !tensors)) return FLJSD_ERR_INVALID_ARG;
   if ((o->param_dtype != FLJSD_F32 && o->param_dtype != FLJSD_BF16) ||
       (o->grad_dtype != FLJSD_F32 && o->grad_dtype != FLJSD_BF16))
@@ -351,14 +371,14 @@ extern "C" fljsd_status fljsd_adamw_step(const fljsd_adamw_options* o,
     return FLJSD_ERR_INVALID_ARG;
   if (!(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) || !(o->eps >= 0) ||
       !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay) ||
-      o->step < 1)
+      (!steps && o->step < 1))
     return FLJSD_ERR_INVALID_ARG;
   if ((uintptr_t)grad_scale & 3u) return FLJSD_ERR_INVALID_ARG;
   const uintptr_t pa = o->param_dtype == FLJSD_BF16 ? 1 : 3, ga = o->grad_dtype == FLJSD_BF16 ? 1 : 3;
   const uintptr_t sa = o->state_bits == 32 ? 3 : 0;
   for (int i = 0; i < count; ++i) {
     const fljsd_adamw_tensor& t = tensors[i];
-    if (t.n < 0) return FLJSD_ERR_INVALID_ARG;
+    if (t.n < 0 || (steps && steps[i] < 1)) return FLJSD_ERR_INVALID_ARG;
     if (t.n == 0) continue;
     if (!t.grad || !t.param || !t.exp_avg || !t.exp_avg_sq || (o->master && !t.master) ||
         (!o->master && t.master))
@@ -372,19 +392,16 @@ extern "C" fljsd_status fljsd_adamw_step(const fljsd_adamw_options* o,
     if (t.n > (int64_t)1 << 40) return FLJSD_ERR_UNSUPPORTED;
   }
   Hyper h;
-  const double t = (double)o->step;
   h.b1 = (float)o->beta1;
   h.omb1 = (float)(1.0 - o->beta1);
   h.b2 = (float)o->beta2;
   h.omb2 = (float)(1.0 - o->beta2);
-  h.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(o->beta2, t)));
   h.eps = (float)o->eps;
   h.keep = (float)(1.0 - o->lr * o->weight_decay);
-  h.step = (float)(o->lr / (1.0 - std::pow(o->beta1, t)));
   h.scale = grad_scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // a smaller table is a smaller parameter block to hand over at launch
-  const cudaError_t e = count <= kFew ? run<kFew>(tensors, count, *o, h, st)
-                                      : run<kMany>(tensors, count, *o, h, st);
+  const cudaError_t e = count <= kFew ? run<kFew>(tensors, steps, count, *o, h, st)
+                                      : run<kMany>(tensors, steps, count, *o, h, st);
   return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
 }

@@ -181,19 +181,19 @@ class AdamW:
         if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
                                        or grad_scale.device != dev):
             raise ValueError(f"grad_scale must be one fp32 value on {dev}")
-        groups = ((self._table_at if out is None else t.ctypes.data, len(t), self.steps + 1),)
-        if self._missed is not None:  # parameters of one number of steps to a call
-            missed = self._missed if out is None else self._missed[~out]
-            parts = [(t[missed == m], self.steps + 1 - int(m)) for m in np.unique(missed)]
-            groups = [(part.ctypes.data, len(part), step) for part, step in parts]
+        at = self._table_at if out is None else t.ctypes.data
+        o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay,
+                                    self.steps + 1, _DT[self.dtype], _DT[dt], self.state_bits,
+                                    int(self.master is not None))
         with on(stream, dev):
             if self._memory is not None:
                 self._memory.use()
-            for at, count, step in groups:
-                o = _lib.make_adamw_options(self.lr, *self.betas, self.eps, self.weight_decay, step,
-                                            _DT[self.dtype], _DT[dt], self.state_bits,
-                                            int(self.master is not None))
-                _lib.fljsd_adamw_step(o, at, count, grad_scale)
+            if self._missed is None:
+                _lib.fljsd_adamw_step(o, at, len(t), grad_scale)
+            else:
+                missed = self._missed if out is None else self._missed[~out]
+                steps = self.steps + 1 - missed
+                _lib.fljsd_adamw_step_each(o, at, steps.ctypes.data, len(t), grad_scale)
         # autograd's own check of what it saved: these have changed
         increment_version(stepped)
         self.steps += 1

@@ -137,3 +137,40 @@ def test_replaced_parameters_and_storages():
     opt.step([g, g])
     torch.cuda.synchronize()
     assert all((t == 5).all() for t in later)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_every_count_another(bits):
+    """Parameters of as many counts as there are: each as alone, in two launches for 450."""
+    from lm_head_jsd_gb300 import AdamW, fljsd_launch_count
+
+    sizes = [(i * 53) % 400 + 1 for i in range(450)]
+    g = torch.Generator().manual_seed(3)
+    ps = [torch.randn(n, generator=g).cuda() for n in sizes]
+    gs = [torch.randn(n, generator=g).cuda() for n in sizes]
+    joint = AdamW([p.clone() for p in ps], state_bits=bits, step=list(range(450)), **HY)
+    before = fljsd_launch_count()
+    joint.step(gs)
+    assert fljsd_launch_count() - before == 2
+    for i, (p, q) in enumerate(zip(ps, joint.params)):
+        one = AdamW([p.clone()], state_bits=bits, step=i, **HY)
+        one.step([gs[i]])
+        assert torch.equal(one.params[0], q), i
+
+
+def test_counts_that_are_refused():
+    import ctypes
+
+    from conftest import build_library
+
+    build_library()
+    from lm_head_jsd_gb300 import _lib as L
+
+    o = L.make_adamw_options(1e-3, 0.9, 0.99, 1e-8, 0.0, 0)  # (its own step is not used)
+    t = (L.fljsd_adamw_tensor * 2)()
+    call = lambda *steps: L.fljsd_adamw_step_each(  # noqa: E731
+        o, ctypes.addressof(t), ctypes.addressof((ctypes.c_int64 * 2)(*steps)), 2, None, stream=0, check=False)
+    assert call(1, 1) == 0  # two tensors without elements: nothing to do
+    assert call(1, 0) == 1 and call(-3, 1) == 1
+    assert L.fljsd_adamw_step_each(o, ctypes.addressof(t), None, 2, None, stream=0, check=False) == 1
