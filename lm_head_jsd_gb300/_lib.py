@@ -184,7 +184,7 @@ def _stream(stream) -> int | None:
         # the handle alone: a Stream object takes longer to make than a launch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -8,11 +8,13 @@ import torch
 from . import _lib
 
 _HERE = nullcontext()
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def require_cuda(name, device):
-    if device.type != "cuda":
-        raise ValueError(f"{name} is on {device}, expected a CUDA device")
+def require_cuda(name, t):
+    """Of a tensor or a device."""
+    if not (t.is_cuda if isinstance(t, torch.Tensor) else t.type == "cuda"):
+        raise ValueError(f"{name} is on {getattr(t, 'device', t)}, expected a CUDA device")
 
 
 def on(stream, device):
@@ -20,7 +22,7 @@ def on(stream, device):
     what it takes is free there and what it drops is not handed out before that stream has
     passed the call; None: on the current stream of its tensors' device."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if device.index == _device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream if isinstance(stream, int) else stream.cuda_stream
         # (0 and 1 are the default stream's)

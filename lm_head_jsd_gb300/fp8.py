@@ -27,7 +27,7 @@ def fp8_quantize(w, *, block_rows=BLOCK, stream=None):
     ld = _check_rows("w", w)
     if w.dtype not in _DT:
         raise ValueError(f"w has dtype {w.dtype}, expected one of {list(_DT)}")
-    require_cuda("w", w.device)
+    require_cuda("w", w)
     rows, cols = w.shape
     ldq, kb = -(-cols // 16) * 16, -(-cols // BLOCK)
     with on(stream, w.device):
@@ -49,7 +49,7 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, out=None, stat
     ldx = _check_rows("x", x)
     ldw = _check_rows("w_codes", w_codes)
     (m, k), n, dev = x.shape, w_codes.shape[0], x.device
-    require_cuda("x", dev)
+    require_cuda("x", x)
     check_status(status, dev)
     if x.dtype not in _DT or out_dtype not in _DT:
         raise ValueError(f"x and out_dtype must be one of {list(_DT)}")

@@ -236,7 +236,7 @@ def _logits_check(logits, labels):
         raise ValueError(f"logits have dtype {logits.dtype}, expected one of {list(_DT)}")
     if logits.stride(1) != 1 and logits.shape[1] > 1:
         raise ValueError("the rows of logits must be contiguous")
-    require_cuda("logits", logits.device)
+    require_cuda("logits", logits)
     if labels is not None:
         _check("labels", labels, torch.int64, logits.device, (logits.shape[0],))
 
@@ -253,17 +253,20 @@ def logits_logprobs(logits, labels=None, *, top_k=0, temperature=1.0, ignore_ind
     int32 on the device that receives the call's status word (0, or FLJSD_ERR_INVALID_ARG
     for a label outside [0, V) other than ignore_index)."""
     _logits_check(logits, labels)
-    check_status(status, logits.device)
-    rows, v = logits.shape
-    with on(stream, logits.device):
-        r = _results(rows, top_k, labels is not None, logits.device)
+    (rows, v), dev = logits.shape, logits.device
+    if status is not None:
+        check_status(status, dev)
+    with on(stream, dev):
+        r = _results(rows, top_k, labels is not None, dev)
         ws = torch.empty(_lib.fljsd_logits_lp_workspace_bytes(rows, v, top_k), dtype=torch.uint8,
-                         device=logits.device)
+                         device=dev)
         _lib.fljsd_logits_lp(rows, v, _row_stride(logits), _DT[logits.dtype], top_k, temperature,
                              ignore_index, logits, labels, r.logp, r.entropy, r.lse, r.norm,
                              r.top_logp, r.top_id, ws)
-        report(status, ws)
-    hand_over(r, stream, logits.device)
+        if status is not None:
+            report(status, ws)
+    if stream is not None:
+        hand_over(r, stream, dev)
     return r
 
 

@@ -171,7 +171,7 @@ class AdamW:
                 return
             t["grad"] = _ptrs(live)
         dt, dev = live[0].dtype, self.device
-        require_cuda("the optimizer", dev)
+        require_cuda("params[0]", self.params[0])
         # (whole-list checks: a step of many small tensors is bound by this function)
         if (dt not in _DT or set(map(_DTYPE, live)) != {dt} or set(map(_DEVICE, live)) != {dev.index}
                 or not all(map(torch.Tensor.is_contiguous, live))

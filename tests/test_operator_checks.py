@@ -50,7 +50,7 @@ def test_host_tensors_are_refused(name):
 def test_calls_run_on_their_tensors_device(monkeypatch):
     from lm_head_jsd_gb300 import _streams
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_streams, "_device", lambda: 0)
     ctx = _streams.on(None, torch.device("cuda", 1))
     assert isinstance(ctx, torch.cuda.device) and ctx.idx == 1
     assert not isinstance(_streams.on(None, torch.device("cuda", 0)), torch.cuda.device)
