@@ -353,9 +353,10 @@ fljsd_status fljsd_ce_forward(const fljsd_ce_problem* problem, const fljsd_plan_
  *   dz_j = (a (1[j = y] - p_j) - b p_j (log p_j + entropy)) / temperature,
  *   grad_input = dz . w,  grad_weight = dz^T . x.
  * All of it is computed in fp32 from unrounded logits; the top alternatives carry
- * no gradient. The fused form does not write the logits, but its workspace has room
- * for the alternatives' candidates, about v top_k / 16 bytes a row (top_k 32: what
- * bf16 logits take), and with FLJSD_LP_BACKWARD for the kept 2 v bytes a row.
+ * no gradient. The fused form returns no logits; its workspace holds, for each row of a
+ * chunk, the alternatives' candidates (about v top_k / 16 bytes: with top_k 32 what bf16
+ * logits take) and with FLJSD_LP_BACKWARD the kept values (2 v bytes); fp32 logits (4 v
+ * bytes) of up to 16 rows with alternatives, and of what runs on the CUDA cores.
  *
  * Rows and values outside the ordinary:
  *  - a row whose label is ignore_index, or outside [0, v), has logp 0, entropy 0

@@ -20,7 +20,8 @@ def require_cuda(name, t):
 def on(stream, device):
     """Where a call allocates and launches: on ``stream`` (a Stream or its handle), so that
     what it takes is free there and what it drops is not handed out before that stream has
-    passed the call; None: on the current stream of its tensors' device."""
+    passed the call; None: on the current stream of its tensors' device. A stream given by
+    its handle must live as long as the results and the objects that were used on it."""
     if stream is None:
         return _HERE if device.index == _device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 gpu = pytest.mark.gpu
-PAUSE = 100_000_000  # clock cycles, some 50 ms: far longer than the calls below
+PAUSE = 200_000_000  # clock cycles, some 100 ms: far longer than the calls below
 
 
 def _problem(bt=40, h=128, v=3000, dtype=torch.bfloat16):
