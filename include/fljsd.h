@@ -498,6 +498,53 @@ fljsd_status fljsd_adamw_step_each(const fljsd_adamw_options* options,
                                    fljsd_stream_t stream);
 
 /*
+ * The norm of many tensors taken together, and clipping. Over the elements g of all
+ * `count` tensors (fp32 and bf16 may be mixed):
+ *   FLJSD_NORM_2: norm = sqrt(sum g^2); FLJSD_NORM_MAX: norm = max |g|;
+ *   factor = min(1, max_norm / (norm + 1e-6)).
+ * Sums are held in fp32 and joined in fp64, in one order: the same tensors have the same
+ * norm in every call on a GPU. Every finite g counts, up to fp32's largest and down to its smallest; a norm
+ * that fp32 does not hold is infinite. A NaN among the gradients makes the norm and the
+ * factor NaN; an infinity makes the norm infinite and the factor 0. No tensors, or none
+ * with elements: norm 0.
+ *
+ * fljsd_grad_norm -- the norm, and where factor is not NULL the factor (max_norm is not
+ * looked at otherwise). grad_scale: device fp32 scalar or NULL (1) that every gradient
+ * counts as multiplied by; the factor then includes it, so that it can be handed to
+ * fljsd_adamw_step as its grad_scale. `out` is not looked at.
+ *
+ * fljsd_clip_grads -- the norm of `grad`, and out = grad * factor in the tensor's dtype,
+ * rounded once. out may be the gradient itself (which is left as it is where the factor
+ * is 1), but no other memory of the call's tensors.
+ *
+ * norm and factor: device fp32 scalars, 4-byte aligned. `tensors` is host memory, read
+ * before the call returns; grad and out are element-aligned device memory (an out that
+ * lies as its gradient does relative to 16 bytes is fastest). Tensors with n == 0 are
+ * left out. workspace: fljsd_grad_norm_workspace_bytes(count) bytes, 16-byte aligned.
+ * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for an unknown dtype
+ * or kind, n < 0, a null or misaligned pointer, a max_norm that is negative or NaN (where
+ * it is looked at); FLJSD_ERR_UNSUPPORTED for n above 2^40; FLJSD_ERR_WORKSPACE;
+ * FLJSD_ERR_CUDA when a launch fails.
+ */
+typedef enum { FLJSD_NORM_MAX = 0, FLJSD_NORM_2 = 2 } fljsd_norm_kind;
+
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype; /* fljsd_dtype */
+  int32_t reserved;
+} fljsd_grad_tensor;
+
+size_t fljsd_grad_norm_workspace_bytes(int32_t count);
+fljsd_status fljsd_grad_norm(const fljsd_grad_tensor* tensors, int32_t count, int32_t kind,
+                             float max_norm, const float* grad_scale, float* norm, float* factor,
+                             void* workspace, size_t workspace_bytes, fljsd_stream_t stream);
+fljsd_status fljsd_clip_grads(const fljsd_grad_tensor* tensors, int32_t count, int32_t kind,
+                              float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                              fljsd_stream_t stream);
+
+/*
  * Product in 8-bit floating point with a scale for each block of 128, for a frozen
  * lm_head (a teacher's, or one that only scores): out = x . w^T with w [n x k]
  * held as e4m3 codes and one fp32 scale for each 128 x 128 block, and x [m x k]

@@ -19,10 +19,13 @@ from ._lib import (  # noqa: F401
     fljsd_tvd,
     fljsd_adamw_step,
     fljsd_adamw_step_each,
+    fljsd_clip_grads,
     fljsd_fp8_linear,
     fljsd_fp8_linear_workspace_bytes,
     fljsd_fp8_quantize,
     fljsd_capture_id,
+    fljsd_grad_norm,
+    fljsd_grad_norm_workspace_bytes,
     fljsd_launch_count,
     fljsd_logits_lp,
     fljsd_logits_lp_backward,
@@ -49,6 +52,7 @@ from .api import (  # noqa: F401
     jsd_logspace,
     tvd,
 )
+from .clip import clip_grads, grad_norm  # noqa: F401
 from .fp8 import fp8_linear, fp8_quantize  # noqa: F401
 from .logprobs import (  # noqa: F401
     FusedLinearLogprobs,

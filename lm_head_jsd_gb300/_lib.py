@@ -64,6 +64,12 @@ class fljsd_adamw_options(ctypes.Structure):
         ("state_bits", ctypes.c_int32), ("master", ctypes.c_int32)]
 
 
+class fljsd_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+FLJSD_NORM_MAX, FLJSD_NORM_2 = 0, 2
 FLJSD_FLAG_T2 = 1
 FLJSD_FLAG_ACCUM_FP32 = 2
 FLJSD_LP_BACKWARD = 4
@@ -139,6 +145,12 @@ def _load():
     lib.fljsd_adamw_step.restype = ctypes.c_int
     lib.fljsd_adamw_step_each.argtypes = [ctypes.POINTER(fljsd_adamw_options), P, P, i32, P, P]
     lib.fljsd_adamw_step_each.restype = ctypes.c_int
+    lib.fljsd_grad_norm_workspace_bytes.argtypes = [i32]
+    lib.fljsd_grad_norm_workspace_bytes.restype = size
+    lib.fljsd_grad_norm.argtypes = [P, i32, i32, f32, P, P, P, P, size, P]
+    lib.fljsd_grad_norm.restype = ctypes.c_int
+    lib.fljsd_clip_grads.argtypes = [P, i32, i32, f32, P, P, size, P]
+    lib.fljsd_clip_grads.restype = ctypes.c_int
     lib.fljsd_fp8_quantize.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P]
     lib.fljsd_fp8_quantize.restype = ctypes.c_int
     lib.fljsd_fp8_linear_workspace_bytes.argtypes = [i64, i64]
@@ -436,6 +448,34 @@ def fljsd_adamw_step_each(options, tensors, steps, count, grad_scale=None, strea
                                    _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_adamw_step_each")
+    return st
+
+
+def fljsd_grad_norm_workspace_bytes(count: int) -> int:
+    return lib.fljsd_grad_norm_workspace_bytes(count)
+
+
+def fljsd_grad_norm(tensors, count, kind, max_norm, grad_scale, norm, factor, workspace,
+                    workspace_bytes=None, stream=None, check=True) -> int:
+    """``tensors``: address of ``count`` fljsd_grad_tensor in host memory."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_grad_norm(tensors, count, kind, max_norm, _ptr(grad_scale), _ptr(norm),
+                             _ptr(factor), _ptr(workspace), workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_grad_norm")
+    return st
+
+
+def fljsd_clip_grads(tensors, count, kind, max_norm, norm, workspace, workspace_bytes=None,
+                     stream=None, check=True) -> int:
+    """``tensors``: address of ``count`` fljsd_grad_tensor in host memory."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_clip_grads(tensors, count, kind, max_norm, _ptr(norm), _ptr(workspace),
+                              workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_clip_grads")
     return st
 
 

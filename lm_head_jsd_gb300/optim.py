@@ -8,8 +8,9 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from ._streams import Memory, on, require_cuda
+from ._streams import Memory, hand_over, on, require_cuda
 from .api import _DT
+from .clip import check_max_norm, table, workspace
 
 _BLOCK = 128  # elements of one 8-bit state block
 
@@ -58,6 +59,7 @@ class AdamW:
             raise ValueError(f"state_bits is {state_bits}, expected 8 or 32")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits = state_bits
+        self.grad_norm = None  # of the last step that was given a max_norm
         counts = np.array(step, dtype=np.int64) if isinstance(step, (list, tuple, np.ndarray)) else None
         if counts is not None and counts.shape != (len(self.params),):
             raise ValueError(f"step has {counts.size} numbers, expected {len(self.params)}")
@@ -145,9 +147,14 @@ class AdamW:
             if sizes is not None and t.numel() != sizes[i]:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {sizes[i]}")
 
-    def step(self, grads=None, *, grad_scale=None, stream=None):
+    def step(self, grads=None, *, grad_scale=None, max_norm=None, stream=None):
         """One step. ``grad_scale``: an fp32 scalar on the device that every gradient is
-        multiplied by."""
+        multiplied by. ``max_norm``: the step goes by gradients scaled (after that) to at
+        most this norm of all of them together, as :func:`clip_grads` does; the gradients
+        stay as they are, and ``grad_norm`` is their norm before that, an fp32 scalar on
+        the device. A norm of NaN makes every stepped value NaN."""
+        if max_norm is not None:
+            check_max_norm(max_norm)
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} parameters")
@@ -188,12 +195,20 @@ class AdamW:
         with on(stream, dev):
             if self._memory is not None:
                 self._memory.use()
+            if max_norm is not None:
+                both = torch.empty(2, dtype=torch.float32, device=dev)  # norm, factor
+                g = table(live)
+                _lib.fljsd_grad_norm(g.ctypes.data, len(g), _lib.FLJSD_NORM_2, max_norm, grad_scale,
+                                     both[0], both[1], workspace(len(g), dev))
+                self.grad_norm, grad_scale = both[0], both[1]
             if self._missed is None:
                 _lib.fljsd_adamw_step(o, at, len(t), grad_scale)
             else:
                 missed = self._missed if out is None else self._missed[~out]
                 steps = self.steps + 1 - missed
                 _lib.fljsd_adamw_step_each(o, at, steps.ctypes.data, len(t), grad_scale)
+        if max_norm is not None:
+            hand_over((self.grad_norm,), stream, dev)
         # autograd's own check of what it saved: these have changed
         increment_version(stepped)
         self.steps += 1
