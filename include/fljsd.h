@@ -581,6 +581,64 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
                               int32_t out_dtype, void* out, int64_t ldo, void* workspace,
                               size_t workspace_bytes, fljsd_stream_t stream);
 
+/*
+ * fljsd_verify -- drafted tokens verified against a target's probabilities, from given
+ * random numbers (speculative decoding). `requests` requests propose `drafts` tokens
+ * together, request b tokens[offsets[b] .. offsets[b + 1]), at most max_drafts each;
+ * offsets NULL: max_drafts each (drafts = requests * max_drafts). Row offsets[b] + b + i of
+ * `target` [drafts + requests x v] holds the target's logits in front of its drafted token
+ * i, the row after its last one those behind it; row offsets[b] + i of `draft` [drafts x v]
+ * holds the logits that the token was drafted from (NULL: the tokens have no
+ * probabilities, as those looked up in a prompt). With a temperature T for each request
+ * (temperatures [requests], or `temperature` for all):
+ *   p = softmax(target / T), q = softmax(draft / T), q = 1 at the drafted token without draft.
+ * A request's tokens d are accepted in turn as long as u_accept q_d < p_d. The first that is
+ * not gives way to a token drawn from max(p - q, 0) (from p where that is 0 everywhere);
+ * where all are, one more is drawn from p. Drawn is the lowest column at which the running
+ * sum of the weights exceeds u_draw [requests] times their sum. Over many random numbers,
+ * uniform in [0, 1), the tokens follow p, whatever the drafts. T = 0: d is accepted where
+ * it is the target's largest logit (of equal ones the lowest column), which is what is drawn.
+ *   out [requests x (max_drafts + 1)]: the accepted tokens, the drawn one, -1 behind;
+ *   accepted [requests]: how many of the drafted tokens were;
+ *   accept_prob [drafts]: min(1, p_d / q_d) of every drafted token (T = 0: 1 or 0), fp32,
+ *   whether or not an earlier one was refused.
+ *
+ * The weights are whole multiples of 2^-43 of the row's largest (of 1 for the difference),
+ * so their sums have one value in any order: the tokens of a request depend on its own
+ * logits and numbers alone, not on the batch or the launch. What is below 2^-44 is never
+ * drawn. Tests are made in fp64.
+ *
+ * Rows and values outside the ordinary:
+ *  - a logit of -inf has probability 0. A target row of nothing else, or with a NaN or
+ *    +inf, accepts nothing; if a token is to be drawn from it, that is -1.
+ *  - a token whose draft row is such a row is refused, and drawn from p alone.
+ *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets fall,
+ *    leave [0, drafts] or span more than max_drafts, or whose temperature on the device is
+ *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0 and -1s. Both
+ *    set the status word (the workspace's first int32) to FLJSD_ERR_INVALID_ARG.
+ *  - u_draw outside [0, 1) is taken to its nearer end, NaN as 0; u_accept of NaN refuses.
+ *  - tokens before the first request's and behind the last one's have accept_prob 0: a
+ *    buffer may be longer than what a step fills. (offsets given; their rows are not read.)
+ *
+ * target and draft in dtype with row strides ld_target and ld_draft (elements, any
+ * element alignment); tokens, offsets, out, accepted int64, u_accept [drafts], u_draw,
+ * temperatures, accept_prob fp32. workspace: fljsd_verify_workspace_bytes bytes, 16-byte
+ * aligned. Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for requests or
+ * v <= 0, drafts or max_drafts < 0, drafts that are not requests * max_drafts without
+ * offsets, a stride below v, an unknown dtype, a temperature that is negative, infinite, NaN
+ * or so small that log2(e) / T is not finite, a null or misaligned pointer (tokens, u_accept and
+ * accept_prob may be NULL with drafts 0); FLJSD_ERR_UNSUPPORTED for v of 2^20 and more,
+ * requests above 2^20, drafts above 2^24, max_drafts above 1024, or requests *
+ * (2 max_drafts + 1) of 2^28 and more; FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
+ */
+size_t fljsd_verify_workspace_bytes(int64_t requests, int64_t drafts);
+fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v, int32_t max_drafts,
+                          int32_t dtype, const void* target, int64_t ld_target, const void* draft,
+                          int64_t ld_draft, const int64_t* tokens, const float* u_accept,
+                          const float* u_draw, const int64_t* offsets, const float* temperatures,
+                          float temperature, int64_t* out, int64_t* accepted, float* accept_prob,
+                          void* workspace, size_t workspace_bytes, fljsd_stream_t stream);
+
 /* Id of the capture into a CUDA graph that `stream` is in, unique in the process; 0 where
  * it is in none (or on an error). A caller that passes kept = 1 to fljsd_lp_backward needs
  * it: the two calls belong to one capture, or to none. */

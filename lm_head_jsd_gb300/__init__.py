@@ -41,6 +41,8 @@ from ._lib import (  # noqa: F401
     fljsd_trace_enable,
     fljsd_trace_read,
     fljsd_trace_reset,
+    fljsd_verify,
+    fljsd_verify_workspace_bytes,
     fljsd_workspace_status,
     make_problem,
 )
@@ -63,5 +65,6 @@ from .logprobs import (  # noqa: F401
     token_logprobs,
 )
 from .optim import AdamW  # noqa: F401
+from .verify import Verified, verify_drafts  # noqa: F401
 
 LIB_PATH = _lib.LIB_PATH

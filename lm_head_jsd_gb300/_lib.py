@@ -151,6 +151,10 @@ def _load():
     lib.fljsd_grad_norm.restype = ctypes.c_int
     lib.fljsd_clip_grads.argtypes = [P, i32, i32, f32, P, P, size, P]
     lib.fljsd_clip_grads.restype = ctypes.c_int
+    lib.fljsd_verify_workspace_bytes.argtypes = [i64, i64]
+    lib.fljsd_verify_workspace_bytes.restype = size
+    lib.fljsd_verify.argtypes = [i64, i64, i64, i32, i32, P, i64, P, i64, *[P] * 5, f32, *[P] * 4, size, P]
+    lib.fljsd_verify.restype = ctypes.c_int
     lib.fljsd_fp8_quantize.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P]
     lib.fljsd_fp8_quantize.restype = ctypes.c_int
     lib.fljsd_fp8_linear_workspace_bytes.argtypes = [i64, i64]
@@ -476,6 +480,24 @@ def fljsd_clip_grads(tensors, count, kind, max_norm, norm, workspace, workspace_
                               workspace_bytes, _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_clip_grads")
+    return st
+
+
+def fljsd_verify_workspace_bytes(requests: int, drafts: int) -> int:
+    return lib.fljsd_verify_workspace_bytes(requests, drafts)
+
+
+def fljsd_verify(requests, drafts, v, max_drafts, dtype, target, ld_target, draft, ld_draft, tokens,
+                 u_accept, u_draw, offsets, temperatures, temperature, out, accepted, accept_prob,
+                 workspace, workspace_bytes=None, stream=None, check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_verify(requests, drafts, v, max_drafts, _dt(dtype), _ptr(target), ld_target,
+                          _ptr(draft), ld_draft, _ptr(tokens), _ptr(u_accept), _ptr(u_draw),
+                          _ptr(offsets), _ptr(temperatures), temperature, _ptr(out), _ptr(accepted),
+                          _ptr(accept_prob), _ptr(workspace), workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_verify")
     return st
 
 
