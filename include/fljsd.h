@@ -582,6 +582,38 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
                               size_t workspace_bytes, fljsd_stream_t stream);
 
 /*
+ * fljsd_low_rank_add -- low-rank adapters of many requests on the output of a projection
+ * that they share (serving; no gradient): for each of `tokens` rows, with a = index[t],
+ *   out_t = y_t + scale_a B_a (A_a x_t);  a = -1: out_t = y_t.
+ * a [adapters x rank x k] and b [adapters x n x rank] bf16, contiguous; scales [adapters]
+ * fp32 or NULL (1); x [tokens x k] bf16 with row stride ldx; y and out [tokens x n] in
+ * dtype with row strides ldy and ldo; out may be y (same address and stride; rows of
+ * index -1 are then not touched), but no other memory of the call. The tokens' order is
+ * free; those of one adapter need not be neighbours. The rank is a multiple of 8 (adapters
+ * of smaller ranks are padded with zeros).
+ * Products are added in fp32; A x, scaled, is carried on as the sum of two bf16 (2^-16 of
+ * it at most is lost), the result is added to y in fp32 and rounded once to dtype. A row's
+ * result does not depend on the other rows.
+ * An index that is neither -1 nor in [0, adapters) counts as -1 and sets the status word
+ * (the workspace's first int32) to FLJSD_ERR_INVALID_ARG; FLJSD_ERR_TIMEOUT there: a
+ * bounded device wait expired and out is not complete.
+ * workspace: fljsd_low_rank_workspace_bytes(tokens, adapters, rank) bytes. b and the
+ * workspace are 16-byte aligned, everything else element-aligned (x and a are fastest on 16
+ * bytes with ldx and k multiples of 8, y and out on two elements with even strides).
+ * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for a dimension <= 0, a
+ * stride below its row, a rank that is no multiple of 8, an unknown dtype, a null or
+ * misaligned pointer, out at y's address with another stride; FLJSD_ERR_UNSUPPORTED for
+ * tokens or k above 2^20, n above 2^26, rank above 128, adapters above 4096;
+ * FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
+ */
+size_t fljsd_low_rank_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank);
+fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t rank, int32_t adapters,
+                                const void* x, int64_t ldx, const void* a, const void* b,
+                                const int64_t* index, const float* scales, int32_t dtype,
+                                const void* y, int64_t ldy, void* out, int64_t ldo, void* workspace,
+                                size_t workspace_bytes, fljsd_stream_t stream);
+
+/*
  * fljsd_verify -- drafted tokens verified against a target's probabilities, from given
  * random numbers (speculative decoding). `requests` requests propose `drafts` tokens
  * together, request b tokens[offsets[b] .. offsets[b + 1]), at most max_drafts each;

@@ -30,6 +30,8 @@ from ._lib import (  # noqa: F401
     fljsd_logits_lp,
     fljsd_logits_lp_backward,
     fljsd_logits_lp_workspace_bytes,
+    fljsd_low_rank_add,
+    fljsd_low_rank_workspace_bytes,
     fljsd_lp_backward,
     fljsd_lp_forward,
     fljsd_lp_plan,
@@ -56,6 +58,7 @@ from .api import (  # noqa: F401
 )
 from .clip import clip_grads, grad_norm  # noqa: F401
 from .fp8 import fp8_linear, fp8_quantize  # noqa: F401
+from .low_rank import low_rank_add  # noqa: F401
 from .logprobs import (  # noqa: F401
     FusedLinearLogprobs,
     Logprobs,

@@ -155,6 +155,11 @@ def _load():
     lib.fljsd_verify_workspace_bytes.restype = size
     lib.fljsd_verify.argtypes = [i64, i64, i64, i32, i32, P, i64, P, i64, *[P] * 5, f32, *[P] * 4, size, P]
     lib.fljsd_verify.restype = ctypes.c_int
+    lib.fljsd_low_rank_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.fljsd_low_rank_workspace_bytes.restype = size
+    lib.fljsd_low_rank_add.argtypes = [i64, i64, i64, i32, i32, P, i64, P, P, P, P, i32, P, i64, P, i64, P,
+                                       size, P]
+    lib.fljsd_low_rank_add.restype = ctypes.c_int
     lib.fljsd_fp8_quantize.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P]
     lib.fljsd_fp8_quantize.restype = ctypes.c_int
     lib.fljsd_fp8_linear_workspace_bytes.argtypes = [i64, i64]
@@ -498,6 +503,22 @@ def fljsd_verify(requests, drafts, v, max_drafts, dtype, target, ld_target, draf
                           _ptr(accept_prob), _ptr(workspace), workspace_bytes, _stream(stream))
     if check and st != FLJSD_OK:
         raise FljsdError(st, "fljsd_verify")
+    return st
+
+
+def fljsd_low_rank_workspace_bytes(tokens: int, adapters: int, rank: int) -> int:
+    return lib.fljsd_low_rank_workspace_bytes(tokens, adapters, rank)
+
+
+def fljsd_low_rank_add(tokens, k, n, rank, adapters, x, ldx, a, b, index, scales, dtype, y, ldy, out, ldo,
+                       workspace, workspace_bytes=None, stream=None, check=True) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.fljsd_low_rank_add(tokens, k, n, rank, adapters, _ptr(x), ldx, _ptr(a), _ptr(b), _ptr(index),
+                                _ptr(scales), _dt(dtype), _ptr(y), ldy, _ptr(out), ldo, _ptr(workspace),
+                                workspace_bytes, _stream(stream))
+    if check and st != FLJSD_OK:
+        raise FljsdError(st, "fljsd_low_rank_add")
     return st
 
 

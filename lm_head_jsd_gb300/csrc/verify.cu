@@ -74,10 +74,17 @@ __device__ __forceinline__ uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // Writes to the same shared variable of CTA `rank`.
 __device__ __forceinline__ void put_remote(void* p, uint32_t rank, unsigned long long x) {
@@ -240,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_rows(const Args a) {
   const bool is_draft = slot > a.max_drafts;
   const int j = is_draft ? slot - a.max_drafts - 1 : slot;
   if (!q.ok || j >= q.drafts + (is_draft ? 0 : 1) || (is_draft && q.c == 0.f)) return;
+  if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
   const int64_t at = q.start + j;
   const T* row = is_draft ? reinterpret_cast<const T*>(a.draft) + at * a.ld_draft
                           : reinterpret_cast<const T*>(a.target) + (at + b) * a.ld_target;
@@ -264,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_rows(const Args a) {
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) m = max_nan(m, sh.warp_top[w]);
   if (a.cluster > 1) {
+    cluster_wait();
     if (tid < a.cluster) put_remote(&sh.top[rank], tid, (unsigned long long)__float_as_uint(m));
     cluster_sync();
     for (int i = 0; i < a.cluster; ++i) m = max_nan(m, __uint_as_float((uint32_t)sh.top[i]));
@@ -370,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank();
   const int64_t b = blockIdx.x / a.cluster;
+  if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
   wait_for_previous();
   const Request q = request(a, b);
   const bool greedy = q.c == 0.f;
@@ -422,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     }
   }
   __syncthreads();
+  if (a.cluster > 1) cluster_wait();
   const int accepted = s_accepted;
   const int64_t at = q.start + accepted;
   RowStat sp{};

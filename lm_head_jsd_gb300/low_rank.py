@@ -1,0 +1,98 @@
+"""Low-rank adapters of many requests on the output of a shared projection (the C entry
+point fljsd_low_rank_add)."""
+from __future__ import annotations
+
+import torch
+from torch.autograd.graph import increment_version
+
+from . import _lib
+from ._streams import check_status, hand_over, on, report, require_cuda
+from .api import _DT
+
+
+def check_rows(name, t):
+    """The row stride of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or 0 in t.shape:
+        raise ValueError(f"{name} must be a matrix")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _span(t):
+    """The addresses that a matrix's elements lie in."""
+    size = t.element_size()
+    return t.data_ptr(), t.data_ptr() + size * ((t.shape[0] - 1) * t.stride(0) + t.shape[1])
+
+
+def check_adapters(x, n, a, b, index, scales):
+    """That adapters fit x [tokens, k] and an output of n columns; their (number, rank)."""
+    (tokens, k), dev = x.shape, x.device
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"x has dtype {x.dtype}, adapters expect torch.bfloat16")
+    if not isinstance(a, torch.Tensor) or a.dim() != 3 or a.shape[0] == 0 or a.shape[1] == 0:
+        raise ValueError("a must be [adapters, rank, k]")
+    count, rank = a.shape[:2]
+    if rank % 8:
+        raise ValueError(f"the rank is {rank}, expected a multiple of 8 (pad a and b with zeros)")
+    for name, t, shape in (("a", a, (count, rank, k)), ("b", b, (count, n, rank))):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != shape
+                or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous torch.bfloat16 tensor {list(shape)} on {dev}")
+    for name, t, dt, shape in (("index", index, torch.int64, (tokens,)), ("scales", scales, torch.float32, (count,))):
+        if t is None and name == "scales":
+            continue
+        if (not isinstance(t, torch.Tensor) or t.dtype != dt or tuple(t.shape) != shape
+                or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on {dev}")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, a, b, scales)):
+        raise ValueError("an input requires a gradient, which adapters here do not give: detach it")
+    return count, rank
+
+
+def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, stream=None):
+    """y + scales[i] b[i] (a[i] x) for each token, i = index of the token (int64 [tokens]; -1:
+    y as it is). y [tokens, n] fp32 or bf16, x [tokens, k] bf16, a [adapters, rank, k] and
+    b [adapters, n, rank] bf16 with a rank that is a multiple of 8 up to 128, scales fp32
+    [adapters] or None (1). ``out``: receives the result, y itself or a tensor like it that
+    shares no memory with any input. For serving: carries no gradient, and an input that
+    would need one is refused. ``status``: an int32 on the device that receives the call's
+    status word (0, FLJSD_ERR_INVALID_ARG for an index out of range, which counts as -1, or
+    FLJSD_ERR_TIMEOUT)."""
+    ldy = check_rows("y", y)
+    ldx = check_rows("x", x)
+    (tokens, n), dev = y.shape, y.device
+    require_cuda("y", y)
+    if y.dtype not in _DT:
+        raise ValueError(f"y has dtype {y.dtype}, expected one of {list(_DT)}")
+    if x.shape[0] != tokens or x.device != dev:
+        raise ValueError(f"x must have {tokens} rows on {dev}")
+    count, rank = check_adapters(x, n, a, b, index, scales)
+    if torch.is_grad_enabled() and y.requires_grad:
+        raise ValueError("y requires a gradient, which low_rank_add does not give: detach it")
+    check_status(status, dev)
+    if out is not None:
+        if (not isinstance(out, torch.Tensor) or out.dtype != y.dtype or tuple(out.shape) != (tokens, n)
+                or out.device != dev):
+            raise ValueError(f"out must be {y.dtype} [{tokens}, {n}] on {dev}")
+        check_rows("out", out)
+        lo, hi = _span(out)
+        same = out.data_ptr() == y.data_ptr() and out.stride(0) == y.stride(0)
+        for name, t in (("x", x),) if same else (("y", y), ("x", x)):
+            begin, end = _span(t)
+            if begin < hi and lo < end:
+                raise ValueError(f"out shares memory with {name}")
+    with on(stream, dev):
+        r = out if out is not None else torch.empty((tokens, n), dtype=y.dtype, device=dev)
+        ws = torch.empty(_lib.fljsd_low_rank_workspace_bytes(tokens, count, rank), dtype=torch.uint8, device=dev)
+        _lib.fljsd_low_rank_add(tokens, x.shape[1], n, rank, count, x, ldx, a, b, index, scales, _DT[y.dtype],
+                                y, ldy, r, check_rows("out", r), ws)
+        report(status, ws)
+    if out is None:
+        hand_over((r,), stream, dev)
+    else:  # autograd's own check of what it saved: this has changed
+        increment_version(out)
+    return r
+
+
+__all__ = ["low_rank_add"]
