@@ -32,19 +32,25 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int kRowCtas = 3;    // of k_verify_rows on an SM
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kKept = 8;       // vectors of 16 bytes that one of them keeps of a row
 constexpr int64_t kMaxV = 1 << 20;  // sums of [w] stay below 2^63
 constexpr double kUnit = 0x1p43;
 constexpr float kC1 = 12.f, kC2 = 0x1.8p-20f;
 constexpr uint32_t kBits1 = 0x41400000u, kBits2 = 0x35c00000u;
 constexpr unsigned long long kNone = ~0ull;
+constexpr double kLog2e = 1.4426950408889634;
+constexpr float kLeastT = 0x1.7154780000000p-128f;  // the least T with a finite log2(e) / T in fp32
 
 enum { kRowOk = 0, kRowBad = 1 };  // bad: NaN, +inf, or nothing but -inf
 
 struct RowStat {
+  double p;   // of the drafted token
   float m;    // largest logit
-  float wd;   // the drafted token's weight
-  unsigned long long total;
+  float inv;  // 1 / total
+  float c;    // log2(e) / T
   int best;   // the first largest (greedy), -1: none
   int state;
 };
@@ -58,7 +64,7 @@ struct Args {
   const float* u_draw;
   const int64_t* offsets;  // [requests + 1] or null
   const float* temperature;  // [requests] or null
-  float t;
+  float t, c;
   int64_t n, requests, v;
   int max_drafts, slots, cluster;
   int64_t* out;
@@ -103,10 +109,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// A double is never divided here but by one lane: an SM has two units for doubles.
 struct Request {
   int64_t start;
   int drafts;
-  float c;  // log2(e) / T; 0: greedy
+  float t;
   bool ok;
 };
 __device__ __forceinline__ Request request(const Args& a, int64_t b) {
@@ -119,10 +126,9 @@ __device__ __forceinline__ Request request(const Args& a, int64_t b) {
     r.start = b * a.max_drafts;
     end = r.start + a.max_drafts;
   }
-  const float t = a.temperature ? a.temperature[b] : a.t;
-  r.c = t == 0.f ? 0.f : (float)(1.4426950408889634 / (double)t);
-  r.ok = r.start >= 0 && r.start <= end && end <= a.n && end - r.start <= a.max_drafts && t >= 0.f &&
-         t < INFINITY && r.c < INFINITY;
+  r.t = a.temperature ? a.temperature[b] : a.t;
+  r.ok = r.start >= 0 && r.start <= end && end <= a.n && end - r.start <= a.max_drafts &&
+         (r.t == 0.f || (r.t >= kLeastT && r.t < INFINITY));
   r.drafts = r.ok ? (int)(end - r.start) : 0;
   return r;
 }
@@ -169,12 +175,17 @@ __device__ __forceinline__ void values(const uint4& q, float2 (&z)[Vec<T>::N / 2
 }
 // The largest of a vector; a NaN stays.
 template <typename T>
-__device__ __forceinline__ float largest(const uint4& q, float m) {
-  float2 z[Vec<T>::N / 2];
-  values<T>(q, z);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::N / 2; ++i) m = max_nan(m, max_nan(z[i].x, z[i].y));
-  return m;
+__device__ __forceinline__ float largest(const uint4& q, float m);
+template <>
+__device__ __forceinline__ float largest<float>(const uint4& q, float m) {
+  return max_nan(max_nan(m, max_nan(__uint_as_float(q.x), __uint_as_float(q.y))),
+                 max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+}
+template <>
+__device__ __forceinline__ float largest<__nv_bfloat16>(const uint4& q, float m) {
+  auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  const __nv_bfloat162 x = __hmax2_nan(__hmax2_nan(two(q.x), two(q.y)), __hmax2_nan(two(q.z), two(q.w)));
+  return max_nan(m, max_nan(__low2float(x), __high2float(x)));
 }
 
 // Two weights relative to m.
@@ -204,15 +215,13 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-
-// What a cluster's CTAs tell each other.
-struct Shared {
-  unsigned long long top[kMaxCluster];   // their maxima
-  unsigned long long sum[kMaxCluster];
-  unsigned long long best[kMaxCluster];
-  unsigned long long warp[kWarps];
-  float warp_top[kWarps];
-};
+// The warp's, of counts of up to 64 values each: |hi| < 2^27, |lo| < 2^28 a thread.
+__device__ __forceinline__ unsigned long long warp_sum(const Count& c, uint32_t n) {
+  const int hi = (int)(c.hi - n * kBits1), lo = (int)(c.lo - n * kBits2);
+  const int h = __reduce_add_sync(0xffffffffu, hi);
+  const int l1 = __reduce_add_sync(0xffffffffu, lo >> 12), l0 = __reduce_add_sync(0xffffffffu, lo & 0xfff);
+  return ((unsigned long long)(uint32_t)h << 23) + ((long long)l1 << 12) + l0;
+}
 
 // Where a row lies: vectors [first, last) of N columns, the first one from the 16-byte
 // boundary at or before the row's start; column j of vector k is k N - lead.
@@ -222,126 +231,420 @@ struct Cut {
   __device__ __forceinline__ Cut(const T* row, int64_t v, int cluster, int rank) {
     lead = (int)(((uintptr_t)row & 15u) / sizeof(T));
     const int all = (int)((v + lead + Vec<T>::N - 1) / Vec<T>::N);
-    const int per = (all + cluster - 1) / cluster;
+    const int per = (all + cluster - 1) >> (31 - __clz(cluster));  // (a power of two)
     first = min(rank * per, all);
     last = min(first + per, all);
   }
 };
 
+// A row that k_verify_rows is to take.
+struct Row {
+  const void* z;  // null: none
+  float c;        // 0: greedy
+  bool is_draft;
+  int64_t stat;   // where the results go
+  int64_t at;     // the drafted token in question, -1 behind the last
+};
 template <typename T>
-constexpr int kept() {  // vectors a thread keeps: 32 columns
-  return 32 / Vec<T>::N;
+__device__ __forceinline__ Row row_of(const Args& a, int64_t unit) {
+  Row r{};
+  const int b = (int)((uint32_t)unit / (uint32_t)a.slots);  // (fewer than 2^31)
+  const int slot = (int)unit - b * a.slots;
+  const Request q = request(a, b);
+  r.is_draft = slot > a.max_drafts;
+  const int j = r.is_draft ? slot - a.max_drafts - 1 : slot;
+  if (!q.ok || j >= q.drafts + (r.is_draft ? 0 : 1) || (r.is_draft && q.t == 0.f)) return r;
+  r.c = q.t == 0.f ? 0.f : a.temperature ? (float)(kLog2e / (double)q.t) : a.c;
+  r.at = j < q.drafts ? q.start + j : -1;
+  r.stat = r.is_draft ? q.start + j : q.start + j + b;
+  r.z = r.is_draft ? reinterpret_cast<const T*>(a.draft) + r.stat * a.ld_draft
+                   : reinterpret_cast<const T*>(a.target) + r.stat * a.ld_target;
+  return r;
 }
 
+// A CTA's part of a row: n vectors, column j0 at its start.
+struct Part {
+  const void* z;  // the row, null: none
+  int64_t j0;
+  int n;
+  float c;
+};
+constexpr int kRing = 4, kTopRing = 8;
+constexpr unsigned long long kWaitNs = 4ull * 1000 * 1000 * 1000;
+struct RowsShared {  // by the row's number
+  unsigned long long full[2], empty[2];       // a row's copy has landed; it has moved on to registers
+  unsigned long long tops[kTopRing], sums[kRing];  // the cluster's have arrived
+  unsigned long long sum[kRing][kMaxCluster * kRowWarps];  // (at the first CTA)
+  float top[kTopRing][kMaxCluster * kRowWarps];            // of the cluster's warps
+  Part part[kRing];
+  struct {  // the control warp's
+    Row row;
+    float zd, m;  // the drafted token's logit, and the row's largest
+  } own[kRing];
+  volatile int abort;
+};
+
+__device__ __forceinline__ uint32_t at_shared(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t at_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at_shared(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_init(const void* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at_shared(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(const void* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(at_shared(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(const void* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(at_shared(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// With a limit, after which the CTA's waits all end and the call's status word says so.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (uint32_t it = 0;; ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort) return false;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t - t0 > kWaitNs) {
+        *abort = 1;
+        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+// (by whole warps: all go on, or none)
+__device__ __forceinline__ bool bar_wait(const void* bar, uint32_t parity, volatile int* abort, int* status) {
+  const uint32_t b = at_shared(bar);
+  bool ok = bar_try(b, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    if (!ok) ok = bar_wait_long(b, parity, abort, status);
+    ok = __all_sync(0xffffffffu, ok) != 0;
+  } else {
+    ok = true;
+  }
+  return ok;
+}
+// Values to another CTA of the cluster, counted by a barrier there.
+__device__ __forceinline__ void send(const float* to, const void* bar, uint32_t rank, float x) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at_cta(to, rank)),
+               "r"(__float_as_uint(x)), "r"(at_cta(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void send(const unsigned long long* to, const void* bar, uint32_t rank, unsigned long long x) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at_cta(to, rank)),
+               "l"(x), "r"(at_cta(bar, rank))
+               : "memory");
+}
+
+// Clusters that stay, a row after the other. A warp of its own finds the rows and has their
+// parts copied to shared memory, two ahead; row i moves on to registers before row i + 2
+// takes its place. Every warp sends what it finds to all CTAs (its maximum) or to the first
+// one (its sum); row i + 1's maximum is sent before row i's is waited for, so nobody waits
+// for what is only just on its way.
+// A place is written again when its last reader is done. Nobody sends row i's maximum
+// without having those of row i - 2 from all CTAs, and none of these comes from a CTA whose
+// control warp has not had that row copied. So by the time of row i + 8's maxima every
+// control warp has had row i + 6 copied, two iterations after it has read row i's, and
+// every other warp has read them before it sent row i + 2's; and by the time of row
+// i + 4's sums the first CTA's control warp has had row i + 4 copied, after it has written
+// row i's.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_verify_rows(const Args a) {
-  constexpr int N = Vec<T>::N, R = kept<T>();
-  __shared__ Shared sh;
+__global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(const Args a) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(128) uint4 s_rows[];  // [2][kKept * kRowThreads]
+  __shared__ __align__(16) RowsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank();
-  const int64_t unit = blockIdx.x / a.cluster, b = unit / a.slots;
-  const int slot = (int)(unit % a.slots);
   let_next_launch();
   if (blockIdx.x == 0 && tid == 0) *a.status = 0;
-  const Request q = request(a, b);
-  const bool is_draft = slot > a.max_drafts;
-  const int j = is_draft ? slot - a.max_drafts - 1 : slot;
-  if (!q.ok || j >= q.drafts + (is_draft ? 0 : 1) || (is_draft && q.c == 0.f)) return;
-  if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
-  const int64_t at = q.start + j;
-  const T* row = is_draft ? reinterpret_cast<const T*>(a.draft) + at * a.ld_draft
-                          : reinterpret_cast<const T*>(a.target) + (at + b) * a.ld_target;
-  const Cut<T> cut(row, a.v, a.cluster, rank);
-  auto column = [&](int k) { return (int64_t)k * N - cut.lead; };
-  uint4 raw[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int k = cut.first + r * kThreads + tid;
-    raw[r] = load(row, k < cut.last ? column(k) : a.v, a.v, true);
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int r = 0; r < R; ++r) m = largest<T>(raw[r], m);
-  for (int k = cut.first + R * kThreads + tid; k < cut.last; k += kThreads)
-    m = largest<T>(load(row, column(k), a.v, true), m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sh.warp_top[warp] = m;
-  __syncthreads();
-  m = sh.warp_top[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) m = max_nan(m, sh.warp_top[w]);
-  if (a.cluster > 1) {
-    cluster_wait();
-    if (tid < a.cluster) put_remote(&sh.top[rank], tid, (unsigned long long)__float_as_uint(m));
-    cluster_sync();
-    for (int i = 0; i < a.cluster; ++i) m = max_nan(m, __uint_as_float((uint32_t)sh.top[i]));
-  }
-  const bool bad = !(fabsf(m) < INFINITY);
-  unsigned long long sum = 0, best = kNone;
-  if (!bad && q.c != 0.f) {
-    Count n;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float2 z[N / 2];
-      values<T>(raw[r], z);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) n.add(weights(z[i], m, q.c));
-    }
-    sum = n.sum(R * N);
-    for (int k = cut.first + R * kThreads + tid; k < cut.last; k += kThreads) {
-      float2 z[N / 2];
-      values<T>(load(row, column(k), a.v, true), z);
-      Count more;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) more.add(weights(z[i], m, q.c));
-      sum += more.sum(N);
-    }
-    sum = warp_sum(sum);
-  } else if (!bad) {
-    auto look = [&](const uint4& x, int64_t j0) {
-      float2 z[N / 2];
-      values<T>(x, z);
-#pragma unroll
-      for (int i = N / 2 - 1; i >= 0; --i) {
-        if (z[i].y == m) best = min(best, (unsigned long long)(j0 + 2 * i + 1));
-        if (z[i].x == m) best = min(best, (unsigned long long)(j0 + 2 * i));
-      }
-    };
-#pragma unroll
-    for (int r = 0; r < R; ++r) look(raw[r], column(cut.first + r * kThreads + tid));
-    for (int k = cut.first + R * kThreads + tid; k < cut.last; k += kThreads)
-      look(load(row, column(k), a.v, true), column(k));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-    sum = best;  // (what the warps hand over)
-  }
-  if (lane == 0) sh.warp[warp] = sum;
-  __syncthreads();
-  const bool greedy = q.c == 0.f;
   if (tid == 0) {
-    sum = sh.warp[0];
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sh.full[i], 1);
+      bar_init(&sh.empty[i], kRowWarps);
+    }
+    for (int i = 0; i < kTopRing; ++i) bar_init(&sh.tops[i], 1);
+    for (int i = 0; i < kRing; ++i) bar_init(&sh.sums[i], 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_sync();
+  auto part_of = [&](int i) -> const Part& { return sh.part[i % kRing]; };
+  auto top_of = [&](int i) {
+    float m = -INFINITY;
+    for (int e = lane; e < a.cluster * kRowWarps; e += 32) m = max_nan(m, sh.top[i % kTopRing][e]);
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
+    return m;
+  };
+  auto has_tops = [&](int i) { return bar_wait(&sh.tops[i % kTopRing], (i / kTopRing) & 1, &sh.abort, a.status); };
+  if (warp == kRowWarps) {  // ---------------- control ----------------
+    // Rows are looked for 32 units at a time, a lane to each.
+    const uint32_t units = (uint32_t)(a.requests * a.slots), step = gridDim.x / a.cluster;
+    uint32_t first_unit = blockIdx.x / a.cluster, found = 0;  // lanes whose row is still to come
+    Row mine{};
+    int64_t mine_j0 = 0;
+    int mine_n = 0, src = 0;
+    float mine_zd = -INFINITY;
+    bool looked_up = false;
+    auto look_up = [&]() {  // the drafted tokens' logits
+      if (looked_up) return;
+      if (rank == 0 && mine.z && mine.at >= 0) {
+        const int64_t d = a.tokens[mine.at];
+        if (d >= 0 && d < a.v) mine_zd = value_at(reinterpret_cast<const T*>(mine.z) + d);
+      }
+      looked_up = true;
+    };
+    auto keep_zd = [&](int j, int lane_of) {
+      look_up();
+      const float zd = __shfl_sync(0xffffffffu, mine_zd, lane_of);
+      if (lane == 0) sh.own[j % kRing].zd = zd;
+    };
+    bool waiting = false;  // row 0's logit is not looked up yet: the first copies go before it
+    int src_first = 0;
+    auto catch_up = [&]() {
+      if (waiting) keep_zd(0, src_first);
+      waiting = false;
+    };
+    auto next_row = [&]() {
+      while (!found && first_unit < units) {
+        catch_up();
+        const uint64_t unit = first_unit + (uint64_t)lane * step;
+        mine = unit < units ? row_of<T>(a, (int64_t)unit) : Row{};
+        if (mine.z) {
+          const Cut<T> cut(reinterpret_cast<const T*>(mine.z), a.v, a.cluster, rank);
+          mine_j0 = (int64_t)cut.first * N - cut.lead;
+          mine_n = cut.last - cut.first;
+        }
+        mine_zd = -INFINITY;
+        looked_up = false;
+        found = __ballot_sync(0xffffffffu, mine.z != nullptr);
+        const uint64_t on = first_unit + 32ull * step;
+        first_unit = on < units ? (uint32_t)on : units;
+      }
+      if (!found) return false;
+      src = __ffs(found) - 1;
+      found &= found - 1;
+      return true;
+    };
+    // row j into its place; false: there is none
+    auto bring = [&](int j, bool& ok) {
+      const bool there = next_row();
+      if (j >= 2) ok = bar_wait(&sh.empty[j & 1], ((j >> 1) & 1) ^ 1, &sh.abort, a.status) && ok;
+      Part q{};
+      if (there) {
+        q.z = reinterpret_cast<const void*>(__shfl_sync(0xffffffffu, (unsigned long long)mine.z, src));
+        q.j0 = __shfl_sync(0xffffffffu, mine_j0, src);
+        q.n = __shfl_sync(0xffffffffu, mine_n, src);
+        q.c = __shfl_sync(0xffffffffu, mine.c, src);
+        const T* z = reinterpret_cast<const T*>(q.z);
+        const int lo = q.n > 0 && q.j0 < 0 ? 1 : 0;
+        const int most = kKept * kRowThreads;
+        int hi = max(lo, q.n > 0 && q.j0 + (int64_t)q.n * N > a.v ? q.n - 1 : q.n);
+        hi = min(hi, most);
+        uint4* to = s_rows + (j & 1) * most;
+        const uint32_t bytes = (uint32_t)(hi - lo) * 16;
+        if (lane == 0 && bytes) {  // (counted below: the row is not there before that)
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  at_shared(to + lo)),
+              "l"(z + q.j0 + (int64_t)lo * N), "r"(bytes), "r"(at_shared(&sh.full[j & 1]))
+              : "memory");
+        }
+        // what is not copied whole: the vectors at the row's ends, and places that stay empty
+        if (lane < lo) to[lane] = load(z, q.j0, a.v, false);
+        constexpr uint32_t w = Vec<T>::kMasked | (sizeof(T) == 4 ? 0u : Vec<T>::kMasked << 16);
+        for (int k = hi + lane; k < most; k += 32)
+          to[k] = k < q.n ? load(z, q.j0 + (int64_t)k * N, a.v, false) : make_uint4(w, w, w, w);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          sh.part[j % kRing] = q;
+          bar_expect(&sh.full[j & 1], bytes);
+          bar_expect(&sh.tops[j % kTopRing], a.cluster * kRowWarps * 4);
+          if (rank == 0) bar_expect(&sh.sums[j % kRing], a.cluster * kRowWarps * 8);
+        }
+        if (lane == src) sh.own[j % kRing].row = mine;
+        if (j == 0) {
+          src_first = src;
+          waiting = true;
+        } else {
+          catch_up();
+          keep_zd(j, src);
+        }
+      } else if (lane == 0) {
+        sh.part[j % kRing] = q;
+        bar_arrive(&sh.full[j & 1]);
+      }
+      __syncwarp();
+      return there;
+    };
+    // what row i leaves to be written
+    auto finish = [&](int i) {
+      if (!bar_wait(&sh.sums[i % kRing], (i / kRing) & 1, &sh.abort, a.status)) return;
+      const auto& own = sh.own[i % kRing];
+      const bool greedy = own.row.c == 0.f;
+      unsigned long long sum = greedy ? kNone : 0ull;
+      for (int e = lane; e < a.cluster * kRowWarps; e += 32) {
+        const unsigned long long x = sh.sum[i % kRing][e];
+        sum = greedy ? min(sum, x) : sum + x;
+      }
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum = greedy ? min(sum, sh.warp[w]) : sum + sh.warp[w];
-    if (a.cluster > 1) put_remote(&sh.sum[rank], 0, sum);
-  }
-  if (a.cluster > 1) cluster_sync();
-  if (rank == 0 && tid == 0) {
-    if (a.cluster > 1) {
-      sum = sh.sum[0];
-      for (int i = 1; i < a.cluster; ++i) sum = greedy ? min(sum, sh.sum[i]) : sum + sh.sum[i];
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long x = __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = greedy ? min(sum, x) : sum + x;
+      }
+      RowStat s{0.0, own.m, 0.f, own.row.c, -1, fabsf(own.m) < INFINITY ? kRowOk : kRowBad};
+      if (s.state == kRowOk && greedy) s.best = (int)sum;
+      if (s.state == kRowOk && !greedy) {
+        // two quotients at once, a lane to each
+        const double wd = (double)ex2(__fmul_rn(__fsub_rn(own.zd, own.m), own.row.c));
+        const double q = (lane == 0 ? wd : 1.0) / ((double)sum / kUnit);
+        s.p = q;
+        s.inv = (float)__shfl_sync(0xffffffffu, q, 1);
+      }
+      if (lane == 0) (own.row.is_draft ? a.stat_d : a.stat_t)[own.row.stat] = s;
+    };
+    bool ok = true;
+    bool here = bring(0, ok), next = here && bring(1, ok);
+    catch_up();
+    int i = 0, brought = here ? 2 : 1;
+    for (; here && ok; ++i) {
+      const bool after = next && bring(i + 2, ok);
+      brought += next;
+      if (rank == 0 && i > 0) finish(i - 1);
+      ok = has_tops(i) && ok;
+      const float m = top_of(i);
+      if (lane == 0) sh.own[i % kRing].m = m;
+      __syncwarp();
+      here = next;
+      next = after;
     }
-    RowStat s{m, 0.f, sum, -1, bad ? kRowBad : kRowOk};
-    if (!bad && greedy) s.best = (int)sum;
-    if (!bad && !greedy && j < q.drafts) {
-      const int64_t d = a.tokens[at];
-      if (d >= 0 && d < a.v) s.wd = ex2(__fmul_rn(__fsub_rn(value_at(row + d), m), q.c));
+    if (rank == 0 && i > 0) finish(i - 1);
+    for (int j = max(0, brought - 2); j < brought; ++j)  // no copy is under way at the end
+      for (int it = 0; it < (1 << 22) && !bar_try(at_shared(&sh.full[j & 1]), (j >> 1) & 1); ++it) {
+      }
+  } else {  // ---------------- columns ----------------
+    auto rest = [&](const Part& q, auto&& f) {  // vectors beyond those kept, read again
+      for (int k = kKept * kRowThreads + tid; k < q.n; k += kRowThreads)
+        f(load(reinterpret_cast<const T*>(q.z), q.j0 + (int64_t)k * N, a.v, true), k);
+    };
+    // whether there is a row i, whose maximum is sent
+    auto send_top = [&](int i) {
+      if (!bar_wait(&sh.full[i & 1], (i >> 1) & 1, &sh.abort, a.status)) return false;
+      const Part& q = part_of(i);
+      if (!q.z) return false;
+      const uint4* mine = s_rows + (i & 1) * kKept * kRowThreads + tid;
+      float m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) m = largest<T>(mine[k * kRowThreads], m);
+      if (q.n > kKept * kRowThreads) rest(q, [&](const uint4& x, int) { m = largest<T>(x, m); });
+      asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
+      if (lane < a.cluster)
+        send(&sh.top[i % kTopRing][rank * kRowWarps + warp], &sh.tops[i % kTopRing], lane, m);
+      return true;
+    };
+    bool here = send_top(0);
+    for (int i = 0; here; ++i) {
+      uint4 raw[kKept];
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) raw[k] = s_rows[((i & 1) * kKept + k) * kRowThreads + tid];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.empty[i & 1]);
+      here = send_top(i + 1);
+      if (!has_tops(i)) break;
+      const float m = top_of(i), c = part_of(i).c;
+      const int n_vecs = part_of(i).n;
+      const bool bad = !(fabsf(m) < INFINITY);
+      unsigned long long sum = 0;
+      if (!bad && c != 0.f) {
+        Count n;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) {
+          float2 x[N / 2];
+          values<T>(raw[k], x);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) n.add(weights(x[e], m, c));
+        }
+        sum = warp_sum(n, kKept * N);
+        if (n_vecs > kKept * kRowThreads) {
+          unsigned long long more = 0;
+          rest(part_of(i), [&](const uint4& q, int) {
+            float2 x[N / 2];
+            values<T>(q, x);
+            Count n;
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) n.add(weights(x[e], m, c));
+            more += n.sum(N);
+          });
+          sum += warp_sum(more);
+        }
+      } else if (!bad) {
+        sum = kNone;
+        const int64_t j0 = part_of(i).j0;
+        auto look = [&](const uint4& q, int k) {
+          float2 x[N / 2];
+          values<T>(q, x);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) {
+            if (x[e].x == m) sum = min(sum, (unsigned long long)(j0 + (int64_t)k * N + 2 * e));
+            if (x[e].y == m) sum = min(sum, (unsigned long long)(j0 + (int64_t)k * N + 2 * e + 1));
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) look(raw[k], k * kRowThreads + tid);
+        rest(part_of(i), look);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum = min(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+      }
+      if (lane == 0) send(&sh.sum[i % kRing][rank * kRowWarps + warp], &sh.sums[i % kRing], 0, sum);
     }
-    (is_draft ? a.stat_d[at] : a.stat_t[at + b]) = s;
   }
+  cluster_sync();  // no CTA leaves while another sends to it
 }
 
-// The whole numbers of one vector of p, or of p - q.
+// Columns [j, j + N) of a row that lies to 16 bytes otherwise than j does: from the two
+// aligned vectors that hold them, where both lie within the row.
+template <typename T>
+__device__ __forceinline__ uint4 load_apart(const T* row, int64_t j, int64_t v) {
+  constexpr int N = Vec<T>::N;
+  if (j < N || j + 2 * N > v) return load(row, j, v, false);
+  const uintptr_t at = (uintptr_t)(row + j);
+  const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+  const uint4 lo = q[0], hi = q[1];
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const int words = (int)(at & 15u) / 4, bits = (int)(at & 3u) * 8;
+  uint4 r;
+  auto pick = [&](int o) {
+    r.x = __funnelshift_r(w[o], w[o + 1], bits);
+    r.y = __funnelshift_r(w[o + 1], w[o + 2], bits);
+    r.z = __funnelshift_r(w[o + 2], w[o + 3], bits);
+    r.w = __funnelshift_r(w[o + 3], w[o + 4 < 8 ? o + 4 : 7], bits);
+  };
+  switch (words) {  // (the same in the whole row)
+    case 0: pick(0); break;
+    case 1: pick(1); break;
+    case 2: pick(2); break;
+    default: pick(3); break;
+  }
+  return r;
+}
+
+// What the next token is drawn from: p, or p - q.
 template <typename T>
 struct Residual {
   const T* p;
@@ -349,11 +652,20 @@ struct Residual {
   float mp, mq, c, ip, iq;
   int64_t v, without;  // a column whose q is 1, or -1
   bool q_whole;        // q lies to 16 bytes as p does
-  __device__ __forceinline__ void get(int64_t j, float2 (&r)[Vec<T>::N / 2]) const {
+  struct Raw {
+    uint4 p, q;
+  };
+  __device__ __forceinline__ Raw fetch(int64_t j) const {
+    Raw r;
+    r.p = load(p, j, v, true);
+    r.q = q ? q_whole ? load(q, j, v, true) : load_apart(q, j, v) : r.p;
+    return r;
+  }
+  __device__ __forceinline__ void get(const Raw& raw, int64_t j, float2 (&r)[Vec<T>::N / 2]) const {
     constexpr int N = Vec<T>::N;
     float2 z[N / 2], y[N / 2];
-    values<T>(load(p, j, v, true), z);
-    if (q) values<T>(load(q, j, v, q_whole), y);
+    values<T>(raw.p, z);
+    values<T>(raw.q, y);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       r[i] = __fmul2_rn(weights(z[i], mp, c), make_float2(ip, ip));
@@ -370,11 +682,41 @@ struct Residual {
   }
 };
 
+struct DrawShared {
+  unsigned long long sum[kMaxCluster];
+  unsigned long long warp[kWarps];
+  int accepted;
+};
+constexpr int kAhead = 2;  // vectors of each row that a thread has in flight
+
+// The first of n sums (a place of its own in each lane, 32 at a time) whose running sum
+// exceeds t; `run`: the sum of those before it.
+template <typename F>
+__device__ __forceinline__ int find_sum(int n, unsigned long long t, unsigned long long& run, const F& sum_of) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const unsigned long long own = i0 + lane < n ? sum_of(i0 + lane) : 0ull;
+    unsigned long long x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t over = __ballot_sync(0xffffffffu, run + x > t);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      run += __shfl_sync(0xffffffffu, x - own, l);
+      return i0 + l;
+    }
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return 0;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   constexpr int N = Vec<T>::N;
-  __shared__ Shared sh;
-  __shared__ int s_accepted;
+  __shared__ DrawShared sh;
   extern __shared__ unsigned long long s_sums[];  // [iterations][kWarps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank();
@@ -382,41 +724,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
   wait_for_previous();
   const Request q = request(a, b);
-  const bool greedy = q.c == 0.f;
+  const bool greedy = q.t == 0.f;
   // the tests, a lane to each; every CTA of the cluster makes them
+  double pd = 0.0, qd = -1.0;  // of this lane's last test; qd < 0: refused anyway
+  int64_t mine_at = -1;
+  auto tell = [&]() {  // the probability of that test's acceptance
+    if (rank == 0 && mine_at >= 0)
+      a.prob[mine_at] = qd < 0.0    ? 0.f
+                        : qd == 0.0 ? (pd > 0.0 ? 1.f : 0.f)
+                        : pd < qd   ? (float)(pd / qd)
+                                    : 1.f;
+  };
   if (warp == 0) {
     int accepted = 0;
     bool going = true, refuse = !q.ok;
     for (int j0 = 0; j0 < q.drafts; j0 += 32) {
+      if (j0 > 0) tell();
       const int j = j0 + lane;
       bool hit = false;
+      mine_at = -1;
+      pd = 0.0;
+      qd = -1.0;
       if (j < q.drafts) {
         const int64_t at = q.start + j, d = a.tokens[at];
         const RowStat st = a.stat_t[at + b];
-        float prob = 0.f;
+        const bool drafted = a.draft && !greedy;
+        const RowStat sd = drafted ? a.stat_d[at] : RowStat{1.0, 0.f, 0.f, 0.f, 0, kRowOk};
+        const float u = a.u[at];
+        mine_at = at;
         const bool in = d >= 0 && d < a.v;
         refuse |= !in;
-        if (in && st.state == kRowOk) {
+        if (in && st.state == kRowOk && sd.state == kRowOk) {
           if (greedy) {
             hit = d == st.best;
-            prob = hit ? 1.f : 0.f;
+            pd = qd = hit ? 1.0 : -1.0;
           } else {
-            const double p = (double)st.wd / ((double)st.total / kUnit);
-            double qd = 1.0;
-            bool known = true;
-            if (a.draft) {
-              const RowStat sd = a.stat_d[at];
-              known = sd.state == kRowOk;
-              qd = known ? (double)sd.wd / ((double)sd.total / kUnit) : 1.0;
-            }
-            if (known) {
-              hit = (double)a.u[at] * qd < p;
-              const double x = qd > 0.0 ? p / qd : p > 0.0 ? 1.0 : 0.0;
-              prob = (float)(x < 1.0 ? x : 1.0);
-            }
+            pd = st.p;
+            qd = sd.p;  // (1 without draft)
+            hit = (double)u * qd < pd;
           }
         }
-        if (rank == 0) a.prob[at] = prob;
       }
       const uint32_t hits = __ballot_sync(0xffffffffu, hit);
       if (going) {
@@ -427,31 +774,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     }
     refuse = __any_sync(0xffffffffu, refuse);
     if (lane == 0) {
-      s_accepted = accepted;
+      sh.accepted = accepted;
       if (refuse && rank == 0) atomicExch(a.status, (int)FLJSD_ERR_INVALID_ARG);
     }
   }
   __syncthreads();
   if (a.cluster > 1) cluster_wait();
-  const int accepted = s_accepted;
+  const int accepted = sh.accepted;
   const int64_t at = q.start + accepted;
   RowStat sp{};
   if (q.ok) sp = a.stat_t[at + b];
   int64_t token = -1;
-  if (rank == 0 && warp == 0) {  // drafts beyond the requests' are none
-    if (b == 0 && a.offsets)
-      for (int64_t i = lane; i < a.n && i < a.offsets[0]; i += 32) a.prob[i] = 0.f;
-    if (b == a.requests - 1 && a.offsets)
-      for (int64_t i = max((int64_t)0, a.offsets[b + 1]) + lane; i < a.n; i += 32) a.prob[i] = 0.f;
-  }
   if (q.ok && greedy) {
     token = sp.best;
   } else if (q.ok && sp.state == kRowOk) {
     Residual<T> res{};
     res.p = reinterpret_cast<const T*>(a.target) + (at + b) * a.ld_target;
     res.mp = sp.m;
-    res.c = q.c;
-    res.ip = (float)(1.0 / ((double)sp.total / kUnit));
+    res.c = sp.c;
+    res.ip = sp.inv;
     res.v = a.v;
     res.without = -1;
     if (accepted < q.drafts) {
@@ -460,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
         if (sd.state == kRowOk) {
           res.q = reinterpret_cast<const T*>(a.draft) + at * a.ld_draft;
           res.mq = sd.m;
-          res.iq = (float)(1.0 / ((double)sd.total / kUnit));
+          res.iq = sd.inv;
           res.q_whole = (((uintptr_t)res.p ^ (uintptr_t)res.q) & 15u) == 0;
         }
       } else {
@@ -469,21 +810,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     }
     const Cut<T> cut(res.p, a.v, a.cluster, rank);
     const int iters = (cut.last - cut.first + kThreads - 1) / kThreads;
+    auto column = [&](int it) {  // past the row where the thread has none
+      const int k = cut.first + it * kThreads + tid;
+      return k < cut.last ? (int64_t)k * N - cut.lead : a.v;
+    };
     unsigned long long before = 0, total = 0, mine = 0;
     for (int turn = 0; turn < 2; ++turn) {
       mine = 0;
-      for (int it = 0; it < iters; ++it) {
-        const int k = cut.first + it * kThreads + tid;
-        float2 r[N / 2];
-        Count n;
-        if (k < cut.last) {
-          res.get((int64_t)k * N - cut.lead, r);
+      for (int it0 = 0; it0 < iters; it0 += kAhead) {
+        typename Residual<T>::Raw raw[kAhead];
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) n.add(r[i]);
+        for (int i = 0; i < kAhead; ++i) raw[i] = res.fetch(it0 + i < iters ? column(it0 + i) : a.v);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float2 r[N / 2];
+          res.get(raw[i], column(it0 + i), r);
+          Count n;
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) n.add(r[e]);
+          const unsigned long long s = warp_sum(n, N);
+          if (lane == 0 && it0 + i < iters) s_sums[(it0 + i) * kWarps + warp] = s;
+          mine += s;
         }
-        const unsigned long long s = warp_sum(k < cut.last ? n.sum(N) : 0ull);
-        if (lane == 0) s_sums[it * kWarps + warp] = s;
-        mine += s;
       }
       if (lane == 0) sh.warp[warp] = mine;
       __syncthreads();
@@ -491,7 +839,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mine += sh.warp[w];
       if (a.cluster > 1) {
-        if (tid < a.cluster) put_remote(&sh.sum[rank], tid, mine);
+        if (warp == 0) {
+          if (lane < a.cluster) put_remote(&sh.sum[rank], lane, mine);
+        }
         cluster_sync();
         before = total = 0;
         for (int i = 0; i < a.cluster; ++i) {
@@ -508,57 +858,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
       __syncthreads();  // (sh.warp is written again)
       if (a.cluster > 1) cluster_sync();
     }
-    const double want = (double)a.u_draw[b] * (double)total;
-    unsigned long long t = want > 0.0 ? want >= (double)total ? total - 1 : (unsigned long long)want : 0ull;
-    t = min(t, total - 1);
-    if (t >= before && t - before < mine && warp == 0) {
+    unsigned long long t = 0;
+    if (warp == 0) {
+      const double want = (double)a.u_draw[b] * (double)total;
+      t = want > 0.0 ? want >= (double)total ? total - 1 : (unsigned long long)want : 0ull;
+      t = min(t, total - 1);
+    }
+    if (warp == 0 && t >= before && t - before < mine) {
       t -= before;
-      // the warp's vectors that hold it: the first of the sums whose running sum exceeds t
+      // the warp's vectors that hold it, the lane's, the column
       unsigned long long run = 0;
-      int found = 0;
-      for (int i0 = 0; i0 < iters * kWarps; i0 += 32) {
-        const int i = i0 + lane;
-        unsigned long long x = i < iters * kWarps ? s_sums[i] : 0ull;
-        const unsigned long long own = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const uint32_t over = __ballot_sync(0xffffffffu, run + x > t);
-        if (over) {
-          const int l = __ffs(over) - 1;
-          found = i0 + l;
-          run += __shfl_sync(0xffffffffu, x - own, l);
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, x, 31);
-      }
+      const int found = find_sum(iters * kWarps, t, run, [&](int i) { return s_sums[i]; });
       const int k = cut.first + (found / kWarps) * kThreads + (found % kWarps) * 32 + lane;
-      const int64_t j0 = (int64_t)k * N - cut.lead;
+      const int64_t j0 = k < cut.last ? (int64_t)k * N - cut.lead : a.v;
+      float2 r[N / 2];
+      res.get(res.fetch(j0), j0, r);
       unsigned long long one[N], x = 0;
-      float2 r[N / 2] = {};
-      if (k < cut.last) res.get(j0, r);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         Count n;
-        n.add(make_float2(r[i].x, 0.f));
-        one[2 * i] = n.sum(2);
-        Count o;
-        o.add(make_float2(r[i].y, 0.f));
-        one[2 * i + 1] = o.sum(2);
+        n.add(make_float2(i & 1 ? r[i / 2].y : r[i / 2].x, 0.f));
+        one[i] = n.sum(2);
+        x += one[i];
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) x += one[i];
-      const unsigned long long own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t over = __ballot_sync(0xffffffffu, run + x > t);
-      if (over && lane == __ffs(over) - 1) {
-        run += x - own;
+      const int l = find_sum(32, t, run, [&](int) { return x; });
+      if (lane == l) {
         int i = 0;
 #pragma unroll
         for (int e = 0; e < N - 1; ++e) {
@@ -575,47 +899,84 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
       if (i != accepted || token != -2)
         a.out[b * (a.max_drafts + 1) + i] = i < accepted ? a.tokens[q.start + i] : i == accepted ? token : -1;
     if (tid == 0) a.accepted[b] = accepted;
+    if (warp == 0) {
+      tell();
+      // drafts before the requests' and behind them are none
+      if (b == 0 && a.offsets)
+        for (int64_t i = lane; i < a.n && i < a.offsets[0]; i += 32) a.prob[i] = 0.f;
+      if (b == a.requests - 1 && a.offsets)
+        for (int64_t i = max((int64_t)0, a.offsets[b + 1]) + lane; i < a.n; i += 32) a.prob[i] = 0.f;
+    }
   }
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
 
-// CTAs to a row: enough that its threads hold it, more where there are few rows.
-int cluster_for(int64_t v, int size, int64_t rows) {
-  const int64_t per = (int64_t)kThreads * 32;  // columns a CTA keeps
+// CTAs to a row, so that each holds `vecs` vectors of it; more where there are few rows.
+int cluster_for(int64_t v, int size, int64_t rows, int vecs) {
+  const int64_t all = (v * size + 30) / 16;  // vectors, wherever the row starts
   int c = 1;
-  while (c < kMaxCluster && c * per < v + 16 / size) c *= 2;
-  while (c < kMaxCluster && rows * c * 2 <= num_sms() && c * 4 * kThreads < v) c *= 2;
+  while (c < kMaxCluster && (int64_t)c * vecs < all) c *= 2;
+  while (c < kMaxCluster && rows * c * 2 <= num_sms() && (int64_t)c * 512 < all) c *= 2;
   return c;
+}
+
+// A kernel's launch in clusters, and how many of them the GPU holds at a time.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2] = {};
+  Launch(int threads, int cluster, size_t smem, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+template <typename K>
+cudaError_t allow(K kernel, size_t smem) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+template <typename T>
+int resident(Launch& l, int cluster) {
+  static int cached[64][kMaxCluster + 1] = {};
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && cached[dev][cluster] > 0) return cached[dev][cluster];
+  l.cfg.gridDim = dim3(cluster);
+  if (cudaOccupancyMaxActiveClusters(&n, k_verify_rows<T>, &l.cfg) != cudaSuccess || n < 1) n = 1;
+  if (dev >= 0 && dev < 64) cached[dev][cluster] = n;
+  return n;
 }
 
 template <typename T>
 cudaError_t launch(Args a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cfg.attrs = attr;
   a.slots = a.max_drafts + 1 + (a.draft ? a.max_drafts : 0);
-  a.cluster = cluster_for(a.v, sizeof(T), a.requests * a.slots);
-  attr[0].val.clusterDim = {(unsigned)a.cluster, 1, 1};
-  cfg.gridDim = dim3((unsigned)(a.requests * a.slots * a.cluster));
-  cfg.numAttrs = 1;
+  const int64_t rows = a.requests * a.slots;
+  a.cluster = cluster_for(a.v, sizeof(T), rows, kKept * kRowThreads);
+  Launch l(kRowThreads + 32, a.cluster, 2 * kKept * kRowThreads * 16, st);
+  cudaError_t e = allow(k_verify_rows<T>, l.cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t fit = resident<T>(l, a.cluster);
+  l.cfg.gridDim = dim3((unsigned)((rows < fit ? rows : fit) * a.cluster));
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_verify_rows<T>, a);
+  e = cudaLaunchKernelEx(&l.cfg, k_verify_rows<T>, a);
   trace_end(FLJSD_KERNEL_SMALL, st);
   if (e != cudaSuccess) return e;
-  a.cluster = cluster_for(a.v, sizeof(T), a.requests);
-  attr[0].val.clusterDim = {(unsigned)a.cluster, 1, 1};
-  cfg.gridDim = dim3((unsigned)(a.requests * a.cluster));
-  const int64_t vecs = (a.v + 2 * Vec<T>::N - 2) / Vec<T>::N;
+  a.cluster = cluster_for(a.v, sizeof(T), a.requests, 2 * kAhead * kThreads);
+  const int64_t vecs = (a.v * (int64_t)sizeof(T) + 30) / 16;
   const int64_t iters = ((vecs + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
-  cfg.dynamicSmemBytes = (size_t)(iters * kWarps * sizeof(unsigned long long));
-  cfg.numAttrs = 2;
+  Launch d(kThreads, a.cluster, (size_t)(iters * kWarps * sizeof(unsigned long long)), st);
+  d.cfg.gridDim = dim3((unsigned)(a.requests * a.cluster));
+  d.cfg.numAttrs = 2;
+  e = allow(k_verify_draw<T>, d.cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  e = cudaLaunchKernelEx(&cfg, k_verify_draw<T>, a);
+  e = cudaLaunchKernelEx(&d.cfg, k_verify_draw<T>, a);
   trace_end(FLJSD_KERNEL_SMALL, st);
   return e;
 }
@@ -654,8 +1015,7 @@ extern "C" fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v
     return FLJSD_ERR_INVALID_ARG;
   if ((uintptr_t)workspace & 15u) return FLJSD_ERR_INVALID_ARG;
   if (!offsets && drafts != requests * (int64_t)max_drafts) return FLJSD_ERR_INVALID_ARG;
-  if (!temperatures && (!(temperature >= 0.f) || !std::isfinite(temperature) || (temperature > 0.f && !std::isfinite(
-                                                      (float)(1.4426950408889634 / (double)temperature)))))
+  if (!temperatures && !(temperature == 0.f || (temperature >= kLeastT && std::isfinite(temperature))))
     return FLJSD_ERR_INVALID_ARG;
   if (v >= kMaxV || requests > (1 << 20) || drafts > (1 << 24) || max_drafts > 1024 ||
       requests * (2 * (int64_t)max_drafts + 1) * kMaxCluster > 0x7fffffffll)
@@ -672,6 +1032,7 @@ extern "C" fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v
   a.offsets = offsets;
   a.temperature = temperatures;
   a.t = temperature;
+  a.c = temperature > 0.f ? (float)(kLog2e / (double)temperature) : 0.f;
   a.n = drafts;
   a.requests = requests;
   a.v = v;
