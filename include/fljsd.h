@@ -603,7 +603,8 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
  * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for a dimension <= 0, a
  * stride below its row, a rank that is no multiple of 8, an unknown dtype, a null or
  * misaligned pointer, out at y's address with another stride; FLJSD_ERR_UNSUPPORTED for
- * tokens or k above 2^20, n above 2^26, rank above 128, adapters above 4096;
+ * tokens or k above 2^20, n above 2^26, rank above 128, adapters above 4096, adapters * n
+ * of 2^31 and more;
  * FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
  */
 size_t fljsd_low_rank_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank);

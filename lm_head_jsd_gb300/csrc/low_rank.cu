@@ -11,10 +11,16 @@
 //    is left (2^-16 of s at most is lost): one would be 2^-8 off, as much as bf16's own rounding.
 //  - k_lr_expand: y + B s for 256 columns at a time. Accumulator rows i of two products
 //    hold columns 2 i and 2 i + 1, so that a thread reads and writes pairs and a warp 64
-//    neighbouring columns of a token.
+//    neighbouring columns of a token. One CTA an SM: warps that copy B's rows and y's ahead,
+//    one that issues the products, and four groups of four warps, each with a ring of rows of
+//    its own (in one ring for all, a group could be a round ahead of another), that take a
+//    block each in turn and add to y where it lies in shared memory, from which it is copied out. (With y
+//    read and written by the adding threads, a pair at a time, addresses and waits took
+//    750 us of 4096 x 128256 bf16 without any product; a copy takes 306.)
 #include "dependent.cuh"
 #include "elect.cuh"
 #include "gemm_tc_kernel.cuh"
+#include "tensor_map.cuh"
 
 namespace fljsd {
 namespace {
@@ -31,10 +37,13 @@ constexpr int kThreads = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kStages = 4;
 constexpr int kXStage = kTile * 128;  // 64 tokens x 64 of k
-constexpr int kBlocks = 4;      // blocks of columns to a CTA of k_lr_expand
+constexpr int kGroups = 4;      // of k_lr_expand's epilogue
+constexpr int kExpandThreads = kGroups * 128 + 64 + kGroups * 32;
+constexpr int kMaxStages = 8;   // of B's rows
+constexpr int kMaxSlots = 16;   // places for rows of y, a ring of them to each group
 
 struct Tile {
-  int adapter, first, count;  // tokens order[first .. first + count)
+  int adapter, count;  // tokens order[number * kTile ..]
 };
 
 struct Args {
@@ -45,7 +54,8 @@ struct Args {
   const float* scales;
   const void* y;
   void* out;
-  bool vec_k, pairs, copy;
+  bool vec_k, copy, same;  // same: y's and out's rows lie to 16 bytes alike
+  int pitch, boxes, stages, s_bufs, slots, blocks;  // bytes of a row of B's boxes, boxes to it; blocks of a job
   int* status;
   int* num_tiles;
   Tile* tiles;
@@ -113,15 +123,15 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int* status)
 // nothing in their results.
 __global__ void __launch_bounds__(kPlanThreads) k_lr_plan(const Args a) {
   extern __shared__ int s_count[];  // [adapters + 1], then the places
-  __shared__ int s_warp[2][kPlanThreads / 32];
-  __shared__ int s_carry[2];
+  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int s_carry;
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = a.adapters + 1;
   int* s_place = s_count + groups;
   let_next_launch();
   for (int i = tid; i < groups; i += kPlanThreads) s_count[i] = 0;
-  if (tid == 0) s_carry[0] = s_carry[1] = s_bad = 0;
+  if (tid == 0) s_carry = s_bad = 0;
   __syncthreads();
   auto group = [&](int64_t t) {  // -1: left as it is
     const int64_t i = a.index[t];
@@ -136,41 +146,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_lr_plan(const Args a) {
   __syncthreads();
   for (int g0 = 0; g0 < groups; g0 += kPlanThreads) {
     const int g = g0 + tid, n = g < groups ? s_count[g] : 0, tiles = (n + kTile - 1) / kTile;
-    int sum = n, sum_t = tiles;  // running sums of tokens and tiles
+    int sum = tiles;  // running
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int p = __shfl_up_sync(0xffffffffu, sum, o), q = __shfl_up_sync(0xffffffffu, sum_t, o);
-      if (lane >= o) {
-        sum += p;
-        sum_t += q;
-      }
+      const int p = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += p;
     }
-    if (lane == 31) {
-      s_warp[0][warp] = sum;
-      s_warp[1][warp] = sum_t;
-    }
+    if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    int before = s_carry[0], before_t = s_carry[1];
-    for (int w = 0; w < warp; ++w) {
-      before += s_warp[0][w];
-      before_t += s_warp[1][w];
-    }
-    before += sum - n;
-    before_t += sum_t - tiles;
+    int before_t = s_carry;
+    for (int w = 0; w < warp; ++w) before_t += s_warp[w];
+    before_t += sum - tiles;
     if (g < groups) {
-      s_place[g] = before;
+      s_place[g] = before_t * kTile;
       for (int i = 0; i < tiles; ++i)
-        a.tiles[before_t + i] = Tile{g < a.adapters ? g : -1, before + i * kTile, min(kTile, n - i * kTile)};
+        a.tiles[before_t + i] = Tile{g < a.adapters ? g : -1, min(kTile, n - i * kTile)};
     }
     __syncthreads();
-    if (tid == kPlanThreads - 1) {
-      s_carry[0] = before + n;
-      s_carry[1] = before_t + tiles;
-    }
+    if (tid == kPlanThreads - 1) s_carry = before_t + tiles;
     __syncthreads();
   }
   if (tid == 0) {
-    *a.num_tiles = s_carry[1];
+    *a.num_tiles = s_carry;
     *a.status = s_bad ? (int)FLJSD_ERR_INVALID_ARG : 0;
   }
   for (int64_t t = tid; t < a.tokens; t += kPlanThreads) {
@@ -202,8 +199,8 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
   wait_for_previous();
   const int t = blockIdx.x / kSplit;
   const bool live = t < *a.num_tiles && a.tiles[t].adapter >= 0;
-  const Tile tile = live ? a.tiles[t] : Tile{0, 0, 0};
-  if (tid < tile.count) s_row[tid] = a.x + (int64_t)a.order[tile.first + tid] * a.ldx;
+  const Tile tile = live ? a.tiles[t] : Tile{0, 0};
+  if (tid < tile.count) s_row[tid] = a.x + (int64_t)a.order[(int64_t)t * kTile + tid] * a.ldx;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -315,12 +312,12 @@ struct Pair;
 template <>
 struct Pair<float> {
   using V = float2;
-  static constexpr int kTokens = 16;  // whose pairs a thread has in flight
+  static constexpr int kTokens = 8;  // whose rows share a place in shared memory
 };
 template <>
 struct Pair<__nv_bfloat16> {
   using V = uint32_t;
-  static constexpr int kTokens = 32;
+  static constexpr int kTokens = 16;
 };
 __device__ __forceinline__ float2 add_to(float2 y, float d0, float d1) { return make_float2(y.x + d0, y.y + d1); }
 __device__ __forceinline__ uint32_t add_to(uint32_t y, float d0, float d1) {
@@ -338,148 +335,402 @@ __device__ __forceinline__ void split(uint32_t v, __nv_bfloat16& a, __nv_bfloat1
   a = __ushort_as_bfloat16((unsigned short)(v & 0xffffu));
   b = __ushort_as_bfloat16((unsigned short)(v >> 16));
 }
-
-// 32 lanes x J columns of accumulators.
-template <int J>
-__device__ __forceinline__ void tmem_get(uint32_t taddr, float (&v)[J]) {
-  static_assert(J == 16 || J == 32, "columns");
-  if constexpr (J == 32) {
-    tmem_ld32(taddr, v);
-  } else {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-  }
+// Bytes of a row's place: a block's columns from the 16-byte boundary before the first.
+template <typename T>
+constexpr int row_bytes() {
+  return kCols * (int)sizeof(T) + 16;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) k_lr_expand(const Args a) {
+// 32 lanes x 8 or 16 columns of accumulators; tmem_landed before they are used.
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+}
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_landed() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+struct ExpandShared {
+  unsigned long long b_full[kMaxStages], b_empty[kMaxStages];  // a block's rows of B
+  unsigned long long s_full[2], s_empty[2];                    // a job's s
+  unsigned long long acc_full[kGroups], acc_empty[kGroups];
+  unsigned long long y_full[kMaxSlots], y_empty[kMaxSlots];    // rows of some tokens
+  uint32_t tmem;
+  volatile int abort;
+};
+// Waits with a limit, after which the CTA's all end and the call's status word says so.
+// (By whole warps. A barrier has one waiting warp or group, which waits for its every phase.)
+__device__ __forceinline__ bool wait_all(ExpandShared* sh, const void* bar, uint32_t parity, int* status) {
+  const uint32_t b = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+  const unsigned long long t0 = globaltimer();
+  bool ok = false;
+  for (uint32_t it = 0; !ok; ++it) {
+    ok = mbar_try_wait(b, parity);
+    if (!ok && (it & 63u) == 63u) {
+      if (sh->abort) break;
+      if (globaltimer() - t0 > kTimeoutNs) {
+        sh->abort = 1;
+        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Rows of B that lie in boxes of `pitch` bytes (32, 64 or 128), swizzled so far.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, int pitch) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)((8 * pitch) >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)(pitch == 32 ? 6 : pitch == 64 ? 4 : 2) << 61;
+}
+
+// Jobs are a tile with `blocks` blocks of columns, all of one tile before the next one's:
+// an adapter's B is still in L2 for its next tile, and the rows of y that are in use at a
+// time lie in few pages (all tiles of a stretch of columns first: 4096 tokens 885 us).
+// ALIGNED: all rows of y and out lie on 16 bytes, their strides and ends too. Otherwise the
+// part of a row between 16-byte boundaries is copied, and up to seven values on either side
+// are read and written one by one.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kExpandThreads, 1)
+    k_lr_expand(const __grid_constant__ CUtensorMap tm_even, const __grid_constant__ CUtensorMap tm_odd, const Args a) {
   using V = typename Pair<T>::V;
-  constexpr int J = Pair<T>::kTokens;
+  constexpr int kRow = row_bytes<T>(), kSize = (int)sizeof(T), kChunk = Pair<T>::kTokens;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ unsigned long long s_done;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_token[kTile];
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const uint32_t base = (smem_u32(smem_raw) + 127u) & ~127u;
-  const int pieces = a.rk / 8;
-  const uint32_t s_at = base, s_half = (uint32_t)kTile * a.rk * 2;  // nearest, rest
-  const uint32_t b_at = s_at + 2 * s_half, b_half = 128u * a.rk * 2;  // even columns, odd ones
+  __shared__ ExpandShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t half = 128u * a.pitch * a.boxes, stage = 2 * half;  // even columns, odd ones
+  const uint32_t s_half = (uint32_t)kTile * a.rk * 2, s_at = base + a.stages * stage;
+  const uint32_t y_at = s_at + a.s_bufs * 2 * s_half;
   if (tid == 0) {
-    mbar_init(smem_u32(&s_done), 1);
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(smem_u32(&sh.b_full[i]), 1);
+      mbar_init(smem_u32(&sh.b_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.s_empty[i]), 1);
+    }
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(smem_u32(&sh.acc_full[i]), 1);
+      mbar_init(smem_u32(&sh.acc_empty[i]), 4);
+    }
+    for (int i = 0; i < kGroups * a.slots; ++i) {
+      mbar_init(smem_u32(&sh.y_full[i]), 1);
+      mbar_init(smem_u32(&sh.y_empty[i]), 1);
+    }
+    sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tensormap(&tm_even);
+    prefetch_tensormap(&tm_odd);
   }
   wait_for_previous();
   // (only now: what it waits for needs tensor memory too)
-  if (warp == 0) tmem_alloc<false>(smem_u32(&s_tmem), 2 * kTile);
+  if (warp == 0) tmem_alloc<false>(smem_u32(&sh.tmem), kGroups * 2 * kTile);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  const int t = blockIdx.x;
-  if (t < *a.num_tiles) {
-    const Tile tile = a.tiles[t];
-    const bool adds = tile.adapter >= 0;
-    if (tid < tile.count) s_token[tid] = a.order[tile.first + tid];
-    if (adds) {
-      const char* image = a.s + (int64_t)t * kTile * a.rk * 4;
-      const int bytes16 = (int)(2 * s_half / 16);
-      for (int i = tid; i < bytes16; i += kThreads) copy16(s_at + i * 16, image + i * 16, true);
-    }
-    __syncthreads();
-    const __nv_bfloat16* B = a.b + (int64_t)(adds ? tile.adapter : 0) * a.n * a.rank;
-    const int n16 = (tile.count + 15) / 16 * 16;
-    const T* y = reinterpret_cast<const T*>(a.y);
-    T* out = reinterpret_cast<T*>(a.out);
-    int64_t block = (int64_t)blockIdx.y * kBlocks;
+  const uint32_t tmem = sh.tmem;
+  const uint32_t tiles = (uint32_t)*a.num_tiles;
+  const uint32_t num_blocks = (uint32_t)((a.n + kCols - 1) / kCols);
+  const uint32_t stretches = (num_blocks + a.blocks - 1) / a.blocks, jobs = tiles * stretches;
+  if (warp == kGroups * 4) {
+    // ---------------- copies ----------------
+    uint32_t filled = 0, s_filled = 0;
     bool ok = true;
-    for (int it = 0; it < kBlocks && block * kCols < a.n; ++it, ++block) {
-      const int64_t col0 = block * kCols;
-      if (adds) {
-        for (int i = tid; i < kCols * pieces; i += kThreads) {
-          const int row = i / pieces, piece = i % pieces;
-          const bool there = col0 + row < a.n && piece * 8 < a.rank;
-          copy16(b_at + (row & 1) * b_half + place(row >> 1, piece, pieces),
-                 there ? B + (col0 + row) * a.rank + piece * 8 : B, there);
-        }
-        copies_commit();
-        copies_wait<0>();
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-          tc_fence_after();
-          for (int h = 0; h < 2; ++h)
-            for (int part = 0; part < 2; ++part)
-              for (int kk = 0; kk < a.rk / 16; ++kk)
-                mma_bf16<false>(tmem + h * kTile, desc(b_at + h * b_half + kk * 256, pieces),
-                                desc(s_at + part * s_half + kk * 256, pieces), idesc_of(n16), part + kk > 0);
-          mma_commit<false>(smem_u32(&s_done));
+    Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
+    for (uint32_t k = blockIdx.x; ok && k < jobs; k += gridDim.x) {
+      const Tile tile = next;
+      const uint32_t t = k / stretches, b0 = k % stretches * a.blocks;
+      if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
+      if (tile.adapter < 0) continue;
+      const uint32_t si = s_filled % a.s_bufs;
+      ok = wait_all(&sh, &sh.s_empty[si], ((s_filled / a.s_bufs) & 1) ^ 1, a.status);
+      if (!ok) break;
+      if (elect_one()) {
+        const uint32_t bar = smem_u32(&sh.s_full[si]), to = s_at + si * 2 * s_half;
+        const char* image = a.s + (int64_t)t * kTile * a.rk * 4;
+        const uint32_t bytes = (uint32_t)((tile.count + 15) / 16 * 16) * a.rk * 2;
+        mbar_arrive_expect_tx(bar, 2 * bytes);
+        for (int h = 0; h < 2; ++h)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  to + h * s_half),
+              "l"(image + (int64_t)h * s_half), "r"(bytes), "r"(bar)
+              : "memory");
+      }
+      __syncwarp();
+      ++s_filled;
+      const int64_t row0 = (int64_t)tile.adapter * a.n;
+      for (uint32_t b = b0; b < b0 + a.blocks && b < num_blocks; ++b) {
+        const uint32_t st = filled % a.stages;
+        ok = wait_all(&sh, &sh.b_empty[st], ((filled / a.stages) & 1) ^ 1, a.status);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&sh.b_full[st]);
+          mbar_arrive_expect_tx(bar, stage);
+          for (int h = 0; h < 2; ++h) {
+            const int64_t row = row0 + (int64_t)b * kCols + h;
+            for (int x = 0; x < a.boxes; ++x)
+              tma_load_2d(base + st * stage + h * half + x * 128 * a.pitch, row & 1 ? &tm_odd : &tm_even, bar, x * 64,
+                          (int)(row >> 1));
+          }
         }
         __syncwarp();
+        ++filled;
       }
-      const int64_t col = col0 + 2 * tid;
-      const bool two = col + 1 < a.n, one = col < a.n;
-      for (int j0 = 0; j0 < tile.count; j0 += J) {
-        V have[J];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (j0 + j < tile.count) {
-            const T* p = y + (int64_t)s_token[j0 + j] * a.ldy + col;
-            if (a.pairs && two) {
-              have[j] = *reinterpret_cast<const V*>(p);
-            } else {
-              T lo = T(0.f), hi = T(0.f);
-              if (one) lo = p[0];
-              if (two) hi = p[1];
-              have[j] = join(lo, hi);
-            }
+    }
+    // no copy is under way at the end
+    for (uint32_t i = 0; i < (uint32_t)a.stages && i < filled; ++i) {
+      const uint32_t f = filled - 1 - i;
+      wait_all(&sh, &sh.b_full[f % a.stages], (f / a.stages) & 1, a.status);
+    }
+    for (uint32_t i = 0; i < (uint32_t)a.s_bufs && i < s_filled; ++i) {
+      const uint32_t f = s_filled - 1 - i;
+      wait_all(&sh, &sh.s_full[f % a.s_bufs], (f / a.s_bufs) & 1, a.status);
+    }
+  } else if (warp == kGroups * 4 + 1) {
+    // ---------------- products ----------------
+    uint32_t taken = 0, s_taken = 0, used = 0;  // used: a bit for each accumulator
+    bool ok = true;
+    Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
+    uint32_t last_group = kGroups;
+    for (uint32_t k = blockIdx.x, seq = 0; ok && k < jobs; k += gridDim.x, seq += a.blocks) {
+      const Tile tile = next;
+      const uint32_t b0 = k % stretches * a.blocks;
+      if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
+      if (tile.adapter < 0) continue;
+      const uint32_t si = s_taken % a.s_bufs;
+      ok = wait_all(&sh, &sh.s_full[si], (s_taken / a.s_bufs) & 1, a.status);
+      const uint32_t id = idesc_of((tile.count + 15) / 16 * 16);
+      for (uint32_t c = 0; ok && c < (uint32_t)a.blocks && b0 + c < num_blocks; ++c) {
+        const uint32_t g = (seq + c) % kGroups, st = taken % a.stages;
+        ok = wait_all(&sh, &sh.acc_empty[g], ((used >> g) & 1) ^ 1, a.status) &&
+             wait_all(&sh, &sh.b_full[st], (taken / a.stages) & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          // (one thread issues all products: their descriptors are sums of what is known)
+          const uint64_t b0d = desc_of(base + st * stage, a.pitch), s0d = desc(s_at + si * 2 * s_half, a.rk / 8);
+          const uint32_t d = tmem + g * 2 * kTile;
+#pragma unroll 1
+          for (int kk = 0; kk < a.rk / 16; ++kk) {
+            const uint64_t bd = b0d + (uint32_t)((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2), sd = s0d + kk * 16;
+            mma_bf16<false>(d, bd, sd, id, kk > 0);
+            mma_bf16<false>(d, bd, sd + (s_half >> 4), id, 1);
+            mma_bf16<false>(d + kTile, bd + (half >> 4), sd, id, kk > 0);
+            mma_bf16<false>(d + kTile, bd + (half >> 4), sd + (s_half >> 4), id, 1);
           }
+          mma_commit<false>(smem_u32(&sh.b_empty[st]));
+          mma_commit<false>(smem_u32(&sh.acc_full[g]));
+          if (c + 1 == (uint32_t)a.blocks || b0 + c + 1 == num_blocks) mma_commit<false>(smem_u32(&sh.s_empty[si]));
         }
-        if (adds) {
-          if (j0 == 0) {
-            if (ok) ok = wait(smem_u32(&s_done), it & 1, a.status);
-            ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
+        used ^= 1u << g;
+        last_group = g;
+        ++taken;
+      }
+      ++s_taken;
+    }
+    if (last_group < kGroups)  // no product runs at the end
+      wait_all(&sh, &sh.acc_full[last_group], ((used >> last_group) & 1) ^ 1, a.status);
+  } else if (warp >= kGroups * 4 + 2) {
+    // ---------------- y's rows for a group, a lane to each ----------------
+    const uint32_t g = warp - (kGroups * 4 + 2);
+    const char* y = reinterpret_cast<const char*>(a.y);
+    uint32_t filled = 0;
+    bool ok = true;
+    // The ends of rows that a copy leaves out: read now, put in place when the next place is
+    // asked for, and their place full only then. (Of a block of few columns all of it.)
+    constexpr int kEnds = ALIGNED ? 1 : 32 / kSize;
+    T kept_value[kEnds];
+    int kept = 0;
+    uint32_t kept_at = 0, open_bar = 0, open_bytes = 0;
+    auto settle = [&]() {
+      if (!open_bar) return;
+#pragma unroll
+      for (int e = 0; e < kEnds; ++e)
+        if (e < kept) *reinterpret_cast<T*>(__cvta_shared_to_generic(kept_at + e * kSize)) = kept_value[e];
+      kept = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(open_bar, open_bytes);
+      open_bar = 0;
+    };
+    auto tile_of = [&](uint32_t k) { return k < jobs ? a.tiles[k / stretches] : Tile{-1, 0}; };
+    auto token_of = [&](uint32_t k, int j) { return k < jobs ? a.order[(int64_t)(k / stretches) * kTile + j] : 0; };
+    Tile next = tile_of(blockIdx.x);
+    int next0 = token_of(blockIdx.x, lane), next1 = token_of(blockIdx.x, lane + 32);
+    for (uint32_t k = blockIdx.x, seq = 0; ok && k < jobs; k += gridDim.x, seq += a.blocks) {
+      const Tile tile = next;
+      const int t0 = next0, t1 = next1;
+      next = tile_of(k + gridDim.x);
+      next0 = token_of(k + gridDim.x, lane);
+      next1 = token_of(k + gridDim.x, lane + 32);
+      const uint32_t b0 = k % stretches * a.blocks;
+      const uint32_t left = min((uint32_t)a.blocks, num_blocks - b0);
+      for (uint32_t c = (g - seq) % kGroups; ok && c < left; c += kGroups) {
+        const int64_t col0 = (int64_t)(b0 + c) * kCols;
+        const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
+        for (int j0 = 0; j0 < tile.count; j0 += kChunk) {
+          const uint32_t slot = g * a.slots + filled % a.slots;
+          if (a.slots == 1) settle();
+          ok = wait_all(&sh, &sh.y_empty[slot], ((filled / a.slots) & 1) ^ 1, a.status);
+          if (!ok) break;
+          const int r = lane % kChunk, j = j0 + r;
+          const int token = __shfl_sync(0xffffffffu, j0 < 32 ? t0 : t1, j & 31);
+          const uintptr_t at = (uintptr_t)(y + ((int64_t)token * a.ldy + col0) * kSize);
+          const uintptr_t lo = (at + 15) & ~(uintptr_t)15, hi = (at + len) & ~(uintptr_t)15;
+          const uint32_t bytes = lane < kChunk && j < tile.count && hi > lo ? (uint32_t)(hi - lo) : 0u;
+          const uint32_t place = y_at + (slot * kChunk + r) * kRow;
+          if (bytes)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    place + (uint32_t)(lo - (at & ~(uintptr_t)15))),
+                "l"(lo), "r"(bytes), "r"(smem_u32(&sh.y_full[slot]))
+                : "memory");
+          const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+          settle();  // the one before
+          if (!ALIGNED && lane < 2 * kChunk && j < tile.count) {
+            // this lane's end of the row: what lies before the first boundary, or behind the last one
+            const uintptr_t end = at + len;
+            const uintptr_t from = lane < kChunk ? at : (hi > lo ? hi : end), to = lane < kChunk ? (hi > lo ? lo : end) : end;
+            const T* p = reinterpret_cast<const T*>(from);
+            kept = (int)((to - from) / kSize);
+            kept_at = place + (uint32_t)(from - (at & ~(uintptr_t)15));
+#pragma unroll
+            for (int e = 0; e < kEnds; ++e)
+              if (e < kept) kept_value[e] = p[e];
+          }
+          open_bar = smem_u32(&sh.y_full[slot]);
+          open_bytes = all;
+          if (ALIGNED) settle();
+          ++filled;
+        }
+      }
+    }
+    settle();
+    for (uint32_t i = 0; i < (uint32_t)a.slots && i < filled; ++i) {  // no copy is under way at the end
+      const uint32_t f = filled - 1 - i;
+      wait_all(&sh, &sh.y_full[g * a.slots + f % a.slots], (f / a.slots) & 1, a.status);
+    }
+  } else {
+    // ---------------- sums ----------------
+    const int g = warp >> 2, quarter = warp & 3;
+    const char* y = reinterpret_cast<const char*>(a.y);
+    char* out = reinterpret_cast<char*>(a.out);
+    const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + g * 2 * kTile;
+    const int mine = 2 * (quarter * 32 + lane) * kSize;  // this thread's pair in a block's row
+    uint32_t used = 0, taken = 0;
+    bool ok = true;  // (where a wait ran out, the group still meets, and leaves out as it is)
+    auto tile_of = [&](uint32_t k) { return k < jobs ? a.tiles[k / stretches] : Tile{-1, 0}; };
+    auto token_of = [&](uint32_t k, int j) { return k < jobs ? a.order[(int64_t)(k / stretches) * kTile + j] : 0; };
+    Tile next = tile_of(blockIdx.x);
+    int next0 = token_of(blockIdx.x, lane), next1 = token_of(blockIdx.x, lane + 32);
+    for (uint32_t k = blockIdx.x, seq = 0; k < jobs; k += gridDim.x, seq += a.blocks) {
+      const Tile tile = next;
+      const int t0 = next0, t1 = next1;
+      next = tile_of(k + gridDim.x);
+      next0 = token_of(k + gridDim.x, lane);
+      next1 = token_of(k + gridDim.x, lane + 32);
+      const bool adds = tile.adapter >= 0;
+      const uint32_t b0 = k % stretches * a.blocks;
+      const uint32_t left = min((uint32_t)a.blocks, num_blocks - b0);
+      const uint32_t chunks = (uint32_t)(tile.count + kChunk - 1) / kChunk;
+      // where a row starts in its place (a block is a multiple of 16 bytes)
+      const int lead0 = ALIGNED ? 0 : (int)((uintptr_t)(y + (int64_t)t0 * a.ldy * kSize) & 15u);
+      const int lead1 = ALIGNED ? 0 : (int)((uintptr_t)(y + (int64_t)t1 * a.ldy * kSize) & 15u);
+      for (uint32_t c = (g - seq) % kGroups; c < left; c += kGroups) {
+        const int64_t col0 = (int64_t)(b0 + c) * kCols;
+        const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
+        const bool ends = !a.same || mine < 16 || mine + 2 * kSize + 16 > len;  // may be such a value
+        for (uint32_t ch = 0; ch < chunks; ++ch) {
+          const uint32_t slot = g * a.slots + taken % a.slots;
+          const uint32_t rows_at = y_at + slot * kChunk * kRow;
+          const int j0 = ch * kChunk, count = min(kChunk, tile.count - j0);
+          const int held = j0 < 32 ? t0 : t1;  // (by lane j & 31)
+          const int held_lead = j0 < 32 ? lead0 : lead1;
+          if (adds && ch == 0) {
+            ok = ok && wait_all(&sh, &sh.acc_full[g], used & 1, a.status);
             tc_fence_after();
           }
-          float d0[J], d1[J];
-          const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + j0;
-          tmem_get<J>(at, d0);
-          tmem_get<J>(at + kTile, d1);
-          if (ok) {
-#pragma unroll
-            for (int j = 0; j < J; ++j) have[j] = add_to(have[j], d0[j], d1[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (j0 + j < tile.count) {
-            T* p = out + (int64_t)s_token[j0 + j] * a.ldo + col;
-            if (a.pairs && two) {
-              *reinterpret_cast<V*>(p) = have[j];
-            } else {
-              T lo, hi;
-              split(have[j], lo, hi);
-              if (one) p[0] = lo;
-              if (two) p[1] = hi;
+          uint32_t d0[kChunk], d1[kChunk];
+          if (adds) {
+            tmem_get(acc + j0, d0);
+            tmem_get(acc + kTile + j0, d1);
+            tmem_landed();
+            if (ch == chunks - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[g]));
+              ++used;
             }
           }
+          ok = ok && wait_all(&sh, &sh.y_full[slot], (taken / a.slots) & 1, a.status);
+          if (ok && (adds || !ALIGNED)) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) {
+              const int lead = ALIGNED ? 0 : __shfl_sync(0xffffffffu, held_lead, (j0 + j) & 31);
+              const int token = ALIGNED ? 0 : __shfl_sync(0xffffffffu, held, (j0 + j) & 31);
+              if (j < count) {
+                T* p = reinterpret_cast<T*>(__cvta_shared_to_generic(rows_at + j * kRow + lead + mine));
+                V v = ALIGNED ? *reinterpret_cast<const V*>(p) : join(p[0], p[1]);
+                if (adds) v = add_to(v, __uint_as_float(d0[j]), __uint_as_float(d1[j]));
+                if (ALIGNED) {
+                  *reinterpret_cast<V*>(p) = v;
+                } else {
+                  T lo, hi;
+                  split(v, lo, hi);
+                  p[0] = lo;
+                  p[1] = hi;
+                  if (ends) {  // what the copy out leaves out
+                    const int first = lead ? 16 : 0, last = (lead + len) & ~15;
+                    T* o = reinterpret_cast<T*>(out + ((int64_t)token * a.ldo + col0) * kSize + mine);
+                    auto copied = [&](int at) { return a.same && at >= first && at + kSize <= last; };
+                    if (mine < len && !copied(lead + mine)) o[0] = lo;
+                    if (mine + kSize < len && !copied(lead + mine + kSize)) o[1] = hi;
+                  }
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+          if (quarter == (int)(taken & 3)) {  // out, a lane to each row
+            if (a.same && ok) {
+              const int token = __shfl_sync(0xffffffffu, held, (j0 + lane % kChunk) & 31);
+              const uintptr_t at = (uintptr_t)(out + ((int64_t)token * a.ldo + col0) * kSize);
+              const uintptr_t lo = (at + 15) & ~(uintptr_t)15, hi = (at + len) & ~(uintptr_t)15;
+              if (lane < count && hi > lo)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(lo),
+                             "r"(rows_at + lane * kRow + (uint32_t)(lo - (at & ~(uintptr_t)15))),
+                             "r"((uint32_t)(hi - lo))
+                             : "memory");
+              bulk_commit();
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(smem_u32(&sh.y_empty[slot]));
+            __syncwarp();
+          }
+          ++taken;
         }
       }
-      tc_fence_before();
-      __syncthreads();
-      tc_fence_after();
     }
+    bulk_wait_all();
   }
+  tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc<false>(tmem, 2 * kTile);
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc<false>(tmem, kGroups * 2 * kTile);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -494,20 +745,31 @@ Layout layout(int64_t tokens, int adapters, int rank) {
   l.max_tiles = tokens / kTile + (groups < tokens ? groups : tokens);
   l.tiles = 256;  // status, number of tiles
   l.order = align_up(l.tiles + l.max_tiles * sizeof(Tile));
-  l.s = align_up(l.order + tokens * sizeof(int));
+  l.s = align_up(l.order + l.max_tiles * kTile * sizeof(int));
   l.bytes = l.s + (size_t)l.max_tiles * kTile * ((rank + 15) / 16 * 16) * 4;
   return l;
 }
 
-template <typename T>
-cudaError_t launch_expand(const Args& a, cudaStream_t st) {
-  const int smem = 128 + (2 * kTile + kCols) * a.rk * 2;
+template <typename T, bool ALIGNED>
+cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
+  const int stage = 2 * 128 * a.pitch * a.boxes, s = 2 * kTile * a.rk * 2, slot = Pair<T>::kTokens * row_bytes<T>();
+  a.s_bufs = a.rank > 64 ? 1 : 2;
+  // a third of shared memory for B's rows, the rest for y's
+  const int room = SMEM_MAX - 1024 - (int)sizeof(ExpandShared) - a.s_bufs * s;
+  a.stages = room / 3 / stage;
+  a.stages = a.stages < 2 ? 2 : a.stages > kMaxStages ? kMaxStages : a.stages;
+  a.slots = (room - a.stages * stage) / slot / kGroups;
+  if (a.slots > kMaxSlots / kGroups) a.slots = kMaxSlots / kGroups;
+  const int smem = 1024 + a.stages * stage + a.s_bufs * s + kGroups * a.slots * slot;
   cudaError_t e =
-      cudaFuncSetAttribute(k_lr_expand<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(k_lr_expand<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (a.n + kCols - 1) / kCols;
-  return launch_dependent(k_lr_expand<T>, dim3(a.max_tiles, (unsigned)((blocks + kBlocks - 1) / kBlocks)),
-                          kThreads, smem, st, a);
+  const int64_t blocks = (a.n + kCols - 1) / kCols, most = a.max_tiles * blocks, sms = num_sms();
+  // (jobs long enough to load s once for many blocks, and eight of them to each CTA)
+  a.blocks = 1;
+  while (a.blocks < 32 && most >= sms * 8 * 2 * a.blocks) a.blocks *= 2;
+  return launch_dependent(k_lr_expand<T, ALIGNED>, dim3((unsigned)(most < sms ? most : sms)), kExpandThreads, smem, st,
+                          even, odd, a);
 }
 
 }  // namespace
@@ -535,7 +797,8 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
       ((uintptr_t)scales & 3u) || (((uintptr_t)y | (uintptr_t)out) & el) || ((uintptr_t)workspace & 15u))
     return FLJSD_ERR_INVALID_ARG;
   if (y == out && ldy != ldo) return FLJSD_ERR_INVALID_ARG;
-  if (tokens > (1 << 20) || k > (1 << 20) || n > (1 << 26) || rank > kMaxRank || adapters > kMaxAdapters)
+  if (tokens > (1 << 20) || k > (1 << 20) || n > (1 << 26) || rank > kMaxRank || adapters > kMaxAdapters ||
+      adapters * n >= (int64_t)1 << 31)
     return FLJSD_ERR_UNSUPPORTED;
   const Layout l = layout(tokens, adapters, rank);
   if (workspace_bytes < l.bytes) return FLJSD_ERR_WORKSPACE;
@@ -555,13 +818,24 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   g.out = out;
   const uintptr_t size = dtype == FLJSD_BF16 ? 2 : 4;
   g.vec_k = (((uintptr_t)x | (uintptr_t)a) & 15u) == 0 && k % 8 == 0 && ldx % 8 == 0;
-  g.pairs = (((uintptr_t)y | (uintptr_t)out) & (2 * size - 1)) == 0 && ldy % 2 == 0 && ldo % 2 == 0;
+  const bool aligned = (((uintptr_t)y | (uintptr_t)out) & 15u) == 0 && ldy * size % 16 == 0 &&
+                       ldo * size % 16 == 0 && n * size % 16 == 0;
+  g.same = (((uintptr_t)y ^ (uintptr_t)out) & 15u) == 0 && (ldy - ldo) * (int64_t)size % 16 == 0;
   g.copy = y != out;
   g.status = reinterpret_cast<int*>(ws);
   g.num_tiles = g.status + 1;
   g.tiles = reinterpret_cast<Tile*>(ws + l.tiles);
   g.order = reinterpret_cast<int*>(ws + l.order);
   g.s = ws + l.s;
+  g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;
+  g.boxes = rank <= 64 ? 1 : 2;
+  // the rows of even numbers among all adapters' columns, and the odd ones
+  CUtensorMap even, odd;
+  const int64_t rows = adapters * n;
+  if (!make_tensor_map(&even, MapType::kBf16, g.b, rank, (rows + 1) / 2, 2 * rank, g.pitch / 2, 128) ||
+      !make_tensor_map(&odd, MapType::kBf16, rows > 1 ? g.b + rank : g.b, rank, rows > 1 ? rows / 2 : 1, 2 * rank,
+                       g.pitch / 2, 128))
+    return FLJSD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int plan_smem = 2 * (adapters + 1) * (int)sizeof(int);
   trace_begin(FLJSD_KERNEL_SMALL, st);
@@ -592,7 +866,10 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   trace_end(FLJSD_KERNEL_SMALL, st);
   if (e != cudaSuccess) return FLJSD_ERR_CUDA;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  e = dtype == FLJSD_BF16 ? launch_expand<__nv_bfloat16>(g, st) : launch_expand<float>(g, st);
+  if (dtype == FLJSD_BF16)
+    e = aligned ? launch_expand<__nv_bfloat16, true>(even, odd, g, st) : launch_expand<__nv_bfloat16, false>(even, odd, g, st);
+  else
+    e = aligned ? launch_expand<float, true>(even, odd, g, st) : launch_expand<float, false>(even, odd, g, st);
   trace_end(FLJSD_KERNEL_SMALL, st);
   return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
 }

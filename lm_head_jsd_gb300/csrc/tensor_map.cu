@@ -31,7 +31,10 @@ bool make_tensor_map(CUtensorMap* m, MapType type, const void* ptr, int64_t inne
   cuuint32_t estr[2] = {1, 1};
   return encode(m, t, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE,
-                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                !swizzle                  ? CU_TENSOR_MAP_SWIZZLE_NONE
+                : box_inner * size == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                : box_inner * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                         : CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
