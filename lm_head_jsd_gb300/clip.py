@@ -95,11 +95,13 @@ def clip_grads(grads, max_norm, *, norm_type=2.0, out=None, stream=None):
         if len(out) != len(every):
             raise ValueError(f"out has {len(out)} tensors, expected {len(every)}")
         outs = [o for o, g in zip(out, every) if g is not None]
-        if any(o is None for o in outs):
+        if not all(map(torch.is_tensor, outs)):
             raise ValueError("out has None where there is a gradient")
-        if _checked("out", outs) != dev or any(
-                o.dtype != g.dtype or o.numel() != g.numel() for o, g in zip(outs, live)):
-            raise ValueError(f"out must have the gradients' dtypes and sizes, on {dev}")
+        require_cuda("out[0]", outs[0])
+        if (list(map(_DTYPE, outs)) != list(map(_DTYPE, live)) or set(map(_DEVICE, outs)) != {dev.index}
+                or list(map(torch.Tensor.numel, outs)) != list(map(torch.Tensor.numel, live))
+                or not all(map(torch.Tensor.is_contiguous, outs))):
+            raise ValueError(f"out must be contiguous, of the gradients' dtypes and sizes, on {dev}")
     t = table(live, outs)
     _apart(t, out is not None)
     with on(stream, dev):

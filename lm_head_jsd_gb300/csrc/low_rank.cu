@@ -22,6 +22,8 @@
 #include "gemm_tc_kernel.cuh"
 #include "tensor_map.cuh"
 
+#include <atomic>
+
 namespace fljsd {
 namespace {
 
@@ -750,6 +752,23 @@ Layout layout(int64_t tokens, int adapters, int rank) {
   return l;
 }
 
+// A kernel's dynamic shared memory, allowed once on each device.
+template <auto KERNEL>
+cudaError_t allow() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, KERNEL);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SMEM_MAX - (int)at.sharedSizeBytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename T, bool ALIGNED>
 cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
   const int stage = 2 * 128 * a.pitch * a.boxes, s = 2 * kTile * a.rk * 2, slot = Pair<T>::kTokens * row_bytes<T>();
@@ -761,8 +780,7 @@ cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args 
   a.slots = (room - a.stages * stage) / slot / kGroups;
   if (a.slots > kMaxSlots / kGroups) a.slots = kMaxSlots / kGroups;
   const int smem = 1024 + a.stages * stage + a.s_bufs * s + kGroups * a.slots * slot;
-  cudaError_t e =
-      cudaFuncSetAttribute(k_lr_expand<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow<k_lr_expand<T, ALIGNED>>();
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.n + kCols - 1) / kCols, most = a.max_tiles * blocks, sms = num_sms();
   // (jobs long enough to load s once for many blocks, and eight of them to each CTA)
@@ -847,7 +865,7 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   int smem = 128 + kStages * stage + kSplit * kOwn * rank * (int)sizeof(float);
   const int reach = 128 + (kStages - 1) * stage + kXStage + 128 * 128;  // the last stage's 128 rows
   if (smem < reach) smem = reach;
-  e = cudaFuncSetAttribute(k_lr_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow<k_lr_shrink>();
   if (e != cudaSuccess) return FLJSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

@@ -25,6 +25,7 @@
 #include "dependent.cuh"
 #include "internal.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace fljsd {
@@ -911,12 +912,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
 
-// CTAs to a row, so that each holds `vecs` vectors of it; more where there are few rows.
-int cluster_for(int64_t v, int size, int64_t rows, int vecs) {
+// CTAs to a row of k_verify_rows: enough to keep all of it, more where there are few rows.
+int cluster_of_rows(int64_t v, int size, int64_t rows) {
   const int64_t all = (v * size + 30) / 16;  // vectors, wherever the row starts
   int c = 1;
-  while (c < kMaxCluster && (int64_t)c * vecs < all) c *= 2;
+  while (c < kMaxCluster && (int64_t)c * kKept * kRowThreads < all) c *= 2;
   while (c < kMaxCluster && rows * c * 2 <= num_sms() && (int64_t)c * 512 < all) c *= 2;
+  return c;
+}
+// CTAs to a request of k_verify_draw: as many as fill the SMs twice over, and have a vector
+// for each thread. (256 requests, V = 128256: 8 CTAs 85 us, 1 CTA DRAW1 us.)
+int cluster_of_draws(int64_t v, int size, int64_t requests) {
+  const int64_t all = (v * size + 30) / 16;
+  int c = 1;
+  while (c < kMaxCluster && requests * c <= num_sms() && (int64_t)c * kThreads < all) c *= 2;
   return c;
 }
 
@@ -936,20 +945,29 @@ struct Launch {
     cfg.numAttrs = 1;
   }
 };
-template <typename K>
-cudaError_t allow(K kernel, size_t smem) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// A kernel's attributes, set once on each device: clusters of 16, dynamic shared memory.
+template <auto KERNEL>
+cudaError_t allow(int smem) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 template <typename T>
 int resident(Launch& l, int cluster) {
-  static int cached[64][kMaxCluster + 1] = {};
+  static std::atomic<int> cached[64][kMaxCluster + 1];
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && cached[dev][cluster] > 0) return cached[dev][cluster];
+  const bool known = dev >= 0 && dev < 64;
+  if (known && (n = cached[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
   l.cfg.gridDim = dim3(cluster);
   if (cudaOccupancyMaxActiveClusters(&n, k_verify_rows<T>, &l.cfg) != cudaSuccess || n < 1) n = 1;
-  if (dev >= 0 && dev < 64) cached[dev][cluster] = n;
+  if (known) cached[dev][cluster].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -957,9 +975,10 @@ template <typename T>
 cudaError_t launch(Args a, cudaStream_t st) {
   a.slots = a.max_drafts + 1 + (a.draft ? a.max_drafts : 0);
   const int64_t rows = a.requests * a.slots;
-  a.cluster = cluster_for(a.v, sizeof(T), rows, kKept * kRowThreads);
-  Launch l(kRowThreads + 32, a.cluster, 2 * kKept * kRowThreads * 16, st);
-  cudaError_t e = allow(k_verify_rows<T>, l.cfg.dynamicSmemBytes);
+  a.cluster = cluster_of_rows(a.v, sizeof(T), rows);
+  constexpr int kRowsBytes = 2 * kKept * kRowThreads * 16, kDrawBytes = 128 * 1024;
+  Launch l(kRowThreads + 32, a.cluster, kRowsBytes, st);
+  cudaError_t e = allow<k_verify_rows<T>>(kRowsBytes);
   if (e != cudaSuccess) return e;
   const int64_t fit = resident<T>(l, a.cluster);
   l.cfg.gridDim = dim3((unsigned)((rows < fit ? rows : fit) * a.cluster));
@@ -967,13 +986,14 @@ cudaError_t launch(Args a, cudaStream_t st) {
   e = cudaLaunchKernelEx(&l.cfg, k_verify_rows<T>, a);
   trace_end(FLJSD_KERNEL_SMALL, st);
   if (e != cudaSuccess) return e;
-  a.cluster = cluster_for(a.v, sizeof(T), a.requests, 2 * kAhead * kThreads);
+  a.cluster = cluster_of_draws(a.v, sizeof(T), a.requests);
   const int64_t vecs = (a.v * (int64_t)sizeof(T) + 30) / 16;
   const int64_t iters = ((vecs + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
+  static_assert((kMaxV * 4 + 30) / 16 / kThreads * kWarps * 8 < kDrawBytes, "sums of one CTA's iterations");
   Launch d(kThreads, a.cluster, (size_t)(iters * kWarps * sizeof(unsigned long long)), st);
   d.cfg.gridDim = dim3((unsigned)(a.requests * a.cluster));
   d.cfg.numAttrs = 2;
-  e = allow(k_verify_draw<T>, d.cfg.dynamicSmemBytes);
+  e = allow<k_verify_draw<T>>(kDrawBytes);
   if (e != cudaSuccess) return e;
   trace_begin(FLJSD_KERNEL_SMALL, st);
   e = cudaLaunchKernelEx(&d.cfg, k_verify_draw<T>, a);
