@@ -39,26 +39,29 @@ def _live(grads):
     return grads, live
 
 
-def _checked(name, ts):
-    """Their device; whole-list checks, for a call of many small tensors is bound by them."""
+def _describe(name, ts):
+    """(device, addresses, sizes, dtypes) of a list that is checked as a whole: a call of many
+    small tensors is bound by this function."""
+    try:
+        devices, at = set(map(_DEVICE, ts)), list(map(torch.Tensor.data_ptr, ts))
+    except TypeError:
+        raise ValueError(f"{name} must be tensors") from None
     require_cuda(f"{name}[0]", ts[0])
-    dev = ts[0].device
-    if (not set(map(_DTYPE, ts)) <= _DT.keys() or set(map(_DEVICE, ts)) != {dev.index}
+    dev, dtypes = ts[0].device, list(map(_DTYPE, ts))
+    if (not set(dtypes) <= _DT.keys() or devices != {dev.index}
             or not all(map(torch.Tensor.is_contiguous, ts))):
         raise ValueError(f"{name} must be contiguous, each of one dtype of {list(_DT)}, and on {dev}")
-    return dev
+    return dev, at, list(map(torch.Tensor.numel, ts)), dtypes
 
 
-def table(grads, outs=None):
-    """fljsd_grad_tensor of each."""
+def table(grads, sizes, dtypes, outs=None):
+    """fljsd_grad_tensor of each, of their addresses, sizes and dtypes (or the one of all)."""
     t = np.zeros(len(grads), dtype=_ENTRY)
-    t["grad"] = list(map(torch.Tensor.data_ptr, grads))
-    t["n"] = list(map(torch.Tensor.numel, grads))
-    kinds = set(map(_DTYPE, grads))
-    t["dtype"] = (_lib.DTYPES[_DT[kinds.pop()]] if len(kinds) == 1
-                  else [_lib.DTYPES[_DT[g.dtype]] for g in grads])
+    t["grad"], t["n"] = grads, sizes
+    one = dtypes if isinstance(dtypes, torch.dtype) else dtypes[0] if len(set(dtypes)) == 1 else None
+    t["dtype"] = [_lib.DTYPES[_DT[d]] for d in dtypes] if one is None else _lib.DTYPES[_DT[one]]
     if outs is not None:
-        t["out"] = t["grad"] if outs is grads else list(map(torch.Tensor.data_ptr, outs))
+        t["out"] = outs
     return t
 
 
@@ -71,8 +74,8 @@ def grad_norm(grads, *, norm_type=2.0, stream=None):
     read back): the root of the sum of their squares, or with ``norm_type`` inf the largest
     magnitude. ``grads``: a tensor or a list of fp32 and bf16 tensors; None is left out."""
     kind, (_, live) = _kind(norm_type), _live(grads)
-    dev = _checked("grads", live)
-    t = table(live)
+    dev, at, sizes, dtypes = _describe("grads", live)
+    t = table(at, sizes, dtypes)
     with on(stream, dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         _lib.fljsd_grad_norm(t.ctypes.data, len(t), kind, 0.0, None, norm, None,
@@ -88,21 +91,17 @@ def clip_grads(grads, max_norm, *, norm_type=2.0, out=None, stream=None):
     every gradient NaN. No tensor may be given twice, or share memory with another."""
     kind, (every, live) = _kind(norm_type), _live(grads)
     check_max_norm(max_norm)
-    dev = _checked("grads", live)
-    outs = live
+    dev, at, sizes, dtypes = _describe("grads", live)
+    outs, outs_at = live, at
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != len(every):
             raise ValueError(f"out has {len(out)} tensors, expected {len(every)}")
         outs = [o for o, g in zip(out, every) if g is not None]
-        if not all(map(torch.is_tensor, outs)):
-            raise ValueError("out has None where there is a gradient")
-        require_cuda("out[0]", outs[0])
-        if (list(map(_DTYPE, outs)) != list(map(_DTYPE, live)) or set(map(_DEVICE, outs)) != {dev.index}
-                or list(map(torch.Tensor.numel, outs)) != list(map(torch.Tensor.numel, live))
-                or not all(map(torch.Tensor.is_contiguous, outs))):
-            raise ValueError(f"out must be contiguous, of the gradients' dtypes and sizes, on {dev}")
-    t = table(live, outs)
+        other, outs_at, *alike = _describe("out", outs)
+        if other != dev or alike != [sizes, dtypes]:
+            raise ValueError(f"out must have the gradients' dtypes and sizes, on {dev}")
+    t = table(at, sizes, dtypes, outs_at)
     _apart(t, out is not None)
     with on(stream, dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)

@@ -31,7 +31,7 @@
 namespace fljsd {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;  // of k_verify_draw
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRowCtas = 3;    // of k_verify_rows on an SM
@@ -652,14 +652,19 @@ struct Residual {
   const T* q;  // or null
   float mp, mq, c, ip, iq;
   int64_t v, without;  // a column whose q is 1, or -1
-  bool q_whole;        // q lies to 16 bytes as p does
+  bool q_whole;        // q lies to 16 bytes as p does (or there is none)
   struct Raw {
     uint4 p, q;
   };
   __device__ __forceinline__ Raw fetch(int64_t j) const {
     Raw r;
-    r.p = load(p, j, v, true);
-    r.q = q ? q_whole ? load(q, j, v, true) : load_apart(q, j, v) : r.p;
+    if (q_whole && j >= 0 && j + Vec<T>::N <= v) {
+      r.p = *reinterpret_cast<const uint4*>(p + j);
+      r.q = q ? *reinterpret_cast<const uint4*>(q + j) : r.p;
+    } else {
+      r.p = load(p, j, v, true);
+      r.q = q ? q_whole ? load(q, j, v, true) : load_apart(q, j, v) : r.p;
+    }
     return r;
   }
   __device__ __forceinline__ void get(const Raw& raw, int64_t j, float2 (&r)[Vec<T>::N / 2]) const {
@@ -718,7 +723,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   constexpr int N = Vec<T>::N;
   __shared__ DrawShared sh;
-  extern __shared__ unsigned long long s_sums[];  // [iterations][kWarps]
+  extern __shared__ unsigned long long s_sums[];  // [turns][kWarps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank();
   const int64_t b = blockIdx.x / a.cluster;
@@ -796,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     res.ip = sp.inv;
     res.v = a.v;
     res.without = -1;
+    res.q_whole = true;
     if (accepted < q.drafts) {
       if (a.draft) {
         const RowStat sd = a.stat_d[at];
@@ -810,29 +816,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
       }
     }
     const Cut<T> cut(res.p, a.v, a.cluster, rank);
-    const int iters = (cut.last - cut.first + kThreads - 1) / kThreads;
-    auto column = [&](int it) {  // past the row where the thread has none
-      const int k = cut.first + it * kThreads + tid;
+    // a warp takes kAhead x 32 neighbouring vectors in a turn
+    const int turns = (cut.last - cut.first + kThreads * kAhead - 1) / (kThreads * kAhead);
+    auto column_of = [&](int t, int w, int i) {  // past the row where there is none
+      const int k = cut.first + ((t * kWarps + w) * kAhead + i) * 32 + lane;
       return k < cut.last ? (int64_t)k * N - cut.lead : a.v;
     };
+    auto column = [&](int it) { return column_of(it / kAhead, warp, it % kAhead); };
     unsigned long long before = 0, total = 0, mine = 0;
     for (int turn = 0; turn < 2; ++turn) {
       mine = 0;
-      for (int it0 = 0; it0 < iters; it0 += kAhead) {
+      for (int t = 0; t < turns; ++t) {
         typename Residual<T>::Raw raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) raw[i] = res.fetch(it0 + i < iters ? column(it0 + i) : a.v);
+        for (int i = 0; i < kAhead; ++i) raw[i] = res.fetch(column(t * kAhead + i));
+        Count n;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           float2 r[N / 2];
-          res.get(raw[i], column(it0 + i), r);
-          Count n;
+          res.get(raw[i], column(t * kAhead + i), r);
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) n.add(r[e]);
-          const unsigned long long s = warp_sum(n, N);
-          if (lane == 0 && it0 + i < iters) s_sums[(it0 + i) * kWarps + warp] = s;
-          mine += s;
         }
+        const unsigned long long s = warp_sum(n, kAhead * N);
+        if (lane == 0) s_sums[t * kWarps + warp] = s;
+        mine += s;
       }
       if (lane == 0) sh.warp[warp] = mine;
       __syncthreads();
@@ -869,11 +877,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
       t -= before;
       // the warp's vectors that hold it, the lane's, the column
       unsigned long long run = 0;
-      const int found = find_sum(iters * kWarps, t, run, [&](int i) { return s_sums[i]; });
-      const int k = cut.first + (found / kWarps) * kThreads + (found % kWarps) * 32 + lane;
-      const int64_t j0 = k < cut.last ? (int64_t)k * N - cut.lead : a.v;
+      const int found = find_sum(turns * kWarps, t, run, [&](int i) { return s_sums[i]; });
+      // of its vectors the 32 that hold it, the lane's, the column
       float2 r[N / 2];
-      res.get(res.fetch(j0), j0, r);
+      int64_t j0 = 0;
+#pragma unroll 1
+      for (int i = 0; i < kAhead; ++i) {
+        j0 = column_of(found / kWarps, found % kWarps, i);
+        res.get(res.fetch(j0), j0, r);
+        Count n;
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) n.add(r[e]);
+        const unsigned long long s = warp_sum(n, N);
+        if (run + s > t) break;
+        run += s;
+      }
       unsigned long long one[N], x = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -988,9 +1006,9 @@ cudaError_t launch(Args a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.cluster = cluster_of_draws(a.v, sizeof(T), a.requests);
   const int64_t vecs = (a.v * (int64_t)sizeof(T) + 30) / 16;
-  const int64_t iters = ((vecs + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
-  static_assert((kMaxV * 4 + 30) / 16 / kThreads * kWarps * 8 < kDrawBytes, "sums of one CTA's iterations");
-  Launch d(kThreads, a.cluster, (size_t)(iters * kWarps * sizeof(unsigned long long)), st);
+  const int64_t turns = ((vecs + a.cluster - 1) / a.cluster + kThreads * kAhead - 1) / (kThreads * kAhead);
+  static_assert((kMaxV * 4 + 30) / 16 / 32 / kAhead * 8 + kWarps * 8 < kDrawBytes, "sums of one CTA's turns");
+  Launch d(kThreads, a.cluster, (size_t)(turns * kWarps * sizeof(unsigned long long)), st);
   d.cfg.gridDim = dim3((unsigned)(a.requests * a.cluster));
   d.cfg.numAttrs = 2;
   e = allow<k_verify_draw<T>>(kDrawBytes);

@@ -197,7 +197,7 @@ class AdamW:
                 self._memory.use()
             if max_norm is not None:
                 both = torch.empty(2, dtype=torch.float32, device=dev)  # norm, factor
-                g = table(live)
+                g = table(t["grad"], t["n"], dt)
                 _lib.fljsd_grad_norm(g.ctypes.data, len(g), _lib.FLJSD_NORM_2, max_norm, grad_scale,
                                      both[0], both[1], workspace(len(g), dev))
                 self.grad_norm, grad_scale = both[0], both[1]
