@@ -57,7 +57,11 @@ struct Args {
   const void* y;
   void* out;
   bool vec_k, copy, same;  // same: y's and out's rows lie to 16 bytes alike
-  int pitch, boxes, stages, s_bufs, slots, blocks;  // bytes of a row of B's boxes, boxes to it; blocks of a job
+  // B's rows in shared memory: bytes of a row of a box, boxes of even (or all) columns, bytes
+  // of a block and between its even columns and the odd ones; all in one box (packed)
+  int pitch, boxes, stage, half;
+  bool packed;
+  int stages, s_bufs, slots, blocks;  // blocks of a job
   int* status;
   int* num_tiles;
   Tile* tiles;
@@ -389,6 +393,18 @@ __device__ __forceinline__ bool wait_all(ExpandShared* sh, const void* bar, uint
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// A place in a ring and the parity of its round. (A division for each use of one took the
+// warp that issues the products half a microsecond a block.)
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++at == n) {
+      at = 0;
+      round ^= 1;
+    }
+  }
+};
+
 // Rows of B that lie in boxes of `pitch` bytes (32, 64 or 128), swizzled so far.
 __device__ __forceinline__ uint64_t desc_of(uint32_t addr, int pitch) {
   return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)((8 * pitch) >> 4) << 32 |
@@ -410,7 +426,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   __shared__ ExpandShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t half = 128u * a.pitch * a.boxes, stage = 2 * half;  // even columns, odd ones
+  const uint32_t half = a.half, stage = a.stage;
   const uint32_t s_half = (uint32_t)kTile * a.rk * 2, s_at = base + a.stages * stage;
   const uint32_t y_at = s_at + a.s_bufs * 2 * s_half;
   if (tid == 0) {
@@ -447,6 +463,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   const uint32_t stretches = (num_blocks + a.blocks - 1) / a.blocks, jobs = tiles * stretches;
   if (warp == kGroups * 4) {
     // ---------------- copies ----------------
+    Ring b_ring, s_ring;
     uint32_t filled = 0, s_filled = 0;
     bool ok = true;
     Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
@@ -455,8 +472,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const uint32_t t = k / stretches, b0 = k % stretches * a.blocks;
       if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
       if (tile.adapter < 0) continue;
-      const uint32_t si = s_filled % a.s_bufs;
-      ok = wait_all(&sh, &sh.s_empty[si], ((s_filled / a.s_bufs) & 1) ^ 1, a.status);
+      const uint32_t si = s_ring.at;
+      ok = wait_all(&sh, &sh.s_empty[si], s_ring.round ^ 1, a.status);
       if (!ok) break;
       if (elect_one()) {
         const uint32_t bar = smem_u32(&sh.s_full[si]), to = s_at + si * 2 * s_half;
@@ -471,23 +488,28 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
               : "memory");
       }
       __syncwarp();
+      s_ring.next(a.s_bufs);
       ++s_filled;
       const int64_t row0 = (int64_t)tile.adapter * a.n;
       for (uint32_t b = b0; b < b0 + a.blocks && b < num_blocks; ++b) {
-        const uint32_t st = filled % a.stages;
-        ok = wait_all(&sh, &sh.b_empty[st], ((filled / a.stages) & 1) ^ 1, a.status);
+        const uint32_t st = b_ring.at;
+        ok = wait_all(&sh, &sh.b_empty[st], b_ring.round ^ 1, a.status);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t bar = smem_u32(&sh.b_full[st]);
           mbar_arrive_expect_tx(bar, stage);
-          for (int h = 0; h < 2; ++h) {
-            const int64_t row = row0 + (int64_t)b * kCols + h;
-            for (int x = 0; x < a.boxes; ++x)
-              tma_load_2d(base + st * stage + h * half + x * 128 * a.pitch, row & 1 ? &tm_odd : &tm_even, bar, x * 64,
-                          (int)(row >> 1));
+          const int64_t row = row0 + (int64_t)b * kCols;
+          if (a.packed) {
+            tma_load_2d(base + st * stage, &tm_even, bar, 0, (int)(row >> 1));
+          } else {
+            for (int h = 0; h < 2; ++h)
+              for (int x = 0; x < a.boxes; ++x)
+                tma_load_2d(base + st * stage + h * half + x * 128 * a.pitch, (row + h) & 1 ? &tm_odd : &tm_even, bar,
+                            x * 64, (int)((row + h) >> 1));
           }
         }
         __syncwarp();
+        b_ring.next(a.stages);
         ++filled;
       }
     }
@@ -502,7 +524,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
   } else if (warp == kGroups * 4 + 1) {
     // ---------------- products ----------------
-    uint32_t taken = 0, s_taken = 0, used = 0;  // used: a bit for each accumulator
+    Ring b_ring, s_ring;
+    uint32_t used = 0;  // a bit for each accumulator
+    // the first descriptors: those of other places, rows and slices are so many 16 bytes on
+    const uint64_t b_first = desc_of(base, a.pitch), s_first = desc(s_at, a.rk / 8);
+    const uint32_t s_low = s_half >> 4, b_odd = half >> 4;
     bool ok = true;
     Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
     uint32_t last_group = kGroups;
@@ -511,26 +537,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const uint32_t b0 = k % stretches * a.blocks;
       if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
       if (tile.adapter < 0) continue;
-      const uint32_t si = s_taken % a.s_bufs;
-      ok = wait_all(&sh, &sh.s_full[si], (s_taken / a.s_bufs) & 1, a.status);
+      const uint32_t si = s_ring.at;
+      ok = wait_all(&sh, &sh.s_full[si], s_ring.round, a.status);
+      const uint64_t s0d = s_first + si * (2 * s_low);
       const uint32_t id = idesc_of((tile.count + 15) / 16 * 16);
       for (uint32_t c = 0; ok && c < (uint32_t)a.blocks && b0 + c < num_blocks; ++c) {
-        const uint32_t g = (seq + c) % kGroups, st = taken % a.stages;
+        const uint32_t g = (seq + c) % kGroups, st = b_ring.at;
         ok = wait_all(&sh, &sh.acc_empty[g], ((used >> g) & 1) ^ 1, a.status) &&
-             wait_all(&sh, &sh.b_full[st], (taken / a.stages) & 1, a.status);
+             wait_all(&sh, &sh.b_full[st], b_ring.round, a.status);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          // (one thread issues all products: their descriptors are sums of what is known)
-          const uint64_t b0d = desc_of(base + st * stage, a.pitch), s0d = desc(s_at + si * 2 * s_half, a.rk / 8);
+          const uint64_t b0d = b_first + st * (stage >> 4);
           const uint32_t d = tmem + g * 2 * kTile;
 #pragma unroll 1
           for (int kk = 0; kk < a.rk / 16; ++kk) {
             const uint64_t bd = b0d + (uint32_t)((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2), sd = s0d + kk * 16;
             mma_bf16<false>(d, bd, sd, id, kk > 0);
-            mma_bf16<false>(d, bd, sd + (s_half >> 4), id, 1);
-            mma_bf16<false>(d + kTile, bd + (half >> 4), sd, id, kk > 0);
-            mma_bf16<false>(d + kTile, bd + (half >> 4), sd + (s_half >> 4), id, 1);
+            mma_bf16<false>(d, bd, sd + s_low, id, 1);
+            mma_bf16<false>(d + kTile, bd + b_odd, sd, id, kk > 0);
+            mma_bf16<false>(d + kTile, bd + b_odd, sd + s_low, id, 1);
           }
           mma_commit<false>(smem_u32(&sh.b_empty[st]));
           mma_commit<false>(smem_u32(&sh.acc_full[g]));
@@ -539,9 +565,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         __syncwarp();
         used ^= 1u << g;
         last_group = g;
-        ++taken;
+        b_ring.next(a.stages);
       }
-      ++s_taken;
+      s_ring.next(a.s_bufs);
     }
     if (last_group < kGroups)  // no product runs at the end
       wait_all(&sh, &sh.acc_full[last_group], ((used >> last_group) & 1) ^ 1, a.status);
@@ -549,6 +575,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     // ---------------- y's rows for a group, a lane to each ----------------
     const uint32_t g = warp - (kGroups * 4 + 2);
     const char* y = reinterpret_cast<const char*>(a.y);
+    Ring ring;
     uint32_t filled = 0;
     bool ok = true;
     // The ends of rows that a copy leaves out: read now, put in place when the next place is
@@ -583,9 +610,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const int64_t col0 = (int64_t)(b0 + c) * kCols;
         const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
         for (int j0 = 0; j0 < tile.count; j0 += kChunk) {
-          const uint32_t slot = g * a.slots + filled % a.slots;
+          const uint32_t slot = g * a.slots + ring.at;
           if (a.slots == 1) settle();
-          ok = wait_all(&sh, &sh.y_empty[slot], ((filled / a.slots) & 1) ^ 1, a.status);
+          ok = wait_all(&sh, &sh.y_empty[slot], ring.round ^ 1, a.status);
           if (!ok) break;
           const int r = lane % kChunk, j = j0 + r;
           const int token = __shfl_sync(0xffffffffu, j0 < 32 ? t0 : t1, j & 31);
@@ -615,6 +642,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
           open_bar = smem_u32(&sh.y_full[slot]);
           open_bytes = all;
           if (ALIGNED) settle();
+          ring.next(a.slots);
           ++filled;
         }
       }
@@ -631,6 +659,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     char* out = reinterpret_cast<char*>(a.out);
     const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + g * 2 * kTile;
     const int mine = 2 * (quarter * 32 + lane) * kSize;  // this thread's pair in a block's row
+    Ring ring;
     uint32_t used = 0, taken = 0;
     bool ok = true;  // (where a wait ran out, the group still meets, and leaves out as it is)
     auto tile_of = [&](uint32_t k) { return k < jobs ? a.tiles[k / stretches] : Tile{-1, 0}; };
@@ -655,7 +684,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
         const bool ends = !a.same || mine < 16 || mine + 2 * kSize + 16 > len;  // may be such a value
         for (uint32_t ch = 0; ch < chunks; ++ch) {
-          const uint32_t slot = g * a.slots + taken % a.slots;
+          const uint32_t slot = g * a.slots + ring.at;
           const uint32_t rows_at = y_at + slot * kChunk * kRow;
           const int j0 = ch * kChunk, count = min(kChunk, tile.count - j0);
           const int held = j0 < 32 ? t0 : t1;  // (by lane j & 31)
@@ -676,7 +705,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
               ++used;
             }
           }
-          ok = ok && wait_all(&sh, &sh.y_full[slot], (taken / a.slots) & 1, a.status);
+          ok = ok && wait_all(&sh, &sh.y_full[slot], ring.round, a.status);
           if (ok && (adds || !ALIGNED)) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
@@ -723,6 +752,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sh.y_empty[slot]));
             __syncwarp();
           }
+          ring.next(a.slots);
           ++taken;
         }
       }
@@ -771,7 +801,7 @@ cudaError_t allow() {
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
-  const int stage = 2 * 128 * a.pitch * a.boxes, s = 2 * kTile * a.rk * 2, slot = Pair<T>::kTokens * row_bytes<T>();
+  const int stage = a.stage, s = 2 * kTile * a.rk * 2, slot = Pair<T>::kTokens * row_bytes<T>();
   a.s_bufs = a.rank > 64 ? 1 : 2;
   // a third of shared memory for B's rows, the rest for y's
   const int room = SMEM_MAX - 1024 - (int)sizeof(ExpandShared) - a.s_bufs * s;
@@ -845,15 +875,31 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   g.tiles = reinterpret_cast<Tile*>(ws + l.tiles);
   g.order = reinterpret_cast<int*>(ws + l.order);
   g.s = ws + l.s;
-  g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;
-  g.boxes = rank <= 64 ? 1 : 2;
-  // the rows of even numbers among all adapters' columns, and the odd ones
+  // B's rows, a column of y each, come as boxes of those of even numbers (among all adapters')
+  // and of odd ones, as wide as the rank up to 64. Two columns of rank 16 or 32 make one row of
+  // a box where no pair is cut: rows of 32 bytes are slow to copy (64 tokens of 64 adapters of
+  // rank 16: PACK0 us, in pairs PACK1).
   CUtensorMap even, odd;
   const int64_t rows = adapters * n;
-  if (!make_tensor_map(&even, MapType::kBf16, g.b, rank, (rows + 1) / 2, 2 * rank, g.pitch / 2, 128) ||
-      !make_tensor_map(&odd, MapType::kBf16, rows > 1 ? g.b + rank : g.b, rank, rows > 1 ? rows / 2 : 1, 2 * rank,
-                       g.pitch / 2, 128))
-    return FLJSD_ERR_CUDA;
+  g.packed = (rank == 16 || rank == 32) && n % 2 == 0;
+  bool made;
+  if (g.packed) {
+    g.pitch = 4 * rank;
+    g.boxes = 1;
+    g.half = 2 * rank;
+    g.stage = 128 * g.pitch;
+    made = make_tensor_map(&even, MapType::kBf16, g.b, 2 * rank, rows / 2, 2 * rank, 2 * rank, 128);
+    odd = even;
+  } else {
+    g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;
+    g.boxes = rank <= 64 ? 1 : 2;
+    g.half = 128 * g.pitch * g.boxes;
+    g.stage = 2 * g.half;
+    made = make_tensor_map(&even, MapType::kBf16, g.b, rank, (rows + 1) / 2, 2 * rank, g.pitch / 2, 128) &&
+           make_tensor_map(&odd, MapType::kBf16, rows > 1 ? g.b + rank : g.b, rank, rows > 1 ? rows / 2 : 1,
+                           2 * rank, g.pitch / 2, 128);
+  }
+  if (!made) return FLJSD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int plan_smem = 2 * (adapters + 1) * (int)sizeof(int);
   trace_begin(FLJSD_KERNEL_SMALL, st);
