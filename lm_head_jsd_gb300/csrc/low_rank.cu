@@ -113,13 +113,16 @@ __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* row, in
 
 // Waits with a limit (10 s), after which the call's status word says so.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 63u && globaltimer() - t0 > kTimeoutNs) {
-      atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
-      return false;
+    if ((it & 255u) == 255u) {  // (reading the timer takes longer than most waits)
+      const unsigned long long t = globaltimer();
+      if (!t0) t0 = t;
+      if (t - t0 > kTimeoutNs) {
+        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        return false;
+      }
     }
   }
 }
@@ -376,14 +379,15 @@ struct ExpandShared {
 // (By whole warps. A barrier has one waiting warp or group, which waits for its every phase.)
 __device__ __forceinline__ bool wait_all(ExpandShared* sh, const void* bar, uint32_t parity, int* status) {
   const uint32_t b = smem_u32(bar);
-  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
-  const unsigned long long t0 = globaltimer();
-  bool ok = false;
+  bool ok = mbar_try_wait(b, parity);
+  unsigned long long t0 = 0;
   for (uint32_t it = 0; !ok; ++it) {
     ok = mbar_try_wait(b, parity);
-    if (!ok && (it & 63u) == 63u) {
+    if (!ok && (it & 255u) == 255u) {  // (reading the timer takes longer than most waits)
       if (sh->abort) break;
-      if (globaltimer() - t0 > kTimeoutNs) {
+      const unsigned long long t = globaltimer();
+      if (!t0) t0 = t;
+      if (t - t0 > kTimeoutNs) {
         sh->abort = 1;
         atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
         break;

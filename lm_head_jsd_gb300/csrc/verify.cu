@@ -312,14 +312,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // With a limit, after which the CTA's waits all end and the call's status word says so.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
-  unsigned long long t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  unsigned long long t0 = 0, t;
   for (uint32_t it = 0;; ++it) {
     if (bar_try(bar, parity)) return true;
-    if ((it & 63u) == 63u) {
+    if ((it & 255u) == 255u) {  // (reading the timer takes longer than most waits)
       if (*abort) return false;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (!t0) t0 = t;
       if (t - t0 > kWaitNs) {
         *abort = 1;
         atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
