@@ -32,6 +32,7 @@ using namespace tcgemm;
 constexpr int kTile = 64;       // tokens of a tile
 constexpr int kCols = 256;      // columns of y that a block of k_lr_expand takes
 constexpr int kMaxRank = 128;
+constexpr int kSmallRank = 32;  // up to which two CTAs share an SM
 constexpr int kMaxAdapters = 4096;
 constexpr int kSplit = 8;       // CTAs of k_lr_shrink to a tile
 constexpr int kOwn = kTile / kSplit;
@@ -39,10 +40,10 @@ constexpr int kThreads = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kStages = 4;
 constexpr int kXStage = kTile * 128;  // 64 tokens x 64 of k
-constexpr int kGroups = 4;      // of k_lr_expand's epilogue
-constexpr int kExpandThreads = kGroups * 128 + 64 + kGroups * 32;
 constexpr int kMaxStages = 8;   // of B's rows
-constexpr int kMaxSlots = 16;   // places for rows of y, a ring of them to each group
+constexpr int kMaxSlots = 4;    // places for rows of y in a group's ring
+// Threads of k_lr_expand with so many groups.
+__host__ __device__ constexpr int expand_threads(int groups) { return groups * 160 + 64; }
 
 struct Tile {
   int adapter, count;  // tokens order[number * kTile ..]
@@ -367,17 +368,19 @@ __device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_landed() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+template <int GROUPS>
 struct ExpandShared {
   unsigned long long b_full[kMaxStages], b_empty[kMaxStages];  // a block's rows of B
   unsigned long long s_full[2], s_empty[2];                    // a job's s
-  unsigned long long acc_full[kGroups], acc_empty[kGroups];
-  unsigned long long y_full[kMaxSlots], y_empty[kMaxSlots];    // rows of some tokens
+  unsigned long long acc_full[GROUPS], acc_empty[GROUPS];
+  unsigned long long y_full[GROUPS * kMaxSlots], y_empty[GROUPS * kMaxSlots];    // rows of some tokens
   uint32_t tmem;
   volatile int abort;
 };
 // Waits with a limit, after which the CTA's all end and the call's status word says so.
 // (By whole warps. A barrier has one waiting warp or group, which waits for its every phase.)
-__device__ __forceinline__ bool wait_all(ExpandShared* sh, const void* bar, uint32_t parity, int* status) {
+template <int GROUPS>
+__device__ __forceinline__ bool wait_all(ExpandShared<GROUPS>* sh, const void* bar, uint32_t parity, int* status) {
   const uint32_t b = smem_u32(bar);
   bool ok = mbar_try_wait(b, parity);
   unsigned long long t0 = 0;
@@ -421,13 +424,14 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, int pitch) {
 // ALIGNED: all rows of y and out lie on 16 bytes, their strides and ends too. Otherwise the
 // part of a row between 16-byte boundaries is copied, and up to seven values on either side
 // are read and written one by one.
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kExpandThreads, 1)
+// GROUPS: four on an SM, in one CTA or in two.
+template <typename T, bool ALIGNED, int GROUPS>
+__global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
     k_lr_expand(const __grid_constant__ CUtensorMap tm_even, const __grid_constant__ CUtensorMap tm_odd, const Args a) {
   using V = typename Pair<T>::V;
   constexpr int kRow = row_bytes<T>(), kSize = (int)sizeof(T), kChunk = Pair<T>::kTokens;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ExpandShared sh;
+  __shared__ ExpandShared<GROUPS> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t half = a.half, stage = a.stage;
@@ -442,11 +446,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.s_empty[i]), 1);
     }
-    for (int i = 0; i < kGroups; ++i) {
+    for (int i = 0; i < GROUPS; ++i) {
       mbar_init(smem_u32(&sh.acc_full[i]), 1);
       mbar_init(smem_u32(&sh.acc_empty[i]), 4);
     }
-    for (int i = 0; i < kGroups * a.slots; ++i) {
+    for (int i = 0; i < GROUPS * a.slots; ++i) {
       mbar_init(smem_u32(&sh.y_full[i]), 1);
       mbar_init(smem_u32(&sh.y_empty[i]), 1);
     }
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   }
   wait_for_previous();
   // (only now: what it waits for needs tensor memory too)
-  if (warp == 0) tmem_alloc<false>(smem_u32(&sh.tmem), kGroups * 2 * kTile);
+  if (warp == 0) tmem_alloc<false>(smem_u32(&sh.tmem), GROUPS * 2 * kTile);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   const uint32_t tiles = (uint32_t)*a.num_tiles;
   const uint32_t num_blocks = (uint32_t)((a.n + kCols - 1) / kCols);
   const uint32_t stretches = (num_blocks + a.blocks - 1) / a.blocks, jobs = tiles * stretches;
-  if (warp == kGroups * 4) {
+  if (warp == GROUPS * 4) {
     // ---------------- copies ----------------
     Ring b_ring, s_ring;
     uint32_t filled = 0, s_filled = 0;
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const uint32_t f = s_filled - 1 - i;
       wait_all(&sh, &sh.s_full[f % a.s_bufs], (f / a.s_bufs) & 1, a.status);
     }
-  } else if (warp == kGroups * 4 + 1) {
+  } else if (warp == GROUPS * 4 + 1) {
     // ---------------- products ----------------
     Ring b_ring, s_ring;
     uint32_t used = 0;  // a bit for each accumulator
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     const uint32_t s_low = s_half >> 4, b_odd = half >> 4;
     bool ok = true;
     Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
-    uint32_t last_group = kGroups;
+    uint32_t last_group = GROUPS;
     for (uint32_t k = blockIdx.x, seq = 0; ok && k < jobs; k += gridDim.x, seq += a.blocks) {
       const Tile tile = next;
       const uint32_t b0 = k % stretches * a.blocks;
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const uint64_t s0d = s_first + si * (2 * s_low);
       const uint32_t id = idesc_of((tile.count + 15) / 16 * 16);
       for (uint32_t c = 0; ok && c < (uint32_t)a.blocks && b0 + c < num_blocks; ++c) {
-        const uint32_t g = (seq + c) % kGroups, st = b_ring.at;
+        const uint32_t g = (seq + c) % GROUPS, st = b_ring.at;
         ok = wait_all(&sh, &sh.acc_empty[g], ((used >> g) & 1) ^ 1, a.status) &&
              wait_all(&sh, &sh.b_full[st], b_ring.round, a.status);
         if (!ok) break;
@@ -573,11 +577,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       }
       s_ring.next(a.s_bufs);
     }
-    if (last_group < kGroups)  // no product runs at the end
+    if (last_group < GROUPS)  // no product runs at the end
       wait_all(&sh, &sh.acc_full[last_group], ((used >> last_group) & 1) ^ 1, a.status);
-  } else if (warp >= kGroups * 4 + 2) {
+  } else if (warp >= GROUPS * 4 + 2) {
     // ---------------- y's rows for a group, a lane to each ----------------
-    const uint32_t g = warp - (kGroups * 4 + 2);
+    const uint32_t g = warp - (GROUPS * 4 + 2);
     const char* y = reinterpret_cast<const char*>(a.y);
     Ring ring;
     uint32_t filled = 0;
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       next1 = token_of(k + gridDim.x, lane + 32);
       const uint32_t b0 = k % stretches * a.blocks;
       const uint32_t left = min((uint32_t)a.blocks, num_blocks - b0);
-      for (uint32_t c = (g - seq) % kGroups; ok && c < left; c += kGroups) {
+      for (uint32_t c = (g - seq) % GROUPS; ok && c < left; c += GROUPS) {
         const int64_t col0 = (int64_t)(b0 + c) * kCols;
         const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
         for (int j0 = 0; j0 < tile.count; j0 += kChunk) {
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       // where a row starts in its place (a block is a multiple of 16 bytes)
       const int lead0 = ALIGNED ? 0 : (int)((uintptr_t)(y + (int64_t)t0 * a.ldy * kSize) & 15u);
       const int lead1 = ALIGNED ? 0 : (int)((uintptr_t)(y + (int64_t)t1 * a.ldy * kSize) & 15u);
-      for (uint32_t c = (g - seq) % kGroups; c < left; c += kGroups) {
+      for (uint32_t c = (g - seq) % GROUPS; c < left; c += GROUPS) {
         const int64_t col0 = (int64_t)(b0 + c) * kCols;
         const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
         const bool ends = !a.same || mine < 16 || mine + 2 * kSize + 16 > len;  // may be such a value
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc<false>(tmem, kGroups * 2 * kTile);
+  if (warp == 0) tmem_dealloc<false>(tmem, GROUPS * 2 * kTile);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -803,25 +807,33 @@ cudaError_t allow() {
   return e;
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, int GROUPS>
 cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
-  const int stage = a.stage, s = 2 * kTile * a.rk * 2, slot = Pair<T>::kTokens * row_bytes<T>();
+  constexpr int kCtas = 4 / GROUPS, kSlot = Pair<T>::kTokens * row_bytes<T>();
+  const int s = 2 * kTile * a.rk * 2;
   a.s_bufs = a.rank > 64 ? 1 : 2;
   // a third of shared memory for B's rows, the rest for y's
-  const int room = SMEM_MAX - 1024 - (int)sizeof(ExpandShared) - a.s_bufs * s;
-  a.stages = room / 3 / stage;
+  const int room = (SMEM_MAX - (kCtas - 1) * 1024) / kCtas - 1024 - (int)sizeof(ExpandShared<GROUPS>) - a.s_bufs * s;
+  a.stages = room / 3 / a.stage;
   a.stages = a.stages < 2 ? 2 : a.stages > kMaxStages ? kMaxStages : a.stages;
-  a.slots = (room - a.stages * stage) / slot / kGroups;
-  if (a.slots > kMaxSlots / kGroups) a.slots = kMaxSlots / kGroups;
-  const int smem = 1024 + a.stages * stage + a.s_bufs * s + kGroups * a.slots * slot;
-  const cudaError_t e = allow<k_lr_expand<T, ALIGNED>>();
+  a.slots = (room - a.stages * a.stage) / kSlot / GROUPS;
+  if (a.slots < 1) return cudaErrorInvalidConfiguration;
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  const int smem = 1024 + a.stages * a.stage + a.s_bufs * s + GROUPS * a.slots * kSlot;
+  const cudaError_t e = allow<k_lr_expand<T, ALIGNED, GROUPS>>();
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (a.n + kCols - 1) / kCols, most = a.max_tiles * blocks, sms = num_sms();
+  const int64_t blocks = (a.n + kCols - 1) / kCols, most = a.max_tiles * blocks, ctas = num_sms() * kCtas;
   // (jobs long enough to load s once for many blocks, and eight of them to each CTA)
   a.blocks = 1;
-  while (a.blocks < 32 && most >= sms * 8 * 2 * a.blocks) a.blocks *= 2;
-  return launch_dependent(k_lr_expand<T, ALIGNED>, dim3((unsigned)(most < sms ? most : sms)), kExpandThreads, smem, st,
-                          even, odd, a);
+  while (a.blocks < 32 && most >= ctas * 8 * 2 * a.blocks) a.blocks *= 2;
+  return launch_dependent(k_lr_expand<T, ALIGNED, GROUPS>, dim3((unsigned)(most < ctas ? most : ctas)),
+                          expand_threads(GROUPS), smem, st, even, odd, a);
+}
+template <typename T>
+cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, const Args& a, bool aligned, cudaStream_t st) {
+  if (a.rank <= kSmallRank)
+    return aligned ? launch_expand<T, true, 2>(even, odd, a, st) : launch_expand<T, false, 2>(even, odd, a, st);
+  return aligned ? launch_expand<T, true, 4>(even, odd, a, st) : launch_expand<T, false, 4>(even, odd, a, st);
 }
 
 }  // namespace
@@ -934,10 +946,8 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   trace_end(FLJSD_KERNEL_SMALL, st);
   if (e != cudaSuccess) return FLJSD_ERR_CUDA;
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  if (dtype == FLJSD_BF16)
-    e = aligned ? launch_expand<__nv_bfloat16, true>(even, odd, g, st) : launch_expand<__nv_bfloat16, false>(even, odd, g, st);
-  else
-    e = aligned ? launch_expand<float, true>(even, odd, g, st) : launch_expand<float, false>(even, odd, g, st);
+  e = dtype == FLJSD_BF16 ? launch_expand<__nv_bfloat16>(even, odd, g, aligned, st)
+                          : launch_expand<float>(even, odd, g, aligned, st);
   trace_end(FLJSD_KERNEL_SMALL, st);
   return e == cudaSuccess ? FLJSD_OK : FLJSD_ERR_CUDA;
 }
