@@ -690,7 +690,6 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       for (uint32_t c = (g - seq) % GROUPS; c < left; c += GROUPS) {
         const int64_t col0 = (int64_t)(b0 + c) * kCols;
         const int len = (int)min((int64_t)kCols, a.n - col0) * kSize;
-        const bool ends = !a.same || mine < 16 || mine + 2 * kSize + 16 > len;  // may be such a value
         for (uint32_t ch = 0; ch < chunks; ++ch) {
           const uint32_t slot = g * a.slots + ring.at;
           const uint32_t rows_at = y_at + slot * kChunk * kRow;
@@ -718,7 +717,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
               const int lead = ALIGNED ? 0 : __shfl_sync(0xffffffffu, held_lead, (j0 + j) & 31);
-              const int token = ALIGNED ? 0 : __shfl_sync(0xffffffffu, held, (j0 + j) & 31);
+              const int token = ALIGNED || a.same ? 0 : __shfl_sync(0xffffffffu, held, (j0 + j) & 31);
               if (j < count) {
                 T* p = reinterpret_cast<T*>(__cvta_shared_to_generic(rows_at + j * kRow + lead + mine));
                 V v = ALIGNED ? *reinterpret_cast<const V*>(p) : join(p[0], p[1]);
@@ -728,14 +727,13 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
                 } else {
                   T lo, hi;
                   split(v, lo, hi);
-                  p[0] = lo;
-                  p[1] = hi;
-                  if (ends) {  // what the copy out leaves out
-                    const int first = lead ? 16 : 0, last = (lead + len) & ~15;
+                  if (a.same) {
+                    p[0] = lo;
+                    p[1] = hi;
+                  } else {  // one by one: out's rows lie otherwise
                     T* o = reinterpret_cast<T*>(out + ((int64_t)token * a.ldo + col0) * kSize + mine);
-                    auto copied = [&](int at) { return a.same && at >= first && at + kSize <= last; };
-                    if (mine < len && !copied(lead + mine)) o[0] = lo;
-                    if (mine + kSize < len && !copied(lead + mine + kSize)) o[1] = hi;
+                    if (mine < len) o[0] = lo;
+                    if (mine + kSize < len) o[1] = hi;
                   }
                 }
               }
@@ -745,14 +743,24 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
           asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
           if (quarter == (int)(taken & 3)) {  // out, a lane to each row
             if (a.same && ok) {
-              const int token = __shfl_sync(0xffffffffu, held, (j0 + lane % kChunk) & 31);
+              const int r = lane % kChunk;
+              const int token = __shfl_sync(0xffffffffu, held, (j0 + r) & 31);
               const uintptr_t at = (uintptr_t)(out + ((int64_t)token * a.ldo + col0) * kSize);
               const uintptr_t lo = (at + 15) & ~(uintptr_t)15, hi = (at + len) & ~(uintptr_t)15;
+              const uint32_t place = rows_at + r * kRow - (uint32_t)(at & ~(uintptr_t)15);  // of address 0
               if (lane < count && hi > lo)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(lo),
-                             "r"(rows_at + lane * kRow + (uint32_t)(lo - (at & ~(uintptr_t)15))),
-                             "r"((uint32_t)(hi - lo))
+                             "r"(place + (uint32_t)lo), "r"((uint32_t)(hi - lo))
                              : "memory");
+              if (!ALIGNED && r < count && lane < 2 * kChunk) {  // this lane's end of the row
+                const uintptr_t end = at + len;
+                uintptr_t from = lane < kChunk ? at : hi > lo ? hi : end;
+                const uintptr_t to = lane < kChunk && hi > lo ? lo : end;
+#pragma unroll 4
+                for (; from < to; from += kSize)
+                  *reinterpret_cast<T*>(from) =
+                      *reinterpret_cast<const T*>(__cvta_shared_to_generic(place + (uint32_t)from));
+              }
               bulk_commit();
               asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
               __syncwarp();
