@@ -22,7 +22,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;                           // 16-byte vectors a thread takes at a time
 constexpr int kChunk = kThreads * kVecs * 16;      // bytes a CTA takes at a time
-constexpr int kCtasPerSm = 8;
+// CTAs of one or few chunks spread their accesses out evenly, as in an AdamW step, but each
+// writes a partial sum (525M bf16: norm with 8, 16 and 32 an SM 173, 156 and 160 us, the
+// clip's second pass 342, 332 and 312).
+constexpr int kNormCtas = 16, kClipCtas = 32;
 constexpr int kFew = 64, kMany = 800;              // tensors in a launch
 
 struct Entry {
@@ -273,8 +276,8 @@ __global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ Table
   }
 }
 
-int ctas(int64_t chunks) {
-  const int64_t most = (int64_t)num_sms() * kCtasPerSm;
+int ctas(int64_t chunks, int per_sm) {
+  const int64_t most = (int64_t)num_sms() * per_sm;
   return (int)(chunks < most ? chunks : most);
 }
 
@@ -308,7 +311,7 @@ cudaError_t norm_of(const fljsd_grad_tensor* ts, int count, const float* grad_sc
                     float* norm, float* factor, double* partial, cudaStream_t st) {
   int n = 0;
   cudaError_t e = each_table<CAP>(ts, count, false, [&](const Table<CAP>& t) {
-    const int grid = ctas(t.first[t.count]);
+    const int grid = ctas(t.first[t.count], kNormCtas);
     trace_begin(FLJSD_KERNEL_SMALL, st);
     k_norm<MAX, CAP><<<grid, kThreads, 0, st>>>(t, partial + n);
     trace_end(FLJSD_KERNEL_SMALL, st);
@@ -339,7 +342,7 @@ cudaError_t clip_all(const fljsd_grad_tensor* ts, int count, const float* factor
   return each_table<CAP>(ts, count, true, [&](const Table<CAP>& t) {
     trace_begin(FLJSD_KERNEL_SMALL, st);
     const cudaError_t e =
-        launch_dependent(k_clip<CAP>, ctas(t.first[t.count]), kThreads, 0, st, t, factor);
+        launch_dependent(k_clip<CAP>, ctas(t.first[t.count], kClipCtas), kThreads, 0, st, t, factor);
     trace_end(FLJSD_KERNEL_SMALL, st);
     return e;
   });
@@ -372,7 +375,7 @@ using namespace fljsd;
 
 extern "C" size_t fljsd_grad_norm_workspace_bytes(int32_t count) {
   const size_t tables = count <= kFew ? 1 : (count + kMany - 1) / kMany;
-  return kFactorBytes + tables * num_sms() * kCtasPerSm * sizeof(double);
+  return kFactorBytes + tables * num_sms() * kNormCtas * sizeof(double);
 }
 
 extern "C" fljsd_status fljsd_grad_norm(const fljsd_grad_tensor* tensors, int32_t count, int32_t kind,
