@@ -591,8 +591,8 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
  * index -1 are then not touched), but no other memory of the call. The tokens' order is
  * free; those of one adapter need not be neighbours. The rank is a multiple of 8 (adapters
  * of smaller ranks are padded with zeros).
- * Products are added in fp32; A x, scaled, is carried on as the sum of two bf16 (2^-16 of
- * it at most is lost), the result is added to y in fp32 and rounded once to dtype. A row's
+ * Products are added in fp32; A x, scaled, is carried on as the sum of two bf16 for y in
+ * bf16 (2^-16 of it at most is lost) and of three for y in fp32 (2^-24); the result is added to y in fp32 and rounded once to dtype. A row's
  * result does not depend on the other rows.
  * An index that is neither -1 nor in [0, adapters) counts as -1 and sets the status word
  * (the workspace's first int32) to FLJSD_ERR_INVALID_ARG; FLJSD_ERR_TIMEOUT there: a

@@ -7,8 +7,9 @@
 // rows as the instruction's 128 rows and the tokens as its columns, so that a tile of one
 // token costs 16 columns and not 128 rows:
 //  - k_lr_shrink: s = scale A x of a tile. A cluster of eight CTAs splits k and adds its
-//    parts in shared memory, in one order. s is written as two bf16, the nearest and what
-//    is left (2^-16 of s at most is lost): one would be 2^-8 off, as much as bf16's own rounding.
+//    parts in shared memory, in one order. s is written as a sum of bf16, the nearest and what
+//    is left: two for y in bf16 (2^-16 of s at most is lost; one would be 2^-8 off, as much as
+//    y's own rounding), three for y in fp32 (2^-24).
 //  - k_lr_expand: y + B s for 256 columns at a time. Accumulator rows i of two products
 //    hold columns 2 i and 2 i + 1, so that a thread reads and writes pairs and a warp 64
 //    neighbouring columns of a token. One CTA an SM: warps that copy B's rows and y's ahead,
@@ -67,7 +68,8 @@ struct Args {
   int* num_tiles;
   Tile* tiles;
   int* order;
-  char* s;  // a tile's s as it lies in shared memory: [nearest, rest] of kTile rows
+  int parts;  // of s: two or three bf16
+  char* s;  // a tile's s as it lies in shared memory: parts of kTile rows
 };
 
 // Operands lie in shared memory as 8 x 16-byte matrices, those of 8 rows side by side.
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
   if (live) {
     const float scale = a.scales ? a.scales[tile.adapter] : 1.f;
     const int pieces = a.rk / 8, tok0 = (int)rank_in_cluster * kOwn;
-    char* image = a.s + (int64_t)t * kTile * a.rk * 4;
+    char* image = a.s + (int64_t)t * kTile * a.rk * 2 * a.parts;
     for (int i = tid; i < kOwn * a.rk; i += kThreads) {
       const int tok = i / a.rk, rr = i % a.rk;
       if (tok0 + tok >= tile.count) break;
@@ -306,13 +308,15 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
         s *= scale;
       }
       if (!s_ok) s = 0.f;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(s);
-      // (an s that bf16 does not hold has nothing left)
-      const float left = s - __bfloat162float(hi);
-      const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(s) < INFINITY && fabsf(left) < INFINITY ? left : 0.f);
       const uint32_t at = place(tok0 + tok, rr / 8, pieces) + (rr % 8) * 2;
-      *reinterpret_cast<__nv_bfloat16*>(image + at) = hi;
-      *reinterpret_cast<__nv_bfloat16*>(image + (int64_t)kTile * a.rk * 2 + at) = lo;
+      float left = s;
+      for (int p = 0; p < a.parts; ++p) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(left);
+        *reinterpret_cast<__nv_bfloat16*>(image + (int64_t)p * kTile * a.rk * 2 + at) = h;
+        // (an s that bf16 does not hold has nothing left)
+        left -= __bfloat162float(h);
+        if (!(fabsf(s) < INFINITY && fabsf(left) < INFINITY)) left = 0.f;
+      }
     }
   }
 }
@@ -323,11 +327,13 @@ template <>
 struct Pair<float> {
   using V = float2;
   static constexpr int kTokens = 8;  // whose rows share a place in shared memory
+  static constexpr int kParts = 3;   // of s
 };
 template <>
 struct Pair<__nv_bfloat16> {
   using V = uint32_t;
   static constexpr int kTokens = 16;
+  static constexpr int kParts = 2;
 };
 __device__ __forceinline__ float2 add_to(float2 y, float d0, float d1) { return make_float2(y.x + d0, y.y + d1); }
 __device__ __forceinline__ uint32_t add_to(uint32_t y, float d0, float d1) {
@@ -429,14 +435,14 @@ template <typename T, bool ALIGNED, int GROUPS>
 __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
     k_lr_expand(const __grid_constant__ CUtensorMap tm_even, const __grid_constant__ CUtensorMap tm_odd, const Args a) {
   using V = typename Pair<T>::V;
-  constexpr int kRow = row_bytes<T>(), kSize = (int)sizeof(T), kChunk = Pair<T>::kTokens;
+  constexpr int kRow = row_bytes<T>(), kSize = (int)sizeof(T), kChunk = Pair<T>::kTokens, kParts = Pair<T>::kParts;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ExpandShared<GROUPS> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t half = a.half, stage = a.stage;
   const uint32_t s_half = (uint32_t)kTile * a.rk * 2, s_at = base + a.stages * stage;
-  const uint32_t y_at = s_at + a.s_bufs * 2 * s_half;
+  const uint32_t y_at = s_at + a.s_bufs * kParts * s_half;
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(smem_u32(&sh.b_full[i]), 1);
@@ -484,11 +490,11 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       ok = wait_all(&sh, &sh.s_empty[si], s_ring.round ^ 1, a.status);
       if (!ok) break;
       if (elect_one()) {
-        const uint32_t bar = smem_u32(&sh.s_full[si]), to = s_at + si * 2 * s_half;
-        const char* image = a.s + (int64_t)t * kTile * a.rk * 4;
+        const uint32_t bar = smem_u32(&sh.s_full[si]), to = s_at + si * kParts * s_half;
+        const char* image = a.s + (int64_t)t * kTile * a.rk * 2 * a.parts;
         const uint32_t bytes = (uint32_t)((tile.count + 15) / 16 * 16) * a.rk * 2;
-        mbar_arrive_expect_tx(bar, 2 * bytes);
-        for (int h = 0; h < 2; ++h)
+        mbar_arrive_expect_tx(bar, kParts * bytes);
+        for (int h = 0; h < kParts; ++h)
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                   to + h * s_half),
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
     uint32_t used = 0;  // a bit for each accumulator
     // the first descriptors: those of other places, rows and slices are so many 16 bytes on
     const uint64_t b_first = desc_of(base, a.pitch), s_first = desc(s_at, a.rk / 8);
-    const uint32_t s_low = s_half >> 4, b_odd = half >> 4;
+    const uint32_t s_next = s_half >> 4, b_odd = half >> 4;
     bool ok = true;
     Tile next = blockIdx.x < jobs ? a.tiles[blockIdx.x / stretches] : Tile{-1, 0};
     uint32_t last_group = GROUPS;
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       if (tile.adapter < 0) continue;
       const uint32_t si = s_ring.at;
       ok = wait_all(&sh, &sh.s_full[si], s_ring.round, a.status);
-      const uint64_t s0d = s_first + si * (2 * s_low);
+      const uint64_t s0d = s_first + si * (kParts * s_next);
       const uint32_t id = idesc_of((tile.count + 15) / 16 * 16);
       for (uint32_t c = 0; ok && c < (uint32_t)a.blocks && b0 + c < num_blocks; ++c) {
         const uint32_t g = (seq + c) % GROUPS, st = b_ring.at;
@@ -561,10 +567,11 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
 #pragma unroll 1
           for (int kk = 0; kk < a.rk / 16; ++kk) {
             const uint64_t bd = b0d + (uint32_t)((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2), sd = s0d + kk * 16;
-            mma_bf16<false>(d, bd, sd, id, kk > 0);
-            mma_bf16<false>(d, bd, sd + s_low, id, 1);
-            mma_bf16<false>(d + kTile, bd + b_odd, sd, id, kk > 0);
-            mma_bf16<false>(d + kTile, bd + b_odd, sd + s_low, id, 1);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+              mma_bf16<false>(d, bd, sd + p * s_next, id, kk + p > 0);
+              mma_bf16<false>(d + kTile, bd + b_odd, sd + p * s_next, id, kk + p > 0);
+            }
           }
           mma_commit<false>(smem_u32(&sh.b_empty[st]));
           mma_commit<false>(smem_u32(&sh.acc_full[g]));
@@ -794,7 +801,7 @@ Layout layout(int64_t tokens, int adapters, int rank) {
   l.tiles = 256;  // status, number of tiles
   l.order = align_up(l.tiles + l.max_tiles * sizeof(Tile));
   l.s = align_up(l.order + l.max_tiles * kTile * sizeof(int));
-  l.bytes = l.s + (size_t)l.max_tiles * kTile * ((rank + 15) / 16 * 16) * 4;
+  l.bytes = l.s + (size_t)l.max_tiles * kTile * ((rank + 15) / 16 * 16) * 6;
   return l;
 }
 
@@ -818,7 +825,7 @@ cudaError_t allow() {
 template <typename T, bool ALIGNED, int GROUPS>
 cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
   constexpr int kCtas = 4 / GROUPS, kSlot = Pair<T>::kTokens * row_bytes<T>();
-  const int s = 2 * kTile * a.rk * 2;
+  const int s = Pair<T>::kParts * kTile * a.rk * 2;
   a.s_bufs = a.rank > 64 ? 1 : 2;
   // a third of shared memory for B's rows, the rest for y's
   const int room = (SMEM_MAX - (kCtas - 1) * 1024) / kCtas - 1024 - (int)sizeof(ExpandShared<GROUPS>) - a.s_bufs * s;
@@ -878,6 +885,7 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   Args g{};
   g.tokens = tokens; g.k = k; g.n = n; g.ldx = ldx; g.ldy = ldy; g.ldo = ldo;
   g.rank = rank;
+  g.parts = dtype == FLJSD_BF16 ? Pair<__nv_bfloat16>::kParts : Pair<float>::kParts;
   g.rk = (rank + 15) / 16 * 16;
   g.adapters = adapters;
   g.max_tiles = (int)l.max_tiles;

@@ -100,9 +100,11 @@ def _want(z):
             d, d_abs = s @ b.T, s.abs() @ b.abs().T
             want[at] += d
             # sums: a rounding (2^-22, whichever way the tensor core rounds) for each instruction of 16 products and each
-            # of eight parts; s as two bf16: 2^-16; the second product likewise, of twice the rank; the sum with y
-            far[at] = (((k + 15) // 16 + 10) * 2.0 ** -22 * s_abs + 2.0 ** -16 * s.abs()) @ b.abs().T
-            far[at] += (rk / 8 + 2) * 2.0 ** -22 * d_abs + 2.0 ** -24 * (y[at].abs() + d_abs)
+            # of eight parts; s as two bf16 2^-16, as three 2^-24; the second product likewise, of twice or three times the
+            # rank; the sum with y
+            lost, parts = (2.0 ** -16, 2) if z["y"].dtype == BF else (2.0 ** -24, 3)
+            far[at] = (((k + 15) // 16 + 10) * 2.0 ** -22 * s_abs + lost * s.abs()) @ b.abs().T
+            far[at] += (parts * rk / 16 + 2) * 2.0 ** -22 * d_abs + 2.0 ** -24 * (y[at].abs() + d_abs)
     return want, far + torch.finfo(z["y"].dtype).eps / 2 * want.abs()
 
 
