@@ -210,9 +210,13 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
   }
   wait_for_previous();
   const int t = blockIdx.x / kSplit;
-  const bool live = t < *a.num_tiles && a.tiles[t].adapter >= 0;
-  const Tile tile = live ? a.tiles[t] : Tile{0, 0};
-  if (tid < tile.count) s_row[tid] = a.x + (int64_t)a.order[(int64_t)t * kTile + tid] * a.ldx;
+  // (three loads at once: a place behind the last tile is there, whatever it holds)
+  const int tiles = *a.num_tiles;
+  Tile tile = a.tiles[t];
+  const int token = tid < kTile ? a.order[(int64_t)t * kTile + tid] : 0;
+  const bool live = t < tiles && tile.adapter >= 0;
+  if (!live) tile = Tile{0, 0};
+  if (tid < tile.count) s_row[tid] = a.x + (int64_t)token * a.ldx;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
