@@ -649,6 +649,7 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  *    leave [0, drafts] or span more than max_drafts, or whose temperature on the device is
  *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0 and -1s. Both
  *    set the status word (the workspace's first int32) to FLJSD_ERR_INVALID_ARG.
+ *  - FLJSD_ERR_TIMEOUT in the status word: a bounded device wait expired, the results are none.
  *  - u_draw outside [0, 1) is taken to its nearer end, NaN as 0; u_accept of NaN refuses.
  *  - tokens before the first request's and behind the last one's have accept_prob 0: a
  *    buffer may be longer than what a step fills. (offsets given; their rows are not read.)
@@ -662,7 +663,7 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  * or so small that log2(e) / T is not finite, a null or misaligned pointer (tokens, u_accept and
  * accept_prob may be NULL with drafts 0); FLJSD_ERR_UNSUPPORTED for v of 2^20 and more,
  * requests above 2^20, drafts above 2^24, max_drafts above 1024, or requests *
- * (2 max_drafts + 1) of 2^28 and more; FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
+ * (2 max_drafts + 1) of 2^27 and more; FLJSD_ERR_WORKSPACE; FLJSD_ERR_CUDA when a launch fails.
  */
 size_t fljsd_verify_workspace_bytes(int64_t requests, int64_t drafts);
 fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v, int32_t max_drafts,

@@ -33,7 +33,10 @@ using namespace tcgemm;
 constexpr int kTile = 64;       // tokens of a tile
 constexpr int kCols = 256;      // columns of y that a block of k_lr_expand takes
 constexpr int kMaxRank = 128;
-constexpr int kSmallRank = 32;  // up to which two CTAs share an SM
+// Up to this rank two CTAs share an SM: the warp that issues the products is the bound where
+// tiles are small (64 tokens of 64 adapters of rank 16 and 32: 111 and 132 us with one, 77 and
+// 118 with two). Above it two rings of B's rows do not fit.
+constexpr int kSmallRank = 32;
 constexpr int kMaxAdapters = 4096;
 constexpr int kSplit = 8;       // CTAs of k_lr_shrink to a tile
 constexpr int kOwn = kTile / kSplit;
@@ -59,11 +62,7 @@ struct Args {
   const void* y;
   void* out;
   bool vec_k, copy, same;  // same: y's and out's rows lie to 16 bytes alike
-  // B's rows in shared memory: bytes of a row of a box, boxes of even (or all) columns, bytes
-  // of a block and between its even columns and the odd ones; all in one box (packed)
-  int pitch, boxes, stage, half;
-  bool packed;
-  int stages, s_bufs, slots, blocks;  // blocks of a job
+  int pitch, boxes, stages, s_bufs, slots, blocks;  // bytes of a row of B's boxes, boxes to it; blocks of a job
   int* status;
   int* num_tiles;
   Tile* tiles;
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
   __shared__ ExpandShared<GROUPS> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t half = a.half, stage = a.stage;
+  const uint32_t half = 128u * a.pitch * a.boxes, stage = 2 * half;  // even columns, odd ones
   const uint32_t s_half = (uint32_t)kTile * a.rk * 2, s_at = base + a.stages * stage;
   const uint32_t y_at = s_at + a.s_bufs * kParts * s_half;
   if (tid == 0) {
@@ -517,14 +516,10 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
           const uint32_t bar = smem_u32(&sh.b_full[st]);
           mbar_arrive_expect_tx(bar, stage);
           const int64_t row = row0 + (int64_t)b * kCols;
-          if (a.packed) {
-            tma_load_2d(base + st * stage, &tm_even, bar, 0, (int)(row >> 1));
-          } else {
-            for (int h = 0; h < 2; ++h)
-              for (int x = 0; x < a.boxes; ++x)
-                tma_load_2d(base + st * stage + h * half + x * 128 * a.pitch, (row + h) & 1 ? &tm_odd : &tm_even, bar,
-                            x * 64, (int)((row + h) >> 1));
-          }
+          for (int h = 0; h < 2; ++h)
+            for (int x = 0; x < a.boxes; ++x)
+              tma_load_2d(base + st * stage + h * half + x * 128 * a.pitch, (row + h) & 1 ? &tm_odd : &tm_even, bar,
+                          x * 64, (int)((row + h) >> 1));
         }
         __syncwarp();
         b_ring.next(a.stages);
@@ -829,16 +824,16 @@ cudaError_t allow() {
 template <typename T, bool ALIGNED, int GROUPS>
 cudaError_t launch_expand(const CUtensorMap& even, const CUtensorMap& odd, Args a, cudaStream_t st) {
   constexpr int kCtas = 4 / GROUPS, kSlot = Pair<T>::kTokens * row_bytes<T>();
-  const int s = Pair<T>::kParts * kTile * a.rk * 2;
+  const int s = Pair<T>::kParts * kTile * a.rk * 2, stage = 2 * 128 * a.pitch * a.boxes;
   a.s_bufs = a.rank > 64 ? 1 : 2;
   // a third of shared memory for B's rows, the rest for y's
   const int room = (SMEM_MAX - (kCtas - 1) * 1024) / kCtas - 1024 - (int)sizeof(ExpandShared<GROUPS>) - a.s_bufs * s;
-  a.stages = room / 3 / a.stage;
+  a.stages = room / 3 / stage;
   a.stages = a.stages < 2 ? 2 : a.stages > kMaxStages ? kMaxStages : a.stages;
-  a.slots = (room - a.stages * a.stage) / kSlot / GROUPS;
+  a.slots = (room - a.stages * stage) / kSlot / GROUPS;
   if (a.slots < 1) return cudaErrorInvalidConfiguration;
   if (a.slots > kMaxSlots) a.slots = kMaxSlots;
-  const int smem = 1024 + a.stages * a.stage + a.s_bufs * s + GROUPS * a.slots * kSlot;
+  const int smem = 1024 + a.stages * stage + a.s_bufs * s + GROUPS * a.slots * kSlot;
   const cudaError_t e = allow<k_lr_expand<T, ALIGNED, GROUPS>>();
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.n + kCols - 1) / kCols, most = a.max_tiles * blocks, ctas = num_sms() * kCtas;
@@ -912,29 +907,15 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   g.order = reinterpret_cast<int*>(ws + l.order);
   g.s = ws + l.s;
   // B's rows, a column of y each, come as boxes of those of even numbers (among all adapters')
-  // and of odd ones, as wide as the rank up to 64. Two columns of rank 16 or 32 make one row of
-  // a box where no pair is cut: rows of 32 bytes are slow to copy (64 tokens of 64 adapters of
-  // rank 16: PACK0 us, in pairs PACK1).
+  // and of odd ones, as wide as the rank up to 64
+  g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;
+  g.boxes = rank <= 64 ? 1 : 2;
   CUtensorMap even, odd;
   const int64_t rows = adapters * n;
-  g.packed = (rank == 16 || rank == 32) && n % 2 == 0;
-  bool made;
-  if (g.packed) {
-    g.pitch = 4 * rank;
-    g.boxes = 1;
-    g.half = 2 * rank;
-    g.stage = 128 * g.pitch;
-    made = make_tensor_map(&even, MapType::kBf16, g.b, 2 * rank, rows / 2, 2 * rank, 2 * rank, 128);
-    odd = even;
-  } else {
-    g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;
-    g.boxes = rank <= 64 ? 1 : 2;
-    g.half = 128 * g.pitch * g.boxes;
-    g.stage = 2 * g.half;
-    made = make_tensor_map(&even, MapType::kBf16, g.b, rank, (rows + 1) / 2, 2 * rank, g.pitch / 2, 128) &&
-           make_tensor_map(&odd, MapType::kBf16, rows > 1 ? g.b + rank : g.b, rank, rows > 1 ? rows / 2 : 1,
-                           2 * rank, g.pitch / 2, 128);
-  }
+  const bool made =
+      make_tensor_map(&even, MapType::kBf16, g.b, rank, (rows + 1) / 2, 2 * rank, g.pitch / 2, 128) &&
+      make_tensor_map(&odd, MapType::kBf16, rows > 1 ? g.b + rank : g.b, rank, rows > 1 ? rows / 2 : 1, 2 * rank,
+                      g.pitch / 2, 128);
   if (!made) return FLJSD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int plan_smem = 2 * (adapters + 1) * (int)sizeof(int);

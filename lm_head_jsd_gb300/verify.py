@@ -52,9 +52,9 @@ def verify_drafts(target_logits, draft_tokens, u_accept, u_draw, *, draft_logits
 
     The tokens follow the target's probabilities. They depend on a request's own logits
     and numbers alone, not on the batch or on how the work is split. Carries no gradient.
-    ``status``: an int32 on the device that receives the call's status word (0, or
+    ``status``: an int32 on the device that receives the call's status word (0,
     FLJSD_ERR_INVALID_ARG where a drafted token, an offset or a temperature is out of
-    range)."""
+    range, or FLJSD_ERR_TIMEOUT)."""
     z = target_logits
     if not isinstance(z, torch.Tensor) or z.dim() != 2 or z.dtype not in _DT:
         raise ValueError(f"target_logits must be a matrix of one of {list(_DT)}")
