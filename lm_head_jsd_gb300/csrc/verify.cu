@@ -648,6 +648,10 @@ __device__ __forceinline__ uint4 load_apart(const T* row, int64_t j, int64_t v) 
   return r;
 }
 
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at_shared(dst)), "l"(src) : "memory");
+}
+
 // What the next token is drawn from: p, or p - q.
 template <typename T>
 struct Residual {
@@ -726,7 +730,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   constexpr int N = Vec<T>::N;
   __shared__ DrawShared sh;
-  extern __shared__ unsigned long long s_sums[];  // [turns][kWarps]
+  extern __shared__ uint4 s_raw[];  // [2][p, q][kAhead][kThreads]: a thread's own, a turn ahead
+  unsigned long long* s_sums = reinterpret_cast<unsigned long long*>(s_raw + 4 * kAhead * kThreads);  // [turns][kWarps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank();
   const int64_t b = blockIdx.x / a.cluster;
@@ -829,10 +834,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     unsigned long long before = 0, total = 0, mine = 0;
     for (int turn = 0; turn < 2; ++turn) {
       mine = 0;
-      for (int t = 0; t < turns; ++t) {
-        typename Residual<T>::Raw raw[kAhead];
+      auto ask = [&](int t) {
+        if (t < turns) {
+          uint4* to = s_raw + (t & 1) * 2 * kAhead * kThreads + tid;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) raw[i] = res.fetch(column(t * kAhead + i));
+          for (int i = 0; i < kAhead; ++i, to += kThreads) {
+            const int64_t j = column(t * kAhead + i);
+            if (res.q_whole && j >= 0 && j + N <= a.v) {
+              copy16(to, res.p + j);
+              if (res.q) copy16(to + kAhead * kThreads, res.q + j);
+            } else {
+              const typename Residual<T>::Raw r = res.fetch(j);
+              to[0] = r.p;
+              to[kAhead * kThreads] = r.q;
+            }
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      ask(0);
+      for (int t = 0; t < turns; ++t) {
+        ask(t + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        typename Residual<T>::Raw raw[kAhead];
+        const uint4* from = s_raw + (t & 1) * 2 * kAhead * kThreads + tid;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          raw[i].p = from[i * kThreads];
+          raw[i].q = res.q ? from[(kAhead + i) * kThreads] : raw[i].p;
+        }
         Count n;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -1010,8 +1040,9 @@ cudaError_t launch(Args a, cudaStream_t st) {
   a.cluster = cluster_of_draws(a.v, sizeof(T), a.requests);
   const int64_t vecs = (a.v * (int64_t)sizeof(T) + 30) / 16;
   const int64_t turns = ((vecs + a.cluster - 1) / a.cluster + kThreads * kAhead - 1) / (kThreads * kAhead);
-  static_assert((kMaxV * 4 + 30) / 16 / 32 / kAhead * 8 + kWarps * 8 < kDrawBytes, "sums of one CTA's turns");
-  Launch d(kThreads, a.cluster, (size_t)(turns * kWarps * sizeof(unsigned long long)), st);
+  constexpr int kRawBytes = 4 * kAhead * kThreads * 16;
+  static_assert((kMaxV * 4 + 30) / 16 / 32 / kAhead * 8 + kWarps * 8 + kRawBytes < kDrawBytes, "sums of one CTA's turns");
+  Launch d(kThreads, a.cluster, kRawBytes + (size_t)(turns * kWarps * sizeof(unsigned long long)), st);
   d.cfg.gridDim = dim3((unsigned)(a.requests * a.cluster));
   d.cfg.numAttrs = 2;
   e = allow<k_verify_draw<T>>(kDrawBytes);
