@@ -177,20 +177,36 @@ __device__ __forceinline__ void values(const uint4& q, float2 (&z)[Vec<T>::N / 2
       z[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 }
-// The largest of a vector; a NaN stays.
+// The largest of a thread's vectors; a NaN stays. (bf16 two at a time, fp32 three.)
 template <typename T>
-__device__ __forceinline__ float largest(const uint4& q, float m);
+struct Top;
 template <>
-__device__ __forceinline__ float largest<float>(const uint4& q, float m) {
-  return max_nan(max_nan(m, max_nan(__uint_as_float(q.x), __uint_as_float(q.y))),
-                 max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
-}
+struct Top<float> {
+  float m = -INFINITY;
+  __device__ __forceinline__ static float most(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+  }
+  __device__ __forceinline__ void add(const uint4& q) {
+    m = most(m, __uint_as_float(q.x), __uint_as_float(q.y));
+    m = most(m, __uint_as_float(q.z), __uint_as_float(q.w));
+  }
+  __device__ __forceinline__ float value() const { return m; }
+};
 template <>
-__device__ __forceinline__ float largest<__nv_bfloat16>(const uint4& q, float m) {
-  auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-  const __nv_bfloat162 x = __hmax2_nan(__hmax2_nan(two(q.x), two(q.y)), __hmax2_nan(two(q.z), two(q.w)));
-  return max_nan(m, max_nan(__low2float(x), __high2float(x)));
-}
+struct Top<__nv_bfloat16> {
+  uint32_t m = 0xff80ff80u;  // -inf, -inf
+  __device__ __forceinline__ void add(const uint4& q) {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 x = __hmax2_nan(
+        two(m), __hmax2_nan(__hmax2_nan(two(q.x), two(q.y)), __hmax2_nan(two(q.z), two(q.w))));
+    m = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  __device__ __forceinline__ float value() const {
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
 
 // Two weights relative to m.
 __device__ __forceinline__ float2 weights(float2 z, float m, float c) {
@@ -553,10 +569,11 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       const Part& q = part_of(i);
       if (!q.z) return false;
       const uint4* mine = s_rows + (i & 1) * kKept * kRowThreads + tid;
-      float m = -INFINITY;
+      Top<T> top;
 #pragma unroll
-      for (int k = 0; k < kKept; ++k) m = largest<T>(mine[k * kRowThreads], m);
-      if (q.n > kKept * kRowThreads) rest(q, [&](const uint4& x, int) { m = largest<T>(x, m); });
+      for (int k = 0; k < kKept; ++k) top.add(mine[k * kRowThreads]);
+      if (q.n > kKept * kRowThreads) rest(q, [&](const uint4& x, int) { top.add(x); });
+      float m = top.value();
       asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
       if (lane < a.cluster)
         send(&sh.top[i % kTopRing][rank * kRowWarps + warp], &sh.tops[i % kTopRing], lane, m);
