@@ -9,6 +9,8 @@ from . import _lib
 from ._streams import check_status, hand_over, on, report, require_cuda
 from .api import _DT
 
+_BF, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
+
 
 def check_rows(name, t):
     """The row stride of a matrix whose rows are contiguous."""
@@ -28,26 +30,40 @@ def _span(t):
 def check_adapters(x, n, a, b, index, scales):
     """That adapters fit x [tokens, k] and an output of n columns; their (number, rank)."""
     (tokens, k), dev = x.shape, x.device
-    if x.dtype != torch.bfloat16:
-        raise ValueError(f"x has dtype {x.dtype}, adapters expect torch.bfloat16")
+    try:  # (in one expression: a call of few tokens is bound by what is looked at)
+        count, rank, depth = a.shape
+        fits = (x.dtype == _BF and a.dtype == _BF and b.dtype == _BF and index.dtype == _I64
+                and depth == k and count > 0 and rank > 0 and rank % 8 == 0
+                and b.shape == (count, n, rank) and index.shape == (tokens,)
+                and a.is_contiguous() and b.is_contiguous() and index.is_contiguous()
+                and a.device == dev and b.device == dev and index.device == dev
+                and (scales is None or (scales.dtype == _F32 and scales.shape == (count,)
+                                        and scales.is_contiguous() and scales.device == dev)))
+    except (AttributeError, ValueError):  # no tensor, or not of three dimensions
+        fits = False
+    if not fits:
+        _refuse(x, n, a, b, index, scales)
+    if torch.is_grad_enabled() and (x.requires_grad or a.requires_grad or b.requires_grad
+                                    or (scales is not None and scales.requires_grad)):
+        raise ValueError("an input requires a gradient, which adapters here do not give: detach it")
+    return count, rank
+
+
+def _refuse(x, n, a, b, index, scales):
+    (tokens, k), dev = x.shape, x.device
+    if x.dtype != _BF:
+        raise ValueError(f"x has dtype {x.dtype}, adapters expect {_BF}")
     if not isinstance(a, torch.Tensor) or a.dim() != 3 or a.shape[0] == 0 or a.shape[1] == 0:
         raise ValueError("a must be [adapters, rank, k]")
     count, rank = a.shape[:2]
     if rank % 8:
         raise ValueError(f"the rank is {rank}, expected a multiple of 8 (pad a and b with zeros)")
-    for name, t, shape in (("a", a, (count, rank, k)), ("b", b, (count, n, rank))):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != shape
+    for name, t, dtype, shape in (("a", a, _BF, (count, rank, k)), ("b", b, _BF, (count, n, rank)),
+                                  ("index", index, _I64, (tokens,)), ("scales", scales, _F32, (count,))):
+        if not (t is None and name == "scales") and (
+                not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape
                 or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{name} must be a contiguous torch.bfloat16 tensor {list(shape)} on {dev}")
-    for name, t, dt, shape in (("index", index, torch.int64, (tokens,)), ("scales", scales, torch.float32, (count,))):
-        if t is None and name == "scales":
-            continue
-        if (not isinstance(t, torch.Tensor) or t.dtype != dt or tuple(t.shape) != shape
-                or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on {dev}")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, a, b, scales)):
-        raise ValueError("an input requires a gradient, which adapters here do not give: detach it")
-    return count, rank
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
 
 
 def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, stream=None):
@@ -83,10 +99,14 @@ def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, strea
             if begin < hi and lo < end:
                 raise ValueError(f"out shares memory with {name}")
     with on(stream, dev):
-        r = out if out is not None else torch.empty((tokens, n), dtype=y.dtype, device=dev)
+        r, ldr = out, n
+        if out is None:
+            r = torch.empty((tokens, n), dtype=y.dtype, device=dev)
+        else:
+            ldr = check_rows("out", out)
         ws = torch.empty(_lib.fljsd_low_rank_workspace_bytes(tokens, count, rank), dtype=torch.uint8, device=dev)
         _lib.fljsd_low_rank_add(tokens, x.shape[1], n, rank, count, x, ldx, a, b, index, scales, _DT[y.dtype],
-                                y, ldy, r, check_rows("out", r), ws)
+                                y, ldy, r, ldr, ws)
         report(status, ws)
     if out is None:
         hand_over((r,), stream, dev)

@@ -11,6 +11,8 @@ from . import _lib
 from ._streams import check_status, hand_over, on, report, require_cuda
 from .api import _DT
 
+_F32, _I64 = torch.float32, torch.int64
+
 
 class Verified(NamedTuple):
     """tokens [requests, max_drafts + 1]: the accepted tokens, the drawn one, -1 behind;
@@ -29,8 +31,8 @@ def _check_vector(name, t, dtype, n, device):
 
 
 def _check_logits(name, z, rows, v, dtype, device):
-    if (not isinstance(z, torch.Tensor) or z.dim() != 2 or tuple(z.shape) != (rows, v)
-            or z.dtype != dtype or z.device != device):
+    if (not isinstance(z, torch.Tensor) or z.shape != (rows, v) or z.dtype != dtype
+            or z.device != device):
         raise ValueError(f"{name} must be {dtype} [{rows}, {v}] on {device}")
     if z.stride(1) != 1 and v > 1 and rows > 0:
         raise ValueError(f"the rows of {name} must be contiguous")
@@ -70,25 +72,29 @@ def verify_drafts(target_logits, draft_tokens, u_accept, u_draw, *, draft_logits
             raise ValueError(f"{n} drafted tokens of {b} requests need offsets")
         max_drafts = n // b
     else:
-        _check_vector("offsets", offsets, torch.int64, b + 1, dev)
+        _check_vector("offsets", offsets, _I64, b + 1, dev)
         if max_drafts is None or max_drafts < 0:
             raise ValueError("offsets need max_drafts, the most that a request may draft")
-    _check_vector("draft_tokens", draft_tokens, torch.int64, n, dev)
-    _check_vector("u_accept", u_accept, torch.float32, n, dev)
-    _check_vector("u_draw", u_draw, torch.float32, b, dev)
+    # (in one expression: a call of few requests is bound by what is looked at)
+    if not (isinstance(u_accept, torch.Tensor) and draft_tokens.dtype == _I64 and u_accept.dtype == _F32
+            and u_draw.dtype == _F32 and u_accept.shape == (n,) and draft_tokens.is_contiguous()
+            and u_accept.is_contiguous() and u_draw.is_contiguous() and draft_tokens.device == dev
+            and u_accept.device == dev and u_draw.device == dev):
+        _check_vector("draft_tokens", draft_tokens, _I64, n, dev)
+        _check_vector("u_accept", u_accept, _F32, n, dev)
+        _check_vector("u_draw", u_draw, _F32, b, dev)
     ld = _check_logits("target_logits", z, n + b, v, z.dtype, dev)
     ldd = v
     if draft_logits is not None:
         ldd = _check_logits("draft_logits", draft_logits, n, v, z.dtype, dev)
     each = None
     if isinstance(temperature, torch.Tensor):
-        _check_vector("temperature", temperature, torch.float32, b, dev)
+        _check_vector("temperature", temperature, _F32, b, dev)
         each, temperature = temperature, 1.0
     check_status(status, dev)
     with on(stream, dev):
-        r = Verified(torch.empty((b, max_drafts + 1), dtype=torch.int64, device=dev),
-                     torch.empty(b, dtype=torch.int64, device=dev),
-                     torch.empty(n, dtype=torch.float32, device=dev))
+        r = Verified(torch.empty((b, max_drafts + 1), dtype=_I64, device=dev),
+                     torch.empty(b, dtype=_I64, device=dev), torch.empty(n, dtype=_F32, device=dev))
         ws = torch.empty(_lib.fljsd_verify_workspace_bytes(b, n), dtype=torch.uint8, device=dev)
         _lib.fljsd_verify(b, n, v, max_drafts, _DT[z.dtype], z, ld, draft_logits if n else None, ldd,
                           draft_tokens, u_accept, u_draw, offsets, each, temperature, *r, ws)
