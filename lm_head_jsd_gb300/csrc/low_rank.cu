@@ -132,6 +132,87 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int* status)
   }
 }
 
+// The group of a token: its adapter, or the last one where rows without an adapter are to be
+// copied; -1: left as it is. `bad`: an index that names none.
+__device__ __forceinline__ int group_of(const Args& a, int64_t t, bool& bad) {
+  const int64_t i = a.index[t];
+  if (i >= 0 && i < a.adapters) return (int)i;
+  bad |= i != -1;
+  return a.copy ? a.adapters : -1;
+}
+
+// Few tokens are sorted where they are first used: every CTA of k_lr_shrink finds its own
+// tile, and its cluster's first one writes it down.
+constexpr int kFewTokens = 1024, kFewGroups = 1024, kFewTiles = 16;
+struct FewShared {
+  int count[kFewGroups];
+  int token[kTile];
+  int warp[kThreads / 32];
+  int group, before, tiles;
+};
+__device__ __forceinline__ Tile find_tile(const Args& a, int t, FewShared& sh, bool writes) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tokens = (int)a.tokens;
+  const int groups = a.adapters + 1;
+  bool bad = false;
+  for (int i = tid; i < groups; i += kThreads) sh.count[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < tokens; i += kThreads) {
+    const int g = group_of(a, i, bad);
+    if (g >= 0) atomicAdd(&sh.count[g], 1);
+  }
+  bad = __syncthreads_or(bad) != 0;
+  if (warp == 0) {  // whose tile this is, and how many there are
+    int group = -1, before = 0, tiles = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const int mine = g0 + lane < groups ? (sh.count[g0 + lane] + kTile - 1) / kTile : 0;
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += p;
+      }
+      const uint32_t over = __ballot_sync(0xffffffffu, tiles + sum > t);
+      if (group < 0 && over) {
+        const int l = __ffs(over) - 1;
+        group = g0 + l;
+        before = tiles + __shfl_sync(0xffffffffu, sum - mine, l);
+      }
+      tiles += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      sh.group = group;
+      sh.before = before;
+      sh.tiles = tiles;
+    }
+  }
+  __syncthreads();
+  const int group = sh.group, lo = (t - sh.before) * kTile;
+  Tile tile{group < a.adapters ? group : -1, 0};
+  if (group >= 0) {
+    tile.count = min(kTile, sh.count[group] - lo);
+    for (int t0 = 0, seen = 0; t0 < tokens && seen < lo + kTile; t0 += kThreads) {
+      const bool in = t0 + tid < tokens && group_of(a, t0 + tid, bad) == group;
+      const uint32_t them = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) sh.warp[warp] = __popc(them);
+      __syncthreads();
+      int at = seen - lo + __popc(them & ((1u << lane) - 1));
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) at += sh.warp[w];
+        seen += sh.warp[w];
+      }
+      if (in && at >= 0 && at < kTile) sh.token[at] = t0 + tid;
+      __syncthreads();
+    }
+    if (writes && tid < tile.count) a.order[(int64_t)t * kTile + tid] = sh.token[tid];
+    if (writes && tid == 0) a.tiles[t] = tile;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.num_tiles = sh.tiles;
+    *a.status = bad ? (int)FLJSD_ERR_INVALID_ARG : 0;
+  }
+  return tile;
+}
+
 // Sorts the tokens by adapter (those without one last, where they are to be copied) and
 // cuts each adapter's into tiles. Which of an adapter's tokens comes first changes
 // nothing in their results.
@@ -147,16 +228,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_lr_plan(const Args a) {
   for (int i = tid; i < groups; i += kPlanThreads) s_count[i] = 0;
   if (tid == 0) s_carry = s_bad = 0;
   __syncthreads();
-  auto group = [&](int64_t t) {  // -1: left as it is
-    const int64_t i = a.index[t];
-    if (i >= 0 && i < a.adapters) return (int)i;
-    if (i != -1) s_bad = 1;
-    return a.copy ? a.adapters : -1;
-  };
+  bool bad = false;
   for (int64_t t = tid; t < a.tokens; t += kPlanThreads) {
-    const int g = group(t);
+    const int g = group_of(a, t, bad);
     if (g >= 0) atomicAdd(&s_count[g], 1);
   }
+  if (bad) s_bad = 1;
   __syncthreads();
   for (int g0 = 0; g0 < groups; g0 += kPlanThreads) {
     const int g = g0 + tid, n = g < groups ? s_count[g] : 0, tiles = (n + kTile - 1) / kTile;
@@ -185,11 +262,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_lr_plan(const Args a) {
     *a.status = s_bad ? (int)FLJSD_ERR_INVALID_ARG : 0;
   }
   for (int64_t t = tid; t < a.tokens; t += kPlanThreads) {
-    const int g = group(t);
+    const int g = group_of(a, t, bad);
     if (g >= 0) a.order[atomicAdd(&s_place[g], 1)] = (int)t;
   }
 }
 
+template <bool FEW>
 __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ unsigned long long s_free[kStages];
@@ -212,11 +290,21 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
   }
   wait_for_previous();
   const int t = blockIdx.x / kSplit;
-  // (three loads at once: a place behind the last tile is there, whatever it holds)
-  const int tiles = *a.num_tiles;
-  Tile tile = a.tiles[t];
-  const int token = tid < kTile ? a.order[(int64_t)t * kTile + tid] : 0;
-  const bool live = t < tiles && tile.adapter >= 0;
+  bool live;
+  Tile tile;
+  int token = 0;
+  if constexpr (FEW) {
+    __shared__ FewShared few;
+    tile = find_tile(a, t, few, rank_in_cluster == 0);
+    if (tid < tile.count) token = few.token[tid];
+    live = tile.count > 0 && tile.adapter >= 0;
+  } else {
+    // (three loads at once: a place behind the last tile is there, whatever it holds)
+    const int tiles = *a.num_tiles;
+    tile = a.tiles[t];
+    if (tid < kTile) token = a.order[(int64_t)t * kTile + tid];
+    live = t < tiles && tile.adapter >= 0;
+  }
   if (!live) tile = Tile{0, 0};
   if (tid < tile.count) s_row[tid] = a.x + (int64_t)token * a.ldx;
   tc_fence_before();
@@ -921,18 +1009,21 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
                       g.pitch / 2, 128);
   if (!made) return FLJSD_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int plan_smem = 2 * (adapters + 1) * (int)sizeof(int);
-  trace_begin(FLJSD_KERNEL_SMALL, st);
-  k_lr_plan<<<1, kPlanThreads, plan_smem, st>>>(g);
-  trace_end(FLJSD_KERNEL_SMALL, st);
-  cudaError_t e = cudaGetLastError();
+  // (one launch fewer, but every tile's CTAs look for it: one token of one adapter 34 us with
+  // k_lr_plan and 28 without, 333 of 5 40.7 and 40.3, 64 of 64 78 and 84, 1000 of 1000 157 and 348)
+  const bool few = l.max_tiles <= kFewTiles && tokens <= kFewTokens && adapters < kFewGroups;
+  cudaError_t e = few ? allow<k_lr_shrink<true>>() : allow<k_lr_shrink<false>>();
   if (e != cudaSuccess) return FLJSD_ERR_CUDA;
+  if (!few) {
+    trace_begin(FLJSD_KERNEL_SMALL, st);
+    k_lr_plan<<<1, kPlanThreads, 2 * (adapters + 1) * (int)sizeof(int), st>>>(g);
+    trace_end(FLJSD_KERNEL_SMALL, st);
+    if (cudaGetLastError() != cudaSuccess) return FLJSD_ERR_CUDA;
+  }
   const int stage = kXStage + rank * 128;
   int smem = 128 + kStages * stage + kSplit * kOwn * rank * (int)sizeof(float);
   const int reach = 128 + (kStages - 1) * stage + kXStage + 128 * 128;  // the last stage's 128 rows
   if (smem < reach) smem = reach;
-  e = allow<k_lr_shrink>();
-  if (e != cudaSuccess) return FLJSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -944,9 +1035,9 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = few ? 1 : 2;  // (behind k_lr_plan)
   trace_begin(FLJSD_KERNEL_SMALL, st);
-  e = cudaLaunchKernelEx(&cfg, k_lr_shrink, g);
+  e = few ? cudaLaunchKernelEx(&cfg, k_lr_shrink<true>, g) : cudaLaunchKernelEx(&cfg, k_lr_shrink<false>, g);
   trace_end(FLJSD_KERNEL_SMALL, st);
   if (e != cudaSuccess) return FLJSD_ERR_CUDA;
   trace_begin(FLJSD_KERNEL_SMALL, st);
