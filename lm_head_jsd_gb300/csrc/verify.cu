@@ -18,13 +18,13 @@
 // 32-bit integers, the constants taken off once.
 //
 // k_verify_rows: clusters take one row after the other and keep it in shared memory and
-// registers between finding its maximum and the sum, so that HBM is read once. Bound by
-// issue (11 instructions a column; 256 requests of 4 drafts, V = 128256 bf16, 591 MB: 154
-// us = 3.8 TB/s). Doubles are divided by one lane: with every thread dividing its own
+// registers between finding its maximum and the sum, so that HBM is read once. Ten
+// instructions a column keep issue half busy, and a cluster goes at its slowest CTA's pace
+// (256 requests of 4 drafts, V = 128256 bf16, 591 MB: 153 us = 3.9 TB/s). Doubles are divided by one lane: with every thread dividing its own
 // the two units for doubles of an SM took the kernels 442 and 132 us.
 // k_verify_draw, a cluster for each request: the tests, then one pass over the row where a
 // token is to be drawn (two rows after a refusal), each warp's vectors with a sum of their
-// own; those the number falls into are read again (the same requests: 49 us).
+// own; those the number falls into are read again (the same requests: 39 us).
 #include "dependent.cuh"
 #include "internal.cuh"
 
@@ -989,7 +989,7 @@ int cluster_of_rows(int64_t v, int size, int64_t rows) {
   return c;
 }
 // CTAs to a request of k_verify_draw: as many as fill the SMs twice over, and have a vector
-// for each thread. (256 requests, V = 128256: 8 CTAs 85 us, 1 CTA 49 us.)
+// for each thread. (256 requests, V = 128256: 8 CTAs 85 us, 1 CTA 49, before rows came a turn ahead.)
 int cluster_of_draws(int64_t v, int size, int64_t requests) {
   const int64_t all = (v * size + 30) / 16;
   int c = 1;
