@@ -488,6 +488,14 @@ def fljsd_clip_grads(tensors, count, kind, max_norm, norm, workspace, workspace_
     return st
 
 
+def call(name, *args) -> None:
+    """The C entry point with addresses as they are, on the current stream: for calls that are
+    bound by the host, where converting a dozen arguments counts."""
+    st = getattr(lib, name)(*args, _stream(None))
+    if st != FLJSD_OK:
+        raise FljsdError(st, name)
+
+
 def fljsd_verify_workspace_bytes(requests: int, drafts: int) -> int:
     return lib.fljsd_verify_workspace_bytes(requests, drafts)
 

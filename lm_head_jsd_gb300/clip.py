@@ -66,7 +66,7 @@ def table(grads, sizes, dtypes, outs=None):
 
 
 def workspace(count, device):
-    return torch.empty(_lib.fljsd_grad_norm_workspace_bytes(count), dtype=torch.uint8, device=device)
+    return torch.empty(_lib.lib.fljsd_grad_norm_workspace_bytes(count), dtype=torch.uint8, device=device)
 
 
 def grad_norm(grads, *, norm_type=2.0, stream=None):
@@ -78,8 +78,9 @@ def grad_norm(grads, *, norm_type=2.0, stream=None):
     t = table(at, sizes, dtypes)
     with on(stream, dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _lib.fljsd_grad_norm(t.ctypes.data, len(t), kind, 0.0, None, norm, None,
-                             workspace(len(t), dev))
+        ws = workspace(len(t), dev)
+        _lib.call("fljsd_grad_norm", t.ctypes.data, len(t), kind, 0.0, None, norm.data_ptr(), None,
+                  ws.data_ptr(), ws.shape[0])
     hand_over((norm,), stream, dev)
     return norm
 
@@ -105,7 +106,9 @@ def clip_grads(grads, max_norm, *, norm_type=2.0, out=None, stream=None):
     _apart(t, out is not None)
     with on(stream, dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _lib.fljsd_clip_grads(t.ctypes.data, len(t), kind, max_norm, norm, workspace(len(t), dev))
+        ws = workspace(len(t), dev)
+        _lib.call("fljsd_clip_grads", t.ctypes.data, len(t), kind, max_norm, norm.data_ptr(),
+                  ws.data_ptr(), ws.shape[0])
     hand_over((norm,), stream, dev)
     # autograd's own check of what it saved: these have changed
     increment_version(outs)

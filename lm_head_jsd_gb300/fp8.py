@@ -8,7 +8,7 @@ from torch.autograd.graph import increment_version
 from . import _lib
 from ._streams import check_status, hand_over, on, report, require_cuda
 from .api import _DT
-from .low_rank import check_adapters, check_rows
+from .low_rank import add, check_adapters, check_rows
 
 BLOCK = 128
 
@@ -67,9 +67,8 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, adapters=None,
                               y, check_rows("out", y), ws)
         report(status, ws)
         if adapters is not None:
-            ws = torch.empty(_lib.fljsd_low_rank_workspace_bytes(m, count, rank), dtype=torch.uint8, device=dev)
-            _lib.fljsd_low_rank_add(m, k, n, rank, count, x, ldx, a, b, index, factors, _DT[out_dtype],
-                                    y, check_rows("out", y), y, check_rows("out", y), ws)
+            ldo = check_rows("out", y)
+            ws = add(m, n, count, rank, x, ldx, a, b, index, factors, y, ldo, y, ldo)
             if status is not None:
                 torch.maximum(status, ws[:4].view(torch.int32).view(status.shape), out=status)
     if out is None:

@@ -66,6 +66,16 @@ def _refuse(x, n, a, b, index, scales):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
 
 
+def add(tokens, n, count, rank, x, ldx, a, b, index, scales, y, ldy, out, ldo):
+    """The call, of arguments that are checked; its workspace."""
+    size = _lib.lib.fljsd_low_rank_workspace_bytes(tokens, count, rank)
+    ws = torch.empty(size, dtype=torch.uint8, device=y.device)
+    _lib.call("fljsd_low_rank_add", tokens, x.shape[1], n, rank, count, x.data_ptr(), ldx, a.data_ptr(),
+              b.data_ptr(), index.data_ptr(), scales.data_ptr() if scales is not None else None,
+              _lib.DTYPES[_DT[y.dtype]], y.data_ptr(), ldy, out.data_ptr(), ldo, ws.data_ptr(), size)
+    return ws
+
+
 def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, stream=None):
     """y + scales[i] b[i] (a[i] x) for each token, i = index of the token (int64 [tokens]; -1:
     y as it is). y [tokens, n] fp32 or bf16, x [tokens, k] bf16, a [adapters, rank, k] and
@@ -104,9 +114,7 @@ def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, strea
             r = torch.empty((tokens, n), dtype=y.dtype, device=dev)
         else:
             ldr = check_rows("out", out)
-        ws = torch.empty(_lib.fljsd_low_rank_workspace_bytes(tokens, count, rank), dtype=torch.uint8, device=dev)
-        _lib.fljsd_low_rank_add(tokens, x.shape[1], n, rank, count, x, ldx, a, b, index, scales, _DT[y.dtype],
-                                y, ldy, r, ldr, ws)
+        ws = add(tokens, n, count, rank, x, ldx, a, b, index, scales, y, ldy, r, ldr)
         report(status, ws)
     if out is None:
         hand_over((r,), stream, dev)

@@ -95,9 +95,14 @@ def verify_drafts(target_logits, draft_tokens, u_accept, u_draw, *, draft_logits
     with on(stream, dev):
         r = Verified(torch.empty((b, max_drafts + 1), dtype=_I64, device=dev),
                      torch.empty(b, dtype=_I64, device=dev), torch.empty(n, dtype=_F32, device=dev))
-        ws = torch.empty(_lib.fljsd_verify_workspace_bytes(b, n), dtype=torch.uint8, device=dev)
-        _lib.fljsd_verify(b, n, v, max_drafts, _DT[z.dtype], z, ld, draft_logits if n else None, ldd,
-                          draft_tokens, u_accept, u_draw, offsets, each, temperature, *r, ws)
+        size = _lib.lib.fljsd_verify_workspace_bytes(b, n)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _lib.call("fljsd_verify", b, n, v, max_drafts, _lib.DTYPES[_DT[z.dtype]], z.data_ptr(), ld,
+                  draft_logits.data_ptr() if draft_logits is not None and n else None, ldd,
+                  draft_tokens.data_ptr(), u_accept.data_ptr(), u_draw.data_ptr(),
+                  offsets.data_ptr() if offsets is not None else None,
+                  each.data_ptr() if each is not None else None, temperature, r.tokens.data_ptr(),
+                  r.accepted.data_ptr(), r.accept_prob.data_ptr(), ws.data_ptr(), size)
         report(status, ws)
     hand_over(r, stream, dev)
     return r
