@@ -3,7 +3,7 @@
 //
 // Bound by reading and writing y (few tokens of many adapters: by reading their B). The
 // tokens are first sorted by adapter and cut into tiles of up to 64 that share one
-// (k_lr_plan); both products of a tile then run on the tensor cores with the adapter's
+// (k_lr_plan, or by k_lr_shrink itself where there are few); both products of a tile then run on the tensor cores with the adapter's
 // rows as the instruction's 128 rows and the tokens as its columns, so that a tile of one
 // token costs 16 columns and not 128 rows:
 //  - k_lr_shrink: s = scale A x of a tile. A cluster of eight CTAs splits k and adds its
@@ -13,7 +13,7 @@
 //  - k_lr_expand: y + B s for 256 columns at a time. Accumulator rows i of two products
 //    hold columns 2 i and 2 i + 1, so that a thread adds to pairs and a warp to 64
 //    neighbouring columns of a token. On an SM (one CTA, or two): warps that copy B's rows
-//    and y's ahead, one that issues the products, and four groups of four warps, each with a
+//    and y's ahead, one that issues the products, and two or four groups of four warps, each with a
 //    ring of rows of its own (in one ring for all a group could be a round ahead of another),
 //    that take a block each in turn and add to y where it lies in shared memory, from which
 //    it is copied out. (With y read and written by the adding threads, a pair at a time,
