@@ -8,7 +8,7 @@ from torch.autograd.graph import increment_version
 from . import _lib
 from ._streams import check_status, hand_over, on, report, require_cuda
 from .api import _DT
-from .low_rank import add, check_adapters, check_rows
+from .low_rank import add, check_adapters, check_apart, check_rows
 
 BLOCK = 128
 
@@ -39,8 +39,9 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, adapters=None,
     ``x.detach()``, or call under ``torch.no_grad()``). ``adapters``: (a, b, index) or
     (a, b, index, scales), added to the product of a bf16 x by :func:`low_rank_add` (x
     itself is not quantised for them; with bf16 results product and sum are rounded one
-    after the other). ``status``: an int32 on the device that receives the call's status
-    word (0, FLJSD_ERR_TIMEOUT, or with adapters FLJSD_ERR_INVALID_ARG)."""
+    after the other); with them ``out`` shares no memory with them or x. ``status``: an
+    int32 on the device that receives the call's status word (0, FLJSD_ERR_TIMEOUT, or
+    with adapters FLJSD_ERR_INVALID_ARG)."""
     if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad:
         raise ValueError("x requires a gradient, which fp8_linear does not give: pass x.detach()")
     ldx = check_rows("x", x)
@@ -60,6 +61,8 @@ def fp8_linear(x, w_codes, w_scales, *, out_dtype=torch.bfloat16, adapters=None,
     if adapters is not None:
         a, b, index, factors = (*adapters, None)[:4]
         count, rank = check_adapters(x, n, a, b, index, factors)
+        if out is not None:  # (all of them are read after the product is written)
+            check_apart(out, x=x, a=a, b=b, index=index, scales=factors)
     with on(stream, dev):
         y = out if out is not None else torch.empty((m, n), dtype=out_dtype, device=dev)
         ws = torch.empty(_lib.fljsd_fp8_linear_workspace_bytes(m, k), dtype=torch.uint8, device=dev)

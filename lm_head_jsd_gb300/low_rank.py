@@ -22,9 +22,28 @@ def check_rows(name, t):
 
 
 def _span(t):
-    """The addresses that a matrix's elements lie in."""
-    size = t.element_size()
-    return t.data_ptr(), t.data_ptr() + size * ((t.shape[0] - 1) * t.stride(0) + t.shape[1])
+    """The addresses that the elements of a tensor lie in."""
+    last = sum((n - 1) * step for n, step in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + t.element_size() * (last + 1)
+
+
+def check_apart(out, **inputs):
+    """That out shares no memory with what is read after its first element is written."""
+    lo, hi = _span(out)
+    for name, t in inputs.items():
+        if t is not None:
+            begin, end = _span(t)
+            if begin < hi and lo < end and not _beside(out, t):
+                raise ValueError(f"out shares memory with {name}")
+
+
+def _beside(out, t):
+    """Whether two matrices are different columns of one."""
+    pitch = out.stride(0) * out.element_size()
+    if t.dim() != 2 or t.stride(0) * t.element_size() != pitch or not pitch:
+        return False
+    at = (t.data_ptr() - out.data_ptr()) % pitch
+    return out.shape[1] * out.element_size() <= at <= pitch - t.shape[1] * t.element_size()
 
 
 def check_adapters(x, n, a, b, index, scales):
@@ -102,12 +121,8 @@ def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, strea
                 or out.device != dev):
             raise ValueError(f"out must be {y.dtype} [{tokens}, {n}] on {dev}")
         check_rows("out", out)
-        lo, hi = _span(out)
         same = out.data_ptr() == y.data_ptr() and out.stride(0) == y.stride(0)
-        for name, t in (("x", x),) if same else (("y", y), ("x", x)):
-            begin, end = _span(t)
-            if begin < hi and lo < end:
-                raise ValueError(f"out shares memory with {name}")
+        check_apart(out, y=None if same else y, x=x, a=a, b=b, index=index, scales=scales)
     with on(stream, dev):
         r, ldr = out, n
         if out is None:

@@ -288,6 +288,49 @@ def test_refusals_on_the_gpu(fl):
         fl.low_rank_add(**{**z, "b": flat[1:].view_as(z["b"])})
 
 
+def test_what_shares_memory(fl):
+    from lm_head_jsd_gb300.low_rank import check_apart
+
+    buf = torch.zeros(6, 64, dtype=BF)
+    out = buf[:, 16:48]
+    for t in (buf[:, :16], buf[:, 48:], buf[:, 48:64], torch.zeros(6, 32, dtype=BF), None):
+        check_apart(out, x=t)
+    for t in (out, buf, buf[:, :17], buf[:, 47:], buf[2:, 20:24], buf[:, :16].view(torch.int32)[:, :8].as_strided((6, 9), (32, 1)),
+              buf.view(-1)[100:120], buf.view(-1)[64 + 16:64 + 17], buf[1:, :].as_strided((2, 3, 8), (24, 8, 1))):
+        with pytest.raises(ValueError, match="out shares memory with x"):
+            check_apart(out, x=t)
+
+
+@gpu
+@pytest.mark.parametrize("name", ["x", "a", "b", "index", "scales"])
+def test_a_result_on_an_input_is_refused(fl, name):
+    z = _make(64, 64, 64, 16, 2)
+    q = fl.fp8_quantize(torch.randn(64, 64, device="cuda"))
+    buf = torch.zeros(64, 64, dtype=BF, device="cuda")
+    if name == "x":
+        z["x"] = buf
+    else:
+        t = z[name]
+        z[name] = buf.view(-1)[:t.numel() * t.element_size() // 2].view(t.dtype).view(t.shape)
+    with pytest.raises(ValueError, match=f"out shares memory with {name}"):
+        fl.low_rank_add(**z, out=buf)
+    with pytest.raises(ValueError, match=f"out shares memory with {name}"):
+        fl.fp8_linear(z["x"], *q, adapters=(z["a"], z["b"], z["index"], z["scales"]), out=buf)
+
+
+@gpu
+def test_input_and_result_in_columns_of_one_matrix(fl):
+    z = _make(70, 64, 100, 16, 3)
+    want = fl.low_rank_add(**z)
+    buf = torch.full((70, 200), 7.0, dtype=BF, device="cuda")
+    x, out = buf[:, 8:72], buf[:, 80:180]
+    x.copy_(z["x"])
+    before = buf.clone()
+    fl.low_rank_add(**{**z, "x": x}, out=out)
+    assert torch.equal(out, want)
+    assert torch.equal(buf[:, :80], before[:, :80]) and torch.equal(buf[:, 180:], before[:, 180:])
+
+
 @gpu
 def test_versions_rise(fl):
     z = _make(6, 64, 100, 16, 2, dtype=torch.float32)
