@@ -8,9 +8,10 @@
 // k_norm: every thread takes 64 bytes at a time, squares and adds them in fp32, and CTAs
 // write one partial each; k_norm_finish adds the partials in a fixed order in fp64, so
 // that a sum has one value whatever the SMs' order. Squares leave fp32's range beyond
-// 2^64 and below 2^-63: a thread whose 64 bytes add up to less than 2^-100 (or to no
-// finite number) takes them again in fp64, which holds the square of every fp32. That is
-// rare, so the common path pays one comparison for 16 or 32 elements.
+// 2^64 and below 2^-63: a thread whose 64 bytes add up to less than 2^-100, or to 2^96 and
+// more, takes them again in fp64, which holds the square of every fp32 and the sum of all.
+// (2^96: a thread has fewer than 2^31 such sums in a launch, so theirs stays below 2^127.)
+// That is rare, so the common path pays two comparisons for 16 or 32 elements.
 // k_clip walks from the last chunk to the first: what k_norm has read last is still in L2.
 #include "dependent.cuh"
 #include "internal.cuh"
@@ -130,7 +131,7 @@ __device__ __forceinline__ void take(const uint4 (&q)[kVecs], Acc& a) {
     }
   }
   const float c = (s[0].x + s[0].y) + (s[1].x + s[1].y);
-  if (c >= 0x1p-100f && c < INFINITY) {
+  if (c >= 0x1p-100f && c < 0x1p96f) {  // (NaN is not)
     a.sum += c;
   } else {
 #pragma unroll 1
