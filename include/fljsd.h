@@ -647,12 +647,14 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  *  - a token whose draft row is such a row is refused, and drawn from p alone.
  *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets fall,
  *    leave [0, drafts] or span more than max_drafts, or whose temperature on the device is
- *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0 and -1s. Both
- *    set the status word (the workspace's first int32) to FLJSD_ERR_INVALID_ARG.
+ *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0, -1s, and
+ *    accept_prob 0 for its tokens. Both set the status word (the workspace's first int32) to
+ *    FLJSD_ERR_INVALID_ARG.
  *  - FLJSD_ERR_TIMEOUT in the status word: a bounded device wait expired, the results are none.
  *  - u_draw outside [0, 1) is taken to its nearer end, NaN as 0; u_accept of NaN refuses.
- *  - tokens before the first request's and behind the last one's have accept_prob 0: a
- *    buffer may be longer than what a step fills. (offsets given; their rows are not read.)
+ *  - tokens of no request, as those before the first one's and behind the last one's, have
+ *    accept_prob 0: a buffer may be longer than what a step fills. (offsets given; their rows are
+ *    not read.)
  *
  * target and draft in dtype with row strides ld_target and ld_draft (elements, any
  * element alignment); tokens, offsets, out, accepted int64, u_accept [drafts], u_draw,

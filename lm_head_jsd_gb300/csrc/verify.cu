@@ -393,6 +393,11 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
   const int rank = (int)cta_rank();
   let_next_launch();
   if (blockIdx.x == 0 && tid == 0) *a.status = 0;
+  // what belongs to no request, or to one that is refused, is accepted with 0: k_verify_draw
+  // writes the other requests' over it
+  if (a.offsets || a.temperature)
+    for (int64_t i = (int64_t)blockIdx.x * (kRowThreads + 32) + tid; i < a.n; i += (int64_t)gridDim.x * (kRowThreads + 32))
+      a.prob[i] = 0.f;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sh.full[i], 1);
@@ -969,14 +974,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
       if (i != accepted || token != -2)
         a.out[b * (a.max_drafts + 1) + i] = i < accepted ? a.tokens[q.start + i] : i == accepted ? token : -1;
     if (tid == 0) a.accepted[b] = accepted;
-    if (warp == 0) {
-      tell();
-      // drafts before the requests' and behind them are none
-      if (b == 0 && a.offsets)
-        for (int64_t i = lane; i < a.n && i < a.offsets[0]; i += 32) a.prob[i] = 0.f;
-      if (b == a.requests - 1 && a.offsets)
-        for (int64_t i = max((int64_t)0, a.offsets[b + 1]) + lane; i < a.n; i += 32) a.prob[i] = 0.f;
-    }
+    if (warp == 0) tell();
   }
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another writes to it
 }
