@@ -645,8 +645,9 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  *  - a logit of -inf has probability 0. A target row of nothing else, or with a NaN or
  *    +inf, accepts nothing; if a token is to be drawn from it, that is -1.
  *  - a token whose draft row is such a row is refused, and drawn from p alone.
- *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets fall,
- *    leave [0, drafts] or span more than max_drafts, or whose temperature on the device is
+ *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets leave
+ *    [0, drafts] or span more than max_drafts, every request from the first one on whose offsets
+ *    fall, and a request whose temperature on the device is
  *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0, -1s, and
  *    accept_prob 0 for its tokens. Both set the status word (the workspace's first int32) to
  *    FLJSD_ERR_INVALID_ARG.

@@ -47,6 +47,7 @@ constexpr float kC1 = 12.f, kC2 = 0x1.8p-20f;
 constexpr uint32_t kBits1 = 0x41400000u, kBits2 = 0x35c00000u;
 constexpr unsigned long long kNone = ~0ull;
 constexpr double kLog2e = 1.4426950408889634;
+constexpr int kNoFall = 0x7fffffff;
 constexpr float kLeastT = 0x1.7154780000000p-128f;  // the least T with a finite log2(e) / T in fp32
 
 enum { kRowOk = 0, kRowBad = 1 };  // bad: NaN, +inf, or nothing but -inf
@@ -76,6 +77,7 @@ struct Args {
   int64_t* accepted;
   float* prob;
   int* status;
+  int* fall;  // the first request whose offsets fall, or kNoFall (offsets given)
   RowStat* stat_t;
   RowStat* stat_d;
 };
@@ -267,14 +269,14 @@ struct Row {
   int64_t at;     // the drafted token in question, -1 behind the last
 };
 template <typename T>
-__device__ __forceinline__ Row row_of(const Args& a, int64_t unit) {
+__device__ __forceinline__ Row row_of(const Args& a, int64_t unit, int fall) {
   Row r{};
   const int b = (int)((uint32_t)unit / (uint32_t)a.slots);  // (fewer than 2^31)
   const int slot = (int)unit - b * a.slots;
   const Request q = request(a, b);
   r.is_draft = slot > a.max_drafts;
   const int j = r.is_draft ? slot - a.max_drafts - 1 : slot;
-  if (!q.ok || j >= q.drafts + (r.is_draft ? 0 : 1) || (r.is_draft && q.t == 0.f)) return r;
+  if (!q.ok || b >= fall || j >= q.drafts + (r.is_draft ? 0 : 1) || (r.is_draft && q.t == 0.f)) return r;
   r.c = q.t == 0.f ? 0.f : a.temperature ? (float)(kLog2e / (double)q.t) : a.c;
   r.at = j < q.drafts ? q.start + j : -1;
   r.stat = r.is_draft ? q.start + j : q.start + j + b;
@@ -396,8 +398,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
   // what belongs to no request, or to one that is refused, is accepted with 0: k_verify_draw
   // writes the other requests' over it
   if (a.offsets || a.temperature)
-    for (int64_t i = (int64_t)blockIdx.x * (kRowThreads + 32) + tid; i < a.n; i += (int64_t)gridDim.x * (kRowThreads + 32))
-      a.prob[i] = 0.f;
+    for (int i = blockIdx.x * (kRowThreads + 32) + tid; i < (int)a.n; i += gridDim.x * (kRowThreads + 32)) a.prob[i] = 0.f;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sh.full[i], 1);
@@ -439,6 +440,21 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       const float zd = __shfl_sync(0xffffffffu, mine_zd, lane_of);
       if (lane == 0) sh.own[j % kRing].zd = zd;
     };
+    // From the first offsets that fall on, a request may claim rows that others have too: whose
+    // statistics stood in the end would be chance. So none of them is taken.
+    int fall = kNoFall, seen = 0;
+    auto look_for_fall = [&](int requests) {
+      while (seen < requests && fall == kNoFall) {
+        int first = kNoFall;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const int b = seen + i * 32 + lane;
+          if (b < requests && a.offsets[b] > a.offsets[b + 1]) first = b;
+        }
+        fall = __reduce_min_sync(0xffffffffu, first);
+        seen = min(seen + 256, requests);
+      }
+    };
     bool waiting = false;  // row 0's logit is not looked up yet: the first copies go before it
     int src_first = 0;
     auto catch_up = [&]() {
@@ -449,7 +465,11 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       while (!found && first_unit < units) {
         catch_up();
         const uint64_t unit = first_unit + (uint64_t)lane * step;
-        mine = unit < units ? row_of<T>(a, (int64_t)unit) : Row{};
+        if (a.offsets) {
+          const uint64_t last = first_unit + 31ull * step;
+          look_for_fall((int)((last < units ? (uint32_t)last : units - 1) / (uint32_t)a.slots) + 1);
+        }
+        mine = unit < units ? row_of<T>(a, (int64_t)unit, fall) : Row{};
         if (mine.z) {
           const Cut<T> cut(reinterpret_cast<const T*>(mine.z), a.v, a.cluster, rank);
           mine_j0 = (int64_t)cut.first * N - cut.lead;
@@ -561,6 +581,10 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       next = after;
     }
     if (rank == 0 && i > 0) finish(i - 1);
+    if (a.offsets && blockIdx.x == 0) {
+      look_for_fall((int)a.requests);
+      if (lane == 0) *a.fall = fall;
+    }
     for (int j = max(0, brought - 2); j < brought; ++j)  // no copy is under way at the end
       for (int it = 0; it < (1 << 22) && !bar_try(at_shared(&sh.full[j & 1]), (j >> 1) & 1); ++it) {
       }
@@ -760,7 +784,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   const int64_t b = blockIdx.x / a.cluster;
   if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
   wait_for_previous();
-  const Request q = request(a, b);
+  Request q = request(a, b);
+  if (a.offsets && b >= *a.fall) {
+    q.ok = false;
+    q.drafts = 0;
+  }
   const bool greedy = q.t == 0.f;
   // the tests, a lane to each; every CTA of the cluster makes them
   double pd = 0.0, qd = -1.0;  // of this lane's last test; qd < 0: refused anyway
@@ -1129,6 +1157,7 @@ extern "C" fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v
   a.accepted = accepted;
   a.prob = accept_prob;
   a.status = reinterpret_cast<int*>(workspace);
+  a.fall = a.status + 1;
   a.stat_t = reinterpret_cast<RowStat*>(reinterpret_cast<char*>(workspace) + kStatusBytes);
   a.stat_d = a.stat_t + requests + drafts;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

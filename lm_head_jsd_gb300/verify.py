@@ -46,7 +46,8 @@ def verify_drafts(target_logits, draft_tokens, u_accept, u_draw, *, draft_logits
     [0, 1) (fp32): ``u_accept`` one for each drafted token, ``u_draw`` one for each request.
 
     ``offsets`` [requests + 1] (int64, on the device): request b drafted
-    draft_tokens[offsets[b]:offsets[b + 1]], at most ``max_drafts`` of them; None: all as
+    draft_tokens[offsets[b]:offsets[b + 1]], at most ``max_drafts`` of them (requests that
+    offsets describe wrongly, and all from the first that fall on, are refused); None: all as
     many. ``target_logits`` [drafts + requests, v], fp32 or bf16: request b's rows from
     offsets[b] + b on, one in front of each drafted token and one behind the last;
     ``draft_logits`` [drafts, v]: what each was drafted from (None: they have no

@@ -92,3 +92,30 @@ def test_a_long_buffer_of_refused_requests(fl):
     n = 300_000
     out, acc, prob, status = _run(fl, _inputs(n, 2, v=2), [0, n // 2, n], 1, [1.0, 1.0])
     assert status == 1 and not prob.any() and not acc.any() and (out == -1).all()
+
+
+# From the first offsets that fall on nothing is taken: what comes then claims tokens and rows that others have too,
+# at a temperature of its own.
+FALLS = [([0, 2, 1, 3], 2), ([0, 5, 3, 6], 5), ([0, 5, 2, 4, 6, 8], 5), ([4, 8, 0, 3, 6, 9], 4), ([0, 3, 2, 6, 1, 12], 12),
+         ([0, 1 << 40, 2, 4], 4), ([3, 0, 3, 6], 3), ([0, 4, 4, 3, 7, 7, 12], 4)]
+
+
+@pytest.mark.parametrize("offsets,max_drafts", FALLS, ids=str)
+def test_offsets_that_fall(fl, offsets, max_drafts):
+    b = len(offsets) - 1
+    fall = next(i for i in range(b) if offsets[i] > offsets[i + 1])
+    valid = [i < fall and 0 <= offsets[i] <= offsets[i + 1] <= 12 and offsets[i + 1] - offsets[i] <= max_drafts for i in range(b)]
+    for seed in range(5):
+        _check(fl, _inputs(12, b, v=5000, seed=seed), offsets, max_drafts, [0.5 + 0.3 * i for i in range(b)], valid)
+
+
+@pytest.mark.parametrize("fall", [0, 1, 255, 256, 700, 2999])
+def test_offsets_that_fall_among_many(fl, fall):
+    b, n = 3000, 6000
+    x, t = _inputs(n, b, v=40), [0.5 + (i % 7) * 0.2 for i in range(b)]
+    ends = [2 * i for i in range(b + 1)]
+    out, acc, prob, status = _run(fl, x, ends, 2, t)
+    assert status == 0
+    o, a, p, status = _run(fl, x, ends[:fall + 1] + [e - 3 for e in ends[fall + 1:]], 2, t)
+    assert status == 1 and torch.equal(o[:fall], out[:fall]) and torch.equal(a[:fall], acc[:fall]) and torch.equal(p[:2 * fall], prob[:2 * fall])
+    assert (o[fall:] == -1).all() and not a[fall:].any() and not p[2 * fall:].any()
