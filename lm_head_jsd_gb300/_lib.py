@@ -170,6 +170,8 @@ def _load():
     lib.fljsd_status_string.restype = ctypes.c_char_p
     lib.fljsd_capture_id.argtypes = [P]
     lib.fljsd_capture_id.restype = ctypes.c_uint64
+    lib.fljsd_test_stall.argtypes = [ctypes.c_int32]
+    lib.fljsd_test_stall.restype = None
     lib.fljsd_launch_count.argtypes = []
     lib.fljsd_launch_count.restype = ctypes.c_int64
     lib.fljsd_launch_count_reset.argtypes = []
@@ -557,6 +559,13 @@ def fljsd_fp8_linear(m, n, k, x_dtype, x, ldx, w_codes, ldw, w_scales, out_dtype
 
 def fljsd_capture_id(stream=None) -> int:
     return lib.fljsd_capture_id(_stream(stream))
+
+
+FLJSD_STALL_VERIFY = 1
+
+
+def fljsd_test_stall(kernels: int) -> None:
+    lib.fljsd_test_stall(kernels)
 
 
 def fljsd_launch_count() -> int:

@@ -17,6 +17,7 @@ namespace fljsd {
 // ---------------------------------------------------------------------------
 namespace {
 std::atomic<int64_t> g_launches{0};
+std::atomic<int> g_stall{0};
 
 struct Trace {
   std::mutex mu;
@@ -37,6 +38,8 @@ void trace_release() {
   g_trace.open = -1;
 }
 }  // namespace
+
+int stalled() { return g_stall.load(std::memory_order_relaxed); }
 
 void trace_begin(int kind, cudaStream_t st) {
   g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -344,6 +347,8 @@ fljsd_status fljsd_backward(const fljsd_problem* p, const float* grad_output, vo
     return FLJSD_ERR_CUDA;
   return FLJSD_OK;
 }
+
+void fljsd_test_stall(int32_t kernels) { g_stall.store(kernels, std::memory_order_relaxed); }
 
 fljsd_status fljsd_workspace_status(const fljsd_plan_t* plan, const void* workspace,
                                     fljsd_stream_t stream_, int32_t* device_status) {

@@ -18,6 +18,10 @@ void trace_end(int kind, cudaStream_t st);
 // counts a kernel launched inside a traced call beyond the call's first
 void count_extra_launch();
 
+// The FLJSD_STALL_* bits of fljsd_test_stall, and the limit of the waits that they shorten.
+int stalled();
+constexpr unsigned long long kStallNs = 50ull * 1000 * 1000;
+
 // Number of SMs of the current device (cached per device).
 int num_sms();
 

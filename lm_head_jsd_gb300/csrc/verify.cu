@@ -46,6 +46,7 @@ constexpr double kUnit = 0x1p43;
 constexpr float kC1 = 12.f, kC2 = 0x1.8p-20f;
 constexpr uint32_t kBits1 = 0x41400000u, kBits2 = 0x35c00000u;
 constexpr unsigned long long kNone = ~0ull;
+constexpr unsigned long long kWaitNs = 4ull * 1000 * 1000 * 1000;  // a wait's limit
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kNoFall = 0x7fffffff;
 constexpr float kLeastT = 0x1.7154780000000p-128f;  // the least T with a finite log2(e) / T in fp32
@@ -77,7 +78,9 @@ struct Args {
   int64_t* accepted;
   float* prob;
   int* status;
-  int* fall;  // the first request whose offsets fall, or kNoFall (offsets given)
+  unsigned long long wait_ns;
+  bool stall;  // (a test's) the last CTA of a cluster copies nothing
+  int* fall;   // the first request whose offsets fall, or kNoFall (offsets given)
   RowStat* stat_t;
   RowStat* stat_d;
 };
@@ -293,7 +296,6 @@ struct Part {
   float c;
 };
 constexpr int kRing = 4, kTopRing = 8;
-constexpr unsigned long long kWaitNs = 4ull * 1000 * 1000 * 1000;
 struct RowsShared {  // by the row's number
   unsigned long long full[2], empty[2];       // a row's copy has landed; it has moved on to registers
   unsigned long long tops[kTopRing], sums[kRing];  // the cluster's have arrived
@@ -333,29 +335,38 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ unsigned long long now() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void pause() {  // 100 us
+  const unsigned long long t0 = now();
+  while (now() - t0 < 100'000) __nanosleep(1000);
+}
 // With a limit, after which the CTA's waits all end and the call's status word says so.
-__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
-  unsigned long long t0 = 0, t;
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, const Args& a) {
+  unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
     if (bar_try(bar, parity)) return true;
     if ((it & 255u) == 255u) {  // (reading the timer takes longer than most waits)
       if (*abort) return false;
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      const unsigned long long t = now();
       if (!t0) t0 = t;
-      if (t - t0 > kWaitNs) {
+      if (t - t0 > a.wait_ns) {
         *abort = 1;
-        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        atomicExch(a.status, (int)FLJSD_ERR_TIMEOUT);
         return false;
       }
     }
   }
 }
 // (by whole warps: all go on, or none)
-__device__ __forceinline__ bool bar_wait(const void* bar, uint32_t parity, volatile int* abort, int* status) {
+__device__ __forceinline__ bool bar_wait(const void* bar, uint32_t parity, volatile int* abort, const Args& a) {
   const uint32_t b = at_shared(bar);
   bool ok = bar_try(b, parity);
   if (!__all_sync(0xffffffffu, ok)) {
-    if (!ok) ok = bar_wait_long(b, parity, abort, status);
+    if (!ok) ok = bar_wait_long(b, parity, abort, a);
     ok = __all_sync(0xffffffffu, ok) != 0;
   } else {
     ok = true;
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
     return m;
   };
-  auto has_tops = [&](int i) { return bar_wait(&sh.tops[i % kTopRing], (i / kTopRing) & 1, &sh.abort, a.status); };
+  auto has_tops = [&](int i) { return bar_wait(&sh.tops[i % kTopRing], (i / kTopRing) & 1, &sh.abort, a); };
   if (warp == kRowWarps) {  // ---------------- control ----------------
     // Rows are looked for 32 units at a time, a lane to each.
     const uint32_t units = (uint32_t)(a.requests * a.slots), step = gridDim.x / a.cluster;
@@ -489,7 +500,9 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     // row j into its place; false: there is none
     auto bring = [&](int j, bool& ok) {
       const bool there = next_row();
-      if (j >= 2) ok = bar_wait(&sh.empty[j & 1], ((j >> 1) & 1) ^ 1, &sh.abort, a.status) && ok;
+      // (where that wait ran out the place and its barriers are not touched)
+      if (j >= 2 && !bar_wait(&sh.empty[j & 1], ((j >> 1) & 1) ^ 1, &sh.abort, a)) ok = false;
+      if (!ok) return false;
       Part q{};
       if (there) {
         q.z = reinterpret_cast<const void*>(__shfl_sync(0xffffffffu, (unsigned long long)mine.z, src));
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
         hi = min(hi, most);
         uint4* to = s_rows + (j & 1) * most;
         const uint32_t bytes = (uint32_t)(hi - lo) * 16;
-        if (lane == 0 && bytes) {  // (counted below: the row is not there before that)
+        if (lane == 0 && bytes && !(a.stall && rank == a.cluster - 1)) {  // (counted below: the row is not there before that)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -541,7 +554,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     };
     // what row i leaves to be written
     auto finish = [&](int i) {
-      if (!bar_wait(&sh.sums[i % kRing], (i / kRing) & 1, &sh.abort, a.status)) return;
+      if (!bar_wait(&sh.sums[i % kRing], (i / kRing) & 1, &sh.abort, a)) return;
       const auto& own = sh.own[i % kRing];
       const bool greedy = own.row.c == 0.f;
       unsigned long long sum = greedy ? kNone : 0ull;
@@ -571,7 +584,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     int i = 0, brought = here ? 2 : 1;
     for (; here && ok; ++i) {
       const bool after = next && bring(i + 2, ok);
-      brought += next;
+      brought += next && ok;
       if (rank == 0 && i > 0) finish(i - 1);
       ok = has_tops(i) && ok;
       const float m = top_of(i);
@@ -585,8 +598,11 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       look_for_fall((int)a.requests);
       if (lane == 0) *a.fall = fall;
     }
+    unsigned long long t0 = 0;
     for (int j = max(0, brought - 2); j < brought; ++j)  // no copy is under way at the end
-      for (int it = 0; it < (1 << 22) && !bar_try(at_shared(&sh.full[j & 1]), (j >> 1) & 1); ++it) {
+      while (!bar_try(at_shared(&sh.full[j & 1]), (j >> 1) & 1)) {
+        if (!t0) t0 = now();
+        if (now() - t0 > a.wait_ns) break;
       }
   } else {  // ---------------- columns ----------------
     auto rest = [&](const Part& q, auto&& f) {  // vectors beyond those kept, read again
@@ -595,7 +611,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     };
     // whether there is a row i, whose maximum is sent
     auto send_top = [&](int i) {
-      if (!bar_wait(&sh.full[i & 1], (i >> 1) & 1, &sh.abort, a.status)) return false;
+      if (!bar_wait(&sh.full[i & 1], (i >> 1) & 1, &sh.abort, a)) return false;
       const Part& q = part_of(i);
       if (!q.z) return false;
       const uint4* mine = s_rows + (i & 1) * kKept * kRowThreads + tid;
@@ -665,7 +681,12 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       if (lane == 0) send(&sh.sum[i % kRing][rank * kRowWarps + warp], &sh.sums[i % kRing], 0, sum);
     }
   }
-  cluster_sync();  // no CTA leaves while another sends to it
+  // No CTA leaves while another sends to it. (Where a wait ran out, what was sent last has not
+  // been waited for: a pause for what this CTA sent, and one for what others did.)
+  const bool aborted = sh.abort != 0;
+  if (aborted) pause();
+  cluster_sync();
+  if (aborted) pause();
 }
 
 // Columns [j, j + N) of a row that lies to 16 bytes otherwise than j does: from the two
@@ -1158,6 +1179,8 @@ extern "C" fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v
   a.prob = accept_prob;
   a.status = reinterpret_cast<int*>(workspace);
   a.fall = a.status + 1;
+  a.stall = (stalled() & FLJSD_STALL_VERIFY) != 0;
+  a.wait_ns = a.stall ? kStallNs : kWaitNs;
   a.stat_t = reinterpret_cast<RowStat*>(reinterpret_cast<char*>(workspace) + kStatusBytes);
   a.stat_d = a.stat_t + requests + drafts;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -1,0 +1,64 @@
+"""Failure detection without a GPU fault: the bounded waits of verification and of the adapters. What others wait for is
+left out, their waits expire after 50 ms, and the status word says so; the next call on the same context is right."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, TIMEOUT = torch.bfloat16, 5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def fl():
+    from conftest import build_library
+
+    build_library()
+    import lm_head_jsd_gb300 as fl
+
+    return fl
+
+
+@pytest.fixture
+def stall(fl):
+    """Switches a kernel's stall on, and off again whatever happens."""
+    yield fl._lib.fljsd_test_stall
+    fl._lib.fljsd_test_stall(0)
+    torch.cuda.synchronize()
+
+
+def _drafts(v, dtype, requests=3, drafts=5, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    n = requests * drafts
+    z = (torch.randn(n + requests, v, device="cuda", generator=g) * 3).to(dtype)
+    zd = (torch.randn(n, v, device="cuda", generator=g) * 3).to(dtype)
+    tok = torch.randint(0, v, (n,), device="cuda", generator=g)
+    return dict(target_logits=z, draft_tokens=tok, u_accept=torch.rand(n, device="cuda", generator=g),
+                u_draw=torch.rand(requests, device="cuda", generator=g), draft_logits=zd)
+
+
+# one CTA to a row, clusters of two and more, rows of which each CTA keeps a part only
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("v", [500, 20000, 128256, 400000])
+def test_verification(fl, stall, v, dtype):
+    x = _drafts(v, dtype)
+    want = fl.verify_drafts(**x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stall(fl._lib.FLJSD_STALL_VERIFY)
+    fl.verify_drafts(**x, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == TIMEOUT
+    stall(0)
+    got = fl.verify_drafts(**x, status=status)
+    assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_verification_of_more_rows_than_clusters(fl, stall):
+    x = _drafts(3000, BF, requests=400)
+    want = fl.verify_drafts(**x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stall(fl._lib.FLJSD_STALL_VERIFY)
+    fl.verify_drafts(**x, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == TIMEOUT
+    stall(0)
+    got = fl.verify_drafts(**x, status=status)
+    assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
