@@ -861,7 +861,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
     refuse = __any_sync(0xffffffffu, refuse);
     if (lane == 0) {
       sh.accepted = accepted;
-      if (refuse && rank == 0) atomicExch(a.status, (int)FLJSD_ERR_INVALID_ARG);
+      // (a wait of k_verify_rows that ran out stays known: there are no results then)
+      static_assert((int)FLJSD_ERR_TIMEOUT > (int)FLJSD_ERR_INVALID_ARG, "the greater one stays");
+      if (refuse && rank == 0) atomicMax(a.status, (int)FLJSD_ERR_INVALID_ARG);
     }
   }
   __syncthreads();

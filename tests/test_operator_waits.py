@@ -62,3 +62,21 @@ def test_verification_of_more_rows_than_clusters(fl, stall):
     stall(0)
     got = fl.verify_drafts(**x, status=status)
     assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("bad", ["token", "temperature", "offsets"])
+def test_verification_of_a_bad_request(fl, stall, bad):
+    """That there are no results is known whatever is wrong with a request."""
+    x, status = _drafts(3000, BF), torch.zeros(1, dtype=torch.int32, device="cuda")
+    if bad == "token":
+        x["draft_tokens"][2] = -1
+    elif bad == "temperature":
+        x["temperature"] = torch.tensor([1.0, -1.0, 1.0], device="cuda")
+    else:
+        x |= dict(offsets=torch.tensor([0, 5, 11, 15], device="cuda"), max_drafts=5)
+    fl.verify_drafts(**x, status=status)
+    assert status.item() == 1
+    stall(fl._lib.FLJSD_STALL_VERIFY)
+    fl.verify_drafts(**x, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == TIMEOUT
