@@ -682,11 +682,14 @@ fljsd_status fljsd_verify(int64_t requests, int64_t drafts, int64_t v, int32_t m
  * it: the two calls belong to one capture, or to none. */
 uint64_t fljsd_capture_id(fljsd_stream_t stream);
 
-/* Test of the failure paths of fljsd_verify: in calls made from now on the kernels named by
- * FLJSD_STALL_* bits leave out something that others wait for, so that their bounded waits expire,
- * after 50 ms: the status word then holds FLJSD_ERR_TIMEOUT, and the context stays usable. 0: as
- * usual. Process-global. */
-#define FLJSD_STALL_VERIFY 1 /* the copies of one CTA of each cluster */
+/* Test of the failure paths of fljsd_verify and fljsd_low_rank_add: in calls made from now on the
+ * kernels named by FLJSD_STALL_* bits wait for something that does not come, so that their
+ * bounded waits expire, after 50 ms: the status word then holds FLJSD_ERR_TIMEOUT, and the context
+ * stays usable. 0: as usual. Process-global. */
+#define FLJSD_STALL_VERIFY 1          /* the copies of one CTA of each cluster */
+#define FLJSD_STALL_LOW_RANK_FIRST 2  /* the products A x */
+#define FLJSD_STALL_LOW_RANK_SECOND 4 /* the copies of B */
+#define FLJSD_STALL_LOW_RANK_Y 8      /* the copies of y */
 void fljsd_test_stall(int32_t kernels);
 
 /* Static, human-readable name of a status code. Never NULL. */

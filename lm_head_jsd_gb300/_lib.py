@@ -561,7 +561,7 @@ def fljsd_capture_id(stream=None) -> int:
     return lib.fljsd_capture_id(_stream(stream))
 
 
-FLJSD_STALL_VERIFY = 1
+FLJSD_STALL_VERIFY, FLJSD_STALL_LOW_RANK_FIRST, FLJSD_STALL_LOW_RANK_SECOND, FLJSD_STALL_LOW_RANK_Y = 1, 2, 4, 8
 
 
 def fljsd_test_stall(kernels: int) -> None:

@@ -71,6 +71,10 @@ struct Args {
   Tile* tiles;
   int* order;
   int parts;  // of s: two or three bf16
+  unsigned long long wait_ns;  // a wait's limit
+  // A test's: no product A x; bytes that are waited for and do not come, of B and of y.
+  bool no_first;
+  uint32_t more_b, more_y;
   char* s;  // a tile's s as it lies in shared memory: parts of kTile rows
 };
 
@@ -116,16 +120,16 @@ __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* row, in
   }
 }
 
-// Waits with a limit (10 s), after which the call's status word says so.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int* status) {
+// Waits with a limit, after which the call's status word says so.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Args& a) {
   unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 255u) {  // (reading the timer takes longer than most waits)
       const unsigned long long t = globaltimer();
       if (!t0) t0 = t;
-      if (t - t0 > kTimeoutNs) {
-        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+      if (t - t0 > a.wait_ns) {
+        atomicExch(a.status, (int)FLJSD_ERR_TIMEOUT);
         return false;
       }
     }
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
     copies_wait<kStages - 2>();
     fence_proxy_async_smem();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && !a.no_first) {
       tc_fence_after();
       const uint32_t xs = base + (uint32_t)stage * stage_bytes, as = xs + kXStage;
 #pragma unroll
@@ -343,14 +347,14 @@ __global__ void __launch_bounds__(kThreads) k_lr_shrink(const Args a) {
     }
     __syncwarp();
     if (c + kStages - 1 < c1) {  // the stage before this one's is free once its products have run
-      if (i > 0 && ok) ok = wait(smem_u32(&s_free[(i - 1) % kStages]), ((i - 1) / kStages) & 1, a.status);
+      if (i > 0 && ok) ok = wait(smem_u32(&s_free[(i - 1) % kStages]), ((i - 1) / kStages) & 1, a);
       ask(c + kStages - 1);
     }
     copies_commit();
   }
   copies_wait<0>();
   const int used = (int)(c1 - c0);
-  if (used > 0) ok = wait(smem_u32(&s_free[(used - 1) % kStages]), ((used - 1) / kStages) & 1, a.status) && ok;
+  if (used > 0) ok = wait(smem_u32(&s_free[(used - 1) % kStages]), ((used - 1) / kStages) & 1, a) && ok;
   if (!ok) s_ok = 0;
   tc_fence_after();
   __syncwarp();
@@ -480,7 +484,7 @@ struct ExpandShared {
 // Waits with a limit, after which the CTA's all end and the call's status word says so.
 // (By whole warps. A barrier has one waiting warp or group, which waits for its every phase.)
 template <int GROUPS>
-__device__ __forceinline__ bool wait_all(ExpandShared<GROUPS>* sh, const void* bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool wait_all(ExpandShared<GROUPS>* sh, const void* bar, uint32_t parity, const Args& a) {
   const uint32_t b = smem_u32(bar);
   bool ok = mbar_try_wait(b, parity);
   unsigned long long t0 = 0;
@@ -490,14 +494,29 @@ __device__ __forceinline__ bool wait_all(ExpandShared<GROUPS>* sh, const void* b
       if (sh->abort) break;
       const unsigned long long t = globaltimer();
       if (!t0) t0 = t;
-      if (t - t0 > kTimeoutNs) {
+      if (t - t0 > a.wait_ns) {
         sh->abort = 1;
-        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
+        atomicExch(a.status, (int)FLJSD_ERR_TIMEOUT);
         break;
       }
     }
   }
   return __all_sync(0xffffffffu, ok) != 0;
+}
+// At the end, for copies and products still under way: with the same limit, all of a warp's
+// together, and not cut short by a wait that has run out elsewhere.
+__device__ __forceinline__ void wait_last(const void* bar, uint32_t parity, unsigned long long& t0, const Args& a) {
+  const uint32_t b = smem_u32(bar);
+  for (uint32_t it = 0; !mbar_try_wait(b, parity); ++it) {
+    if ((it & 255u) != 255u) continue;
+    const unsigned long long t = globaltimer();
+    if (!t0) t0 = t;
+    if (t - t0 > a.wait_ns) {
+      atomicExch(a.status, (int)FLJSD_ERR_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
 }
 
 // A place in a ring and the parity of its round. (A division for each use of one took the
@@ -581,7 +600,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
       if (tile.adapter < 0) continue;
       const uint32_t si = s_ring.at;
-      ok = wait_all(&sh, &sh.s_empty[si], s_ring.round ^ 1, a.status);
+      ok = wait_all(&sh, &sh.s_empty[si], s_ring.round ^ 1, a);
       if (!ok) break;
       if (elect_one()) {
         const uint32_t bar = smem_u32(&sh.s_full[si]), to = s_at + si * kParts * s_half;
@@ -601,11 +620,11 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       const int64_t row0 = (int64_t)tile.adapter * a.n;
       for (uint32_t b = b0; b < b0 + a.blocks && b < num_blocks; ++b) {
         const uint32_t st = b_ring.at;
-        ok = wait_all(&sh, &sh.b_empty[st], b_ring.round ^ 1, a.status);
+        ok = wait_all(&sh, &sh.b_empty[st], b_ring.round ^ 1, a);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t bar = smem_u32(&sh.b_full[st]);
-          mbar_arrive_expect_tx(bar, stage);
+          mbar_arrive_expect_tx(bar, stage + a.more_b);
           const int64_t row = row0 + (int64_t)b * kCols;
           for (int h = 0; h < 2; ++h)
             for (int x = 0; x < a.boxes; ++x)
@@ -618,13 +637,14 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       }
     }
     // no copy is under way at the end
+    unsigned long long t0 = 0;
     for (uint32_t i = 0; i < (uint32_t)a.stages && i < filled; ++i) {
       const uint32_t f = filled - 1 - i;
-      wait_all(&sh, &sh.b_full[f % a.stages], (f / a.stages) & 1, a.status);
+      wait_last(&sh.b_full[f % a.stages], (f / a.stages) & 1, t0, a);
     }
     for (uint32_t i = 0; i < (uint32_t)a.s_bufs && i < s_filled; ++i) {
       const uint32_t f = s_filled - 1 - i;
-      wait_all(&sh, &sh.s_full[f % a.s_bufs], (f / a.s_bufs) & 1, a.status);
+      wait_last(&sh.s_full[f % a.s_bufs], (f / a.s_bufs) & 1, t0, a);
     }
   } else if (warp == GROUPS * 4 + 1) {
     // ---------------- products ----------------
@@ -642,13 +662,13 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       if (k + gridDim.x < jobs) next = a.tiles[(k + gridDim.x) / stretches];
       if (tile.adapter < 0) continue;
       const uint32_t si = s_ring.at;
-      ok = wait_all(&sh, &sh.s_full[si], s_ring.round, a.status);
+      ok = wait_all(&sh, &sh.s_full[si], s_ring.round, a);
       const uint64_t s0d = s_first + si * (kParts * s_next);
       const uint32_t id = idesc_of((tile.count + 15) / 16 * 16);
       for (uint32_t c = 0; ok && c < (uint32_t)a.blocks && b0 + c < num_blocks; ++c) {
         const uint32_t g = (seq + c) % GROUPS, st = b_ring.at;
-        ok = wait_all(&sh, &sh.acc_empty[g], ((used >> g) & 1) ^ 1, a.status) &&
-             wait_all(&sh, &sh.b_full[st], b_ring.round, a.status);
+        ok = wait_all(&sh, &sh.acc_empty[g], ((used >> g) & 1) ^ 1, a) &&
+             wait_all(&sh, &sh.b_full[st], b_ring.round, a);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -674,8 +694,9 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       }
       s_ring.next(a.s_bufs);
     }
+    unsigned long long t0 = 0;
     if (last_group < GROUPS)  // no product runs at the end
-      wait_all(&sh, &sh.acc_full[last_group], ((used >> last_group) & 1) ^ 1, a.status);
+      wait_last(&sh.acc_full[last_group], ((used >> last_group) & 1) ^ 1, t0, a);
   } else if (warp >= GROUPS * 4 + 2) {
     // ---------------- y's rows for a group, a lane to each ----------------
     const uint32_t g = warp - (GROUPS * 4 + 2);
@@ -717,7 +738,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
         for (int j0 = 0; j0 < tile.count; j0 += kChunk) {
           const uint32_t slot = g * a.slots + ring.at;
           if (a.slots == 1) settle();
-          ok = wait_all(&sh, &sh.y_empty[slot], ring.round ^ 1, a.status);
+          ok = wait_all(&sh, &sh.y_empty[slot], ring.round ^ 1, a);
           if (!ok) break;
           const int r = lane % kChunk, j = j0 + r;
           const int token = __shfl_sync(0xffffffffu, j0 < 32 ? t0 : t1, j & 31);
@@ -745,7 +766,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
               if (e < kept) kept_value[e] = p[e];
           }
           open_bar = smem_u32(&sh.y_full[slot]);
-          open_bytes = all;
+          open_bytes = all + a.more_y;
           if (ALIGNED) settle();
           ring.next(a.slots);
           ++filled;
@@ -753,9 +774,10 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
       }
     }
     settle();
+    unsigned long long since = 0;
     for (uint32_t i = 0; i < (uint32_t)a.slots && i < filled; ++i) {  // no copy is under way at the end
       const uint32_t f = filled - 1 - i;
-      wait_all(&sh, &sh.y_full[g * a.slots + f % a.slots], (f / a.slots) & 1, a.status);
+      wait_last(&sh.y_full[g * a.slots + f % a.slots], (f / a.slots) & 1, since, a);
     }
   } else {
     // ---------------- sums ----------------
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
           const int held = j0 < 32 ? t0 : t1;  // (by lane j & 31)
           const int held_lead = j0 < 32 ? lead0 : lead1;
           if (adds && ch == 0) {
-            ok = ok && wait_all(&sh, &sh.acc_full[g], used & 1, a.status);
+            ok = ok && wait_all(&sh, &sh.acc_full[g], used & 1, a);
             tc_fence_after();
           }
           uint32_t d0[kChunk], d1[kChunk];
@@ -809,7 +831,7 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
               ++used;
             }
           }
-          ok = ok && wait_all(&sh, &sh.y_full[slot], ring.round, a.status);
+          ok = ok && wait_all(&sh, &sh.y_full[slot], ring.round, a);
           if (ok && (adds || !ALIGNED)) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
@@ -862,7 +884,8 @@ __global__ void __launch_bounds__(expand_threads(GROUPS), 4 / GROUPS)
               asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
               __syncwarp();
             }
-            if (lane == 0) mbar_arrive(smem_u32(&sh.y_empty[slot]));
+            // (after a wait that ran out the place may still be filled: it is not given back)
+            if (lane == 0 && ok) mbar_arrive(smem_u32(&sh.y_empty[slot]));
             __syncwarp();
           }
           ring.next(a.slots);
@@ -997,6 +1020,11 @@ extern "C" fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n,
   g.tiles = reinterpret_cast<Tile*>(ws + l.tiles);
   g.order = reinterpret_cast<int*>(ws + l.order);
   g.s = ws + l.s;
+  const int stall = stalled();
+  g.no_first = stall & FLJSD_STALL_LOW_RANK_FIRST;
+  g.more_b = stall & FLJSD_STALL_LOW_RANK_SECOND ? 16 : 0;
+  g.more_y = stall & FLJSD_STALL_LOW_RANK_Y ? 16 : 0;
+  g.wait_ns = g.no_first || g.more_b || g.more_y ? kStallNs : kTimeoutNs;
   // B's rows, a column of y each, come as boxes of those of even numbers (among all adapters')
   // and of odd ones, as wide as the rank up to 64
   g.pitch = rank <= 16 ? 32 : rank <= 32 ? 64 : 128;

@@ -80,3 +80,45 @@ def test_verification_of_a_bad_request(fl, stall, bad):
     fl.verify_drafts(**x, status=status)
     torch.cuda.synchronize()
     assert status.item() == TIMEOUT
+
+
+def _adapters(tokens, k, n, rank, adapters, dtype):
+    g = torch.Generator("cuda").manual_seed(tokens + n)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    return dict(y=r(tokens, n).to(dtype), x=r(tokens, k).to(BF), a=(r(adapters, rank, k) / k ** 0.5).to(BF), b=r(adapters, n, rank).to(BF),
+                index=torch.randint(0, adapters, (tokens,), device="cuda", generator=g))
+
+
+# few tiles and many, one CTA on an SM and two, rows on 16 bytes and others, jobs of one block and of several
+@pytest.mark.parametrize("name", ["FIRST", "SECOND", "Y"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("case", [(5, 200, 512, 16, 2), (100, 520, 4099, 16, 70), (130, 64, 20000, 64, 3), (300, 1000, 33333, 128, 4)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_adapters(fl, stall, case, dtype, name):
+    z = _adapters(*case, dtype)
+    want = fl.low_rank_add(**z)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stall(getattr(fl._lib, f"FLJSD_STALL_LOW_RANK_{name}"))
+    fl.low_rank_add(**z, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == TIMEOUT
+    stall(0)
+    assert torch.equal(fl.low_rank_add(**z, status=status), want) and status.item() == 0
+
+
+def test_adapters_on_the_8_bit_head(fl, stall):
+    z = _adapters(40, 256, 1000, 16, 3, BF)
+    q = fl.fp8_quantize(torch.randn(1000, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(1)))
+    call = lambda: fl.fp8_linear(z["x"], *q, adapters=(z["a"], z["b"], index), status=status)  # noqa: E731
+    status, index = torch.zeros(1, dtype=torch.int32, device="cuda"), z["index"].clone()
+    want = call()
+    index[3] = 7  # (an index that names no adapter does not hide it)
+    stall(fl._lib.FLJSD_STALL_LOW_RANK_SECOND)
+    call()
+    torch.cuda.synchronize()
+    assert status.item() == TIMEOUT
+    stall(0)
+    call()
+    assert status.item() == 1
+    index.copy_(z["index"])
+    assert torch.equal(call(), want) and status.item() == 0
