@@ -12,9 +12,9 @@ from .api import _DT
 _BF, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
 
 
-def check_rows(name, t):
-    """The row stride of a matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or 0 in t.shape:
+def check_rows(name, t, least=1):
+    """The row stride of a matrix of at least so many rows, which are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < least or not t.shape[1]:
         raise ValueError(f"{name} must be a matrix")
     if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
@@ -97,15 +97,15 @@ def add(tokens, n, count, rank, x, ldx, a, b, index, scales, y, ldy, out, ldo):
 
 def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, stream=None):
     """y + scales[i] b[i] (a[i] x) for each token, i = index of the token (int64 [tokens]; -1:
-    y as it is). y [tokens, n] fp32 or bf16, x [tokens, k] bf16, a [adapters, rank, k] and
+    y as it is). y [tokens, n] (no tokens too) fp32 or bf16, x [tokens, k] bf16, a [adapters, rank, k] and
     b [adapters, n, rank] bf16 with a rank that is a multiple of 8 up to 128, scales fp32
     [adapters] or None (1). ``out``: receives the result, y itself or a tensor like it that
     shares no memory with any input. For serving: carries no gradient, and an input that
     would need one is refused. ``status``: an int32 on the device that receives the call's
     status word (0, FLJSD_ERR_INVALID_ARG for an index out of range, which counts as -1, or
     FLJSD_ERR_TIMEOUT)."""
-    ldy = check_rows("y", y)
-    ldx = check_rows("x", x)
+    ldy = check_rows("y", y, 0)
+    ldx = check_rows("x", x, 0)
     (tokens, n), dev = y.shape, y.device
     require_cuda("y", y)
     if y.dtype not in _DT:
@@ -120,17 +120,19 @@ def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, strea
         if (not isinstance(out, torch.Tensor) or out.dtype != y.dtype or tuple(out.shape) != (tokens, n)
                 or out.device != dev):
             raise ValueError(f"out must be {y.dtype} [{tokens}, {n}] on {dev}")
-        check_rows("out", out)
+        ldr = check_rows("out", out, 0)
         same = out.data_ptr() == y.data_ptr() and out.stride(0) == y.stride(0)
-        check_apart(out, y=None if same else y, x=x, a=a, b=b, index=index, scales=scales)
+        if tokens:
+            check_apart(out, y=None if same else y, x=x, a=a, b=b, index=index, scales=scales)
     with on(stream, dev):
-        r, ldr = out, n
+        r = out
         if out is None:
-            r = torch.empty((tokens, n), dtype=y.dtype, device=dev)
-        else:
-            ldr = check_rows("out", out)
-        ws = add(tokens, n, count, rank, x, ldx, a, b, index, scales, y, ldy, r, ldr)
-        report(status, ws)
+            r, ldr = torch.empty((tokens, n), dtype=y.dtype, device=dev), n
+        if tokens:
+            ws = add(tokens, n, count, rank, x, ldx, a, b, index, scales, y, ldy, r, ldr)
+            report(status, ws)
+        elif status is not None:
+            status.zero_()
     if out is None:
         hand_over((r,), stream, dev)
     else:  # autograd's own check of what it saved: this has changed
