@@ -121,7 +121,9 @@ def low_rank_add(y, x, a, b, index, scales=None, *, out=None, status=None, strea
                 or out.device != dev):
             raise ValueError(f"out must be {y.dtype} [{tokens}, {n}] on {dev}")
         ldr = check_rows("out", out, 0)
-        same = out.data_ptr() == y.data_ptr() and out.stride(0) == y.stride(0)
+        same = out.data_ptr() == y.data_ptr() and (ldr == ldy or tokens == 1)
+        if same:
+            ldr = ldy
         if tokens:
             check_apart(out, y=None if same else y, x=x, a=a, b=b, index=index, scales=scales)
     with on(stream, dev):
