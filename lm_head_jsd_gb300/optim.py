@@ -152,7 +152,7 @@ class AdamW:
         multiplied by. ``max_norm``: the step goes by gradients scaled (after that) to at
         most this norm of all of them together, as :func:`clip_grads` does; the gradients
         stay as they are, and ``grad_norm`` is their norm before that, an fp32 scalar on
-        the device. A norm of NaN makes every stepped value NaN."""
+        the device (0 without any gradients). A norm of NaN makes every stepped value NaN."""
         if max_norm is not None:
             check_max_norm(max_norm)
         grads = [p.grad for p in self.params] if grads is None else list(grads)
@@ -175,6 +175,11 @@ class AdamW:
             sizes = [n for g, n in zip(grads, sizes) if g is not None]
             stepped = [x for x, g in zip(stepped, grads * 2) if g is not None]
             if not live:
+                if max_norm is not None:  # (the norm of none)
+                    require_cuda("params[0]", self.params[0])
+                    with on(stream, self.device):
+                        self.grad_norm = torch.zeros((), dtype=torch.float32, device=self.device)
+                    hand_over((self.grad_norm,), stream, self.device)
                 return
             t["grad"] = _ptrs(live)
         dt, dev = live[0].dtype, self.device
