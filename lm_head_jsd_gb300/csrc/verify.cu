@@ -267,19 +267,21 @@ struct Cut {
 struct Row {
   const void* z;  // null: none
   float c;        // 0: greedy
+  int request;
   bool is_draft;
   int64_t stat;   // where the results go
   int64_t at;     // the drafted token in question, -1 behind the last
 };
 template <typename T>
-__device__ __forceinline__ Row row_of(const Args& a, int64_t unit, int fall) {
+__device__ __forceinline__ Row row_of(const Args& a, int64_t unit) {
   Row r{};
   const int b = (int)((uint32_t)unit / (uint32_t)a.slots);  // (fewer than 2^31)
   const int slot = (int)unit - b * a.slots;
   const Request q = request(a, b);
+  r.request = b;
   r.is_draft = slot > a.max_drafts;
   const int j = r.is_draft ? slot - a.max_drafts - 1 : slot;
-  if (!q.ok || b >= fall || j >= q.drafts + (r.is_draft ? 0 : 1) || (r.is_draft && q.t == 0.f)) return r;
+  if (!q.ok || j >= q.drafts + (r.is_draft ? 0 : 1) || (r.is_draft && q.t == 0.f)) return r;
   r.c = q.t == 0.f ? 0.f : a.temperature ? (float)(kLog2e / (double)q.t) : a.c;
   r.at = j < q.drafts ? q.start + j : -1;
   r.stat = r.is_draft ? q.start + j : q.start + j + b;
@@ -306,6 +308,8 @@ struct RowsShared {  // by the row's number
     Row row;
     float zd, m;  // the drafted token's logit, and the row's largest
   } own[kRing];
+  unsigned long long fell;  // the column warps have looked for offsets that fall
+  int fall[kRowWarps];      // the first that each has found, or kNoFall
   volatile int abort;
 };
 
@@ -340,12 +344,15 @@ __device__ __forceinline__ unsigned long long now() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-__device__ __forceinline__ void pause() {  // 100 us
+__device__ __noinline__ void pause() {  // 100 us
   const unsigned long long t0 = now();
   while (now() - t0 < 100'000) __nanosleep(1000);
 }
-// With a limit, after which the CTA's waits all end and the call's status word says so.
-__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, const Args& a) {
+// With a limit, after which the CTA's waits all end and the call's status word says so. (Not
+// inlined, as pause() is not: a kernel of few rows is a chain of first passes through its code,
+// and with a copy of this at each wait the row kernel took 25.9 us of 64 ragged requests, without
+// 25.0.)
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, int* status, unsigned long long ns) {
   unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
     if (bar_try(bar, parity)) return true;
@@ -353,9 +360,9 @@ __device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, vol
       if (*abort) return false;
       const unsigned long long t = now();
       if (!t0) t0 = t;
-      if (t - t0 > a.wait_ns) {
+      if (t - t0 > ns) {
         *abort = 1;
-        atomicExch(a.status, (int)FLJSD_ERR_TIMEOUT);
+        atomicExch(status, (int)FLJSD_ERR_TIMEOUT);
         return false;
       }
     }
@@ -366,7 +373,7 @@ __device__ __forceinline__ bool bar_wait(const void* bar, uint32_t parity, volat
   const uint32_t b = at_shared(bar);
   bool ok = bar_try(b, parity);
   if (!__all_sync(0xffffffffu, ok)) {
-    if (!ok) ok = bar_wait_long(b, parity, abort, a);
+    if (!ok) ok = bar_wait_long(b, parity, abort, a.status, a.wait_ns);
     ok = __all_sync(0xffffffffu, ok) != 0;
   } else {
     ok = true;
@@ -406,10 +413,6 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
   const int rank = (int)cta_rank();
   let_next_launch();
   if (blockIdx.x == 0 && tid == 0) *a.status = 0;
-  // what belongs to no request, or to one that is refused, is accepted with 0: k_verify_draw
-  // writes the other requests' over it
-  if (a.offsets || a.temperature)
-    for (int i = blockIdx.x * (kRowThreads + 32) + tid; i < (int)a.n; i += gridDim.x * (kRowThreads + 32)) a.prob[i] = 0.f;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sh.full[i], 1);
@@ -417,6 +420,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     }
     for (int i = 0; i < kTopRing; ++i) bar_init(&sh.tops[i], 1);
     for (int i = 0; i < kRing; ++i) bar_init(&sh.sums[i], 1);
+    bar_init(&sh.fell, kRowWarps);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -451,21 +455,6 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       const float zd = __shfl_sync(0xffffffffu, mine_zd, lane_of);
       if (lane == 0) sh.own[j % kRing].zd = zd;
     };
-    // From the first offsets that fall on, a request may claim rows that others have too: whose
-    // statistics stood in the end would be chance. So none of them is taken.
-    int fall = kNoFall, seen = 0;
-    auto look_for_fall = [&](int requests) {
-      while (seen < requests && fall == kNoFall) {
-        int first = kNoFall;
-#pragma unroll
-        for (int i = 7; i >= 0; --i) {
-          const int b = seen + i * 32 + lane;
-          if (b < requests && a.offsets[b] > a.offsets[b + 1]) first = b;
-        }
-        fall = __reduce_min_sync(0xffffffffu, first);
-        seen = min(seen + 256, requests);
-      }
-    };
     bool waiting = false;  // row 0's logit is not looked up yet: the first copies go before it
     int src_first = 0;
     auto catch_up = [&]() {
@@ -476,11 +465,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       while (!found && first_unit < units) {
         catch_up();
         const uint64_t unit = first_unit + (uint64_t)lane * step;
-        if (a.offsets) {
-          const uint64_t last = first_unit + 31ull * step;
-          look_for_fall((int)((last < units ? (uint32_t)last : units - 1) / (uint32_t)a.slots) + 1);
-        }
-        mine = unit < units ? row_of<T>(a, (int64_t)unit, fall) : Row{};
+        mine = unit < units ? row_of<T>(a, (int64_t)unit) : Row{};
         if (mine.z) {
           const Cut<T> cut(reinterpret_cast<const T*>(mine.z), a.v, a.cluster, rank);
           mine_j0 = (int64_t)cut.first * N - cut.lead;
@@ -552,6 +537,15 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       __syncwarp();
       return there;
     };
+    int fall = -1;  // as the other warps have found it
+    auto first_fall = [&]() {
+      if (fall < 0) {
+        fall = kNoFall;
+        if (a.offsets && bar_wait(&sh.fell, 0, &sh.abort, a))
+          for (int w = 0; w < kRowWarps; ++w) fall = min(fall, sh.fall[w]);
+      }
+      return fall;
+    };
     // what row i leaves to be written
     auto finish = [&](int i) {
       if (!bar_wait(&sh.sums[i % kRing], (i / kRing) & 1, &sh.abort, a)) return;
@@ -576,7 +570,8 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
         s.p = q;
         s.inv = (float)__shfl_sync(0xffffffffu, q, 1);
       }
-      if (lane == 0) (own.row.is_draft ? a.stat_d : a.stat_t)[own.row.stat] = s;
+      const bool stands = own.row.request < first_fall();
+      if (lane == 0 && stands) (own.row.is_draft ? a.stat_d : a.stat_t)[own.row.stat] = s;
     };
     bool ok = true;
     bool here = bring(0, ok), next = here && bring(1, ok);
@@ -595,8 +590,8 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
     }
     if (rank == 0 && i > 0) finish(i - 1);
     if (a.offsets && blockIdx.x == 0) {
-      look_for_fall((int)a.requests);
-      if (lane == 0) *a.fall = fall;
+      const int first = first_fall();
+      if (lane == 0) *a.fall = first;
     }
     unsigned long long t0 = 0;
     for (int j = max(0, brought - 2); j < brought; ++j)  // no copy is under way at the end
@@ -626,6 +621,29 @@ __global__ void __launch_bounds__(kRowThreads + 32, kRowCtas) k_verify_rows(cons
       return true;
     };
     bool here = send_top(0);
+    // While the first maxima are on their way:
+    // What belongs to no request, or to one that is refused, is accepted with 0: k_verify_draw
+    // writes the other requests' over it.
+    if (a.offsets || a.temperature)
+      for (int i = blockIdx.x * kRowThreads + tid; i < (int)a.n; i += gridDim.x * kRowThreads) a.prob[i] = 0.f;
+    // From the first offsets that fall on, a request may claim rows that others have too: whose
+    // statistics stood in the end would be chance. So theirs are not written.
+    if (a.offsets && rank == 0) {
+      int first = kNoFall;
+      for (int b0 = tid; b0 < (int)a.requests && first == kNoFall; b0 += 4 * kRowThreads) {
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          const int b = b0 + i * kRowThreads;
+          if (b < (int)a.requests && a.offsets[b] > a.offsets[b + 1]) first = b;
+        }
+      }
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) {
+        sh.fall[warp] = first;
+        bar_arrive(&sh.fell);
+      }
+      __syncwarp();
+    }
     for (int i = 0; here; ++i) {
       uint4 raw[kKept];
 #pragma unroll
@@ -805,8 +823,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify_draw(const Args a) {
   const int64_t b = blockIdx.x / a.cluster;
   if (a.cluster > 1) cluster_arrive();  // (none is written to before it has started)
   wait_for_previous();
+  const int fall = a.offsets ? *a.fall : kNoFall;
   Request q = request(a, b);
-  if (a.offsets && b >= *a.fall) {
+  if (b >= fall) {
     q.ok = false;
     q.drafts = 0;
   }
