@@ -592,14 +592,15 @@ fljsd_status fljsd_fp8_linear(int64_t m, int64_t n, int64_t k, int32_t x_dtype, 
  * free; those of one adapter need not be neighbours. The rank is a multiple of 8 (adapters
  * of smaller ranks are padded with zeros).
  * Products are added in fp32; A x, scaled, is carried on as the sum of two bf16 for y in
- * bf16 (2^-16 of it at most is lost) and of three for y in fp32 (2^-24); the result is added to y in fp32 and rounded once to dtype. A row's
- * result does not depend on the other rows.
+ * bf16 (2^-16 of it at most is lost) and of three for y in fp32 (2^-24); the result is added to y
+ * in fp32 and rounded once to dtype. A row's result does not depend on the other rows.
  * An index that is neither -1 nor in [0, adapters) counts as -1 and sets the status word
  * (the workspace's first int32) to FLJSD_ERR_INVALID_ARG; FLJSD_ERR_TIMEOUT there: a
  * bounded device wait expired and out is not complete.
  * workspace: fljsd_low_rank_workspace_bytes(tokens, adapters, rank) bytes. b and the
- * workspace are 16-byte aligned, everything else element-aligned (x and a are fastest on 16
- * bytes with ldx and k multiples of 8, y and out on two elements with even strides).
+ * workspace are 16-byte aligned, everything else element-aligned. (x and a are fastest on 16
+ * bytes with ldx and k multiples of 8, y and out on 16 bytes with ldy, ldo and n multiples of 16
+ * bytes: 8 bf16, 4 fp32. Other rows of y and out are added to one value at a time.)
  * Errors, found before anything is launched: FLJSD_ERR_INVALID_ARG for a dimension <= 0, a
  * stride below its row, a rank that is no multiple of 8, an unknown dtype, a null or
  * misaligned pointer, out at y's address with another stride; FLJSD_ERR_UNSUPPORTED for
@@ -647,9 +648,8 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  *  - a token whose draft row is such a row is refused, and drawn from p alone.
  *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets leave
  *    [0, drafts] or span more than max_drafts, every request from the first one on whose offsets
- *    fall, and a request whose temperature on the device is
- *    negative, infinite, NaN or so small that log2(e) / T is not finite, has accepted 0, -1s, and
- *    accept_prob 0 for its tokens. Both set the status word (the workspace's first int32) to
+ *    fall, and a request whose temperature on the device is negative, infinite, NaN or so small
+ *    that log2(e) / T is not finite, has accepted 0, -1s, and accept_prob 0 for its tokens. Both set the status word (the workspace's first int32) to
  *    FLJSD_ERR_INVALID_ARG.
  *  - FLJSD_ERR_TIMEOUT in the status word: a bounded device wait expired, the results are none
  *    (whatever else was wrong).

@@ -18,11 +18,14 @@
 // 32-bit integers, the constants taken off once.
 //
 // k_verify_rows: clusters take one row after the other and keep it in shared memory and
-// registers between finding its maximum and the sum, so that HBM is read once. Ten
-// instructions a column keep issue half busy (53%; the top stall is long scoreboard):
-// 256 requests of 4 drafts, V = 128256 bf16, 591 MB in 153 us = 3.9 TB/s. Doubles are
-// divided by one lane: with every thread dividing its own the two units for doubles of an
-// SM took the kernels 442 and 132 us.
+// registers between finding its maximum and the sum, so that HBM is read once. 256 requests of
+// 4 drafts, V = 128256 bf16: 591 MB in 153 us = 3.9 TB/s. Neither HBM nor issue (55%) is full:
+// of 10.3 instructions a column some six are its own (a thread's eight columns take 48), the
+// others a warp's share of the row's exchange, of waits and maxima, which 64 columns a thread
+// carry. Doubles are divided by one lane: with every thread dividing its own the two units for
+// doubles of an SM took the kernels 442 and 132 us.
+// Rows go to clusters by stride over all that a batch may have, so of ragged requests one
+// cluster may take twice as many as the mean, and the kernel as long as that one.
 // k_verify_draw, a cluster for each request: the tests, then one pass over the row where a
 // token is to be drawn (two rows after a refusal), each warp's vectors with a sum of their
 // own; those the number falls into are read again (the same requests: 39 us).

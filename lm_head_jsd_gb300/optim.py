@@ -152,7 +152,10 @@ class AdamW:
         multiplied by. ``max_norm``: the step goes by gradients scaled (after that) to at
         most this norm of all of them together, as :func:`clip_grads` does; the gradients
         stay as they are, and ``grad_norm`` is their norm before that, an fp32 scalar on
-        the device (0 without any gradients). A norm of NaN makes every stepped value NaN."""
+        the device (0 without any gradients). A norm of NaN makes every stepped value NaN.
+        The norm is that of this call's gradients alone. Several objects that share one (say of
+        bf16 and of fp32 parameters) take its factor each: ``norm = grad_norm(all gradients)``,
+        ``step(..., grad_scale=(max_norm / (norm + 1e-6)).clamp(max=1))``."""
         if max_norm is not None:
             check_max_norm(max_norm)
         grads = [p.grad for p in self.params] if grads is None else list(grads)
