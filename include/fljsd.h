@@ -649,8 +649,8 @@ fljsd_status fljsd_low_rank_add(int64_t tokens, int64_t k, int64_t n, int32_t ra
  *  - a drafted token outside [0, v) is refused (accept_prob 0); a request whose offsets leave
  *    [0, drafts] or span more than max_drafts, every request from the first one on whose offsets
  *    fall, and a request whose temperature on the device is negative, infinite, NaN or so small
- *    that log2(e) / T is not finite, has accepted 0, -1s, and accept_prob 0 for its tokens. Both set the status word (the workspace's first int32) to
- *    FLJSD_ERR_INVALID_ARG.
+ *    that log2(e) / T is not finite, has accepted 0, -1s, and accept_prob 0 for its tokens. Both
+ *    set the status word (the workspace's first int32) to FLJSD_ERR_INVALID_ARG.
  *  - FLJSD_ERR_TIMEOUT in the status word: a bounded device wait expired, the results are none
  *    (whatever else was wrong).
  *  - u_draw outside [0, 1) is taken to its nearer end, NaN as 0; u_accept of NaN refuses.
